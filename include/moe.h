@@ -398,6 +398,156 @@ moe_status_t moe_local_finalize_rerouting(const moe_bf16_t *local_y, const int32
                                           moe_stream_t stream);
 
 /*
+ * Balance loss of the router and its counts (the page has no counterpart: it
+ * describes inference; the loss is what a top-k router is trained with).
+ * With p = softmax(logits[t]), c[s, e] the assignments of sequence s to
+ * expert e and n_s its tokens that take part:
+ *   prob_mean[s, e] = (1 / n_s) sum_t p[t, e]            (0 where n_s = 0)
+ *   loss = (coef / S+) sum_s E / (k n_s) sum_e c[s, e] prob_mean[s, e]
+ * over the S+ sequences with n_s > 0 (0 if there is none); a uniform router
+ * has loss = coef.
+ *   logits      [T, E] fp32, finite or -inf; topk_idx [T, k] (moe_gate_topk's)
+ *   token_mask  [T] bytes, 0 = the token takes no part and its row is not
+ *               read (it may hold anything); NULL = all take part
+ *   seq_offsets [S+1] int32 device, ascending inside [0, T]: sequence s owns
+ *               tokens [seq_offsets[s], seq_offsets[s+1]); tokens outside
+ *               every sequence take no part.  NULL (with S = 1): all tokens.
+ *   loss [1] fp32, counts [S, E] int32, prob_mean [S, E] fp32,
+ *   n_tokens [S] int32: out
+ * S <= 65536.  Sums are fp32 in a fixed order: the result is deterministic.
+ * Expert ids outside [0, E) set MOE_DEV_BAD_EXPERT_ID and are not counted;
+ * bad bounds set MOE_DEV_BAD_OFFSETS.  T may be 0.  Workspace:
+ * moe_balance_loss_workspace_size() bytes, 256-byte aligned; its contents are
+ * scratch, every byte a call reads it has written.
+ */
+moe_status_t moe_balance_loss_workspace_size(int32_t T, int32_t E, int32_t S, size_t *bytes);
+moe_status_t moe_balance_loss(const float *logits, const int32_t *topk_idx,
+                              const uint8_t *token_mask, const int32_t *seq_offsets, int32_t S,
+                              int32_t T, int32_t E, int32_t k, float coef, float *loss,
+                              int32_t *counts, float *prob_mean, int32_t *n_tokens,
+                              void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                              moe_stream_t stream);
+
+/*
+ * Backward pass of moe_gate_topk and moe_balance_loss: the gradient of the
+ * logits.  The expert choice and the counts have no gradient.
+ *   d_topk_w [T, k] fp32: gradient of topk_w (renormalised with MOE_RENORM as
+ *            the forward call was), or NULL = none (topk_idx may then be NULL)
+ *   counts [S, E], n_tokens [S]: moe_balance_loss's outputs for the same
+ *            logits, mask, bounds and coef, or both NULL = no balance term
+ *            (coef, d_loss, seq_offsets and S are then ignored)
+ *   d_loss   [1] fp32 device: gradient of the loss, or NULL = 1
+ *   d_logits [T, E] fp32 out; a masked token's row is zero, whatever its
+ *            logits, indices and d_topk_w hold.
+ * Of a slot list that names an expert twice every slot counts; ids outside
+ * [0, E) set MOE_DEV_BAD_EXPERT_ID and those slots are left out.
+ */
+moe_status_t moe_gate_topk_backward(const float *logits, const int32_t *topk_idx,
+                                    const float *d_topk_w, const uint8_t *token_mask,
+                                    const int32_t *seq_offsets, int32_t S, const int32_t *counts,
+                                    const int32_t *n_tokens, const float *d_loss, float coef,
+                                    int32_t T, int32_t E, int32_t k, uint32_t flags,
+                                    float *d_logits, int32_t *dev_status, moe_stream_t stream);
+
+/*
+ * Backward pass of moe_finalize_routing:
+ *   d_y_exp[row, :] = topk_w[t, j] * d_out[t, :],  row = expanded_row_idx[t*k+j]
+ *   d_topk_w[t, j]  = sum_h d_out[t, h] * y_exp[row, h]
+ * (the shared term's gradient is d_out itself).
+ *   d_out [T, H] bf16 (fp32 with MOE_OUT_F32); y_exp, d_y_exp [T*k, H] bf16
+ *   (fp32 with MOE_Y_F32), d_y_exp not overlapping an input; topk_w,
+ *   d_topk_w [T, k] fp32, the dot products summed in fp32 in a fixed order.
+ * A slot whose row is negative has d_topk_w = 0; rows that no slot names are
+ * left untouched.  A row >= T*k sets MOE_DEV_BAD_OFFSETS and is left out.
+ * H % 8 == 0, k <= 32.
+ */
+moe_status_t moe_finalize_routing_backward(const void *d_out, const void *y_exp,
+                                           const int32_t *expanded_row_idx, const float *topk_w,
+                                           int32_t T, int32_t H, int32_t k, uint32_t flags,
+                                           void *d_y_exp, float *d_topk_w, int32_t *dev_status,
+                                           moe_stream_t stream);
+
+/*
+ * Microscaled 4-bit matrices: e2m1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives) under one scale byte per block of columns:
+ *   MOE_FP4_MX  blocks of 32; value = element * 2^(byte - 127)
+ *   MOE_FP4_NV  blocks of 16; value = element * e4m3(byte) * 2^scale_exp
+ * scale_exp (-60..60; 0 with MOE_FP4_MX) belongs to the whole matrix: it moves
+ * the range of the e4m3 scales (2^-9 .. 448) to that of the data.
+ *   q   [rows, K/2] bytes, the lower column of a pair in the low four bits
+ *   sf  the scale bytes in 512-byte tiles of 128 rows x 4 blocks (the form the
+ *       tensor cores take): row r, block b of a tile at (r % 32) * 16 +
+ *       (r / 32) * 4 + b; a 128-row block's tiles follow each other along K.
+ *       Rows sorted by group (`offsets` below): group g's row blocks start at
+ *       block offsets[g] / 128 + g.  moe_fp4_scales_size() gives the bytes
+ *       (G = 0: one ungrouped matrix, as weights are: [G * N, K] rows).
+ * Both 16-byte aligned.  K % 128 == 0, K <= 2^20.
+ */
+enum { MOE_FP4_MX = 0, MOE_FP4_NV = 1 };
+typedef struct {
+    uint8_t *q;
+    uint8_t *sf;
+    int32_t format;      /* MOE_FP4_MX or MOE_FP4_NV */
+    int32_t scale_exp;
+} moe_fp4_t;
+
+moe_status_t moe_fp4_scales_size(int32_t rows, int32_t K, int32_t G, int32_t format,
+                                 size_t *bytes);
+
+/*
+ * Quantise bf16 rows (the counterpart of init_routing's permute where the
+ * experts' weights are held in 4 bits): token t's row of x [T, K] goes to rows
+ * expanded_row_idx[t*k + j], j < k, of `out` ([T*k, K]); with expanded_row_idx
+ * NULL (and k = 1) to row t.
+ *   MX: scale 2^(floor(log2 amax) - 2) of the block's largest magnitude amax,
+ *       not below 2^-127;  NV: e4m3(amax / 6 / 2^scale_exp), nearest even, at
+ *       most 448.  Elements: nearest e2m1 of value / scale, ties to even,
+ *       beyond 6 to 6; zeros where the scale is zero.
+ *   offsets [G+1]: groups of the rows (fixes the scale layout); NULL with G = 0
+ * Rows that no slot names, negative rows and rows past offsets[G] are left
+ * untouched; a row >= T*k sets MOE_DEV_BAD_OFFSETS and is left out.
+ * k <= 32, G <= 1024.
+ * moe_fp4_dequantize gives the values back: x [n, K] bf16 out, exact (rows
+ * past offsets[G] are left untouched).
+ */
+moe_status_t moe_fp4_quantize(const moe_bf16_t *x, int32_t T, int32_t K,
+                              const int32_t *expanded_row_idx, int32_t k, const int32_t *offsets,
+                              int32_t G, const moe_fp4_t *out, int32_t *dev_status,
+                              moe_stream_t stream);
+moe_status_t moe_fp4_dequantize(const moe_fp4_t *m, int32_t n, int32_t K, const int32_t *offsets,
+                                int32_t G, moe_bf16_t *x, moe_stream_t stream);
+
+/*
+ * Grouped products of 4-bit operands on the block-scaled tensor cores, fp32
+ * accumulation ("GMM使能&&Routing优化", "MoE TP优化 / 计算分解"; group g owns
+ * rows [offsets[g], offsets[g+1]) of a, as in moe_grouped_mlp):
+ *   matmul:  y[r, :] = a[r] . w[g]^T          w [G, N, K], y [n, N] bf16, or
+ *            fp32 with MOE_Y_F32
+ *   swiglu:  act[r, :] = bf16(SiLU(gate) * up), gate = a[r] . w13[g, 0..I-1]^T,
+ *            up = a[r] . w13[g, I..2I-1]^T     w13 [G, 2I, K]
+ *            act [n, I] bf16, or act4: the same bf16 values quantised as
+ *            moe_fp4_quantize does (exactly one of the two, the other NULL)
+ *   mlp:     act = swiglu(expanded_x, w13) in 4 bits, y = matmul(act, w2);
+ *            w13 [G, 2I, H], w2 [G, H, I], act [n, I] written
+ * All matrices of a call have one format; `a` and `act` are grouped by
+ * offsets, the weights' scales are ungrouped [G*rows, K].  Rows past
+ * offsets[G] are left untouched.  K, N, I multiples of 128, G <= 1024.  Bad
+ * offsets set MOE_DEV_BAD_OFFSETS; nothing is written then.
+ */
+moe_status_t moe_fp4_grouped_matmul(const moe_fp4_t *a, const int32_t *offsets, int32_t G,
+                                    const moe_fp4_t *w, int32_t n, int32_t K, int32_t N,
+                                    uint32_t flags, void *y, int32_t *dev_status,
+                                    moe_stream_t stream);
+moe_status_t moe_fp4_grouped_swiglu(const moe_fp4_t *a, const int32_t *offsets, int32_t G,
+                                    const moe_fp4_t *w13, int32_t n, int32_t K, int32_t I,
+                                    moe_bf16_t *act, const moe_fp4_t *act4, int32_t *dev_status,
+                                    moe_stream_t stream);
+moe_status_t moe_fp4_grouped_mlp(const moe_fp4_t *expanded_x, const int32_t *offsets, int32_t G,
+                                 const moe_fp4_t *w13, const moe_fp4_t *w2, int32_t n, int32_t H,
+                                 int32_t I, uint32_t flags, const moe_fp4_t *act, void *y,
+                                 int32_t *dev_status, moe_stream_t stream);
+
+/*
  * Diagnostics (the page has no counterpart): enqueue a kernel that waits,
  * through the same bounded wait every pipeline here uses, on a barrier that
  * nothing completes.  After about one second it ORs MOE_DEV_TIMEOUT into

@@ -45,7 +45,11 @@ EXPORTS = ("moe_status_string", "moe_rmsnorm_gate", "moe_rmsnorm_sumsq",
            "moe_grouped_mlp", "moe_finalize_routing", "moe_layer_workspace_size",
            "moe_layer_forward", "moe_layer_forward_timed", "moe_layer_forward_streams",
            "moe_layer_forward_host", "moe_local_rerouting",
-           "moe_local_finalize_rerouting", "moe_selftest_wait_timeout")
+           "moe_local_finalize_rerouting", "moe_selftest_wait_timeout",
+           "moe_balance_loss_workspace_size", "moe_balance_loss", "moe_gate_topk_backward",
+           "moe_finalize_routing_backward", "moe_fp4_scales_size", "moe_fp4_quantize",
+           "moe_fp4_dequantize", "moe_fp4_grouped_matmul", "moe_fp4_grouped_swiglu",
+           "moe_fp4_grouped_mlp")
 NUM_STAGES = 6
 STAGE_NAMES = ("router", "route_scan_scatter", "permute", "gemm_w13_swiglu", "gemm_down",
                "finalize")
@@ -62,6 +66,13 @@ class MoeDesc(ctypes.Structure):
                 ("k", ctypes.c_int32), ("I", ctypes.c_int32), ("I_shared", ctypes.c_int32),
                 ("rms_eps", ctypes.c_float), ("flags", ctypes.c_uint32)]
 
+
+class _Fp4(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("sf", ctypes.c_void_p), ("format", ctypes.c_int32),
+                ("scale_exp", ctypes.c_int32)]
+
+
+FP4_FORMATS = {"mx": 0, "nv": 1}
 
 _lock = threading.Lock()
 _lib = None
@@ -106,6 +117,17 @@ def lib() -> ctypes.CDLL:
                                               P, SZ, P, P, P, P, P, P],
                 "moe_layer_forward_host": [ctypes.POINTER(MoeDesc), I32, P, P, P, P, P, P, P, P,
                                            P, P, P, P, SZ, P, P, P, P, P],
+                "moe_balance_loss_workspace_size": [I32, I32, I32, PSZ],
+                "moe_balance_loss": [P, P, P, P, I32, I32, I32, I32, F, P, P, P, P, P, SZ, P, P],
+                "moe_gate_topk_backward": [P, P, P, P, P, I32, P, P, P, F, I32, I32, I32, U32, P,
+                                           P, P],
+                "moe_finalize_routing_backward": [P, P, P, P, I32, I32, I32, U32, P, P, P, P],
+                "moe_fp4_scales_size": [I32, I32, I32, I32, PSZ],
+                "moe_fp4_quantize": [P, I32, I32, P, I32, P, I32, P, P, P],
+                "moe_fp4_dequantize": [P, I32, I32, P, I32, P, P],
+                "moe_fp4_grouped_matmul": [P, P, I32, P, I32, I32, I32, U32, P, P, P],
+                "moe_fp4_grouped_swiglu": [P, P, I32, P, I32, I32, I32, P, P, P, P],
+                "moe_fp4_grouped_mlp": [P, P, I32, P, P, I32, I32, I32, U32, P, P, P, P],
             }
             for name, args in sigs.items():
                 fn = getattr(L, name)
@@ -321,6 +343,276 @@ def finalize_routing(y_exp, row_idx, topk_w, shared=None, out_f32=False):
     _call("moe_finalize_routing", _ptr(y_exp), _ptr(row_idx), _ptr(topk_w), _ptr(shared), T, H,
           k, flags, _ptr(out), _stream(y_exp.device))
     return out
+
+
+# ------------------------------------------------------- training the router
+def _same_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _shape(t, shape, name):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _router_args(logits, topk_idx, token_mask, seq_offsets):
+    _check(logits, torch.float32, "logits")
+    _check(topk_idx, torch.int32, "topk_idx")
+    _check(seq_offsets, torch.int32, "seq_offsets")
+    if token_mask is not None and token_mask.dtype != torch.bool:
+        _check(token_mask, torch.uint8, "token_mask")
+    T, E = logits.shape
+    _shape(token_mask, (T,), "token_mask")
+    if topk_idx is not None:
+        _shape(topk_idx, (T, topk_idx.shape[-1]), "topk_idx")
+    if seq_offsets is not None and (seq_offsets.dim() != 1 or seq_offsets.numel() < 2):
+        raise ValueError("seq_offsets: [S + 1] with S >= 1")
+    _same_device(logits.device, topk_idx=topk_idx, token_mask=token_mask, seq_offsets=seq_offsets)
+    return T, E, 1 if seq_offsets is None else seq_offsets.numel() - 1
+
+
+def balance_loss(logits, topk_idx, coef=1.0, token_mask=None, seq_offsets=None, status=None):
+    """Balance loss of the router over the sequences given by ``seq_offsets``
+    (int32 [S+1]; None: all tokens are one), without the tokens whose
+    ``token_mask`` (bool or uint8 [T]) is zero.
+    -> dict(loss fp32 [], counts int32 [S, E], prob_mean fp32 [S, E],
+    n_tokens int32 [S], coef); gate_topk_backward takes the dict."""
+    T, E, S = _router_args(logits, topk_idx, token_mask, seq_offsets)
+    k = topk_idx.shape[1]
+    dev = logits.device
+    n = ctypes.c_size_t(0)
+    _call("moe_balance_loss_workspace_size", T, E, S, ctypes.byref(n))
+    with torch.cuda.device(dev):
+        loss = torch.empty((), dtype=torch.float32, device=dev)
+        counts = torch.empty((S, E), dtype=torch.int32, device=dev)
+        prob = torch.empty((S, E), dtype=torch.float32, device=dev)
+        n_tokens = torch.empty(S, dtype=torch.int32, device=dev)
+        ws = torch.empty(n.value, dtype=torch.uint8, device=dev)
+        _call("moe_balance_loss", _ptr(logits), _ptr(topk_idx), _ptr(token_mask),
+              _ptr(seq_offsets), S, T, E, k, float(coef), _ptr(loss), _ptr(counts), _ptr(prob),
+              _ptr(n_tokens), _ptr(ws), n.value, _ptr(status), _stream(dev))
+    return dict(loss=loss, counts=counts, prob_mean=prob, n_tokens=n_tokens, coef=float(coef))
+
+
+def gate_topk_backward(logits, topk_idx, d_topk_w=None, renorm=True, balance=None, d_loss=None,
+                       token_mask=None, seq_offsets=None, status=None):
+    """Gradient of the gate's logits (fp32 [T, E]) from ``d_topk_w`` (the
+    gradient of gate_topk's weights, or None) and, with ``balance`` (what
+    balance_loss returned for the same logits, mask and bounds), from the
+    balance loss times ``d_loss`` (fp32 [1] or [], None: 1)."""
+    T, E, S = _router_args(logits, topk_idx, token_mask, seq_offsets)
+    dev = logits.device
+    _check(d_topk_w, torch.float32, "d_topk_w")
+    _check(d_loss, torch.float32, "d_loss")
+    k = topk_idx.shape[1]
+    _shape(d_topk_w, (T, k), "d_topk_w")
+    counts = n_tokens = None
+    coef = 0.0
+    if balance is not None:
+        counts, n_tokens, coef = balance["counts"], balance["n_tokens"], balance["coef"]
+        _check(counts, torch.int32, "counts")
+        _check(n_tokens, torch.int32, "n_tokens")
+        _shape(counts, (S, E), "counts")
+        _shape(n_tokens, (S,), "n_tokens")
+        if d_loss is not None and d_loss.numel() != 1:
+            raise ValueError("d_loss must hold one value")
+    _same_device(dev, d_topk_w=d_topk_w, d_loss=d_loss, counts=counts, n_tokens=n_tokens)
+    with torch.cuda.device(dev):
+        d = torch.empty_like(logits)
+        _call("moe_gate_topk_backward", _ptr(logits), _ptr(topk_idx), _ptr(d_topk_w),
+              _ptr(token_mask), _ptr(seq_offsets), S, _ptr(counts), _ptr(n_tokens), _ptr(d_loss),
+              coef, T, E, k, RENORM if renorm else 0, _ptr(d), _ptr(status), _stream(dev))
+    return d
+
+
+def finalize_routing_backward(d_out, y_exp, row_idx, topk_w, status=None):
+    """-> (d_y_exp like y_exp, d_topk_w fp32 [T, k]) from the gradient of
+    finalize_routing's output (bf16 or fp32).  The shared rows' gradient is
+    d_out itself.  Rows of d_y_exp that row_idx does not name are not set."""
+    for t, name in ((d_out, "d_out"), (y_exp, "y_exp")):
+        if t.dtype != torch.float32:
+            _check(t, torch.bfloat16, name)
+    _check(row_idx, torch.int32, "row_idx")
+    _check(topk_w, torch.float32, "topk_w")
+    T, k = topk_w.shape
+    H = y_exp.shape[1]
+    dev = y_exp.device
+    _shape(d_out, (T, H), "d_out")
+    _shape(y_exp, (T * k, H), "y_exp")
+    if row_idx.numel() != T * k:
+        raise ValueError("row_idx must hold T * k rows")
+    _same_device(dev, d_out=d_out, row_idx=row_idx, topk_w=topk_w)
+    flags = (OUT_F32 if d_out.dtype == torch.float32 else 0) | \
+        (Y_F32 if y_exp.dtype == torch.float32 else 0)
+    with torch.cuda.device(dev):
+        d_y = torch.empty_like(y_exp)
+        d_w = torch.empty_like(topk_w)
+        _call("moe_finalize_routing_backward", _ptr(d_out), _ptr(y_exp), _ptr(row_idx),
+              _ptr(topk_w), T, H, k, flags, _ptr(d_y), _ptr(d_w), _ptr(status), _stream(dev))
+    return d_y, d_w
+
+
+# ------------------------------------------------------------ 4-bit operands
+@dataclasses.dataclass
+class Fp4Matrix:
+    """A microscaled 4-bit matrix: codes ``q`` (uint8 [rows, K/2], weights
+    [G, rows, K/2]), scale tiles ``sf`` (uint8, see include/moe.h), ``fmt``
+    "mx" or "nv" and, for "nv", the exponent of the whole matrix."""
+    q: torch.Tensor
+    sf: torch.Tensor
+    fmt: str = "mx"
+    scale_exp: int = 0
+
+    @property
+    def K(self) -> int:
+        return self.q.shape[-1] * 2
+
+
+def fp4_scales_size(rows, K, fmt="mx", groups=0) -> int:
+    """Bytes of the scale tiles of ``rows`` rows (in ``groups`` groups; 0 for
+    an ungrouped matrix such as a weight)."""
+    n = ctypes.c_size_t(0)
+    _call("moe_fp4_scales_size", rows, K, groups, _fp4_format(fmt), ctypes.byref(n))
+    return n.value
+
+
+def _fp4_format(fmt) -> int:
+    if fmt not in FP4_FORMATS:
+        raise ValueError(f"fmt must be one of {sorted(FP4_FORMATS)}, got {fmt!r}")
+    return FP4_FORMATS[fmt]
+
+
+def _fp4_empty(rows, K, fmt, scale_exp, groups, dev) -> Fp4Matrix:
+    return Fp4Matrix(torch.empty((rows, K // 2), dtype=torch.uint8, device=dev),
+                     torch.empty(fp4_scales_size(rows, K, fmt, groups), dtype=torch.uint8,
+                                 device=dev), fmt, int(scale_exp))
+
+
+def _fp4_arg(m: Fp4Matrix, name, groups, dev, rows=None):
+    """The C struct of a matrix, its buffers checked against the layout."""
+    _check(m.q, torch.uint8, name + ".q")
+    _check(m.sf, torch.uint8, name + ".sf")
+    n = m.q.numel() // max(m.q.shape[-1], 1) if rows is None else rows
+    if m.sf.numel() < fp4_scales_size(n, m.K, m.fmt, groups):
+        raise ValueError(f"{name}.sf is smaller than its scale tiles")
+    _same_device(dev, **{name + ".q": m.q, name + ".sf": m.sf})
+    return ctypes.byref(_Fp4(_ptr(m.q), _ptr(m.sf), _fp4_format(m.fmt), m.scale_exp))
+
+
+def fp4_quantize(x, fmt="mx", scale_exp=0, row_idx=None, k=1, offsets=None,
+                 status=None) -> Fp4Matrix:
+    """bf16 rows to 4 bits.  With ``row_idx`` (init_routing's, int32 [T*k]) and
+    ``offsets``, token rows go to their k rows in expert order.  A weight
+    [G, N, K] keeps its shape in ``q`` and is quantised ungrouped.  Rows that
+    row_idx does not name are not set."""
+    _check(x, torch.bfloat16, "x")
+    _check(row_idx, torch.int32, "row_idx")
+    _check(offsets, torch.int32, "offsets")
+    K = x.shape[-1]
+    T = x.numel() // K if K else 0
+    dev = x.device
+    if row_idx is not None and row_idx.numel() != T * k:
+        raise ValueError("row_idx must hold T * k rows")
+    if row_idx is None and k != 1:
+        raise ValueError("k needs row_idx")
+    _same_device(dev, row_idx=row_idx, offsets=offsets)
+    G = 0 if offsets is None else offsets.numel() - 1
+    with torch.cuda.device(dev):
+        m = _fp4_empty(T * k, K, fmt, scale_exp, G, dev)
+        _call("moe_fp4_quantize", _ptr(x), T, K, _ptr(row_idx), k, _ptr(offsets), G,
+              _fp4_arg(m, "out", G, dev), _ptr(status), _stream(dev))
+    if x.dim() != 2:
+        m.q = m.q.view(*x.shape[:-1], K // 2)
+    return m
+
+
+def fp4_dequantize(m: Fp4Matrix, offsets=None):
+    """-> bf16 values of a 4-bit matrix, exact (``offsets`` as it was made
+    with; rows past the last group are not set)."""
+    _check(offsets, torch.int32, "offsets")
+    dev = m.q.device
+    _same_device(dev, offsets=offsets)
+    G = 0 if offsets is None else offsets.numel() - 1
+    n = m.q.numel() // max(m.q.shape[-1], 1)
+    with torch.cuda.device(dev):
+        x = torch.empty((*m.q.shape[:-1], m.K), dtype=torch.bfloat16, device=dev)
+        _call("moe_fp4_dequantize", _fp4_arg(m, "m", G, dev), n, m.K, _ptr(offsets), G, _ptr(x),
+              _stream(dev))
+    return x
+
+
+def _fp4_product(a, offsets, w, name):
+    """(n, K, G, rows of a group's weights) of a grouped 4-bit product."""
+    _check(offsets, torch.int32, "offsets")
+    if a.q.dim() != 2 or w.q.dim() != 3 or a.K != w.K:
+        raise ValueError(f"{name}: a [n, K/2] and weights [G, rows, K/2] of the same K")
+    G, rows, _ = w.q.shape
+    if offsets.numel() != G + 1:
+        raise ValueError(f"{name}: offsets must hold G + 1 rows")
+    _same_device(a.q.device, offsets=offsets)
+    return a.q.shape[0], a.K, G, rows
+
+
+def fp4_grouped_matmul(a: Fp4Matrix, offsets, w: Fp4Matrix, out_f32=False, out=None, status=None):
+    """y = a . w[group]^T -> [n, N] bf16 (fp32 with out_f32).  Rows past the
+    last group are left as they were in ``out`` (not set without it)."""
+    n, K, G, N = _fp4_product(a, offsets, w, "fp4_grouped_matmul")
+    dev = a.q.device
+    dt = torch.float32 if out_f32 else torch.bfloat16
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty((n, N), dtype=dt, device=dev)
+        _check(out, dt, "out")
+        _shape(out, (n, N), "out")
+        _call("moe_fp4_grouped_matmul", _fp4_arg(a, "a", G, dev), _ptr(offsets), G,
+              _fp4_arg(w, "w", 0, dev), n, K, N, Y_F32 if out_f32 else 0, _ptr(out),
+              _ptr(status), _stream(dev))
+    return out
+
+
+def fp4_grouped_swiglu(a: Fp4Matrix, offsets, w13: Fp4Matrix, quantize=False, scale_exp=0,
+                       out=None, status=None):
+    """act = SiLU(gate) * up of the merged w13 [G, 2I, K] -> bf16 [n, I], or
+    with ``quantize`` the same values in 4 bits (an Fp4Matrix of a's format,
+    grouped by ``offsets``)."""
+    n, K, G, rows = _fp4_product(a, offsets, w13, "fp4_grouped_swiglu")
+    I = rows // 2
+    dev = a.q.device
+    with torch.cuda.device(dev):
+        if quantize:
+            if out is None:
+                out = _fp4_empty(n, I, a.fmt, scale_exp, G, dev)
+            _shape(out.q, (n, I // 2), "out.q")
+            bf, q4 = None, _fp4_arg(out, "out", G, dev)
+        else:
+            if out is None:
+                out = torch.empty((n, I), dtype=torch.bfloat16, device=dev)
+            _check(out, torch.bfloat16, "out")
+            _shape(out, (n, I), "out")
+            bf, q4 = _ptr(out), None
+        _call("moe_fp4_grouped_swiglu", _fp4_arg(a, "a", G, dev), _ptr(offsets), G,
+              _fp4_arg(w13, "w13", 0, dev), n, K, I, bf, q4, _ptr(status), _stream(dev))
+    return out
+
+
+def fp4_grouped_mlp(expanded_x: Fp4Matrix, offsets, w13: Fp4Matrix, w2: Fp4Matrix, y_f32=False,
+                    act_exp=0, status=None):
+    """-> (act Fp4Matrix [n, I], y bf16 [n, H], fp32 with y_f32)."""
+    n, H, G, rows = _fp4_product(expanded_x, offsets, w13, "fp4_grouped_mlp")
+    I = rows // 2
+    if tuple(w2.q.shape) != (G, H, I // 2):
+        raise ValueError("w2 must be [G, H, I/2]")
+    dev = expanded_x.q.device
+    with torch.cuda.device(dev):
+        act = _fp4_empty(n, I, expanded_x.fmt, act_exp, G, dev)
+        y = torch.empty((n, H), dtype=torch.float32 if y_f32 else torch.bfloat16, device=dev)
+        _call("moe_fp4_grouped_mlp", _fp4_arg(expanded_x, "expanded_x", G, dev), _ptr(offsets), G,
+              _fp4_arg(w13, "w13", 0, dev), _fp4_arg(w2, "w2", 0, dev), n, H, I,
+              Y_F32 if y_f32 else 0, _fp4_arg(act, "act", G, dev), _ptr(y), _ptr(status),
+              _stream(dev))
+    return act, y
 
 
 def make_desc(T, H, E, k, I, I_shared=0, rmsnorm=False, eps=1e-6, renorm=True,
