@@ -20,6 +20,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <stdlib.h>
+
 #include <algorithm>
 #include <mutex>
 
@@ -51,6 +53,7 @@ struct Params {
     CUtensorMap tmB;        // codes of W: [G, rows, K / 2] bytes, likewise
     CUtensorMap tmSA;       // scale tiles of A and W: [tiles, 128] 32-bit words
     CUtensorMap tmSB;
+    CUtensorMap tmO;        // output, 32-row x 64-byte boxes (pair kernel, not SWIGLU_Q)
     const int32_t *offsets;
     int32_t G, n, K, N;     // N: output columns
     int32_t nt;             // column tiles per row block
@@ -92,45 +95,105 @@ __host__ __device__ constexpr uint32_t idesc(int M, int N, int id) {
            (static_cast<uint32_t>(M >> 7) << 27) | (static_cast<uint32_t>(id) << 29);
 }
 
-template <int FMT>
-__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t id,
-                                        uint32_t sa, uint32_t sb, uint32_t accumulate) {
-    if (FMT == MOE_FP4_MX)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X"
-            " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(id), "r"(sa), "r"(sb), "r"(accumulate)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X"
-            " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(id), "r"(sa), "r"(sb), "r"(accumulate)
-            : "memory");
+// One lane of a converged warp.  The loops below that issue TMA and tcgen05
+// instructions run under this test and not under `lane == 0`: the compiler then
+// knows that one lane is active and feeds the instructions' uniform operands
+// directly.  Measured: 43 cycles an MMA or scale copy to issue against 80,
+// where an MMA of 256 x 256 x 64 takes 128 and a slice of four needs six to
+// twelve copies besides.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
 }
 
+// D (+)= A * B^T with the scales at sa (rows of A) and sb (rows of B).
+// CG = 2: M = 256 over a CTA pair, each CTA holding its 128 rows of A (and
+// their scales), half the rows of B and the scales of all of them.
+#define MOE_MMA_FP4(GROUP, KIND)                                                              \
+    asm volatile("{\n\t.reg .pred p;\n\t"                                                     \
+                 "setp.ne.b32 p, %6, 0;\n\t"                                                  \
+                 "tcgen05.mma.cta_group::" GROUP ".kind::" KIND                               \
+                 " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),                           \
+                 "l"(a), "l"(b), "r"(id), "r"(sa), "r"(sb), "r"(accumulate)                   \
+                 : "memory")
+template <int FMT, int CG>
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t id,
+                                        uint32_t sa, uint32_t sb, uint32_t accumulate) {
+    if (FMT == MOE_FP4_MX && CG == 1)
+        MOE_MMA_FP4("1", "mxf4.block_scale.scale_vec::2X");
+    else if (FMT == MOE_FP4_MX)
+        MOE_MMA_FP4("2", "mxf4.block_scale.scale_vec::2X");
+    else if (CG == 1)
+        MOE_MMA_FP4("1", "mxf4nvf4.block_scale.scale_vec::4X");
+    else
+        MOE_MMA_FP4("2", "mxf4nvf4.block_scale.scale_vec::4X");
+}
+#undef MOE_MMA_FP4
+
 // One 512-byte scale tile (32 rows of 16 bytes) into four columns of tensor
-// memory, repeated in its four lane quarters.  Ordered before the MMAs this
-// thread issues afterwards, and behind those it issued before.
+// memory, repeated in its four lane quarters (CG = 2: in both CTAs, each from
+// its own shared memory).  Ordered before the MMAs this thread issues
+// afterwards, and behind those it issued before.
+template <int CG>
 __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
     uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
     d |= static_cast<uint64_t>(128u >> 4) << 16;
     d |= static_cast<uint64_t>(128u >> 4) << 32;      // 8-row groups of 16-byte rows
     d |= static_cast<uint64_t>(1u) << 46;
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+    if (CG == 1)
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d)
+                     : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d)
+                     : "memory");
 }
 
 struct Tile {
-    int g, m_blk, row0, row_end, n_blk;
+    int g, row0, row_end, n_blk;
 };
+
+// Checks the group offsets and lists the tiles: s_prefix[g] = tiles (of BMT
+// rows) of the groups before g.  Returns false for bad offsets.  All threads.
+template <int BMT>
+__device__ bool list_tiles(const Params &p, int *s_off, int *s_prefix, volatile int *s_bad) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    for (int g = tid; g <= p.G; g += blockDim.x) s_off[g] = p.offsets[g];
+    if (tid == 0) *s_bad = 0;
+    __syncthreads();
+    if (tid < 32) {
+        int run = 0;
+        bool bad = false;
+        for (int g0 = 0; g0 < p.G; g0 += 32) {
+            const int g = g0 + lane;
+            int tiles = 0;
+            if (g < p.G) {
+                const int a = s_off[g], b = s_off[g + 1];
+                if (a < 0 || b < a || b > p.n) bad = true;
+                tiles = b > a ? ((b - a + BMT - 1) / BMT) * p.nt : 0;
+            }
+            int inc = tiles;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, inc, off);
+                if (lane >= off) inc += o;
+            }
+            if (g < p.G) s_prefix[g] = run + inc - tiles;
+            run += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        if (lane == 0) s_prefix[p.G] = run;
+        if (__any_sync(0xffffffffu, bad) && lane == 0) *s_bad = 1;
+    }
+    __syncthreads();
+    return *s_bad == 0;
+}
 
 // Tiles of a group: rows fastest while the group has fewer rows than its
 // weights (a weight tile is read from L2 by its row blocks one after the
 // other), columns fastest otherwise.
+template <int BMT>
 __device__ __forceinline__ Tile decode_tile(const Params &p, int tile, const int *s_off,
                                             const int *s_prefix) {
     int lo = 0, hi = p.G - 1;
@@ -143,13 +206,12 @@ __device__ __forceinline__ Tile decode_tile(const Params &p, int tile, const int
     }
     Tile t;
     const int cnt = s_off[lo + 1] - s_off[lo];
-    const int mt = (cnt + BM - 1) / BM;
+    const int mt = (cnt + BMT - 1) / BMT;
     const int local = tile - s_prefix[lo];
     const bool nfast = cnt > p.wrows;
     t.g = lo;
-    t.m_blk = nfast ? local / p.nt : local % mt;
     t.n_blk = nfast ? local % p.nt : local / mt;
-    t.row0 = s_off[lo] + t.m_blk * BM;
+    t.row0 = s_off[lo] + (nfast ? local / p.nt : local % mt) * BMT;
     t.row_end = s_off[lo + 1];
     return t;
 }
@@ -212,35 +274,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
     int *s_prefix = reinterpret_cast<int *>(smem + C::PREFIX_OFF);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    if (tid == 0) {
-        *s_abort = 0;
-        *s_bad = 0;
-    }
-    for (int g = tid; g <= p.G; g += THREADS) s_off[g] = p.offsets[g];
-    __syncthreads();
-    if (warp == 0) {
-        int run = 0;
-        bool bad = false;
-        for (int g0 = 0; g0 < p.G; g0 += 32) {
-            const int g = g0 + lane;
-            int tiles = 0;
-            if (g < p.G) {
-                const int a = s_off[g], b = s_off[g + 1];
-                if (a < 0 || b < a || b > p.n) bad = true;
-                tiles = b > a ? ((b - a + BM - 1) / BM) * p.nt : 0;
-            }
-            int inc = tiles;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int o = __shfl_up_sync(0xffffffffu, inc, off);
-                if (lane >= off) inc += o;
-            }
-            if (g < p.G) s_prefix[g] = run + inc - tiles;
-            run += __shfl_sync(0xffffffffu, inc, 31);
-        }
-        if (lane == 0) s_prefix[p.G] = run;
-        if (__any_sync(0xffffffffu, bad) && lane == 0) *s_bad = 1;
-    }
+    if (tid == 0) *s_abort = 0;
     if (tid == 32) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 1);
@@ -252,8 +286,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
         mbar_init(drain, 1);
         fence_barrier_init();
     }
-    __syncthreads();
-    if (*s_bad) {
+    if (!list_tiles<BM>(p, s_off, s_prefix, s_bad)) {
         if (tid == 0 && blockIdx.x == 0) report(p.dev_status, MOE_DEV_BAD_OFFSETS);
         return;
     }
@@ -271,7 +304,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
 
     if (warp == 0) {
         // ================= TMA producer
-        if (lane == 0) {
+        if (elect_one()) {
             tma_prefetch_desc(&p.tmA);
             tma_prefetch_desc(&p.tmB);
             tma_prefetch_desc(&p.tmSA);
@@ -281,7 +314,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
             int armed[STAGES];
             for (int s = 0; s < STAGES; ++s) armed[s] = -1;
             for (int tile = blockIdx.x; tile < total && !*s_abort; tile += gridDim.x) {
-                const Tile t = decode_tile(p, tile, s_off, s_prefix);
+                const Tile t = decode_tile<BM>(p, tile, s_off, s_prefix);
                 const int sa_blk = static_cast<int>(scale_row_block(t.g, s_off[t.g], t.row0));
                 const int b0 = MODE == MODE_STORE ? t.n_blk * BN : t.n_blk * 128;
                 const int b1 = MODE == MODE_STORE ? b0 + 128 : p.N + b0;
@@ -322,7 +355,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
         __syncwarp();
     } else if (warp == 1) {
         // ================= MMA issuer
-        if (lane == 0) {
+        if (elect_one()) {
             int stage = 0;
             uint32_t phase = 0;
             int acc = 0;
@@ -347,9 +380,9 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
                     const uint32_t sb = sa + C::SA_BYTES;
 #pragma unroll
                     for (int i = 0; i < C::TILES; ++i) {
-                        copy_scales(sa_t + 4 * i, sa + i * kScaleTile);
-                        copy_scales(sb_t + 8 * i, sb + i * kScaleTile);
-                        copy_scales(sb_t + 8 * i + 4, sb + C::SA_BYTES + i * kScaleTile);
+                        copy_scales<1>(sa_t + 4 * i, sa + i * kScaleTile);
+                        copy_scales<1>(sb_t + 8 * i, sb + i * kScaleTile);
+                        copy_scales<1>(sb_t + 8 * i + 4, sb + C::SA_BYTES + i * kScaleTile);
                     }
                     // the last slice may hold 128 columns only
                     const int steps = min(BK, p.K - kb * BK) / 64;
@@ -357,7 +390,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
                         const int i = FMT == MOE_FP4_MX ? kk / 2 : kk;
                         const uint32_t id = FMT == MOE_FP4_MX && (kk & 1) ? idesc<FMT>(BM, BN, 2)
                                                                           : idesc<FMT>(BM, BN, 0);
-                        mma_fp4<FMT>(d, sdesc_kmajor_sw128(a + kk * 32),
+                        mma_fp4<FMT, 1>(d, sdesc_kmajor_sw128(a + kk * 32),
                                      sdesc_kmajor_sw128(b + kk * 32), id, sa_t + 4 * i,
                                      sb_t + 8 * i, (kb | kk) != 0 ? 1u : 0u);
                     }
@@ -384,7 +417,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
-            const Tile t = decode_tile(p, tile, s_off, s_prefix);
+            const Tile t = decode_tile<BM>(p, tile, s_off, s_prefix);
             if (!mbar_wait_bounded(&tfull[acc], acc_phase, s_abort, p.dev_status)) break;
             tc_fence_after();
             const int row = t.row0 + quarter * 32 + lane;
@@ -477,6 +510,361 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
     }
 }
 
+// ------------------------------------------------------------------ CTA pairs
+// The same product on 256 x 256 tiles of a cluster of two CTAs
+// (tcgen05.mma.cta_group::2).  A one-CTA tile needs 12 KB of operands for an
+// MMA of 128 cycles, more than an SM takes in (64 bytes a cycle); a pair
+// stages 8 KB per CTA for the same time, half of B each.
+//   SWIGLU: the even CTA stages the 128 gate rows, the odd CTA the up rows.
+// The scales of B are needed whole in both CTAs' tensor memory.  Scale copies
+// go to two sets of columns in turn, two scale tiles at a time, so that a set
+// is not rewritten while the MMAs in front still read it.
+// Two producer threads per CTA, one for A and one for B, halve the issue time
+// of a stage.  Output leaves through TMA stores of 32-row boxes.
+constexpr int BM2 = 256;
+constexpr int STAGES2 = 5;
+constexpr int THREADS2 = 224;              // A producer, MMA, 4 epilogue warps, B producer
+constexpr int EPI_BYTES = 32 * 64;         // one output box: 32 rows of 64 bytes
+
+template <int FMT>
+struct Cfg2 {
+    static constexpr int TILES = Cfg<FMT>::TILES;
+    static constexpr int SA_BYTES = TILES * kScaleTile;
+    static constexpr int SB_BYTES = 2 * SA_BYTES;
+    static constexpr int A_LOAD = A_BYTES + SA_BYTES;             // per CTA
+    static constexpr int B_LOAD = B_BYTES / 2 + SB_BYTES;
+    static constexpr int STAGE = A_LOAD + B_LOAD;
+    static constexpr int EPI_OFF = STAGES2 * STAGE;
+    static constexpr int BAR_OFF = EPI_OFF + 4 * 2 * EPI_BYTES;
+    static constexpr int NBARS = 2 * STAGES2 + 4;
+    static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
+    static constexpr int OFFS_OFF = MISC_OFF + 16;
+    static constexpr int PREFIX_OFF = OFFS_OFF + (MAX_GROUPS + 1) * 4;
+    static constexpr int SMEM = 1024 + PREFIX_OFF + (MAX_GROUPS + 2) * 4;
+    static constexpr int SETS = TILES / 2;                        // scale sets per stage
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+    static_assert(STAGE % 1024 == 0, "swizzled tiles need 1 KB alignment");
+    static_assert(SF_COL + 2 * 24 <= TMEM_COLS, "scale columns");
+};
+
+// One 32-row x 64-byte output box (lane i holds row row0 + i as 16 words from
+// column col on) through one of the warp's two staging boxes, in the 64-byte
+// swizzle of the output map, and out as a TMA store.
+__device__ __forceinline__ void emit_box(uint8_t *ebox, int &eb, int lane, const uint32_t (&w)[16],
+                                         const CUtensorMap *map, int col, int row0) {
+    uint8_t *box = ebox + eb * EPI_BYTES;
+    if (lane == 0) bulk_wait_read<1>();      // the store that last used this box has read it
+    __syncwarp();
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch)
+        *reinterpret_cast<uint4 *>(box + lane * 64 + ((ch ^ ((lane >> 1) & 3)) << 4)) =
+            make_uint4(w[4 * ch], w[4 * ch + 1], w[4 * ch + 2], w[4 * ch + 3]);
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) {
+        tma_store_2d(map, box, col, row0);
+        bulk_commit();
+    }
+    eb ^= 1;
+}
+
+template <int FMT, int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS2, 1)
+    fp4_gemm_pair_kernel(const __grid_constant__ Params p) {
+    using C = Cfg2<FMT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);   // even CTA's are used
+    uint64_t *empty = full + STAGES2;
+    uint64_t *tfull = empty + STAGES2;      // [2]
+    uint64_t *tempty = tfull + 2;           // even CTA's is used
+    uint64_t *drain = tempty + 1;
+    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF);
+    volatile int *s_abort = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 4);
+    volatile int *s_bad = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 8);
+    int *s_off = reinterpret_cast<int *>(smem + C::OFFS_OFF);
+    int *s_prefix = reinterpret_cast<int *>(smem + C::PREFIX_OFF);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = static_cast<int>(cluster_ctarank());
+    const bool leader = rank == 0;
+    const int first_tile = static_cast<int>(cluster_id_x());
+    const int step = static_cast<int>(gridDim.x) / 2;
+
+    if (tid == 0) *s_abort = 0;
+    if (tid == 32) {
+        for (int s = 0; s < STAGES2; ++s) {
+            mbar_init(&full[s], 2);          // the even CTA's two producers arm their shares
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(&tfull[0], 1);
+        mbar_init(&tfull[1], 1);
+        mbar_init(tempty, 8);                // four epilogue warps of both CTAs
+        mbar_init(drain, 1);
+        fence_barrier_init();
+    }
+    // both CTAs read the same offsets, so both leave here together
+    if (!list_tiles<BM2>(p, s_off, s_prefix, s_bad)) {
+        if (tid == 0 && blockIdx.x == 0) report(p.dev_status, MOE_DEV_BAD_OFFSETS);
+        return;
+    }
+    const int total = s_prefix[p.G];
+    if (warp == 1) {
+        tmem_alloc_pair(s_tmem, TMEM_COLS);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();                      // barriers and TMEM of both CTAs are ready
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    const uint32_t lead_full = mapa_shared(smem_u32(full), 0);
+    const uint32_t lead_tempty = mapa_shared(smem_u32(tempty), 0);
+    const int kblocks = (p.K + BK - 1) / BK;
+    const int ktiles = p.K / Fp4<FMT>::TILE_K;
+
+    if (warp == 0 || warp == 6) {
+        // ================= TMA producers: warp 0 A, warp 6 B, each with its scales
+        if (elect_one()) {
+            const bool is_a = warp == 0;
+            tma_prefetch_desc(is_a ? &p.tmA : &p.tmB);
+            tma_prefetch_desc(is_a ? &p.tmSA : &p.tmSB);
+            int stage = 0;
+            uint32_t phase = 0;
+            int armed[STAGES2];
+            for (int s = 0; s < STAGES2; ++s) armed[s] = -1;
+            for (int tile = first_tile; tile < total && !*s_abort; tile += step) {
+                const Tile t = decode_tile<BM2>(p, tile, s_off, s_prefix);
+                const int sa_blk =
+                    static_cast<int>(scale_row_block(t.g, s_off[t.g], t.row0)) + rank;
+                const int b0 = MODE == MODE_STORE ? t.n_blk * BN : t.n_blk * 128;
+                const int b1 = MODE == MODE_STORE ? b0 + 128 : p.N + b0;
+                const int64_t wblk = static_cast<int64_t>(t.g) * (p.wrows / 128);
+                const int sa0 = sa_blk * ktiles;
+                const int sb0 = static_cast<int>((wblk + b0 / 128) * ktiles);
+                const int sb1 = static_cast<int>((wblk + b1 / 128) * ktiles);
+                bool ok = true;
+                for (int kb = 0; kb < kblocks; ++kb) {
+                    if (!mbar_wait_bounded(&empty[stage], phase ^ 1, s_abort, p.dev_status)) {
+                        ok = false;
+                        break;
+                    }
+                    armed[stage] = static_cast<int>(phase);
+                    uint8_t *a = smem + stage * C::STAGE;
+                    uint8_t *b = a + A_BYTES;
+                    uint8_t *sa = b + B_BYTES / 2;
+                    uint8_t *sb = sa + C::SA_BYTES;
+                    const uint32_t fb = lead_full + 8u * static_cast<uint32_t>(stage);
+                    const int k0 = kb * (BK / 2), t0 = kb * C::TILES;
+                    if (leader)
+                        mbar_arrive_expect_tx(&full[stage], 2u * (is_a ? C::A_LOAD : C::B_LOAD));
+                    if (is_a) {
+                        tma_load_2d_pair(a, &p.tmA, fb, k0, t.row0 + 128 * rank);
+                        tma_load_2d_pair(sa, &p.tmSA, fb, 0, sa0 + t0);
+                    } else {
+                        tma_load_3d_pair(b, &p.tmB, fb, k0, rank == 0 ? b0 : b1, t.g);
+                        tma_load_2d_pair(sb, &p.tmSB, fb, 0, sb0 + t0);
+                        tma_load_2d_pair(sb + C::SA_BYTES, &p.tmSB, fb, 0, sb1 + t0);
+                    }
+                    if (++stage == STAGES2) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (!ok) break;
+            }
+            if (*s_abort && leader) {
+                for (int s = 0; s < STAGES2; ++s)
+                    if (armed[s] >= 0) mbar_wait_drain(&full[s], static_cast<uint32_t>(armed[s]));
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ================= MMA issuer (even CTA only)
+        if (leader && elect_one()) {
+            int stage = 0;
+            uint32_t phase = 0;
+            int acc = 0;
+            uint32_t free_phase = 1;
+            uint32_t set = 0;
+            bool issued = false;
+            for (int tile = first_tile; tile < total && !*s_abort; tile += step) {
+                if (!mbar_wait_bounded_cluster(tempty, free_phase, s_abort, p.dev_status)) break;
+                free_phase ^= 1;
+                tc_fence_after();
+                const uint32_t d = tmem + static_cast<uint32_t>(acc * ACC1);
+                bool ok = true;
+                for (int kb = 0; kb < kblocks; ++kb) {
+                    if (!mbar_wait_bounded(&full[stage], phase, s_abort, p.dev_status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a = smem_u32(smem + stage * C::STAGE);
+                    const uint32_t b = a + A_BYTES;
+                    const uint32_t sa = b + B_BYTES / 2;
+                    const uint32_t sb = sa + C::SA_BYTES;
+                    const int steps = min(BK, p.K - kb * BK) / 64;
+                    constexpr int PER = 4 / C::SETS;              // MMAs per scale set
+#pragma unroll
+                    for (int h = 0; h < C::SETS; ++h) {
+                        const uint32_t sa_t = tmem + SF_COL + set * 24u, sb_t = sa_t + 8;
+                        if (h * PER >= steps) break;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t o = (2 * h + i) * kScaleTile;
+                            copy_scales<2>(sa_t + 4 * i, sa + o);
+                            copy_scales<2>(sb_t + 8 * i, sb + o);
+                            copy_scales<2>(sb_t + 8 * i + 4, sb + C::SA_BYTES + o);
+                        }
+                        set ^= 1;
+#pragma unroll
+                        for (int j = 0; j < PER; ++j) {
+                            const int kk = h * PER + j;
+                            if (kk >= steps) break;
+                            const int i = FMT == MOE_FP4_MX ? j / 2 : j;
+                            const uint32_t id = FMT == MOE_FP4_MX && (j & 1)
+                                                    ? idesc<FMT>(BM2, BN, 2)
+                                                    : idesc<FMT>(BM2, BN, 0);
+                            mma_fp4<FMT, 2>(d, sdesc_kmajor_sw128(a + kk * 32),
+                                            sdesc_kmajor_sw128(b + kk * 32), id, sa_t + 4 * i,
+                                            sb_t + 8 * i, (kb | kk) != 0 ? 1u : 0u);
+                        }
+                    }
+                    issued = true;
+                    tc_commit_pair_mc(&empty[stage], 0x3);
+                    if (++stage == STAGES2) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (!ok) break;
+                tc_commit_pair_mc(&tfull[acc], 0x3);
+                acc ^= 1;
+            }
+            if (*s_abort && issued) {
+                tc_commit_pair_mc(drain, 0x1);
+                mbar_wait_drain(drain, 0);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ================= epilogue (warps 2..5 of both CTAs)
+        const int quarter = warp & 3;
+        uint8_t *ebox = smem + C::EPI_OFF + (warp - 2) * 2 * EPI_BYTES;
+        int eb = 0;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        for (int tile = first_tile; tile < total; tile += step) {
+            const Tile t = decode_tile<BM2>(p, tile, s_off, s_prefix);
+            if (!mbar_wait_bounded(&tfull[acc], acc_phase, s_abort, p.dev_status)) break;
+            tc_fence_after();
+            const int row_base = t.row0 + 128 * rank + quarter * 32;
+            const int row = row_base + lane;
+            const bool ok = row < t.row_end;
+            const bool boxed = row_base + 32 <= t.row_end;   // else a group's last rows: by lane
+            const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
+                                   static_cast<uint32_t>(acc * ACC1);
+            if (MODE != MODE_STORE) {
+                const int first = acc == 0 ? 64 : 0;         // the shared columns' half first
+#pragma unroll 1
+                for (int i = 0; i < 4; ++i) {
+                    const int c = (first + 32 * i) & 127;
+                    float g[32], u[32];
+                    __syncwarp();
+                    tmem_ld32(taddr + c, g);
+                    tmem_ld32(taddr + 128 + c, u);
+                    tmem_ld_wait();
+                    if (i == 1) {
+                        __syncwarp();
+                        tc_fence_before();
+                        if (lane == 0) mbar_arrive_cluster(lead_tempty);
+                    }
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int v = 0; v < 16; ++v)
+                        pk[v] = pack_bf16x2(swiglu(g[2 * v] * p.alpha, u[2 * v] * p.alpha),
+                                            swiglu(g[2 * v + 1] * p.alpha, u[2 * v + 1] * p.alpha));
+                    const int col = t.n_blk * 128 + c;
+                    if (MODE == MODE_SWIGLU_Q) {
+                        if (ok) emit_quantized<FMT>(p, pk, t.g, s_off[t.g], row, col);
+                    } else if (boxed) {
+                        emit_box(ebox, eb, lane, pk, &p.tmO, col, row_base);
+                    } else if (ok) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) +
+                                                               static_cast<int64_t>(row) * p.N + col);
+#pragma unroll
+                        for (int v = 0; v < 4; ++v)
+                            dst[v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2],
+                                                pk[4 * v + 3]);
+                    }
+                }
+            } else {
+                const int first = acc == 0 ? BN - 64 : 0;
+#pragma unroll 1
+                for (int i = 0; i < BN / 32; ++i) {
+                    const int c = (first + 32 * i) & (BN - 1);
+                    float v[32];
+                    __syncwarp();
+                    tmem_ld32(taddr + c, v);
+                    tmem_ld_wait();
+                    if (i == 1) {
+                        __syncwarp();
+                        tc_fence_before();
+                        if (lane == 0) mbar_arrive_cluster(lead_tempty);
+                    }
+                    const int col = t.n_blk * BN + c;
+                    if (col >= p.N) continue;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] *= p.alpha;
+                    uint32_t w[16];
+                    if (p.out_f32) {
+                        float *dst = static_cast<float *>(p.out) + static_cast<int64_t>(row) * p.N + col;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(v[16 * h + j]);
+                            if (boxed) {
+                                emit_box(ebox, eb, lane, w, &p.tmO, col + 16 * h, row_base);
+                            } else if (ok) {
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    reinterpret_cast<uint4 *>(dst + 16 * h)[j] = make_uint4(
+                                        w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+                        if (boxed) {
+                            emit_box(ebox, eb, lane, w, &p.tmO, col, row_base);
+                        } else if (ok) {
+                            uint4 *dst = reinterpret_cast<uint4 *>(
+                                static_cast<uint16_t *>(p.out) + static_cast<int64_t>(row) * p.N + col);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2],
+                                                    w[4 * j + 3]);
+                        }
+                    }
+                }
+            }
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1;
+        }
+        if (lane == 0) bulk_wait<0>();       // every output box written
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();      // no CTA leaves while its peer may still signal or read it
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, TMEM_COLS);
+    }
+}
+
 // ------------------------------------------------------------------ host side
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
                                    const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
@@ -523,9 +911,76 @@ bool scale_map(CUtensorMap *m, const uint8_t *sf, int64_t tiles, int box) {
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Output [rows, cols] as 32-row x 64-byte boxes, 64-byte swizzled.
+bool out_map(CUtensorMap *m, void *out, int64_t rows, int64_t cols, bool f32) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t esz = f32 ? 4 : 2;
+    cuuint64_t dim[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    cuuint64_t stride[1] = {static_cast<cuuint64_t>(cols) * esz};
+    cuuint32_t boxd[2] = {static_cast<cuuint32_t>(64 / esz), 32}, es[2] = {1, 1};
+    return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, out,
+              dim, stride, boxd, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// CTA pairs take the products with many rows per group.
+bool use_pair(int n, int G) {
+    static const int64_t least = [] {
+        const char *v = getenv("MOE_FP4_PAIR_ROWS");
+        return v ? atoll(v) : 256ll;
+    }();
+    return n / G >= least;
+}
+
 template <int FMT, int MODE>
-cudaError_t launch(const Params &p, cudaStream_t stream) {
+cudaError_t launch_pair(const Params &p, cudaStream_t stream) {
+    using C = Cfg2<FMT>;
+    static std::mutex mu;
+    static int max_clusters[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    int limit = num_sms() / 2;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (dev >= 64 || max_clusters[dev] == 0) {
+            const cudaError_t e =
+                cudaFuncSetAttribute(fp4_gemm_pair_kernel<FMT, MODE>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+            if (e != cudaSuccess) return e;
+            // no more clusters than can be resident at once
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(static_cast<unsigned>(num_sms()), 1, 1);
+            cfg.blockDim = dim3(THREADS2, 1, 1);
+            cfg.dynamicSmemBytes = C::SMEM;
+            cfg.stream = stream;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, fp4_gemm_pair_kernel<FMT, MODE>, &cfg) !=
+                    cudaSuccess ||
+                n <= 0) {
+                cudaGetLastError();
+                n = limit;
+            }
+            limit = std::min(n, limit);
+            if (dev < 64) max_clusters[dev] = limit;
+        } else {
+            limit = max_clusters[dev];
+        }
+    }
+    const int64_t tiles = (static_cast<int64_t>(p.n / BM2) + p.G) * p.nt;
+    const int clusters = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(limit, tiles)));
+    fp4_gemm_pair_kernel<FMT, MODE><<<2 * clusters, THREADS2, C::SMEM, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <int FMT, int MODE>
+cudaError_t launch(Params &p, cudaStream_t stream) {
     using C = Cfg<FMT>;
+    if (use_pair(p.n, p.G)) {
+        if (MODE != MODE_SWIGLU_Q && !out_map(&p.tmO, p.out, p.n, p.N, p.out_f32 != 0))
+            return cudaErrorInvalidValue;
+        return launch_pair<FMT, MODE>(p, stream);
+    }
     static std::mutex mu;
     static bool attr_done[64] = {};
     int dev = 0;

@@ -221,7 +221,7 @@ def test_grouped_swiglu_and_its_quantised_form(fmt, ea, ew, groups, K, I):
     pos = ref.scale_positions(n, I // ref.BLOCK[fmt], off)[:end]
     assert np.array_equal(fused.sf.cpu().numpy()[pos], byte)
     # and mlp is the two products in a row
-    H = 384
+    H = K
     w2, w2v = _matrix(_f64(_rows((len(off) - 1) * H, I, 31, 0.05)), fmt, 0 if fmt == "mx" else ew)
     w2.q = w2.q.view(len(off) - 1, H, I // 2)
     act, ym = moe.fp4_grouped_mlp(a, offc, w, w2, y_f32=True, status=st)
