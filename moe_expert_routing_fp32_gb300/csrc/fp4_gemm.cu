@@ -1,22 +1,31 @@
 // fp4_gemm.cu -- grouped expert matmuls on microscaled 4-bit operands.
 //
 // With A[r] = sum over blocks of scale * code along K and W[g] likewise,
-//   STORE:   y[r, n] = A[r] . W[g, n]                      (bf16 or fp32)
-//   SWIGLU:  act[r, n] = bf16(SiLU(A[r] . W[g, n]) * (A[r] . W[g, I + n]))
+//   STORE:    y[r, n] = A[r] . W[g, n]                      (bf16 or fp32)
+//   SWIGLU:   act[r, n] = bf16(SiLU(A[r] . W[g, n]) * (A[r] . W[g, I + n]))
 //   SWIGLU_Q: act quantised again (the next product's operand)
 // for the rows r of group g, accumulated in fp32 by the block-scaled
 // tcgen05.mma (kind::mxf4 for blocks of 32, kind::mxf4nvf4 for blocks of 16),
 // which multiplies the scales in.
 //
-// One persistent CTA per SM takes 128-row x 256-column tiles in list order.
-// A stage holds 256 columns of K: 16 KB of A and 32 KB of B as 128-byte rows
-// (the same swizzled K-major tiles as a bf16 slice of 64), and the scale
-// tiles, which one thread copies into tensor memory ahead of the stage's four
-// MMAs (K = 64 each).  Tensor memory has 512 columns: two 256-column
-// accumulators would leave none for the scales, so accumulator 1 starts at
-// column 192 and shares 64 columns with accumulator 0; the epilogue drains
-// the shared columns first and releases the next tile then, and only that
-// part of a drain is not overlapped.
+// A persistent kernel takes tiles of CG * 128 rows x 256 columns in list
+// order, on one CTA (CG = 1) or a pair (CG = 2, tcgen05 cta_group::2, half of
+// B in each CTA).  A stage of the shared-memory ring holds 256 columns of K:
+// the operands as 128-byte rows (the swizzled K-major tiles a bf16 slice of 64
+// has), and the scale tiles, which are copied into tensor memory ahead of the
+// MMAs that use them.
+//
+// What bounds it.  An MMA of 256 x 256 x 64 takes 128 cycles (measured; 9.5
+// PFLOP/s at 2.07 GHz), and issuing one, or one of the scale copies, takes its
+// thread some 40, so a slice of 256 columns (512 cycles of MMAs, 4 MMAs and 6
+// to 12 copies) does not leave one thread room for anything else; and tensor
+// memory holds no two 256-column accumulators beside the scales, so with one
+// accumulator per tile the MMAs stop while it is drained (some 2,000 of 8,192
+// cycles at K = 4096).  Both go away by halves: a tile is two half tiles of 128
+// columns, each with an issuing thread of its own, and the half tiles take
+// three 128-column accumulators in turn.  The thread of half 0 runs ahead on
+// the staged slices while half 1 waits for an accumulator, from then on stays
+// ahead, and half 0 is drained while half 1 still computes.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -34,17 +43,19 @@ moe_status_t fp4_check(int format, int scale_exp);
 
 namespace {
 
-constexpr int BM = 128;
-constexpr int BN = 256;
+constexpr int BM = 128;                    // rows of a tile per CTA
+constexpr int BN = 256;                    // columns of a tile
+constexpr int HN = 128;                    // columns of a half tile
 constexpr int BK = 256;                    // elements of K per stage: 128 bytes
-constexpr int STAGES = 4;
-constexpr int THREADS = 192;
-constexpr int A_BYTES = BM * BK / 2;
-constexpr int B_BYTES = BN * BK / 2;
 constexpr int MAX_GROUPS = 1024;
-constexpr int ACC1 = 192;                  // first column of accumulator 1
-constexpr int SF_COL = 448;                // scales: columns 448..511
+constexpr int A_BYTES = BM * BK / 2;
+constexpr int NACC = 3;                    // accumulators of HN columns
+constexpr int SF_COL = NACC * HN;          // scales: the columns behind them
+constexpr int SF_SET = 16;                 // columns of a scale set: two tiles of A, two of B
 constexpr int TMEM_COLS = 512;
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 128 + 32 * EPI_WARPS;   // A and B producers, two issuers, epilogue
+constexpr int EPI_BYTES = 32 * 128;        // an output box: 32 rows of 128 bytes
 
 enum { MODE_STORE = 0, MODE_SWIGLU = 1, MODE_SWIGLU_Q = 2 };
 
@@ -53,7 +64,7 @@ struct Params {
     CUtensorMap tmB;        // codes of W: [G, rows, K / 2] bytes, likewise
     CUtensorMap tmSA;       // scale tiles of A and W: [tiles, 128] 32-bit words
     CUtensorMap tmSB;
-    CUtensorMap tmO;        // output, 32-row x 64-byte boxes (pair kernel, not SWIGLU_Q)
+    CUtensorMap tmO;        // output, 32-row x 128-byte boxes (pair kernel, not SWIGLU_Q)
     const int32_t *offsets;
     int32_t G, n, K, N;     // N: output columns
     int32_t nt;             // column tiles per row block
@@ -67,21 +78,28 @@ struct Params {
     int32_t *dev_status;
 };
 
-template <int FMT>
+template <int FMT, int CG>
 struct Cfg {
-    static constexpr int TILES = BK / Fp4<FMT>::TILE_K;        // scale tiles per stage along K
-    static constexpr int SA_BYTES = TILES * kScaleTile;
-    static constexpr int SB_BYTES = 2 * SA_BYTES;
-    static constexpr int STAGE = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
-    static constexpr int BAR_OFF = STAGES * STAGE;
-    static constexpr int NBARS = 2 * STAGES + 4;               // full, empty, tfull[2], tempty, drain
+    // four one-CTA stages, or five pair stages and the output boxes, fill shared memory
+    static constexpr int STAGES = CG == 1 ? 4 : 5;
+    static constexpr int BOXES = CG == 1 ? 0 : EPI_WARPS;
+    static constexpr int TILES = BK / Fp4<FMT>::TILE_K;          // scale tiles per stage along K
+    static constexpr int B_HALF = HN / CG * BK / 2;              // this CTA's rows of a half of B
+    static constexpr int SF_BYTES = TILES * kScaleTile;          // of 128 rows
+    static constexpr int A_LOAD = A_BYTES + SF_BYTES;
+    static constexpr int B_LOAD = 2 * B_HALF + 2 * SF_BYTES;
+    static constexpr int STAGE = A_LOAD + B_LOAD;
+    static constexpr int EPI_OFF = STAGES * STAGE;
+    static constexpr int BAR_OFF = EPI_OFF + BOXES * EPI_BYTES;
+    static constexpr int NBARS = 2 * STAGES + 2 * NACC + 2;      // full, empty, tfull, tempty, drain
     static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
     static constexpr int OFFS_OFF = MISC_OFF + 16;
-    static constexpr int PREFIX_OFF = OFFS_OFF + (MAX_GROUPS + 1) * 4;
-    static constexpr int SMEM = 1024 + PREFIX_OFF + (MAX_GROUPS + 2) * 4;
-    static_assert(SMEM <= 227 * 1024, "shared memory");
+    // the group offsets and tile prefixes take the rest
+    static constexpr int smem(int G) { return 1024 + OFFS_OFF + (2 * G + 2) * 4; }
+    static constexpr int MAX_G = (227 * 1024 - 1024 - OFFS_OFF - 8) / 8;
+    static_assert(MAX_G >= (CG == 1 ? MAX_GROUPS : 256), "shared memory");
     static_assert(STAGE % 1024 == 0, "swizzled tiles need 1 KB alignment");
-    static_assert(SF_COL + 4 * TILES + 8 * TILES <= TMEM_COLS, "scale columns");
+    static_assert(SF_COL + 2 * 2 * SF_SET <= TMEM_COLS, "scale columns");
 };
 
 // Instruction descriptor of the block-scaled MMA: e2m1 operands, both K-major,
@@ -107,6 +125,32 @@ __device__ __forceinline__ bool elect_one() {
         "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(p));
     return p != 0;
+}
+
+// Bounded wait (as mbar_wait_bounded) whose first 64 polls read no timer: a
+// %globaltimer read takes far longer than a hand-over between two roles, and
+// here one sits on the path from a finished accumulator to the next tile's
+// first MMA.  Cluster-scope acquire.
+__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                       int32_t *dev_status) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait_cluster(bar, parity)) return true;
+        if ((it & 63u) == 0u) {
+            if (*abort) return false;
+            const uint64_t t = global_timer_ns();
+            if (t0 == 0) t0 = t;
+            if (t - t0 > kWaitLimitNs || it > (1u << 30)) {
+                *abort = 1;
+                report(dev_status, MOE_DEV_TIMEOUT);
+                return false;
+            }
+        }
+    }
+}
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                           int32_t *dev_status) {
+    return mbar_try_wait_cluster(bar, parity) || wait_slow(bar, parity, abort, dev_status);
 }
 
 // D (+)= A * B^T with the scales at sa (rows of A) and sb (rows of B).
@@ -149,6 +193,37 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
     else
         asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d)
                      : "memory");
+}
+
+// One half tile's MMAs over STEPS * 64 columns of K of a stage (4, or 2 in a
+// last slice of 128 columns): operand tiles at a and b, scale tiles at sa and
+// sb in shared memory.  Two scale tiles of A and two of B at a time go to one
+// of this thread's two sets of columns, in turn, so that a set is not rewritten
+// while the MMAs just in front still read it.
+template <int FMT, int CG, int STEPS>
+__device__ __forceinline__ void issue_slice(uint32_t d, uint32_t a, uint32_t b, uint32_t sa,
+                                            uint32_t sb, uint32_t sf_col, uint32_t &set,
+                                            bool accumulate) {
+    constexpr int PER = FMT == MOE_FP4_MX ? 4 : 2;       // MMAs per set
+    constexpr uint32_t ID0 = idesc<FMT>(128 * CG, HN, 0), ID2 = idesc<FMT>(128 * CG, HN, 2);
+#pragma unroll
+    for (int h = 0; h < (STEPS + PER - 1) / PER; ++h) {
+        const uint32_t sa_t = sf_col + set * SF_SET, sb_t = sa_t + 8;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            copy_scales<CG>(sa_t + 4 * i, sa + (2 * h + i) * kScaleTile);
+            copy_scales<CG>(sb_t + 4 * i, sb + (2 * h + i) * kScaleTile);
+        }
+        set ^= 1;
+#pragma unroll
+        for (int j = 0; j < (STEPS < PER ? STEPS : PER); ++j) {
+            const int kk = h * PER + j;
+            const int i = FMT == MOE_FP4_MX ? j / 2 : j;
+            mma_fp4<FMT, CG>(d, sdesc_kmajor_sw128(a + kk * 32), sdesc_kmajor_sw128(b + kk * 32),
+                             FMT == MOE_FP4_MX && (j & 1) ? ID2 : ID0, sa_t + 4 * i, sb_t + 4 * i,
+                             (kk > 0 || accumulate) ? 1u : 0u);
+        }
+    }
 }
 
 struct Tile {
@@ -216,18 +291,17 @@ __device__ __forceinline__ Tile decode_tile(const Params &p, int tile, const int
     return t;
 }
 
-__device__ __forceinline__ float swiglu(float g, float u) {
-    return __fdividef(g, 1.0f + __expf(-g)) * u;
-}
+__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
 
-// 32 consecutive act columns of one row: codes and scale bytes.
+// 64 act columns of one row (bf16 pairs, from column col on): codes and scale
+// bytes, as moe_fp4_quantize forms them.
 template <int FMT>
-__device__ __forceinline__ void emit_quantized(const Params &p, const uint32_t (&pk)[16], int g,
+__device__ __forceinline__ void emit_quantized(const Params &p, const uint32_t (&pk)[32], int g,
                                                int start, int row, int col) {
-    uint32_t code[4], sc = 0;
     constexpr int W = Fp4<FMT>::BLOCK / 2;            // words of a block
+    uint32_t code[8], sc = 0;
 #pragma unroll
-    for (int b = 0; b < 16 / W; ++b) {
+    for (int b = 0; b < 32 / W; ++b) {
         uint32_t am = 0;
 #pragma unroll
         for (int i = 0; i < W / 4; ++i) {
@@ -244,378 +318,111 @@ __device__ __forceinline__ void emit_quantized(const Params &p, const uint32_t (
             code[b * (W / 4) + i] = quantize8<FMT>(w, factor);
         }
     }
-    *reinterpret_cast<uint4 *>(p.q + static_cast<int64_t>(row) * (p.N / 2) + col / 2) =
-        make_uint4(code[0], code[1], code[2], code[3]);
+    uint4 *q = reinterpret_cast<uint4 *>(p.q + static_cast<int64_t>(row) * (p.N / 2) + col / 2);
+    q[0] = make_uint4(code[0], code[1], code[2], code[3]);
+    q[1] = make_uint4(code[4], code[5], code[6], code[7]);
     const int64_t tiles = p.N / Fp4<FMT>::TILE_K;
     uint8_t *dst = p.sf +
                    (scale_row_block(g, start, row) * tiles + col / Fp4<FMT>::TILE_K) * kScaleTile +
                    scale_row_offset(row - start) + col / Fp4<FMT>::BLOCK % 4;
     if (FMT == MOE_FP4_MX)
-        *dst = static_cast<uint8_t>(sc);
-    else
         *reinterpret_cast<uint16_t *>(dst) = static_cast<uint16_t>(sc);
+    else
+        *reinterpret_cast<uint32_t *>(dst) = sc;
 }
 
-template <int FMT, int MODE>
-__global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_constant__ Params p) {
-    using C = Cfg<FMT>;
+// 128 bytes of each of an epilogue warp's 32 rows (lane i: row row0 + i, 64
+// bf16 or 32 fp32 values from column col on).  With a box, rows all inside the
+// group leave through it, in the 128-byte swizzle of the output map, as one TMA
+// store; otherwise, and for a group's last rows, each lane stores its own.
+template <typename T>
+__device__ __forceinline__ void emit_words(const Params &p, uint8_t *box, int lane, bool boxed,
+                                           bool ok, const uint32_t (&w)[32], int col, int row0) {
+    if (boxed) {
+        if (lane == 0) bulk_wait_read<0>();      // the last store has read the box
+        __syncwarp();
+#pragma unroll
+        for (int ch = 0; ch < 8; ++ch)
+            *reinterpret_cast<uint4 *>(box + lane * 128 + ((ch ^ (lane & 7)) << 4)) =
+                make_uint4(w[4 * ch], w[4 * ch + 1], w[4 * ch + 2], w[4 * ch + 3]);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_2d(&p.tmO, box, col, row0);
+            bulk_commit();
+        }
+    } else if (ok) {
+        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) +
+                                               static_cast<int64_t>(row0 + lane) * p.N + col);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    }
+}
+
+// Waits for half tile number u's accumulator (or, with `freed`, for it to be
+// free again): number u takes accumulator u % NACC for the u / NACC-th time.
+__device__ __forceinline__ bool wait_acc(uint64_t *bars, uint32_t u, bool freed,
+                                         volatile int *abort, int32_t *dev_status) {
+    return wait_phase(&bars[u % NACC], ((u / NACC) & 1u) ^ (freed ? 1u : 0u), abort, dev_status);
+}
+
+template <int FMT, int MODE, int CG>
+__device__ __forceinline__ void fp4_gemm(const Params &p) {
+    using C = Cfg<FMT, CG>;
+    constexpr int STAGES = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    // a pair's MMAs are issued by its even CTA: full, tempty are used there
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);
     uint64_t *empty = full + STAGES;
-    uint64_t *tfull = empty + STAGES;       // [2] accumulator complete
-    uint64_t *tempty = tfull + 2;           // shared columns drained, once per tile
-    uint64_t *drain = tempty + 1;
+    uint64_t *tfull = empty + STAGES;       // [NACC]
+    uint64_t *tempty = tfull + NACC;        // [NACC]
+    uint64_t *drain = tempty + NACC;        // [2], one per issuing thread
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF);
     volatile int *s_abort = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 4);
     volatile int *s_bad = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 8);
     int *s_off = reinterpret_cast<int *>(smem + C::OFFS_OFF);
-    int *s_prefix = reinterpret_cast<int *>(smem + C::PREFIX_OFF);
+    int *s_prefix = s_off + p.G + 1;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = CG == 2 ? static_cast<int>(cluster_ctarank()) : 0;
+    const bool leader = rank == 0;
+    const int first_tile = static_cast<int>(blockIdx.x) / CG;
+    const int step = static_cast<int>(gridDim.x) / CG;
 
     if (tid == 0) *s_abort = 0;
     if (tid == 32) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&full[s], 2);          // each producer arms its share
+            mbar_init(&empty[s], 2);         // both issuers' MMAs have read it
         }
-        mbar_init(&tfull[0], 1);
-        mbar_init(&tfull[1], 1);
-        mbar_init(tempty, 128);
-        mbar_init(drain, 1);
+        for (int i = 0; i < NACC; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], CG * EPI_WARPS);
+        }
+        mbar_init(&drain[0], 1);
+        mbar_init(&drain[1], 1);
         fence_barrier_init();
     }
-    if (!list_tiles<BM>(p, s_off, s_prefix, s_bad)) {
+    // both CTAs of a pair read the same offsets, so both leave here together
+    if (!list_tiles<BM * CG>(p, s_off, s_prefix, s_bad)) {
         if (tid == 0 && blockIdx.x == 0) report(p.dev_status, MOE_DEV_BAD_OFFSETS);
         return;
     }
     const int total = s_prefix[p.G];
     if (warp == 1) {
-        tmem_alloc(s_tmem, TMEM_COLS);
-        tmem_relinquish();
+        if (CG == 1) {
+            tmem_alloc(s_tmem, TMEM_COLS);
+            tmem_relinquish();
+        } else {
+            tmem_alloc_pair(s_tmem, TMEM_COLS);
+            tmem_relinquish_pair();
+        }
     }
     tc_fence_before();
     __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *s_tmem;
-    const int kblocks = (p.K + BK - 1) / BK;
-    const int ktiles = p.K / Fp4<FMT>::TILE_K;
-
-    if (warp == 0) {
-        // ================= TMA producer
-        if (elect_one()) {
-            tma_prefetch_desc(&p.tmA);
-            tma_prefetch_desc(&p.tmB);
-            tma_prefetch_desc(&p.tmSA);
-            tma_prefetch_desc(&p.tmSB);
-            int stage = 0;
-            uint32_t phase = 0;
-            int armed[STAGES];
-            for (int s = 0; s < STAGES; ++s) armed[s] = -1;
-            for (int tile = blockIdx.x; tile < total && !*s_abort; tile += gridDim.x) {
-                const Tile t = decode_tile<BM>(p, tile, s_off, s_prefix);
-                const int sa_blk = static_cast<int>(scale_row_block(t.g, s_off[t.g], t.row0));
-                const int b0 = MODE == MODE_STORE ? t.n_blk * BN : t.n_blk * 128;
-                const int b1 = MODE == MODE_STORE ? b0 + 128 : p.N + b0;
-                const int64_t wblk = static_cast<int64_t>(t.g) * (p.wrows / 128);
-                bool ok = true;
-                for (int kb = 0; kb < kblocks; ++kb) {
-                    if (!mbar_wait_bounded(&empty[stage], phase ^ 1, s_abort, p.dev_status)) {
-                        ok = false;
-                        break;
-                    }
-                    armed[stage] = static_cast<int>(phase);
-                    uint8_t *a = smem + stage * C::STAGE;
-                    uint8_t *b = a + A_BYTES;
-                    uint8_t *sa = b + B_BYTES;
-                    uint8_t *sb = sa + C::SA_BYTES;
-                    mbar_arrive_expect_tx(&full[stage], C::STAGE);
-                    const int k0 = kb * (BK / 2), t0 = kb * C::TILES;
-                    tma_load_2d(a, &p.tmA, &full[stage], k0, t.row0);
-                    tma_load_3d(b, &p.tmB, &full[stage], k0, b0, t.g);
-                    tma_load_3d(b + B_BYTES / 2, &p.tmB, &full[stage], k0, b1, t.g);
-                    tma_load_2d(sa, &p.tmSA, &full[stage], 0, sa_blk * ktiles + t0);
-                    tma_load_2d(sb, &p.tmSB, &full[stage], 0,
-                                static_cast<int>((wblk + b0 / 128) * ktiles) + t0);
-                    tma_load_2d(sb + C::SA_BYTES, &p.tmSB, &full[stage], 0,
-                                static_cast<int>((wblk + b1 / 128) * ktiles) + t0);
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
-                }
-                if (!ok) break;
-            }
-            if (*s_abort) {
-                for (int s = 0; s < STAGES; ++s)
-                    if (armed[s] >= 0) mbar_wait_drain(&full[s], static_cast<uint32_t>(armed[s]));
-            }
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        // ================= MMA issuer
-        if (elect_one()) {
-            int stage = 0;
-            uint32_t phase = 0;
-            int acc = 0;
-            uint32_t free_phase = 1;        // the first tile finds both accumulators free
-            bool issued = false;
-            const uint32_t sa_t = tmem + SF_COL, sb_t = sa_t + 4 * C::TILES;
-            for (int tile = blockIdx.x; tile < total && !*s_abort; tile += gridDim.x) {
-                if (!mbar_wait_bounded(tempty, free_phase, s_abort, p.dev_status)) break;
-                free_phase ^= 1;
-                tc_fence_after();
-                const uint32_t d = tmem + static_cast<uint32_t>(acc * ACC1);
-                bool ok = true;
-                for (int kb = 0; kb < kblocks; ++kb) {
-                    if (!mbar_wait_bounded(&full[stage], phase, s_abort, p.dev_status)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t a = smem_u32(smem + stage * C::STAGE);
-                    const uint32_t b = a + A_BYTES;
-                    const uint32_t sa = b + B_BYTES;
-                    const uint32_t sb = sa + C::SA_BYTES;
-#pragma unroll
-                    for (int i = 0; i < C::TILES; ++i) {
-                        copy_scales<1>(sa_t + 4 * i, sa + i * kScaleTile);
-                        copy_scales<1>(sb_t + 8 * i, sb + i * kScaleTile);
-                        copy_scales<1>(sb_t + 8 * i + 4, sb + C::SA_BYTES + i * kScaleTile);
-                    }
-                    // the last slice may hold 128 columns only
-                    const int steps = min(BK, p.K - kb * BK) / 64;
-                    for (int kk = 0; kk < steps; ++kk) {
-                        const int i = FMT == MOE_FP4_MX ? kk / 2 : kk;
-                        const uint32_t id = FMT == MOE_FP4_MX && (kk & 1) ? idesc<FMT>(BM, BN, 2)
-                                                                          : idesc<FMT>(BM, BN, 0);
-                        mma_fp4<FMT, 1>(d, sdesc_kmajor_sw128(a + kk * 32),
-                                     sdesc_kmajor_sw128(b + kk * 32), id, sa_t + 4 * i,
-                                     sb_t + 8 * i, (kb | kk) != 0 ? 1u : 0u);
-                    }
-                    issued = true;
-                    tc_commit(&empty[stage]);
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
-                }
-                if (!ok) break;
-                tc_commit(&tfull[acc]);
-                acc ^= 1;
-            }
-            if (*s_abort && issued) {
-                tc_commit(drain);
-                mbar_wait_drain(drain, 0);
-            }
-        }
-        __syncwarp();
-    } else {
-        // ================= epilogue (warps 2..5)
-        const int quarter = warp & 3;               // TMEM lane quarter of this warp
-        int acc = 0;
-        uint32_t acc_phase = 0;
-        for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
-            const Tile t = decode_tile<BM>(p, tile, s_off, s_prefix);
-            if (!mbar_wait_bounded(&tfull[acc], acc_phase, s_abort, p.dev_status)) break;
-            tc_fence_after();
-            const int row = t.row0 + quarter * 32 + lane;
-            const bool ok = row < t.row_end;
-            const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
-                                   static_cast<uint32_t>(acc * ACC1);
-            if (MODE != MODE_STORE) {
-                // the shared 64 columns hold up columns 64.. of accumulator 0
-                // and gate columns ..63 of accumulator 1: that half goes first
-                const int first = acc == 0 ? 64 : 0;
-#pragma unroll 1
-                for (int i = 0; i < 4; ++i) {
-                    const int c = (first + 32 * i) & 127;
-                    if (i == 2) {
-                        __syncwarp();
-                        tc_fence_before();
-                        mbar_arrive(tempty);
-                    }
-                    float g[32], u[32];
-                    __syncwarp();
-                    tmem_ld32(taddr + c, g);
-                    tmem_ld32(taddr + 128 + c, u);
-                    tmem_ld_wait();
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int v = 0; v < 16; ++v)
-                        pk[v] = pack_bf16x2(swiglu(g[2 * v] * p.alpha, u[2 * v] * p.alpha),
-                                            swiglu(g[2 * v + 1] * p.alpha, u[2 * v + 1] * p.alpha));
-                    if (!ok) continue;
-                    const int col = t.n_blk * 128 + c;
-                    if (MODE == MODE_SWIGLU_Q) {
-                        emit_quantized<FMT>(p, pk, t.g, s_off[t.g], row, col);
-                    } else {
-                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) +
-                                                               static_cast<int64_t>(row) * p.N + col);
-#pragma unroll
-                        for (int v = 0; v < 4; ++v)
-                            dst[v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2],
-                                                pk[4 * v + 3]);
-                    }
-                }
-            } else {
-                const int first = acc == 0 ? BN - 64 : 0;
-#pragma unroll 1
-                for (int i = 0; i < BN / 32; ++i) {
-                    const int c = (first + 32 * i) & (BN - 1);
-                    if (i == 2) {
-                        __syncwarp();
-                        tc_fence_before();
-                        mbar_arrive(tempty);
-                    }
-                    float v[32];
-                    __syncwarp();
-                    tmem_ld32(taddr + c, v);
-                    tmem_ld_wait();
-                    const int col = t.n_blk * BN + c;
-                    if (!ok || col >= p.N) continue;
-                    const int64_t off = static_cast<int64_t>(row) * p.N + col;
-                    if (p.out_f32) {
-                        float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + off);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            dst[j] = make_float4(v[4 * j] * p.alpha, v[4 * j + 1] * p.alpha,
-                                                 v[4 * j + 2] * p.alpha, v[4 * j + 3] * p.alpha);
-                    } else {
-                        uint4 *dst =
-                            reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + off);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                w[x] = pack_bf16x2(v[8 * j + 2 * x] * p.alpha,
-                                                   v[8 * j + 2 * x + 1] * p.alpha);
-                            dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
-                    }
-                }
-            }
-            acc ^= 1;
-            if (acc == 0) acc_phase ^= 1;
-        }
-    }
-
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 1) {
-        tc_fence_after();
-        tmem_dealloc(tmem, TMEM_COLS);
-    }
-}
-
-// ------------------------------------------------------------------ CTA pairs
-// The same product on 256 x 256 tiles of a cluster of two CTAs
-// (tcgen05.mma.cta_group::2).  A one-CTA tile needs 12 KB of operands for an
-// MMA of 128 cycles, more than an SM takes in (64 bytes a cycle); a pair
-// stages 8 KB per CTA for the same time, half of B each.
-//   SWIGLU: the even CTA stages the 128 gate rows, the odd CTA the up rows.
-// The scales of B are needed whole in both CTAs' tensor memory.  Scale copies
-// go to two sets of columns in turn, two scale tiles at a time, so that a set
-// is not rewritten while the MMAs in front still read it.
-// Two producer threads per CTA, one for A and one for B, halve the issue time
-// of a stage.  Output leaves through TMA stores of 32-row boxes.
-constexpr int BM2 = 256;
-constexpr int STAGES2 = 5;
-constexpr int THREADS2 = 224;              // A producer, MMA, 4 epilogue warps, B producer
-constexpr int EPI_BYTES = 32 * 64;         // one output box: 32 rows of 64 bytes
-
-template <int FMT>
-struct Cfg2 {
-    static constexpr int TILES = Cfg<FMT>::TILES;
-    static constexpr int SA_BYTES = TILES * kScaleTile;
-    static constexpr int SB_BYTES = 2 * SA_BYTES;
-    static constexpr int A_LOAD = A_BYTES + SA_BYTES;             // per CTA
-    static constexpr int B_LOAD = B_BYTES / 2 + SB_BYTES;
-    static constexpr int STAGE = A_LOAD + B_LOAD;
-    static constexpr int EPI_OFF = STAGES2 * STAGE;
-    static constexpr int BAR_OFF = EPI_OFF + 4 * 2 * EPI_BYTES;
-    static constexpr int NBARS = 2 * STAGES2 + 4;
-    static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
-    static constexpr int OFFS_OFF = MISC_OFF + 16;
-    static constexpr int PREFIX_OFF = OFFS_OFF + (MAX_GROUPS + 1) * 4;
-    static constexpr int SMEM = 1024 + PREFIX_OFF + (MAX_GROUPS + 2) * 4;
-    static constexpr int SETS = TILES / 2;                        // scale sets per stage
-    static_assert(SMEM <= 227 * 1024, "shared memory");
-    static_assert(STAGE % 1024 == 0, "swizzled tiles need 1 KB alignment");
-    static_assert(SF_COL + 2 * 24 <= TMEM_COLS, "scale columns");
-};
-
-// One 32-row x 64-byte output box (lane i holds row row0 + i as 16 words from
-// column col on) through one of the warp's two staging boxes, in the 64-byte
-// swizzle of the output map, and out as a TMA store.
-__device__ __forceinline__ void emit_box(uint8_t *ebox, int &eb, int lane, const uint32_t (&w)[16],
-                                         const CUtensorMap *map, int col, int row0) {
-    uint8_t *box = ebox + eb * EPI_BYTES;
-    if (lane == 0) bulk_wait_read<1>();      // the store that last used this box has read it
-    __syncwarp();
-#pragma unroll
-    for (int ch = 0; ch < 4; ++ch)
-        *reinterpret_cast<uint4 *>(box + lane * 64 + ((ch ^ ((lane >> 1) & 3)) << 4)) =
-            make_uint4(w[4 * ch], w[4 * ch + 1], w[4 * ch + 2], w[4 * ch + 3]);
-    fence_proxy_async();
-    __syncwarp();
-    if (lane == 0) {
-        tma_store_2d(map, box, col, row0);
-        bulk_commit();
-    }
-    eb ^= 1;
-}
-
-template <int FMT, int MODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS2, 1)
-    fp4_gemm_pair_kernel(const __grid_constant__ Params p) {
-    using C = Cfg2<FMT>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);   // even CTA's are used
-    uint64_t *empty = full + STAGES2;
-    uint64_t *tfull = empty + STAGES2;      // [2]
-    uint64_t *tempty = tfull + 2;           // even CTA's is used
-    uint64_t *drain = tempty + 1;
-    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF);
-    volatile int *s_abort = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 4);
-    volatile int *s_bad = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 8);
-    int *s_off = reinterpret_cast<int *>(smem + C::OFFS_OFF);
-    int *s_prefix = reinterpret_cast<int *>(smem + C::PREFIX_OFF);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rank = static_cast<int>(cluster_ctarank());
-    const bool leader = rank == 0;
-    const int first_tile = static_cast<int>(cluster_id_x());
-    const int step = static_cast<int>(gridDim.x) / 2;
-
-    if (tid == 0) *s_abort = 0;
-    if (tid == 32) {
-        for (int s = 0; s < STAGES2; ++s) {
-            mbar_init(&full[s], 2);          // the even CTA's two producers arm their shares
-            mbar_init(&empty[s], 1);
-        }
-        mbar_init(&tfull[0], 1);
-        mbar_init(&tfull[1], 1);
-        mbar_init(tempty, 8);                // four epilogue warps of both CTAs
-        mbar_init(drain, 1);
-        fence_barrier_init();
-    }
-    // both CTAs read the same offsets, so both leave here together
-    if (!list_tiles<BM2>(p, s_off, s_prefix, s_bad)) {
-        if (tid == 0 && blockIdx.x == 0) report(p.dev_status, MOE_DEV_BAD_OFFSETS);
-        return;
-    }
-    const int total = s_prefix[p.G];
-    if (warp == 1) {
-        tmem_alloc_pair(s_tmem, TMEM_COLS);
-        tmem_relinquish_pair();
-    }
-    tc_fence_before();
-    __syncthreads();
-    cluster_sync_all();                      // barriers and TMEM of both CTAs are ready
+    if (CG == 2) cluster_sync_all();         // barriers and TMEM of both CTAs are ready
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
     const uint32_t lead_full = mapa_shared(smem_u32(full), 0);
@@ -623,50 +430,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS2, 1)
     const int kblocks = (p.K + BK - 1) / BK;
     const int ktiles = p.K / Fp4<FMT>::TILE_K;
 
-    if (warp == 0 || warp == 6) {
-        // ================= TMA producers: warp 0 A, warp 6 B, each with its scales
+    if (warp == 0 || warp == 3) {
+        // ================= TMA producers: warp 0 A, warp 3 B, each with its scales
         if (elect_one()) {
             const bool is_a = warp == 0;
             tma_prefetch_desc(is_a ? &p.tmA : &p.tmB);
             tma_prefetch_desc(is_a ? &p.tmSA : &p.tmSB);
             int stage = 0;
             uint32_t phase = 0;
-            int armed[STAGES2];
-            for (int s = 0; s < STAGES2; ++s) armed[s] = -1;
+            int armed[STAGES];
+            for (int s = 0; s < STAGES; ++s) armed[s] = -1;
+            auto load2 = [&](void *dst, const CUtensorMap *m, int s, int c0, int c1) {
+                if (CG == 1)
+                    tma_load_2d(dst, m, &full[s], c0, c1);
+                else
+                    tma_load_2d_pair(dst, m, lead_full + 8u * static_cast<uint32_t>(s), c0, c1);
+            };
+            auto load3 = [&](void *dst, const CUtensorMap *m, int s, int c0, int c1, int c2) {
+                if (CG == 1)
+                    tma_load_3d(dst, m, &full[s], c0, c1, c2);
+                else
+                    tma_load_3d_pair(dst, m, lead_full + 8u * static_cast<uint32_t>(s), c0, c1, c2);
+            };
             for (int tile = first_tile; tile < total && !*s_abort; tile += step) {
-                const Tile t = decode_tile<BM2>(p, tile, s_off, s_prefix);
-                const int sa_blk =
-                    static_cast<int>(scale_row_block(t.g, s_off[t.g], t.row0)) + rank;
-                const int b0 = MODE == MODE_STORE ? t.n_blk * BN : t.n_blk * 128;
-                const int b1 = MODE == MODE_STORE ? b0 + 128 : p.N + b0;
+                const Tile t = decode_tile<BM * CG>(p, tile, s_off, s_prefix);
+                const int sa0 =
+                    (static_cast<int>(scale_row_block(t.g, s_off[t.g], t.row0)) + rank) * ktiles;
+                // the halves' first rows of B, and this CTA's
+                const int b0 = MODE == MODE_STORE ? t.n_blk * BN : t.n_blk * HN;
+                const int b1 = MODE == MODE_STORE ? b0 + HN : p.N + b0;
+                const int br = rank * (HN / CG);
                 const int64_t wblk = static_cast<int64_t>(t.g) * (p.wrows / 128);
-                const int sa0 = sa_blk * ktiles;
                 const int sb0 = static_cast<int>((wblk + b0 / 128) * ktiles);
                 const int sb1 = static_cast<int>((wblk + b1 / 128) * ktiles);
                 bool ok = true;
                 for (int kb = 0; kb < kblocks; ++kb) {
-                    if (!mbar_wait_bounded(&empty[stage], phase ^ 1, s_abort, p.dev_status)) {
+                    if (!wait_phase(&empty[stage], phase ^ 1, s_abort, p.dev_status)) {
                         ok = false;
                         break;
                     }
                     armed[stage] = static_cast<int>(phase);
                     uint8_t *a = smem + stage * C::STAGE;
                     uint8_t *b = a + A_BYTES;
-                    uint8_t *sa = b + B_BYTES / 2;
-                    uint8_t *sb = sa + C::SA_BYTES;
-                    const uint32_t fb = lead_full + 8u * static_cast<uint32_t>(stage);
+                    uint8_t *sf = b + 2 * C::B_HALF;
                     const int k0 = kb * (BK / 2), t0 = kb * C::TILES;
                     if (leader)
-                        mbar_arrive_expect_tx(&full[stage], 2u * (is_a ? C::A_LOAD : C::B_LOAD));
+                        mbar_arrive_expect_tx(&full[stage], CG * (is_a ? C::A_LOAD : C::B_LOAD));
                     if (is_a) {
-                        tma_load_2d_pair(a, &p.tmA, fb, k0, t.row0 + 128 * rank);
-                        tma_load_2d_pair(sa, &p.tmSA, fb, 0, sa0 + t0);
+                        load2(a, &p.tmA, stage, k0, t.row0 + BM * rank);
+                        load2(sf, &p.tmSA, stage, 0, sa0 + t0);
                     } else {
-                        tma_load_3d_pair(b, &p.tmB, fb, k0, rank == 0 ? b0 : b1, t.g);
-                        tma_load_2d_pair(sb, &p.tmSB, fb, 0, sb0 + t0);
-                        tma_load_2d_pair(sb + C::SA_BYTES, &p.tmSB, fb, 0, sb1 + t0);
+                        load3(b, &p.tmB, stage, k0, b0 + br, t.g);
+                        load3(b + C::B_HALF, &p.tmB, stage, k0, b1 + br, t.g);
+                        load2(sf + C::SF_BYTES, &p.tmSB, stage, 0, sb0 + t0);
+                        load2(sf + 2 * C::SF_BYTES, &p.tmSB, stage, 0, sb1 + t0);
                     }
-                    if (++stage == STAGES2) {
+                    if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1;
                     }
@@ -674,195 +493,171 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS2, 1)
                 if (!ok) break;
             }
             if (*s_abort && leader) {
-                for (int s = 0; s < STAGES2; ++s)
+                for (int s = 0; s < STAGES; ++s)
                     if (armed[s] >= 0) mbar_wait_drain(&full[s], static_cast<uint32_t>(armed[s]));
             }
         }
         __syncwarp();
-    } else if (warp == 1) {
-        // ================= MMA issuer (even CTA only)
+    } else if (warp == 1 || warp == 2) {
+        // ================= MMA issuers: warp 1 half 0, warp 2 half 1 (even CTA only)
         if (leader && elect_one()) {
+            const int h = warp - 1;
             int stage = 0;
             uint32_t phase = 0;
-            int acc = 0;
-            uint32_t free_phase = 1;
+            uint32_t u = static_cast<uint32_t>(h);          // half tile number
             uint32_t set = 0;
+            const uint32_t sf_col = tmem + SF_COL + static_cast<uint32_t>(h) * 2 * SF_SET;
+            const bool tail = p.K % BK != 0;                // the last slice holds 128 columns
             bool issued = false;
             for (int tile = first_tile; tile < total && !*s_abort; tile += step) {
-                if (!mbar_wait_bounded_cluster(tempty, free_phase, s_abort, p.dev_status)) break;
-                free_phase ^= 1;
+                if (!wait_acc(tempty, u, true, s_abort, p.dev_status)) break;
                 tc_fence_after();
-                const uint32_t d = tmem + static_cast<uint32_t>(acc * ACC1);
+                const uint32_t d = tmem + (u % NACC) * HN;
                 bool ok = true;
                 for (int kb = 0; kb < kblocks; ++kb) {
-                    if (!mbar_wait_bounded(&full[stage], phase, s_abort, p.dev_status)) {
+                    if (!wait_phase(&full[stage], phase, s_abort, p.dev_status)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t a = smem_u32(smem + stage * C::STAGE);
-                    const uint32_t b = a + A_BYTES;
-                    const uint32_t sa = b + B_BYTES / 2;
-                    const uint32_t sb = sa + C::SA_BYTES;
-                    const int steps = min(BK, p.K - kb * BK) / 64;
-                    constexpr int PER = 4 / C::SETS;              // MMAs per scale set
-#pragma unroll
-                    for (int h = 0; h < C::SETS; ++h) {
-                        const uint32_t sa_t = tmem + SF_COL + set * 24u, sb_t = sa_t + 8;
-                        if (h * PER >= steps) break;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint32_t o = (2 * h + i) * kScaleTile;
-                            copy_scales<2>(sa_t + 4 * i, sa + o);
-                            copy_scales<2>(sb_t + 8 * i, sb + o);
-                            copy_scales<2>(sb_t + 8 * i + 4, sb + C::SA_BYTES + o);
-                        }
-                        set ^= 1;
-#pragma unroll
-                        for (int j = 0; j < PER; ++j) {
-                            const int kk = h * PER + j;
-                            if (kk >= steps) break;
-                            const int i = FMT == MOE_FP4_MX ? j / 2 : j;
-                            const uint32_t id = FMT == MOE_FP4_MX && (j & 1)
-                                                    ? idesc<FMT>(BM2, BN, 2)
-                                                    : idesc<FMT>(BM2, BN, 0);
-                            mma_fp4<FMT, 2>(d, sdesc_kmajor_sw128(a + kk * 32),
-                                            sdesc_kmajor_sw128(b + kk * 32), id, sa_t + 4 * i,
-                                            sb_t + 8 * i, (kb | kk) != 0 ? 1u : 0u);
-                        }
-                    }
+                    const uint32_t b = a + A_BYTES + h * C::B_HALF;
+                    const uint32_t sa = a + A_BYTES + 2 * C::B_HALF;
+                    const uint32_t sb = sa + (1 + h) * C::SF_BYTES;
+                    if (kb + 1 < kblocks || !tail)
+                        issue_slice<FMT, CG, 4>(d, a, b, sa, sb, sf_col, set, kb != 0);
+                    else
+                        issue_slice<FMT, CG, 2>(d, a, b, sa, sb, sf_col, set, kb != 0);
                     issued = true;
-                    tc_commit_pair_mc(&empty[stage], 0x3);
-                    if (++stage == STAGES2) {
+                    if (CG == 1)
+                        tc_commit(&empty[stage]);
+                    else
+                        tc_commit_pair_mc(&empty[stage], 0x3);
+                    if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1;
                     }
                 }
                 if (!ok) break;
-                tc_commit_pair_mc(&tfull[acc], 0x3);
-                acc ^= 1;
+                if (CG == 1)
+                    tc_commit(&tfull[u % NACC]);
+                else
+                    tc_commit_pair_mc(&tfull[u % NACC], 0x3);
+                u += 2;
             }
             if (*s_abort && issued) {
-                tc_commit_pair_mc(drain, 0x1);
-                mbar_wait_drain(drain, 0);
+                // unwinding: every MMA issued so far ends before TMEM is freed
+                if (CG == 1)
+                    tc_commit(&drain[h]);
+                else
+                    tc_commit_pair_mc(&drain[h], 0x1);
+                mbar_wait_drain(&drain[h], 0);
             }
         }
         __syncwarp();
     } else {
-        // ================= epilogue (warps 2..5 of both CTAs)
+        // ================= epilogue (warps 4.. of every CTA)
+        // Two warps share a TMEM lane quarter; each takes 64 columns of a half.
         const int quarter = warp & 3;
-        uint8_t *ebox = smem + C::EPI_OFF + (warp - 2) * 2 * EPI_BYTES;
-        int eb = 0;
-        int acc = 0;
-        uint32_t acc_phase = 0;
-        for (int tile = first_tile; tile < total; tile += step) {
-            const Tile t = decode_tile<BM2>(p, tile, s_off, s_prefix);
-            if (!mbar_wait_bounded(&tfull[acc], acc_phase, s_abort, p.dev_status)) break;
+        const int c0 = 64 * ((warp - 4) >> 2);
+        uint8_t *box = smem + C::EPI_OFF + (warp - 4) * EPI_BYTES;
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        uint32_t u = 0;
+        // both 32-column parts of this warp's share of half tile u, and release it
+        auto drain_half = [&](float (&x)[32], float (&y)[32]) -> bool {
+            if (!wait_acc(tfull, u, false, s_abort, p.dev_status)) return false;
             tc_fence_after();
-            const int row_base = t.row0 + 128 * rank + quarter * 32;
-            const int row = row_base + lane;
-            const bool ok = row < t.row_end;
-            const bool boxed = row_base + 32 <= t.row_end;   // else a group's last rows: by lane
-            const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
-                                   static_cast<uint32_t>(acc * ACC1);
+            const uint32_t taddr = tmem + lanes + (u % NACC) * HN + static_cast<uint32_t>(c0);
+            __syncwarp();
+            tmem_ld32(taddr, x);
+            tmem_ld32(taddr + 32, y);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(lead_tempty + 8u * (u % NACC));
+            ++u;
+            return true;
+        };
+        for (int tile = first_tile; tile < total; tile += step) {
+            const Tile t = decode_tile<BM * CG>(p, tile, s_off, s_prefix);
+            const int row0 = t.row0 + BM * rank + quarter * 32;
+            const bool ok = row0 + lane < t.row_end;
+            const bool boxed = C::BOXES > 0 && row0 + 32 <= t.row_end;
             if (MODE != MODE_STORE) {
-                const int first = acc == 0 ? 64 : 0;         // the shared columns' half first
-#pragma unroll 1
-                for (int i = 0; i < 4; ++i) {
-                    const int c = (first + 32 * i) & 127;
-                    float g[32], u[32];
-                    __syncwarp();
-                    tmem_ld32(taddr + c, g);
-                    tmem_ld32(taddr + 128 + c, u);
-                    tmem_ld_wait();
-                    if (i == 1) {
-                        __syncwarp();
-                        tc_fence_before();
-                        if (lane == 0) mbar_arrive_cluster(lead_tempty);
-                    }
-                    uint32_t pk[16];
+                // half 0 is the gate, half 1 the same columns of up
+                float g0[32], g1[32], u0[32], u1[32];
+                if (!drain_half(g0, g1)) break;
 #pragma unroll
-                    for (int v = 0; v < 16; ++v)
-                        pk[v] = pack_bf16x2(swiglu(g[2 * v] * p.alpha, u[2 * v] * p.alpha),
-                                            swiglu(g[2 * v + 1] * p.alpha, u[2 * v + 1] * p.alpha));
-                    const int col = t.n_blk * 128 + c;
-                    if (MODE == MODE_SWIGLU_Q) {
-                        if (ok) emit_quantized<FMT>(p, pk, t.g, s_off[t.g], row, col);
-                    } else if (boxed) {
-                        emit_box(ebox, eb, lane, pk, &p.tmO, col, row_base);
-                    } else if (ok) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) +
-                                                               static_cast<int64_t>(row) * p.N + col);
-#pragma unroll
-                        for (int v = 0; v < 4; ++v)
-                            dst[v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2],
-                                                pk[4 * v + 3]);
-                    }
+                for (int i = 0; i < 32; ++i) {
+                    g0[i] = silu(g0[i] * p.alpha);
+                    g1[i] = silu(g1[i] * p.alpha);
                 }
+                if (!drain_half(u0, u1)) break;
+                const int col = t.n_blk * HN + c0;
+                uint32_t w[32];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    w[i] = pack_bf16x2(g0[2 * i] * (u0[2 * i] * p.alpha),
+                                       g0[2 * i + 1] * (u0[2 * i + 1] * p.alpha));
+                    w[16 + i] = pack_bf16x2(g1[2 * i] * (u1[2 * i] * p.alpha),
+                                            g1[2 * i + 1] * (u1[2 * i + 1] * p.alpha));
+                }
+                if (MODE != MODE_SWIGLU_Q)
+                    emit_words<uint16_t>(p, box, lane, boxed, ok, w, col, row0);
+                else if (ok)
+                    emit_quantized<FMT>(p, w, t.g, s_off[t.g], row0 + lane, col);
             } else {
-                const int first = acc == 0 ? BN - 64 : 0;
+                bool more = true;
 #pragma unroll 1
-                for (int i = 0; i < BN / 32; ++i) {
-                    const int c = (first + 32 * i) & (BN - 1);
-                    float v[32];
-                    __syncwarp();
-                    tmem_ld32(taddr + c, v);
-                    tmem_ld_wait();
-                    if (i == 1) {
-                        __syncwarp();
-                        tc_fence_before();
-                        if (lane == 0) mbar_arrive_cluster(lead_tempty);
-                    }
-                    const int col = t.n_blk * BN + c;
-                    if (col >= p.N) continue;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] *= p.alpha;
-                    uint32_t w[16];
+                for (int h = 0; h < 2; ++h) {
+                    float v[2][32];
+                    more = drain_half(v[0], v[1]);
+                    if (!more) break;
+                    const int col = t.n_blk * BN + h * HN + c0;
+                    if (col >= p.N) continue;                // N = 128 mod 256: no such columns
+                    uint32_t w[32];
                     if (p.out_f32) {
-                        float *dst = static_cast<float *>(p.out) + static_cast<int64_t>(row) * p.N + col;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
+                        for (int i = 0; i < 2; ++i) {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(v[16 * h + j]);
-                            if (boxed) {
-                                emit_box(ebox, eb, lane, w, &p.tmO, col + 16 * h, row_base);
-                            } else if (ok) {
-#pragma unroll
-                                for (int j = 0; j < 4; ++j)
-                                    reinterpret_cast<uint4 *>(dst + 16 * h)[j] = make_uint4(
-                                        w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-                            }
+                            for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(v[i][j] * p.alpha);
+                            emit_words<float>(p, box, lane, boxed, ok, w, col + 32 * i, row0);
                         }
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-                        if (boxed) {
-                            emit_box(ebox, eb, lane, w, &p.tmO, col, row_base);
-                        } else if (ok) {
-                            uint4 *dst = reinterpret_cast<uint4 *>(
-                                static_cast<uint16_t *>(p.out) + static_cast<int64_t>(row) * p.N + col);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2],
-                                                    w[4 * j + 3]);
-                        }
+                        for (int j = 0; j < 32; ++j)
+                            w[j] = pack_bf16x2(v[j / 16][2 * (j % 16)] * p.alpha,
+                                               v[j / 16][2 * (j % 16) + 1] * p.alpha);
+                        emit_words<uint16_t>(p, box, lane, boxed, ok, w, col, row0);
                     }
                 }
+                if (!more) break;
             }
-            acc ^= 1;
-            if (acc == 0) acc_phase ^= 1;
         }
-        if (lane == 0) bulk_wait<0>();       // every output box written
+        if (C::BOXES > 0 && lane == 0) bulk_wait<0>();   // every output box written
         __syncwarp();
     }
 
     tc_fence_before();
     __syncthreads();
-    cluster_sync_all();      // no CTA leaves while its peer may still signal or read it
+    if (CG == 2) cluster_sync_all();     // no CTA leaves while its peer may still signal or read it
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc_pair(tmem, TMEM_COLS);
+        if (CG == 1)
+            tmem_dealloc(tmem, TMEM_COLS);
+        else
+            tmem_dealloc_pair(tmem, TMEM_COLS);
     }
+}
+
+template <int FMT, int MODE>
+__global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_constant__ Params p) {
+    fp4_gemm<FMT, MODE, 1>(p);
+}
+template <int FMT, int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    fp4_gemm_pair_kernel(const __grid_constant__ Params p) {
+    fp4_gemm<FMT, MODE, 2>(p);
 }
 
 // ------------------------------------------------------------------ host side
@@ -911,16 +706,16 @@ bool scale_map(CUtensorMap *m, const uint8_t *sf, int64_t tiles, int box) {
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Output [rows, cols] as 32-row x 64-byte boxes, 64-byte swizzled.
+// Output [rows, cols] as 32-row x 128-byte boxes, swizzled.
 bool out_map(CUtensorMap *m, void *out, int64_t rows, int64_t cols, bool f32) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t esz = f32 ? 4 : 2;
     cuuint64_t dim[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
     cuuint64_t stride[1] = {static_cast<cuuint64_t>(cols) * esz};
-    cuuint32_t boxd[2] = {static_cast<cuuint32_t>(64 / esz), 32}, es[2] = {1, 1};
+    cuuint32_t boxd[2] = {static_cast<cuuint32_t>(128 / esz), 32}, es[2] = {1, 1};
     return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, out,
-              dim, stride, boxd, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+              dim, stride, boxd, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -930,12 +725,12 @@ bool use_pair(int n, int G) {
         const char *v = getenv("MOE_FP4_PAIR_ROWS");
         return v ? atoll(v) : 256ll;
     }();
-    return n / G >= least;
+    return n / G >= least && G <= std::min(Cfg<MOE_FP4_MX, 2>::MAX_G, Cfg<MOE_FP4_NV, 2>::MAX_G);
 }
 
 template <int FMT, int MODE>
 cudaError_t launch_pair(const Params &p, cudaStream_t stream) {
-    using C = Cfg2<FMT>;
+    using C = Cfg<FMT, 2>;
     static std::mutex mu;
     static int max_clusters[64] = {};
     int dev = 0;
@@ -946,13 +741,13 @@ cudaError_t launch_pair(const Params &p, cudaStream_t stream) {
         if (dev >= 64 || max_clusters[dev] == 0) {
             const cudaError_t e =
                 cudaFuncSetAttribute(fp4_gemm_pair_kernel<FMT, MODE>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
             if (e != cudaSuccess) return e;
             // no more clusters than can be resident at once
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(static_cast<unsigned>(num_sms()), 1, 1);
-            cfg.blockDim = dim3(THREADS2, 1, 1);
-            cfg.dynamicSmemBytes = C::SMEM;
+            cfg.blockDim = dim3(THREADS, 1, 1);
+            cfg.dynamicSmemBytes = C::smem(C::MAX_G);
             cfg.stream = stream;
             int n = 0;
             if (cudaOccupancyMaxActiveClusters(&n, fp4_gemm_pair_kernel<FMT, MODE>, &cfg) !=
@@ -967,15 +762,15 @@ cudaError_t launch_pair(const Params &p, cudaStream_t stream) {
             limit = max_clusters[dev];
         }
     }
-    const int64_t tiles = (static_cast<int64_t>(p.n / BM2) + p.G) * p.nt;
+    const int64_t tiles = (static_cast<int64_t>(p.n / (2 * BM)) + p.G) * p.nt;
     const int clusters = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(limit, tiles)));
-    fp4_gemm_pair_kernel<FMT, MODE><<<2 * clusters, THREADS2, C::SMEM, stream>>>(p);
+    fp4_gemm_pair_kernel<FMT, MODE><<<2 * clusters, THREADS, C::smem(p.G), stream>>>(p);
     return cudaGetLastError();
 }
 
 template <int FMT, int MODE>
 cudaError_t launch(Params &p, cudaStream_t stream) {
-    using C = Cfg<FMT>;
+    using C = Cfg<FMT, 1>;
     if (use_pair(p.n, p.G)) {
         if (MODE != MODE_SWIGLU_Q && !out_map(&p.tmO, p.out, p.n, p.N, p.out_f32 != 0))
             return cudaErrorInvalidValue;
@@ -989,7 +784,7 @@ cudaError_t launch(Params &p, cudaStream_t stream) {
         std::lock_guard<std::mutex> lock(mu);
         if (dev >= 64 || !attr_done[dev]) {
             const cudaError_t e = cudaFuncSetAttribute(
-                fp4_gemm_kernel<FMT, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+                fp4_gemm_kernel<FMT, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
             if (e != cudaSuccess) return e;
             if (dev < 64) attr_done[dev] = true;
         }
@@ -997,7 +792,7 @@ cudaError_t launch(Params &p, cudaStream_t stream) {
     // at most this many tiles: ceil(rows / 128) summed over the groups
     const int64_t tiles = (static_cast<int64_t>(p.n / BM) + p.G) * p.nt;
     const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms(), tiles)));
-    fp4_gemm_kernel<FMT, MODE><<<grid, THREADS, C::SMEM, stream>>>(p);
+    fp4_gemm_kernel<FMT, MODE><<<grid, THREADS, C::smem(p.G), stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -1008,11 +803,11 @@ struct Product {
 };
 
 template <int FMT>
-bool make_maps(Params &p, const Product &d, int wrows) {
+bool make_maps(Params &p, const Product &d, int wrows, bool pair) {
     constexpr int TK = Fp4<FMT>::TILE_K;
     const int64_t ktiles = d.K / TK;
     return code_map(&p.tmA, d.a->q, 2, 1, d.n, d.K, BM) &&
-           code_map(&p.tmB, d.w->q, 3, d.G, wrows, d.K, 128) &&
+           code_map(&p.tmB, d.w->q, 3, d.G, wrows, d.K, pair ? HN / 2 : HN) &&
            scale_map(&p.tmSA, d.a->sf, (d.n / 128 + d.G) * ktiles, BK / TK) &&
            scale_map(&p.tmSB, d.w->sf, static_cast<int64_t>(d.G) * (wrows / 128) * ktiles, BK / TK);
 }
@@ -1022,7 +817,8 @@ cudaError_t launch_product(const Product &d, int mode, void *out, bool out_f32,
     const bool mx = d.a->format == MOE_FP4_MX;
     const int wrows = mode == MODE_STORE ? d.N : 2 * d.N;
     Params p{};
-    if (!(mx ? make_maps<MOE_FP4_MX>(p, d, wrows) : make_maps<MOE_FP4_NV>(p, d, wrows)))
+    const bool pair = use_pair(d.n, d.G);
+    if (!(mx ? make_maps<MOE_FP4_MX>(p, d, wrows, pair) : make_maps<MOE_FP4_NV>(p, d, wrows, pair)))
         return cudaErrorInvalidValue;
     p.offsets = d.offsets;
     p.G = d.G;
