@@ -130,12 +130,14 @@ __device__ __forceinline__ bool elect_one() {
 // Bounded wait (as mbar_wait_bounded) whose first 64 polls read no timer: a
 // %globaltimer read takes far longer than a hand-over between two roles, and
 // here one sits on the path from a finished accumulator to the next tile's
-// first MMA.  Cluster-scope acquire.
+// first MMA.  No wait here publishes ordinary memory between CTAs (operands
+// come by TMA, accumulators through tensor memory, each with its own ordering),
+// so CTA scope is enough.
 __device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort,
                                        int32_t *dev_status) {
     uint64_t t0 = 0;
     for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait_cluster(bar, parity)) return true;
+        if (mbar_try_wait(bar, parity)) return true;
         if ((it & 63u) == 0u) {
             if (*abort) return false;
             const uint64_t t = global_timer_ns();
@@ -148,9 +150,15 @@ __device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, volatile 
         }
     }
 }
+// Arrive on a barrier of the pair's even CTA once this warp's tensor memory
+// loads have ended (tcgen05.wait::ld and the fence before it order those; a
+// cluster-scope release would also wait for its output stores).
+__device__ __forceinline__ void arrive_drained(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volatile int *abort,
                                            int32_t *dev_status) {
-    return mbar_try_wait_cluster(bar, parity) || wait_slow(bar, parity, abort, dev_status);
+    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort, dev_status);
 }
 
 // D (+)= A * B^T with the scales at sa (rows of A) and sb (rows of B).
@@ -574,7 +582,7 @@ __device__ __forceinline__ void fp4_gemm(const Params &p) {
             tmem_ld_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(lead_tempty + 8u * (u % NACC));
+            if (lane == 0) arrive_drained(lead_tempty + 8u * (u % NACC));
             ++u;
             return true;
         };
