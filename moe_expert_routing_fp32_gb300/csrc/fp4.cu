@@ -151,7 +151,7 @@ fp4_dequantize_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__
             uint32_t o[4];
 #pragma unroll
             for (int p = 0; p < 4; ++p)
-                o[p] = pack_bf16x2(e2m1_value(w >> (8 * p)) * s, e2m1_value(w >> (8 * p + 4)) * s);
+                o[p] = bf16x2(e2m1_value(w >> (8 * p)) * s, e2m1_value(w >> (8 * p + 4)) * s);
             dst[c / 8] = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }

@@ -51,6 +51,14 @@ __device__ __forceinline__ int find_group(const int *off, int G, int r) {
     return (off[lo] >= 0 && off[lo] <= r && r < off[lo + 1]) ? lo : -1;
 }
 
+// Two fp32 values to packed bf16 (nearest even) in one conversion; two single
+// conversions and a merge take four times as long in a kernel's epilogue.
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // Four packed e2m1 pairs: the eight values' codes, value i in bits [4i, 4i+4)
 // (nearest, ties to even, magnitudes beyond 6 to 6).
 __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {

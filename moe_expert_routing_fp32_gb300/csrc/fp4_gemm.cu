@@ -275,27 +275,24 @@ __device__ bool list_tiles(const Params &p, int *s_off, int *s_prefix, volatile 
 
 // Tiles of a group: rows fastest while the group has fewer rows than its
 // weights (a weight tile is read from L2 by its row blocks one after the
-// other), columns fastest otherwise.
+// other), columns fastest otherwise.  A role's tiles only ascend, so the group
+// is found by walking on from the last one's (`g`); a search per tile costs the
+// roles several hundred cycles of latency each.
 template <int BMT>
-__device__ __forceinline__ Tile decode_tile(const Params &p, int tile, const int *s_off,
+__device__ __forceinline__ Tile decode_tile(const Params &p, int tile, int &g, const int *s_off,
                                             const int *s_prefix) {
-    int lo = 0, hi = p.G - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (s_prefix[mid] <= tile)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
+    while (s_prefix[g + 1] <= tile) ++g;
     Tile t;
-    const int cnt = s_off[lo + 1] - s_off[lo];
-    const int mt = (cnt + BMT - 1) / BMT;
-    const int local = tile - s_prefix[lo];
+    const int start = s_off[g], end = s_off[g + 1], cnt = end - start;
+    const int local = tile - s_prefix[g];
     const bool nfast = cnt > p.wrows;
-    t.g = lo;
-    t.n_blk = nfast ? local % p.nt : local / mt;
-    t.row0 = s_off[lo] + (nfast ? local / p.nt : local % mt) * BMT;
-    t.row_end = s_off[lo + 1];
+    const int inner = nfast ? p.nt : (cnt + BMT - 1) / BMT;
+    const int hi = static_cast<int>(static_cast<unsigned>(local) / static_cast<unsigned>(inner));
+    const int lo = local - hi * inner;
+    t.g = g;
+    t.n_blk = nfast ? lo : hi;
+    t.row0 = start + (nfast ? hi : lo) * BMT;
+    t.row_end = end;
     return t;
 }
 
@@ -460,8 +457,9 @@ __device__ __forceinline__ void fp4_gemm(const Params &p) {
                 else
                     tma_load_3d_pair(dst, m, lead_full + 8u * static_cast<uint32_t>(s), c0, c1, c2);
             };
+            int g = 0;
             for (int tile = first_tile; tile < total && !*s_abort; tile += step) {
-                const Tile t = decode_tile<BM * CG>(p, tile, s_off, s_prefix);
+                const Tile t = decode_tile<BM * CG>(p, tile, g, s_off, s_prefix);
                 const int sa0 =
                     (static_cast<int>(scale_row_block(t.g, s_off[t.g], t.row0)) + rank) * ktiles;
                 // the halves' first rows of B, and this CTA's
@@ -586,8 +584,9 @@ __device__ __forceinline__ void fp4_gemm(const Params &p) {
             ++u;
             return true;
         };
+        int g = 0;
         for (int tile = first_tile; tile < total; tile += step) {
-            const Tile t = decode_tile<BM * CG>(p, tile, s_off, s_prefix);
+            const Tile t = decode_tile<BM * CG>(p, tile, g, s_off, s_prefix);
             const int row0 = t.row0 + BM * rank + quarter * 32;
             const bool ok = row0 + lane < t.row_end;
             const bool boxed = C::BOXES > 0 && row0 + 32 <= t.row_end;
@@ -605,9 +604,9 @@ __device__ __forceinline__ void fp4_gemm(const Params &p) {
                 uint32_t w[32];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    w[i] = pack_bf16x2(g0[2 * i] * (u0[2 * i] * p.alpha),
+                    w[i] = bf16x2(g0[2 * i] * (u0[2 * i] * p.alpha),
                                        g0[2 * i + 1] * (u0[2 * i + 1] * p.alpha));
-                    w[16 + i] = pack_bf16x2(g1[2 * i] * (u1[2 * i] * p.alpha),
+                    w[16 + i] = bf16x2(g1[2 * i] * (u1[2 * i] * p.alpha),
                                             g1[2 * i + 1] * (u1[2 * i + 1] * p.alpha));
                 }
                 if (MODE != MODE_SWIGLU_Q)
@@ -634,7 +633,7 @@ __device__ __forceinline__ void fp4_gemm(const Params &p) {
                     } else {
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            w[j] = pack_bf16x2(v[j / 16][2 * (j % 16)] * p.alpha,
+                            w[j] = bf16x2(v[j / 16][2 * (j % 16)] * p.alpha,
                                                v[j / 16][2 * (j % 16) + 1] * p.alpha);
                         emit_words<uint16_t>(p, box, lane, boxed, ok, w, col, row0);
                     }

@@ -19,7 +19,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "common.cuh"
+#include "fp4.cuh"
 #include "internal.h"
 
 namespace moe {
@@ -540,7 +540,7 @@ finalize_backward_kernel(const void *__restrict__ d_out, const void *__restrict_
                         for (int i = 0; i < 4; ++i) {
                             acc[u] += d[2 * i] * __uint_as_float(wd[i] << 16);
                             acc[u] += d[2 * i + 1] * __uint_as_float(wd[i] & 0xFFFF0000u);
-                            o[i] = pack_bf16x2(w[u] * d[2 * i], w[u] * d[2 * i + 1]);
+                            o[i] = bf16x2(w[u] * d[2 * i], w[u] * d[2 * i + 1]);
                         }
                         *(reinterpret_cast<uint4 *>(static_cast<uint16_t *>(d_y) +
                                                     static_cast<int64_t>(row[u]) * H) + v) =
