@@ -2,12 +2,12 @@
 //
 // Both kernels are copies with arithmetic on the way and bound by HBM: per
 // element 2 bytes in and 1/2 + 1/block bytes out for every row written, or
-// the reverse.  A warp takes 1024 columns of one row: four passes of 256
-// columns, a lane holding 8 of them (16 bytes), so loads and stores are whole
-// 512- and 128-byte lines and a block's largest magnitude needs two shuffles
-// (32 columns) or one (16).  With `row_idx` a token's row is read and
+// the reverse.  A warp takes 1024 columns of a row, a lane 32 of them: whole
+// blocks, so a block's largest magnitude is found without another lane, and 16
+// bytes of codes to a store.  With `row_idx` a token's row is read and
 // quantised once and written to each of its k rows in expert order, the
 // permute of the bf16 path at a quarter of its bytes.
+//
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -46,122 +46,175 @@ fp4_quantize_kernel(const uint16_t *__restrict__ x, const int32_t *__restrict__ 
                     int K, int k, int n, const int32_t *__restrict__ offsets, int G,
                     float inv_unit, float unit, uint8_t *__restrict__ q, uint8_t *__restrict__ sf,
                     int32_t *dev_status) {
-    constexpr int LPB = Fp4<FMT>::BLOCK / 8;         // lanes sharing a block
+    constexpr int BLOCKS = 32 / Fp4<FMT>::BLOCK;     // scale blocks of a lane's 32 columns
+    constexpr int LPT = 4 / BLOCKS;                  // lanes sharing a tile's four blocks
     __shared__ int s_off[kMaxGroups + 1];
     load_offsets(s_off, offsets, G);
     const int lane = threadIdx.x & 31;
     const int pieces = (K + Q_COLS - 1) / Q_COLS;
     const int64_t units = static_cast<int64_t>(T) * pieces;
     const int64_t tile_row = static_cast<int64_t>(K / Fp4<FMT>::TILE_K) * kScaleTile;
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * (Q_THREADS / 32);
-    for (int64_t u = blockIdx.x * static_cast<int64_t>(Q_THREADS / 32) + (threadIdx.x >> 5);
-         u < units; u += warps) {
+    const int per_cta = blockDim.x / 32;
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * per_cta;
+    for (int64_t u = blockIdx.x * static_cast<int64_t>(per_cta) + (threadIdx.x >> 5); u < units;
+         u += warps) {
         const int t = static_cast<int>(u / pieces);
-        const int c0 = static_cast<int>(u % pieces) * Q_COLS;
+        const int c = static_cast<int>(u % pieces) * Q_COLS + lane * 32;
         // lane j holds destination j: its row and where its scales go
         int my_row = -1;
+        if (lane < k) my_row = row_idx ? row_idx[static_cast<int64_t>(t) * k + lane] : t;
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (c < K)
+                v[i] = __ldg(reinterpret_cast<const uint4 *>(x + static_cast<int64_t>(t) * K + c) + i);
+        }
         int64_t my_sf = -1;
-        if (lane < k) {
-            my_row = row_idx ? row_idx[static_cast<int64_t>(t) * k + lane] : t;
-            if (my_row >= n) {
-                report(dev_status, MOE_DEV_BAD_OFFSETS);
-                my_row = -1;
-            }
-            if (my_row >= 0) my_sf = row_scales(s_off, G, my_row, tile_row);
-            if (my_sf < 0) my_row = -1;              // behind the last group: left as it was
+        if (my_row >= n) report(dev_status, MOE_DEV_BAD_OFFSETS);
+        if (my_row >= 0 && my_row < n) my_sf = row_scales(s_off, G, my_row, tile_row);
+        if (my_sf < 0) my_row = -1;                  // behind the last group: left as it was
+        uint32_t am[4], code[4], sc = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            am[i] = amax8(w);
         }
-        const uint4 *src = reinterpret_cast<const uint4 *>(x + static_cast<int64_t>(t) * K);
-        uint32_t code[Q_COLS / 256];
-        uint32_t sc[Q_COLS / 256];
 #pragma unroll
-        for (int i = 0; i < Q_COLS / 256; ++i) {
-            const int c = c0 + i * 256 + lane * 8;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (c < K) v = __ldg(src + c / 8);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            uint32_t am = amax8(w);
-#pragma unroll
-            for (int o = 1; o < LPB; o <<= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
+        for (int b = 0; b < BLOCKS; ++b) {
             float factor;
-            uint32_t b = block_scale<FMT>(am, inv_unit, unit, factor);
-            code[i] = quantize8<FMT>(w, factor);
-            // the four scale bytes of a tile's row end up in its first lane
-            b |= __shfl_down_sync(0xffffffffu, b, LPB) << 8;
-            b |= __shfl_down_sync(0xffffffffu, b, 2 * LPB) << 16;
-            sc[i] = b;
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = b * 4 / BLOCKS; i < (b + 1) * 4 / BLOCKS; ++i) m = max(m, am[i]);
+            sc |= block_scale<FMT>(m, inv_unit, unit, factor) << (8 * b);
+#pragma unroll
+            for (int i = b * 4 / BLOCKS; i < (b + 1) * 4 / BLOCKS; ++i) {
+                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                code[i] = quantize8<FMT>(w, factor);
+            }
         }
+        // the four scale bytes of a tile's row end up in its first lane
+#pragma unroll
+        for (int o = 1; o < LPT; o <<= 1)
+            sc |= __shfl_down_sync(0xffffffffu, sc, o) << (8 * BLOCKS * o);
         for (int j = 0; j < k; ++j) {
             const int row = __shfl_sync(0xffffffffu, my_row, j);
             const int64_t so = __shfl_sync(0xffffffffu, my_sf, j);
-            if (row < 0) continue;
-            uint32_t *dst = reinterpret_cast<uint32_t *>(q + static_cast<int64_t>(row) * (K / 2));
-#pragma unroll
-            for (int i = 0; i < Q_COLS / 256; ++i) {
-                const int c = c0 + i * 256 + lane * 8;
-                if (c >= K) break;
-                dst[c / 8] = code[i];
-                if (lane % (4 * LPB) == 0)
-                    *reinterpret_cast<uint32_t *>(sf + so + c / Fp4<FMT>::TILE_K * kScaleTile) =
-                        sc[i];
-            }
+            if (row < 0 || c >= K) continue;
+            *reinterpret_cast<uint4 *>(q + static_cast<int64_t>(row) * (K / 2) + c / 2) =
+                make_uint4(code[0], code[1], code[2], code[3]);
+            if (lane % LPT == 0)
+                *reinterpret_cast<uint32_t *>(sf + so + static_cast<int64_t>(c / Fp4<FMT>::TILE_K) *
+                                                            kScaleTile) = sc;
         }
     }
 }
 
-// e2m1 code -> value, exactly.
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-    const uint32_t e = (c >> 1) & 3u, m = c & 1u;
-    const float v = e == 0 ? 0.5f * static_cast<float>(m)
-                           : __uint_as_float(((e + 126u) << 23) | (m << 22));
-    return (c & 8u) ? -v : v;
+// Two e2m1 codes (a byte) to fp32, times s, as packed bf16; the products have
+// at most six significant bits, so nothing is rounded.
+__device__ __forceinline__ uint32_t dequantize2(uint32_t byte, float s) {
+    uint32_t h;
+    asm("{\n\t.reg .b8 c;\n\tcvt.u8.u32 c, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, c;\n\t}"
+        : "=r"(h)
+        : "r"(byte));
+    float lo, hi;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(h));
+    return bf16x2(lo * s, hi * s);
 }
 
+// A warp takes 1024 columns of the rows r, r + 32, r + 64 and r + 96 of a
+// 128-row scale block: their scale bytes share 16 bytes of every tile, loaded
+// once.  A row's eight passes of 128 columns write 8 bytes a lane.
 template <int FMT>
 __global__ void __launch_bounds__(Q_THREADS)
 fp4_dequantize_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ sf,
                       const int32_t *__restrict__ offsets, int G, int n, int K, float unit,
                       uint16_t *__restrict__ out) {
+    constexpr int TK = Fp4<FMT>::TILE_K;
     __shared__ int s_off[kMaxGroups + 1];
     load_offsets(s_off, offsets, G);
     const int lane = threadIdx.x & 31;
     const int pieces = (K + Q_COLS - 1) / Q_COLS;
-    const int64_t units = static_cast<int64_t>(n) * pieces;
-    const int64_t tile_row = static_cast<int64_t>(K / Fp4<FMT>::TILE_K) * kScaleTile;
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * (Q_THREADS / 32);
-    for (int64_t u = blockIdx.x * static_cast<int64_t>(Q_THREADS / 32) + (threadIdx.x >> 5);
-         u < units; u += warps) {
-        const int r = static_cast<int>(u / pieces);
+    const int64_t blocks = offsets ? static_cast<int64_t>(n / 128) + G : (static_cast<int64_t>(n) + 127) / 128;
+    const int64_t units = blocks * 32 * pieces;
+    const int ktiles = K / TK;
+    const int per_cta = blockDim.x / 32;
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * per_cta;
+    for (int64_t u = blockIdx.x * static_cast<int64_t>(per_cta) + (threadIdx.x >> 5); u < units;
+         u += warps) {
         const int c0 = static_cast<int>(u % pieces) * Q_COLS;
-        const int64_t so = row_scales(s_off, G, r, tile_row);
-        if (so < 0) continue;
-        const uint32_t *src = reinterpret_cast<const uint32_t *>(q + static_cast<int64_t>(r) * (K / 2));
-        uint4 *dst = reinterpret_cast<uint4 *>(out + static_cast<int64_t>(r) * K);
+        const int64_t rb = u / pieces;
+        const int r32 = static_cast<int>(rb & 31);
+        const int64_t blk = rb >> 5;
+        // the last group whose blocks begin at or before this one
+        int g = 0;
+        if (offsets) {
+            int hi = G - 1;
+            while (g < hi) {
+                const int mid = (g + hi + 1) >> 1;
+                if (scale_row_block(mid, s_off[mid], s_off[mid]) <= blk)
+                    g = mid;
+                else
+                    hi = mid - 1;
+            }
+        }
+        const int start = s_off[g], end = offsets ? min(s_off[g + 1], n) : n;
+        const int64_t first = start + (blk - scale_row_block(g, start, start)) * 128 + r32;
+        if (start < 0 || blk < scale_row_block(g, start, start) || first >= end) continue;
+        // lane i < tiles of the piece: 16 scale bytes of tile i, one word per row
+        const int t0 = c0 / TK;
+        uint4 sc = make_uint4(0u, 0u, 0u, 0u);
+        if (lane < Q_COLS / TK && t0 + lane < ktiles)
+            sc = __ldg(reinterpret_cast<const uint4 *>(
+                sf + (blk * ktiles + t0 + lane) * kScaleTile + r32 * 16));
+        const uint32_t words[4] = {sc.x, sc.y, sc.z, sc.w};
 #pragma unroll
-        for (int i = 0; i < Q_COLS / 256; ++i) {
-            const int c = c0 + i * 256 + lane * 8;
-            if (c >= K) break;
-            const uint32_t w = __ldg(src + c / 8);
-            const uint32_t b = sf[so + static_cast<int64_t>(c / Fp4<FMT>::TILE_K) * kScaleTile +
-                                  c / Fp4<FMT>::BLOCK % 4];
-            float s;
-            if (FMT == MOE_FP4_MX)
-                s = b == 0 ? __uint_as_float(1u << 22) : __uint_as_float(b << 23);
-            else
-                s = e4m3_value(b) * unit;
-            uint32_t o[4];
+        for (int j = 0; j < 4; ++j) {
+            const int64_t row = first + 32 * j;
+            if (row >= end) break;
+            const uint8_t *src = q + row * (K / 2);
+            uint16_t *dst = out + row * K;
+            uint32_t w[4];
 #pragma unroll
-            for (int p = 0; p < 4; ++p)
-                o[p] = bf16x2(e2m1_value(w >> (8 * p)) * s, e2m1_value(w >> (8 * p + 4)) * s);
-            dst[c / 8] = make_uint4(o[0], o[1], o[2], o[3]);
+            for (int i = 0; i < 4; ++i) {
+                const int c = c0 + i * 256 + lane * 8;
+                w[i] = c < K ? __ldg(reinterpret_cast<const uint32_t *>(src + c / 2)) : 0u;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int cl = i * 256 + lane * 8;
+                const uint32_t b = __shfl_sync(0xffffffffu, words[j], cl / TK) >>
+                                       (8 * (cl / Fp4<FMT>::BLOCK % 4)) & 0xFFu;
+                float s;
+                if (FMT == MOE_FP4_MX)
+                    s = b == 0 ? __uint_as_float(1u << 22) : __uint_as_float(b << 23);
+                else
+                    s = e4m3_value(b) * unit;
+                if (c0 + cl < K)
+                    *reinterpret_cast<uint4 *>(dst + c0 + cl) =
+                        make_uint4(dequantize2(w[i] & 0xFFu, s), dequantize2(w[i] >> 8 & 0xFFu, s),
+                                   dequantize2(w[i] >> 16 & 0xFFu, s), dequantize2(w[i] >> 24, s));
+            }
         }
     }
 }
 
 inline bool a16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-int q_grid(int64_t units) {
-    return static_cast<int>(std::max<int64_t>(
-        1, std::min<int64_t>(ceil_div(units, Q_THREADS / 32), static_cast<int64_t>(num_sms()) * 8)));
+// Warps for `units` pieces: eight to a CTA and eight CTAs to an SM at most; few
+// units spread over the SMs in smaller CTAs (64 rows of 4096 columns: 256 units
+// on 128 CTAs instead of 32).
+struct QShape {
+    int grid, threads;
+};
+QShape q_shape(int64_t units) {
+    const int64_t sms = num_sms();
+    int per = Q_THREADS / 32;
+    while (per > 1 && ceil_div(units, per) < 2 * sms) per /= 2;
+    return {static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(ceil_div(units, per), sms * 8))),
+            per * 32};
 }
 
 }  // namespace
@@ -205,15 +258,15 @@ extern "C" moe_status_t moe_fp4_quantize(const moe_bf16_t *x, int32_t T, int32_t
         return MOE_ERR_INVALID_ARG;
     if (!current_device_ok()) return MOE_ERR_NO_DEVICE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int grid = q_grid(static_cast<int64_t>(T) * ceil_div(K, Q_COLS));
+    const QShape qs = q_shape(static_cast<int64_t>(T) * ceil_div(K, Q_COLS));
     const int groups = offsets ? G : 1;
     const float unit = pow2f(out->scale_exp), inv = pow2f(-out->scale_exp);
     if (out->format == MOE_FP4_MX)
-        fp4_quantize_kernel<MOE_FP4_MX><<<grid, Q_THREADS, 0, s>>>(
+        fp4_quantize_kernel<MOE_FP4_MX><<<qs.grid, qs.threads, 0, s>>>(
             x, expanded_row_idx, T, K, k, T * k, offsets, groups, inv, unit, out->q, out->sf,
             dev_status);
     else
-        fp4_quantize_kernel<MOE_FP4_NV><<<grid, Q_THREADS, 0, s>>>(
+        fp4_quantize_kernel<MOE_FP4_NV><<<qs.grid, qs.threads, 0, s>>>(
             x, expanded_row_idx, T, K, k, T * k, offsets, groups, inv, unit, out->q, out->sf,
             dev_status);
     return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
@@ -231,14 +284,15 @@ extern "C" moe_status_t moe_fp4_dequantize(const moe_fp4_t *m, int32_t n, int32_
     if (!x || !m->q || !m->sf || !a16(x) || !a16(m->q) || !a16(m->sf)) return MOE_ERR_INVALID_ARG;
     if (!current_device_ok()) return MOE_ERR_NO_DEVICE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int grid = q_grid(static_cast<int64_t>(n) * ceil_div(K, Q_COLS));
+    const QShape qs = q_shape((offsets ? n / 128 + static_cast<int64_t>(G) : ceil_div(n, 128)) * 32 *
+                              ceil_div(K, Q_COLS));
     const int groups = offsets ? G : 1;
     const float unit = pow2f(m->scale_exp);
     if (m->format == MOE_FP4_MX)
-        fp4_dequantize_kernel<MOE_FP4_MX><<<grid, Q_THREADS, 0, s>>>(m->q, m->sf, offsets, groups, n,
+        fp4_dequantize_kernel<MOE_FP4_MX><<<qs.grid, qs.threads, 0, s>>>(m->q, m->sf, offsets, groups, n,
                                                                     K, unit, x);
     else
-        fp4_dequantize_kernel<MOE_FP4_NV><<<grid, Q_THREADS, 0, s>>>(m->q, m->sf, offsets, groups, n,
+        fp4_dequantize_kernel<MOE_FP4_NV><<<qs.grid, qs.threads, 0, s>>>(m->q, m->sf, offsets, groups, n,
                                                                     K, unit, x);
     return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
