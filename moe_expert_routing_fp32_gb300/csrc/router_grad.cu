@@ -11,9 +11,11 @@
 //   w_j = p_{i_j} / sum_l p_{i_l}:  d logits[i_j] += w_j (dw_j - sum_l w_l dw_l)
 //   w_j = p_{i_j}:  d logits[e] += sum_{j: i_j = e} p_e dw_j - p_e sum_l p_{i_l} dw_l.
 //
-// Bound: the logits are read once by each pass and the gradient written once.
-// A group of lanes (16 for E <= 64 in whole float4s, else 32) holds one
-// token's row in registers; nothing is staged through shared memory.
+// Bound: the logits are read once by each pass and the gradient written once;
+// in practice the instructions of a row's reductions count as much.  A group of
+// 8, 16 or 32 lanes holds a token's row in registers, as few lanes as leave
+// each up to 16 values: a reduction over 8 lanes takes three shuffles for four
+// tokens, one over 32 takes five for one.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -61,16 +63,20 @@ struct Row {
             const int e = (c * LPT + l) * VEC;
             if (e >= E) continue;
             if (VEC == 4)
-                *reinterpret_cast<float4 *>(row + e) =
-                    make_float4(z[c * 4], z[c * 4 + 1], z[c * 4 + 2], z[c * 4 + 3]);
+                __stcs(reinterpret_cast<float4 *>(row + e),
+                       make_float4(z[c * 4], z[c * 4 + 1], z[c * 4 + 2], z[c * 4 + 3]));
             else
-                row[e] = z[c];
+                __stcs(row + e, z[c]);
         }
     }
 };
 
 template <int LPT>
 __device__ __forceinline__ float group_max(float v) {
+    if constexpr (LPT == 32) {
+        asm volatile("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(v));
+        return v;
+    }
 #pragma unroll
     for (int o = LPT / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
@@ -82,27 +88,50 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
-// z -> p in place; returns (max, 1 / sum).  A row with no finite logit gives
-// zeros.
-template <int LPT, int N>
-__device__ __forceinline__ float2 softmax_row(float (&z)[N]) {
-    float m = kNegInf;
-#pragma unroll
-    for (int i = 0; i < N; ++i) m = fmaxf(m, z[i]);
-    m = group_max<LPT>(m);
-    if (m == kNegInf) m = 0.0f;
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        z[i] = expf(z[i] - m);
-        s += z[i];
-    }
-    s = group_sum<LPT>(s);
-    const float r = s > 0.0f ? 1.0f / s : 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) z[i] *= r;
-    return make_float2(m, r);
+constexpr float kLog2e = 1.4426950408889634f;
+// exp(z - m); the difference first, so that the lowest values and -inf work.
+__device__ __forceinline__ float exp_from(float z, float m) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"((z - m) * kLog2e));
+    return r;
 }
+
+// z -> p in place for U rows; returns (max, 1 / sum) of each.  A row with
+// no finite logit gives zeros.
+template <int LPT, int U, int N>
+__device__ __forceinline__ void softmax_rows(float (&z)[U][N], float2 (&mr)[U]) {
+    float s[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        float m = kNegInf;
+#pragma unroll
+        for (int i = 0; i < N; ++i) m = fmaxf(m, z[u][i]);
+        m = group_max<LPT>(m);
+        mr[u].x = m == kNegInf ? 0.0f : m;
+        s[u] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            z[u][i] = exp_from(z[u][i], mr[u].x);
+            s[u] += z[u][i];
+        }
+    }
+#pragma unroll
+    for (int o = LPT / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int u = 0; u < U; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        mr[u].y = s[u] > 0.0f ? __fdividef(1.0f, s[u]) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[u][i] *= mr[u].y;
+    }
+}
+
+// Rows that a group of lanes takes at a time, the next ones being loaded
+// meanwhile: two of up to 8 values a lane.  One alone keeps 20 KB an SM in
+// flight, and HBM wants about 35.
+template <int N>
+constexpr int rows_at_once = N <= 8 ? 2 : 1;
 
 // ascending bounds inside [0, T]
 __device__ bool bounds_ok(const int32_t *seq, int S, int T) {
@@ -123,13 +152,17 @@ __global__ void __launch_bounds__(R_THREADS)
 balance_partial_kernel(const float *__restrict__ logits, const int32_t *__restrict__ topk_idx,
                        const uint8_t *__restrict__ mask, const int32_t *__restrict__ seq, int S,
                        int T, int E, int k, int per, float *__restrict__ psum,
-                       int32_t *__restrict__ pcnt, int32_t *__restrict__ pn, int32_t *dev_status) {
+                       int32_t *__restrict__ pcnt, int32_t *__restrict__ pn, unsigned int *done,
+                       int32_t *dev_status) {
     using R = Row<VEC, LPT, NC>;
     constexpr int G = R_THREADS / LPT;        // token groups of the CTA
+    constexpr int SPL = 32 / LPT;             // slots per lane
+    constexpr int U = rows_at_once<R::N>;
     extern __shared__ float s_dyn[];          // [R_WARPS][E] sums, then [E] counts
     float *s_sum = s_dyn;
     int *s_cnt = reinterpret_cast<int *>(s_dyn + R_WARPS * E);
     __shared__ int s_n;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *done = 0;
     if (seq && !bounds_ok(seq, S, T)) return;   // reported by the combining kernel
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int l = threadIdx.x % LPT, grp = threadIdx.x / LPT;
@@ -156,31 +189,62 @@ balance_partial_kernel(const float *__restrict__ logits, const int32_t *__restri
 #pragma unroll
         for (int i = 0; i < R::N; ++i) acc[i] = 0.0f;
         int n = 0;
-        for (int t0 = a; t0 < b; t0 += G) {
-            const int t = t0 + grp;
-            const bool on = t < b && (!mask || mask[t] != 0);
-            float z[R::N];
+        // the next tokens' rows and slots are loaded while these are summed
+        float zn[U][R::N];
+        int en[U][SPL];
+        bool next_on[U];
+        auto fetch = [&](int t0) {
 #pragma unroll
-            for (int i = 0; i < R::N; ++i) z[i] = kNegInf;
-            if (on) R::load(logits + static_cast<int64_t>(t) * E, E, l, kNegInf, z);
-            softmax_row<LPT>(z);
+            for (int v = 0; v < U; ++v) {
+                const int t = t0 + v * G + grp;
+                next_on[v] = t < b && (!mask || mask[t] != 0);
 #pragma unroll
-            for (int i = 0; i < R::N; ++i) acc[i] += z[i];
-            if (on) {
+                for (int i = 0; i < R::N; ++i) zn[v][i] = kNegInf;
+#pragma unroll
+                for (int u = 0; u < SPL; ++u) en[v][u] = 0;
+                if (!next_on[v]) continue;
+                R::load(logits + static_cast<int64_t>(t) * E, E, l, kNegInf, zn[v]);
+#pragma unroll
+                for (int u = 0; u < SPL; ++u)
+                    if (u * LPT + l < k) en[v][u] = topk_idx[static_cast<int64_t>(t) * k + u * LPT + l];
+            }
+        };
+        fetch(a);
+        for (int t0 = a; t0 < b; t0 += U * G) {
+            float z[U][R::N];
+            int e[U][SPL];
+            bool on[U];
+#pragma unroll
+            for (int v = 0; v < U; ++v) {
+                on[v] = next_on[v];
+#pragma unroll
+                for (int i = 0; i < R::N; ++i) z[v][i] = zn[v][i];
+#pragma unroll
+                for (int u = 0; u < SPL; ++u) e[v][u] = en[v][u];
+            }
+            fetch(t0 + U * G);
+            float2 mr[U];
+            softmax_rows<LPT, U>(z, mr);
+#pragma unroll
+            for (int v = 0; v < U; ++v) {
+#pragma unroll
+                for (int i = 0; i < R::N; ++i) acc[i] += z[v][i];
+                if (!on[v]) continue;
                 n += l == 0;
-                for (int j = l; j < k; j += LPT) {
-                    const int e = topk_idx[static_cast<int64_t>(t) * k + j];
-                    if (e >= 0 && e < E)
-                        atomicAdd(&s_cnt[e], 1);
+#pragma unroll
+                for (int u = 0; u < SPL; ++u) {
+                    if (u * LPT + l >= k) continue;
+                    if (e[v][u] >= 0 && e[v][u] < E)
+                        atomicAdd(&s_cnt[e[v][u]], 1);
                     else
                         report(dev_status, MOE_DEV_BAD_EXPERT_ID);
                 }
             }
         }
-        if (LPT == 16) {
 #pragma unroll
-            for (int i = 0; i < R::N; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], 16);
-        }
+        for (int o = LPT; o < 32; o <<= 1)
+#pragma unroll
+            for (int i = 0; i < R::N; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
         if (lane < LPT) {
 #pragma unroll
             for (int i = 0; i < R::N; ++i) {
@@ -202,98 +266,104 @@ balance_partial_kernel(const float *__restrict__ logits, const int32_t *__restri
     }
 }
 
-// One cluster of C_CTAS joins the partials: CTA r takes the columns
-// [r E / C, (r + 1) E / C) of every sequence, in chunk order, and its share of
-// the loss; the shares meet in CTA 0.
-constexpr int C_CTAS = 8;
+// Joins the partials: a CTA takes C_COLS columns of one sequence, its 32 warps
+// the chunks in turn, and leaves the columns' share of the loss; the CTA that
+// finishes last adds the shares in order.  `done` is zeroed by the partial
+// kernel's first CTA, which this kernel runs behind.
+constexpr int C_COLS = 32;
+constexpr int C_THREADS = 1024;
 
-__global__ void __cluster_dims__(C_CTAS, 1, 1) __launch_bounds__(R_THREADS)
+__global__ void __launch_bounds__(C_THREADS)
 balance_combine_kernel(const float *__restrict__ psum, const int32_t *__restrict__ pcnt,
                        const int32_t *__restrict__ pn, const int32_t *__restrict__ seq, int S,
                        int T, int E, int k, int per, float coef, float *__restrict__ loss,
                        int32_t *__restrict__ counts, float *__restrict__ prob_mean,
-                       int32_t *__restrict__ n_tokens, int32_t *dev_status) {
-    __shared__ float s_share[C_CTAS];
-    __shared__ float s_red[R_WARPS];
-    __shared__ float s_p[R_THREADS];
-    __shared__ int s_c[R_THREADS];
-    __shared__ int s_nred[R_WARPS];
-    const uint32_t rank = cluster_ctarank();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const bool ok = !seq || bounds_ok(seq, S, T);
-    if (!ok && rank == 0 && tid == 0) report(dev_status, MOE_DEV_BAD_OFFSETS);
-    const int e0 = static_cast<int>(static_cast<int64_t>(rank) * E / C_CTAS);
-    const int e1 = static_cast<int>(static_cast<int64_t>(rank + 1) * E / C_CTAS);
-    const int cols = e1 - e0;
-    int width = 1;                             // columns side by side: a power of two
-    while (width < cols && width < 32) width <<= 1;
-    const int par = R_THREADS / width;         // chunks side by side
-    float share = 0.0f;
-    int live = 0;
-    for (int s = 0; ok && s < S; ++s) {
-        const int a = seq ? seq[s] : 0, b = seq ? seq[s + 1] : T;
-        const int f = a / per, last = b > a ? (b - 1) / per : f - 1;
-        int n = 0;
-        for (int c = f + tid; c <= last; c += R_THREADS) n += pn[c + s];
-        n = __reduce_add_sync(0xffffffffu, n);
-        __syncthreads();
-        if (lane == 0) s_nred[warp] = n;
-        __syncthreads();
-        n = 0;
-#pragma unroll
-        for (int w = 0; w < R_WARPS; ++w) n += s_nred[w];
-        if (rank == 0 && tid == 0) n_tokens[s] = n;
-        live += n > 0;
-        const float rn = n > 0 ? 1.0f / static_cast<float>(n) : 0.0f;
-        const int used = min(par, last - f + 1);
-        float dot = 0.0f;
-        for (int eb = e0; eb < e1; eb += width) {
-            const int e = eb + tid % width;
-            float v = 0.0f;
-            int cn = 0;
-            if (e < e1) {
-                for (int c = f + tid / width; c <= last; c += par) {
-                    const int64_t at = (static_cast<int64_t>(c) + s) * E + e;
-                    v += psum[at];
-                    cn += pcnt[at];
-                }
-            }
-            __syncthreads();
-            s_p[tid] = v;
-            s_c[tid] = cn;
-            __syncthreads();
-            if (tid < width && e < e1) {
-                v = 0.0f;
-                cn = 0;
-                for (int c = 0; c < used; ++c) {
-                    v += s_p[c * width + tid];
-                    cn += s_c[c * width + tid];
-                }
-                const float pm = v * rn;
-                prob_mean[static_cast<int64_t>(s) * E + e] = pm;
-                counts[static_cast<int64_t>(s) * E + e] = cn;
-                dot += static_cast<float>(cn) * pm;
-            }
+                       int32_t *__restrict__ n_tokens, float *shares, unsigned int *done,
+                       int32_t *dev_status) {
+    __shared__ float s_p[32][C_COLS + 1];
+    __shared__ int s_c[32][C_COLS + 1];
+    __shared__ int s_n[32];
+    __shared__ bool s_last;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (seq && !bounds_ok(seq, S, T)) {
+        if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
+            report(dev_status, MOE_DEV_BAD_OFFSETS);
+        return;
+    }
+    const int s = blockIdx.x, e = blockIdx.y * C_COLS + lane;
+    const int a = seq ? seq[s] : 0, b = seq ? seq[s + 1] : T;
+    const int first = a / per, last = b > a ? (b - 1) / per : first - 1;
+    float v = 0.0f;
+    int cn = 0, n = 0;
+    if (e < E) {
+#pragma unroll 4
+        for (int c = first + warp; c <= last; c += 32) {
+            const int64_t at = (static_cast<int64_t>(c) + s) * E + e;
+            v += psum[at];
+            cn += pcnt[at];
         }
-        share += dot * rn;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) share += __shfl_xor_sync(0xffffffffu, share, o);
-    if (lane == 0) s_red[warp] = share;
+    for (int c = first + static_cast<int>(threadIdx.x); c <= last; c += C_THREADS) n += pn[c + s];
+    n = __reduce_add_sync(0xffffffffu, n);
+    s_p[warp][lane] = v;
+    s_c[warp][lane] = cn;
+    if (lane == 0) s_n[warp] = n;
     __syncthreads();
-    cluster_sync_all();                        // every CTA of the cluster has started
-    if (tid == 0) {
-        float v = 0.0f;
+    n = __reduce_add_sync(0xffffffffu, s_n[lane]);
+    const float rn = n > 0 ? 1.0f / static_cast<float>(n) : 0.0f;
+    // warp w adds column w's 32 parts (its lanes in a tree)
+    v = s_p[lane][warp];
+    cn = __reduce_add_sync(0xffffffffu, s_c[lane][warp]);
 #pragma unroll
-        for (int w = 0; w < R_WARPS; ++w) v += s_red[w];
-        st_shared_cluster_u32(mapa_shared(smem_u32(&s_share[rank]), 0), __float_as_uint(v));
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const int col = blockIdx.y * C_COLS + warp;
+    const float pm = v * rn;
+    __syncthreads();
+    if (lane == 0) {
+        s_p[0][warp] = col < E ? static_cast<float>(cn) * pm : 0.0f;
+        if (col < E) {
+            prob_mean[static_cast<int64_t>(s) * E + col] = pm;
+            counts[static_cast<int64_t>(s) * E + col] = cn;
+        }
     }
-    cluster_sync_all();
-    if (rank == 0 && tid == 0 && ok) {
-        float v = 0.0f;
+    __syncthreads();
+    if (warp == 0) {
+        float share = s_p[0][lane];
 #pragma unroll
-        for (int r = 0; r < C_CTAS; ++r) v += s_share[r];
-        *loss = live > 0 ? coef * static_cast<float>(E) / (static_cast<float>(k) * live) * v : 0.0f;
+        for (int o = 16; o > 0; o >>= 1) share += __shfl_xor_sync(0xffffffffu, share, o);
+        if (lane == 0) {
+            shares[static_cast<int64_t>(s) * gridDim.y + blockIdx.y] = share * rn;
+            if (blockIdx.y == 0) n_tokens[s] = n;
+            __threadfence();
+            s_last = atomicAdd(done, 1u) == gridDim.x * gridDim.y - 1;
+        }
+    }
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    // the last CTA: every thread its strided shares in order, then a tree
+    const int total = static_cast<int>(gridDim.x * gridDim.y);
+    float sum = 0.0f;
+    int live = 0;
+    for (int i = threadIdx.x; i < total; i += C_THREADS) sum += __ldcg(shares + i);
+    for (int i = threadIdx.x; i < S; i += C_THREADS) live += __ldcg(n_tokens + i) > 0;
+    live = __reduce_add_sync(0xffffffffu, live);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) {
+        s_p[1][warp] = sum;
+        s_n[warp] = live;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        sum = s_p[1][lane];
+        live = __reduce_add_sync(0xffffffffu, s_n[lane]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0)
+            *loss = live > 0
+                        ? coef * static_cast<float>(E) / (static_cast<float>(k) * live) * sum
+                        : 0.0f;
     }
 }
 
@@ -310,8 +380,13 @@ topk_backward_kernel(const float *__restrict__ logits, const int32_t *__restrict
     using R = Row<VEC, LPT, NC>;
     constexpr int G = R_THREADS / LPT;
     constexpr int SPL = 32 / LPT;              // slots per lane
+    constexpr int U = rows_at_once<R::N>;
     __shared__ int s_live;
     const int l = threadIdx.x % LPT, grp = threadIdx.x / LPT;
+    extern __shared__ float4 s_buf[];          // [G][columns]: a group's slot terms
+    float *buf = reinterpret_cast<float *>(s_buf) + grp * (LPT * R::N);
+    if (d_topk_w)
+        for (int i = l; i < LPT * R::N; i += LPT) buf[i] = 0.0f;
     float unit = 0.0f;                         // coef E d_loss / (S+ k)
     if (counts) {
         if (seq && !bounds_ok(seq, S, T)) {
@@ -328,7 +403,8 @@ topk_backward_kernel(const float *__restrict__ logits, const int32_t *__restrict
             unit = coef * static_cast<float>(E) / (static_cast<float>(k) * s_live) *
                    (d_loss ? *d_loss : 1.0f);
     }
-    const int c0 = blockIdx.x * per, c1 = min(T, c0 + per);
+    // last chunk first: the forward pass left the ends of the logits in L2
+    const int c0 = (gridDim.x - 1 - blockIdx.x) * per, c1 = min(T, c0 + per);
     int seq_end = -1;                          // the held sequence's end
     int s_cur = 0;
     bool inside = false;
@@ -336,115 +412,166 @@ topk_backward_kernel(const float *__restrict__ logits, const int32_t *__restrict
     float scale = 0.0f;
 #pragma unroll
     for (int i = 0; i < R::N; ++i) cnt[i] = 0.0f;
-    for (int t0 = c0; t0 < c1; t0 += G) {
-        const int t = t0 + grp;
-        const bool on = t < c1 && (!mask || mask[t] != 0);
-        if (counts && on && t >= seq_end) {
-            // the token's sequence, its counts and its factor
-            int s = s_cur;
-            if (seq) {
-                while (s < S && seq[s + 1] <= t) ++s;
-                inside = s < S && seq[s] <= t;
-                seq_end = s < S ? (inside ? seq[s + 1] : seq[s]) : 0x7fffffff;
-            } else {
-                inside = true;
-                seq_end = 0x7fffffff;
-            }
-            s_cur = s;
-            scale = 0.0f;
-            if (inside) {
-                const float n = static_cast<float>(max(n_tokens[s], 1));
-                scale = unit / (n * n);
+    // the next tokens' rows, slots and weights' gradients are loaded meanwhile
+    float zn[U][R::N], dn[U][SPL];
+    int en[U][SPL];
+    bool next_on[U];
+    auto fetch = [&](int t0) {
 #pragma unroll
-                for (int i = 0; i < R::N; ++i) {
-                    const int e = R::col(l, i);
-                    cnt[i] = e < E ? static_cast<float>(counts[static_cast<int64_t>(s) * E + e])
-                                   : 0.0f;
+        for (int v = 0; v < U; ++v) {
+            const int t = t0 + v * G + grp;
+            next_on[v] = t < c1 && (!mask || mask[t] != 0);
+#pragma unroll
+            for (int i = 0; i < R::N; ++i) zn[v][i] = kNegInf;
+#pragma unroll
+            for (int u = 0; u < SPL; ++u) {
+                en[v][u] = -1;
+                dn[v][u] = 0.0f;
+            }
+            if (!next_on[v]) continue;
+            R::load(logits + static_cast<int64_t>(t) * E, E, l, kNegInf, zn[v]);
+            if (!d_topk_w) continue;
+#pragma unroll
+            for (int u = 0; u < SPL; ++u)
+                if (u * LPT + l < k) {
+                    en[v][u] = topk_idx[static_cast<int64_t>(t) * k + u * LPT + l];
+                    dn[v][u] = d_topk_w[static_cast<int64_t>(t) * k + u * LPT + l];
+                }
+        }
+    };
+    fetch(c0);
+    for (int t0 = c0; t0 < c1; t0 += U * G) {
+        float p[U][R::N], g[U][SPL], z[U][SPL];
+        int idx[U][SPL];
+        bool on[U];
+#pragma unroll
+        for (int v = 0; v < U; ++v) {
+            const int t = t0 + v * G + grp;
+            on[v] = next_on[v];
+#pragma unroll
+            for (int i = 0; i < R::N; ++i) p[v][i] = zn[v][i];
+#pragma unroll
+            for (int u = 0; u < SPL; ++u) {
+                idx[v][u] = en[v][u];
+                g[v][u] = dn[v][u];
+                z[v][u] = kNegInf;
+                if (!d_topk_w || !on[v] || u * LPT + l >= k) continue;
+                if (idx[v][u] >= 0 && idx[v][u] < E) {
+                    z[v][u] = __ldg(logits + static_cast<int64_t>(t) * E + idx[v][u]);
+                } else {
+                    report(dev_status, MOE_DEV_BAD_EXPERT_ID);
+                    idx[v][u] = -1;
+                    g[v][u] = 0.0f;
                 }
             }
         }
-        const float *row = logits + static_cast<int64_t>(t) * E;
-        float p[R::N];
+        fetch(t0 + U * G);
+        float2 mr[U];
+        softmax_rows<LPT, U>(p, mr);
 #pragma unroll
-        for (int i = 0; i < R::N; ++i) p[i] = kNegInf;
-        if (on) R::load(row, E, l, kNegInf, p);
-        const float2 mr = softmax_row<LPT>(p);
-        float dot = 0.0f;
+        for (int v = 0; v < U; ++v) {
+            const int t = t0 + v * G + grp;
+            if (counts && on[v] && t >= seq_end) {
+                // the token's sequence, its counts and its factor
+                int s = s_cur;
+                if (seq) {
+                    while (s < S && seq[s + 1] <= t) ++s;
+                    inside = s < S && seq[s] <= t;
+                    seq_end = s < S ? (inside ? seq[s + 1] : seq[s]) : 0x7fffffff;
+                } else {
+                    inside = true;
+                    seq_end = 0x7fffffff;
+                }
+                s_cur = s;
+                scale = 0.0f;
+                if (inside) {
+                    const float n = static_cast<float>(max(n_tokens[s], 1));
+                    scale = unit / (n * n);
 #pragma unroll
-        for (int i = 0; i < R::N; ++i) dot += p[i] * cnt[i];
-        dot = group_sum<LPT>(dot);
-        float sub = 0.0f;                      // sum_l p_l dw_l without renormalisation
-        int idx[SPL];
-        float g[SPL];
-        if (d_topk_w) {
-            float z[SPL], m = kNegInf;
-#pragma unroll
-            for (int u = 0; u < SPL; ++u) {
-                const int j = u * LPT + l;
-                idx[u] = -1;
-                g[u] = 0.0f;
-                z[u] = kNegInf;
-                if (on && j < k) {
-                    const int e = topk_idx[static_cast<int64_t>(t) * k + j];
-                    if (e >= 0 && e < E) {
-                        idx[u] = e;
-                        g[u] = d_topk_w[static_cast<int64_t>(t) * k + j];
-                        z[u] = __ldg(row + e);
-                    } else {
-                        report(dev_status, MOE_DEV_BAD_EXPERT_ID);
+                    for (int i = 0; i < R::N; ++i) {
+                        const int e = R::col(l, i);
+                        cnt[i] = e < E ? static_cast<float>(counts[static_cast<int64_t>(s) * E + e])
+                                       : 0.0f;
                     }
                 }
-                m = fmaxf(m, z[u]);
             }
-            float w[SPL], ws = 0.0f, wd = 0.0f;
-            if (renorm) {
-                m = group_max<LPT>(m);
-                if (m == kNegInf) m = 0.0f;
-            } else {
-                m = mr.x;
-            }
+            float dot = 0.0f;
 #pragma unroll
-            for (int u = 0; u < SPL; ++u) {
-                w[u] = expf(z[u] - m);
-                if (!renorm) w[u] *= mr.y;
-                ws += w[u];
-                wd += w[u] * g[u];
-            }
-            wd = group_sum<LPT>(wd);
-            if (renorm) {
-                ws = group_sum<LPT>(ws);
-                const float r = ws > 0.0f ? 1.0f / ws : 0.0f;
-                wd *= r;
+            for (int i = 0; i < R::N; ++i) dot += p[v][i] * cnt[i];
+            dot = group_sum<LPT>(dot);
+            float sub = 0.0f;                  // sum_l p_l dw_l without renormalisation
+            if (d_topk_w) {
+                float w[SPL], ws = 0.0f, wd = 0.0f, m = mr[v].x;
+                if (renorm) {
+                    m = kNegInf;
 #pragma unroll
-                for (int u = 0; u < SPL; ++u) g[u] = w[u] * r * (g[u] - wd);
-            } else {
-                sub = wd;
+                    for (int u = 0; u < SPL; ++u) m = fmaxf(m, z[v][u]);
+                    m = group_max<LPT>(m);
+                    if (m == kNegInf) m = 0.0f;
+                }
 #pragma unroll
-                for (int u = 0; u < SPL; ++u) g[u] *= w[u];
-            }
-        }
+                for (int u = 0; u < SPL; ++u) {
+                    w[u] = exp_from(z[v][u], m);
+                    if (!renorm) w[u] *= mr[v].y;
+                    ws += w[u];
+                    wd += w[u] * g[v][u];
+                }
+                wd = group_sum<LPT>(wd);
+                if (renorm) {
+                    ws = group_sum<LPT>(ws);
+                    const float r = ws > 0.0f ? __fdividef(1.0f, ws) : 0.0f;
+                    wd *= r;
 #pragma unroll
-        for (int i = 0; i < R::N; ++i) p[i] *= scale * (cnt[i] - dot) - sub;
-        if (d_topk_w) {
-            // hand every slot's term to the lane that holds its column, in slot order
+                    for (int u = 0; u < SPL; ++u) g[v][u] = w[u] * r * (g[v][u] - wd);
+                } else {
+                    sub = wd;
 #pragma unroll
-            for (int u = 0; u < SPL; ++u) {
-                const int slots = min(LPT, k - u * LPT);
-                for (int j = 0; j < slots; ++j) {
-                    const int e = __shfl_sync(0xffffffffu, idx[u], j, LPT);
-                    const float v = __shfl_sync(0xffffffffu, g[u], j, LPT);
-#pragma unroll
-                    for (int i = 0; i < R::N; ++i)
-                        if (R::col(l, i) == e) p[i] += v;
+                    for (int u = 0; u < SPL; ++u) g[v][u] *= w[u];
                 }
             }
-        }
-        if (t < c1) {
-            if (!on) {
 #pragma unroll
-                for (int i = 0; i < R::N; ++i) p[i] = 0.0f;
+            for (int i = 0; i < R::N; ++i) p[v][i] *= scale * (cnt[i] - dot) - sub;
+            if (d_topk_w) {
+                // Each slot's term goes to the lane of its column through the
+                // group's row of shared memory (zeros between tokens).  A slot
+                // whose mark another one has overwritten names the same expert.
+                __syncwarp();
+#pragma unroll
+                for (int u = 0; u < SPL; ++u)
+                    if (idx[v][u] >= 0) buf[idx[v][u]] = __int_as_float(1 + u * LPT + l);
+                __syncwarp();
+                bool twice = false;
+#pragma unroll
+                for (int u = 0; u < SPL; ++u)
+                    if (idx[v][u] >= 0) twice |= __float_as_int(buf[idx[v][u]]) != 1 + u * LPT + l;
+                twice = __any_sync(0xffffffffu, twice);
+                __syncwarp();
+#pragma unroll
+                for (int u = 0; u < SPL; ++u)
+                    if (idx[v][u] >= 0) buf[idx[v][u]] = twice ? 0.0f : g[v][u];
+                if (twice) {                   // in slot order
+                    for (int j = 0; j < k; ++j) {
+                        __syncwarp();
+#pragma unroll
+                        for (int u = 0; u < SPL; ++u)
+                            if (j == u * LPT + l && idx[v][u] >= 0) buf[idx[v][u]] += g[v][u];
+                    }
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < R::N; ++i) p[v][i] += buf[R::col(l, i)];
+                __syncwarp();
+#pragma unroll
+                for (int u = 0; u < SPL; ++u)
+                    if (idx[v][u] >= 0) buf[idx[v][u]] = 0.0f;
             }
-            R::store(d_logits + static_cast<int64_t>(t) * E, E, l, p);
+            if (t < c1) {
+                if (!on[v]) {
+#pragma unroll
+                    for (int i = 0; i < R::N; ++i) p[v][i] = 0.0f;
+                }
+                R::store(d_logits + static_cast<int64_t>(t) * E, E, l, p[v]);
+            }
         }
     }
 }
@@ -587,9 +714,12 @@ template <typename F>
 void with_row_shape(int E, bool vec, F f) {
 #define MOE_SHAPE(V, L, N) f(std::integral_constant<int, V>(), std::integral_constant<int, L>(), std::integral_constant<int, N>())
     if (vec) {
-        if (E <= 64) MOE_SHAPE(4, 16, 1);
-        else if (E <= 128) MOE_SHAPE(4, 32, 1);
-        else if (E <= 256) MOE_SHAPE(4, 32, 2);
+        if (E <= 32) MOE_SHAPE(4, 8, 1);
+        else if (E <= 64) MOE_SHAPE(4, 8, 2);
+        else if (E <= 128) MOE_SHAPE(4, 8, 4);
+        else if (E <= 192) MOE_SHAPE(4, 16, 3);
+        else if (E <= 256) MOE_SHAPE(4, 16, 4);
+        else if (E <= 384) MOE_SHAPE(4, 32, 3);
         else if (E <= 512) MOE_SHAPE(4, 32, 4);
         else MOE_SHAPE(4, 32, 8);
     } else {
@@ -617,7 +747,9 @@ extern "C" moe_status_t moe_balance_loss_workspace_size(int32_t T, int32_t E, in
     if (!bytes || T < 0 || E <= 0 || S <= 0) return MOE_ERR_INVALID_ARG;
     if (E > 1024 || S > 65536) return MOE_ERR_UNSUPPORTED_SHAPE;
     const size_t P = static_cast<size_t>(chunks_of(T).count) + S;
-    *bytes = 2 * align256(P * E * 4) + align256(P * 4);
+    // the partials, the shares of the loss and their counter
+    *bytes = 2 * align256(P * E * 4) + align256(P * 4) +
+             align256(static_cast<size_t>(S) * ceil_div(E, C_COLS) * 4) + 256;
     return MOE_OK;
 }
 
@@ -646,18 +778,28 @@ extern "C" moe_status_t moe_balance_loss(const float *logits, const int32_t *top
     float *psum = reinterpret_cast<float *>(ws);
     int32_t *pcnt = reinterpret_cast<int32_t *>(ws + align256(P * E * 4));
     int32_t *pn = reinterpret_cast<int32_t *>(ws + 2 * align256(P * E * 4));
-    if (T > 0) {
-        const size_t smem = static_cast<size_t>(R_WARPS + 1) * E * 4;   // at most 36 KB
-        with_row_shape(E, whole_vectors(E, logits, nullptr), [&](auto v, auto l, auto n) {
-            balance_partial_kernel<v.value, l.value, n.value><<<ch.count, R_THREADS, smem, s>>>(
-                logits, topk_idx, token_mask, seq_offsets, S, T, E, k, ch.per, psum, pcnt, pn,
-                dev_status);
-        });
-        if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+    float *shares = reinterpret_cast<float *>(ws + 2 * align256(P * E * 4) + align256(P * 4));
+    unsigned int *done = reinterpret_cast<unsigned int *>(ws + need - 256);
+    if (T == 0) {
+        const size_t SE = static_cast<size_t>(S) * E * 4;
+        if (cudaMemsetAsync(loss, 0, 4, s) != cudaSuccess ||
+            cudaMemsetAsync(counts, 0, SE, s) != cudaSuccess ||
+            cudaMemsetAsync(prob_mean, 0, SE, s) != cudaSuccess ||
+            cudaMemsetAsync(n_tokens, 0, static_cast<size_t>(S) * 4, s) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        return MOE_OK;
     }
-    balance_combine_kernel<<<C_CTAS, R_THREADS, 0, s>>>(psum, pcnt, pn, seq_offsets, S, T, E, k,
-                                                        ch.per, coef, loss, counts, prob_mean,
-                                                        n_tokens, dev_status);
+    const size_t smem = static_cast<size_t>(R_WARPS + 1) * E * 4;   // at most 36 KB
+    with_row_shape(E, whole_vectors(E, logits, nullptr), [&](auto v, auto l, auto n) {
+        balance_partial_kernel<v.value, l.value, n.value><<<ch.count, R_THREADS, smem, s>>>(
+            logits, topk_idx, token_mask, seq_offsets, S, T, E, k, ch.per, psum, pcnt, pn, done,
+            dev_status);
+    });
+    if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+    const dim3 grid(static_cast<unsigned>(S), static_cast<unsigned>(ceil_div(E, C_COLS)));
+    balance_combine_kernel<<<grid, C_THREADS, 0, s>>>(psum, pcnt, pn, seq_offsets, S, T, E, k,
+                                                      ch.per, coef, loss, counts, prob_mean,
+                                                      n_tokens, shares, done, dev_status);
     return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -677,7 +819,9 @@ extern "C" moe_status_t moe_gate_topk_backward(
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const Chunks ch = chunks_of(T);
     with_row_shape(E, whole_vectors(E, logits, d_logits), [&](auto v, auto l, auto n) {
-        topk_backward_kernel<v.value, l.value, n.value><<<ch.count, R_THREADS, 0, s>>>(
+        // a row of columns per group: at most 32 KB
+        const size_t smem = static_cast<size_t>(R_THREADS) * v.value * n.value * 4;
+        topk_backward_kernel<v.value, l.value, n.value><<<ch.count, R_THREADS, smem, s>>>(
             logits, topk_idx, d_topk_w, token_mask, seq_offsets, S, counts, n_tokens, d_loss, coef,
             T, E, k, (flags & MOE_RENORM) != 0, ch.per, d_logits, dev_status);
     });
