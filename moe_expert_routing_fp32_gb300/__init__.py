@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 import threading
 from typing import Optional
@@ -152,17 +153,44 @@ def _ptr(t: Optional[torch.Tensor]):
         raise ValueError("libmoe takes CUDA tensors only")
     if not t.is_contiguous():
         raise ValueError("libmoe takes contiguous tensors only")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
-def _stream(device) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+# the handle of a device's current stream without the Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(device) -> int:
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _call(name: str, *args):
-    st = getattr(lib(), name)(*args)
+    st = getattr(_lib or lib(), name)(*args)
     if st != MOE_OK:
         raise MoeError(name, st)
+
+
+class _Here:
+    """Nothing to switch: the tensors' device is the current one."""
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+_here = _Here()
+
+
+def _on(dev):
+    """The context in which a call for tensors on ``dev`` is made (entering
+    torch.cuda.device costs more than the call where nothing changes)."""
+    if dev.type == "cuda" and dev.index == torch.cuda.current_device():
+        return _here
+    return torch.cuda.device(dev)
 
 
 def _check(t, dtype, name):
@@ -373,6 +401,13 @@ def _router_args(logits, topk_idx, token_mask, seq_offsets):
     return T, E, 1 if seq_offsets is None else seq_offsets.numel() - 1
 
 
+@functools.lru_cache(maxsize=256)
+def _balance_workspace(T, E, S, device_index) -> int:
+    n = ctypes.c_size_t(0)
+    _call("moe_balance_loss_workspace_size", T, E, S, ctypes.byref(n))
+    return n.value
+
+
 def balance_loss(logits, topk_idx, coef=1.0, token_mask=None, seq_offsets=None, status=None):
     """Balance loss of the router over the sequences given by ``seq_offsets``
     (int32 [S+1]; None: all tokens are one), without the tokens whose
@@ -382,17 +417,16 @@ def balance_loss(logits, topk_idx, coef=1.0, token_mask=None, seq_offsets=None, 
     T, E, S = _router_args(logits, topk_idx, token_mask, seq_offsets)
     k = topk_idx.shape[1]
     dev = logits.device
-    n = ctypes.c_size_t(0)
-    _call("moe_balance_loss_workspace_size", T, E, S, ctypes.byref(n))
-    with torch.cuda.device(dev):
+    with _on(dev):
+        nbytes = _balance_workspace(T, E, S, dev.index)
         loss = torch.empty((), dtype=torch.float32, device=dev)
         counts = torch.empty((S, E), dtype=torch.int32, device=dev)
         prob = torch.empty((S, E), dtype=torch.float32, device=dev)
         n_tokens = torch.empty(S, dtype=torch.int32, device=dev)
-        ws = torch.empty(n.value, dtype=torch.uint8, device=dev)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         _call("moe_balance_loss", _ptr(logits), _ptr(topk_idx), _ptr(token_mask),
-              _ptr(seq_offsets), S, T, E, k, float(coef), _ptr(loss), _ptr(counts), _ptr(prob),
-              _ptr(n_tokens), _ptr(ws), n.value, _ptr(status), _stream(dev))
+              _ptr(seq_offsets), S, T, E, k, float(coef), loss.data_ptr(), counts.data_ptr(),
+              prob.data_ptr(), n_tokens.data_ptr(), ws.data_ptr(), nbytes, _ptr(status), _stream(dev))
     return dict(loss=loss, counts=counts, prob_mean=prob, n_tokens=n_tokens, coef=float(coef))
 
 
@@ -419,11 +453,11 @@ def gate_topk_backward(logits, topk_idx, d_topk_w=None, renorm=True, balance=Non
         if d_loss is not None and d_loss.numel() != 1:
             raise ValueError("d_loss must hold one value")
     _same_device(dev, d_topk_w=d_topk_w, d_loss=d_loss, counts=counts, n_tokens=n_tokens)
-    with torch.cuda.device(dev):
+    with _on(dev):
         d = torch.empty_like(logits)
         _call("moe_gate_topk_backward", _ptr(logits), _ptr(topk_idx), _ptr(d_topk_w),
               _ptr(token_mask), _ptr(seq_offsets), S, _ptr(counts), _ptr(n_tokens), _ptr(d_loss),
-              coef, T, E, k, RENORM if renorm else 0, _ptr(d), _ptr(status), _stream(dev))
+              coef, T, E, k, RENORM if renorm else 0, d.data_ptr(), _ptr(status), _stream(dev))
     return d
 
 
@@ -446,11 +480,12 @@ def finalize_routing_backward(d_out, y_exp, row_idx, topk_w, status=None):
     _same_device(dev, d_out=d_out, row_idx=row_idx, topk_w=topk_w)
     flags = (OUT_F32 if d_out.dtype == torch.float32 else 0) | \
         (Y_F32 if y_exp.dtype == torch.float32 else 0)
-    with torch.cuda.device(dev):
+    with _on(dev):
         d_y = torch.empty_like(y_exp)
         d_w = torch.empty_like(topk_w)
         _call("moe_finalize_routing_backward", _ptr(d_out), _ptr(y_exp), _ptr(row_idx),
-              _ptr(topk_w), T, H, k, flags, _ptr(d_y), _ptr(d_w), _ptr(status), _stream(dev))
+              _ptr(topk_w), T, H, k, flags, d_y.data_ptr(), d_w.data_ptr(), _ptr(status),
+              _stream(dev))
     return d_y, d_w
 
 
@@ -470,6 +505,7 @@ class Fp4Matrix:
         return self.q.shape[-1] * 2
 
 
+@functools.lru_cache(maxsize=256)
 def fp4_scales_size(rows, K, fmt="mx", groups=0) -> int:
     """Bytes of the scale tiles of ``rows`` rows (in ``groups`` groups; 0 for
     an ungrouped matrix such as a weight)."""
@@ -519,7 +555,7 @@ def fp4_quantize(x, fmt="mx", scale_exp=0, row_idx=None, k=1, offsets=None,
         raise ValueError("k needs row_idx")
     _same_device(dev, row_idx=row_idx, offsets=offsets)
     G = 0 if offsets is None else offsets.numel() - 1
-    with torch.cuda.device(dev):
+    with _on(dev):
         m = _fp4_empty(T * k, K, fmt, scale_exp, G, dev)
         _call("moe_fp4_quantize", _ptr(x), T, K, _ptr(row_idx), k, _ptr(offsets), G,
               _fp4_arg(m, "out", G, dev), _ptr(status), _stream(dev))
@@ -536,7 +572,7 @@ def fp4_dequantize(m: Fp4Matrix, offsets=None):
     _same_device(dev, offsets=offsets)
     G = 0 if offsets is None else offsets.numel() - 1
     n = m.q.numel() // max(m.q.shape[-1], 1)
-    with torch.cuda.device(dev):
+    with _on(dev):
         x = torch.empty((*m.q.shape[:-1], m.K), dtype=torch.bfloat16, device=dev)
         _call("moe_fp4_dequantize", _fp4_arg(m, "m", G, dev), n, m.K, _ptr(offsets), G, _ptr(x),
               _stream(dev))
@@ -561,7 +597,7 @@ def fp4_grouped_matmul(a: Fp4Matrix, offsets, w: Fp4Matrix, out_f32=False, out=N
     n, K, G, N = _fp4_product(a, offsets, w, "fp4_grouped_matmul")
     dev = a.q.device
     dt = torch.float32 if out_f32 else torch.bfloat16
-    with torch.cuda.device(dev):
+    with _on(dev):
         if out is None:
             out = torch.empty((n, N), dtype=dt, device=dev)
         _check(out, dt, "out")
@@ -580,7 +616,7 @@ def fp4_grouped_swiglu(a: Fp4Matrix, offsets, w13: Fp4Matrix, quantize=False, sc
     n, K, G, rows = _fp4_product(a, offsets, w13, "fp4_grouped_swiglu")
     I = rows // 2
     dev = a.q.device
-    with torch.cuda.device(dev):
+    with _on(dev):
         if quantize:
             if out is None:
                 out = _fp4_empty(n, I, a.fmt, scale_exp, G, dev)
@@ -605,7 +641,7 @@ def fp4_grouped_mlp(expanded_x: Fp4Matrix, offsets, w13: Fp4Matrix, w2: Fp4Matri
     if tuple(w2.q.shape) != (G, H, I // 2):
         raise ValueError("w2 must be [G, H, I/2]")
     dev = expanded_x.q.device
-    with torch.cuda.device(dev):
+    with _on(dev):
         act = _fp4_empty(n, I, expanded_x.fmt, act_exp, G, dev)
         y = torch.empty((n, H), dtype=torch.float32 if y_f32 else torch.bfloat16, device=dev)
         _call("moe_fp4_grouped_mlp", _fp4_arg(expanded_x, "expanded_x", G, dev), _ptr(offsets), G,
