@@ -29,8 +29,6 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include <stdlib.h>
-
 #include <algorithm>
 #include <mutex>
 
@@ -726,13 +724,15 @@ bool out_map(CUtensorMap *m, void *out, int64_t rows, int64_t cols, bool f32) {
               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// CTA pairs take the products with many rows per group.
+// CTA pairs take the products with more than one 128-row block per group on
+// average.  Measured with 64 groups (us, pair against one CTA):
+//   rows/group    128         160         192         256         512         1024
+//   K=4096 SwiGLU 109 : 106   110 : 122   111 : 124   139 : 144   206 : 231   365 : 426
+//   K=2048 matmul  68 : 68     70 : 85     71 : 85     85 : 96    128 : 160   223 : 303
+// and below, where the weights' bytes decide, one CTA (32 rows: 103 : 92, 58 : 52).
 bool use_pair(int n, int G) {
-    static const int64_t least = [] {
-        const char *v = getenv("MOE_FP4_PAIR_ROWS");
-        return v ? atoll(v) : 256ll;
-    }();
-    return n / G >= least && G <= std::min(Cfg<MOE_FP4_MX, 2>::MAX_G, Cfg<MOE_FP4_NV, 2>::MAX_G);
+    return n > static_cast<int64_t>(BM) * G &&
+           G <= std::min(Cfg<MOE_FP4_MX, 2>::MAX_G, Cfg<MOE_FP4_NV, 2>::MAX_G);
 }
 
 template <int FMT, int MODE>

@@ -75,10 +75,10 @@ template <int LPT>
 __device__ __forceinline__ float group_max(float v) {
     if constexpr (LPT == 32) {
         asm volatile("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(v));
-        return v;
-    }
+    } else {
 #pragma unroll
-    for (int o = LPT / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+        for (int o = LPT / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    }
     return v;
 }
 template <int LPT>
