@@ -374,31 +374,44 @@ def finalize_routing(y_exp, row_idx, topk_w, shared=None, out_f32=False):
 
 
 # ------------------------------------------------------- training the router
-def _same_device(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
-
-
-def _shape(t, shape, name):
-    if t is not None and tuple(t.shape) != tuple(shape):
+def _arg(t, dtype, dev, shape, name):
+    """The address of an optional tensor, checked in one place: its type, its
+    device (the call's), its shape (None: any) and that it is contiguous."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"libmoe takes contiguous tensors only ({name})")
+    return t.data_ptr()
+
+
+def _status_arg(status, dev):
+    return _arg(status, torch.int32, dev, None, "status")
 
 
 def _router_args(logits, topk_idx, token_mask, seq_offsets):
-    _check(logits, torch.float32, "logits")
-    _check(topk_idx, torch.int32, "topk_idx")
-    _check(seq_offsets, torch.int32, "seq_offsets")
-    if token_mask is not None and token_mask.dtype != torch.bool:
-        _check(token_mask, torch.uint8, "token_mask")
+    """(T, E, k, S, device, the four addresses) of the router's operators."""
     T, E = logits.shape
-    _shape(token_mask, (T,), "token_mask")
-    if topk_idx is not None:
-        _shape(topk_idx, (T, topk_idx.shape[-1]), "topk_idx")
-    if seq_offsets is not None and (seq_offsets.dim() != 1 or seq_offsets.numel() < 2):
-        raise ValueError("seq_offsets: [S + 1] with S >= 1")
-    _same_device(logits.device, topk_idx=topk_idx, token_mask=token_mask, seq_offsets=seq_offsets)
-    return T, E, 1 if seq_offsets is None else seq_offsets.numel() - 1
+    k = topk_idx.shape[-1]
+    dev = logits.device
+    lg = _arg(logits, torch.float32, dev, None, "logits")
+    idx = _arg(topk_idx, torch.int32, dev, (T, k), "topk_idx")
+    mask = seq = None
+    S = 1
+    if token_mask is not None:
+        mask = _arg(token_mask, torch.bool if token_mask.dtype == torch.bool else torch.uint8, dev,
+                    (T,), "token_mask")
+    if seq_offsets is not None:
+        S = seq_offsets.numel() - 1
+        if S < 1:
+            raise ValueError("seq_offsets: [S + 1] with S >= 1")
+        seq = _arg(seq_offsets, torch.int32, dev, (S + 1,), "seq_offsets")
+    return T, E, k, S, dev, (lg, idx, mask, seq)
 
 
 @functools.lru_cache(maxsize=256)
@@ -414,9 +427,9 @@ def balance_loss(logits, topk_idx, coef=1.0, token_mask=None, seq_offsets=None, 
     ``token_mask`` (bool or uint8 [T]) is zero.
     -> dict(loss fp32 [], counts int32 [S, E], prob_mean fp32 [S, E],
     n_tokens int32 [S], coef); gate_topk_backward takes the dict."""
-    T, E, S = _router_args(logits, topk_idx, token_mask, seq_offsets)
-    k = topk_idx.shape[1]
-    dev = logits.device
+    T, E, k, S, dev, (lg, idx, mask, seq) = _router_args(logits, topk_idx, token_mask, seq_offsets)
+    st = _status_arg(status, dev)
+    coef = float(coef)
     with _on(dev):
         nbytes = _balance_workspace(T, E, S, dev.index)
         loss = torch.empty((), dtype=torch.float32, device=dev)
@@ -424,10 +437,10 @@ def balance_loss(logits, topk_idx, coef=1.0, token_mask=None, seq_offsets=None, 
         prob = torch.empty((S, E), dtype=torch.float32, device=dev)
         n_tokens = torch.empty(S, dtype=torch.int32, device=dev)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        _call("moe_balance_loss", _ptr(logits), _ptr(topk_idx), _ptr(token_mask),
-              _ptr(seq_offsets), S, T, E, k, float(coef), loss.data_ptr(), counts.data_ptr(),
-              prob.data_ptr(), n_tokens.data_ptr(), ws.data_ptr(), nbytes, _ptr(status), _stream(dev))
-    return dict(loss=loss, counts=counts, prob_mean=prob, n_tokens=n_tokens, coef=float(coef))
+        _call("moe_balance_loss", lg, idx, mask, seq, S, T, E, k, coef, loss.data_ptr(),
+              counts.data_ptr(), prob.data_ptr(), n_tokens.data_ptr(), ws.data_ptr(), nbytes, st,
+              _stream(dev))
+    return dict(loss=loss, counts=counts, prob_mean=prob, n_tokens=n_tokens, coef=coef)
 
 
 def gate_topk_backward(logits, topk_idx, d_topk_w=None, renorm=True, balance=None, d_loss=None,
@@ -436,56 +449,53 @@ def gate_topk_backward(logits, topk_idx, d_topk_w=None, renorm=True, balance=Non
     gradient of gate_topk's weights, or None) and, with ``balance`` (what
     balance_loss returned for the same logits, mask and bounds), from the
     balance loss times ``d_loss`` (fp32 [1] or [], None: 1)."""
-    T, E, S = _router_args(logits, topk_idx, token_mask, seq_offsets)
-    dev = logits.device
-    _check(d_topk_w, torch.float32, "d_topk_w")
-    _check(d_loss, torch.float32, "d_loss")
-    k = topk_idx.shape[1]
-    _shape(d_topk_w, (T, k), "d_topk_w")
-    counts = n_tokens = None
+    T, E, k, S, dev, (lg, idx, mask, seq) = _router_args(logits, topk_idx, token_mask, seq_offsets)
+    dw = _arg(d_topk_w, torch.float32, dev, (T, k), "d_topk_w")
+    st = _status_arg(status, dev)
+    counts = n_tokens = dl = None
     coef = 0.0
     if balance is not None:
-        counts, n_tokens, coef = balance["counts"], balance["n_tokens"], balance["coef"]
-        _check(counts, torch.int32, "counts")
-        _check(n_tokens, torch.int32, "n_tokens")
-        _shape(counts, (S, E), "counts")
-        _shape(n_tokens, (S,), "n_tokens")
-        if d_loss is not None and d_loss.numel() != 1:
-            raise ValueError("d_loss must hold one value")
-    _same_device(dev, d_topk_w=d_topk_w, d_loss=d_loss, counts=counts, n_tokens=n_tokens)
+        coef = balance["coef"]
+        counts = _arg(balance["counts"], torch.int32, dev, (S, E), "counts")
+        n_tokens = _arg(balance["n_tokens"], torch.int32, dev, (S,), "n_tokens")
+        if d_loss is not None:
+            if d_loss.numel() != 1:
+                raise ValueError("d_loss must hold one value")
+            dl = _arg(d_loss, torch.float32, dev, None, "d_loss")
     with _on(dev):
         d = torch.empty_like(logits)
-        _call("moe_gate_topk_backward", _ptr(logits), _ptr(topk_idx), _ptr(d_topk_w),
-              _ptr(token_mask), _ptr(seq_offsets), S, _ptr(counts), _ptr(n_tokens), _ptr(d_loss),
-              coef, T, E, k, RENORM if renorm else 0, d.data_ptr(), _ptr(status), _stream(dev))
+        _call("moe_gate_topk_backward", lg, idx, dw, mask, seq, S, counts, n_tokens, dl, coef, T,
+              E, k, RENORM if renorm else 0, d.data_ptr(), st, _stream(dev))
     return d
+
+
+def _bf16_or_f32(t, name):
+    if t.dtype != torch.float32 and t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    return t.dtype
 
 
 def finalize_routing_backward(d_out, y_exp, row_idx, topk_w, status=None):
     """-> (d_y_exp like y_exp, d_topk_w fp32 [T, k]) from the gradient of
     finalize_routing's output (bf16 or fp32).  The shared rows' gradient is
     d_out itself.  Rows of d_y_exp that row_idx does not name are not set."""
-    for t, name in ((d_out, "d_out"), (y_exp, "y_exp")):
-        if t.dtype != torch.float32:
-            _check(t, torch.bfloat16, name)
-    _check(row_idx, torch.int32, "row_idx")
-    _check(topk_w, torch.float32, "topk_w")
     T, k = topk_w.shape
     H = y_exp.shape[1]
     dev = y_exp.device
-    _shape(d_out, (T, H), "d_out")
-    _shape(y_exp, (T * k, H), "y_exp")
+    dt, yt = _bf16_or_f32(d_out, "d_out"), _bf16_or_f32(y_exp, "y_exp")
+    do = _arg(d_out, dt, dev, (T, H), "d_out")
+    y = _arg(y_exp, yt, dev, (T * k, H), "y_exp")
+    rows = _arg(row_idx, torch.int32, dev, None, "row_idx")
+    w = _arg(topk_w, torch.float32, dev, None, "topk_w")
+    st = _status_arg(status, dev)
     if row_idx.numel() != T * k:
         raise ValueError("row_idx must hold T * k rows")
-    _same_device(dev, d_out=d_out, row_idx=row_idx, topk_w=topk_w)
-    flags = (OUT_F32 if d_out.dtype == torch.float32 else 0) | \
-        (Y_F32 if y_exp.dtype == torch.float32 else 0)
+    flags = (OUT_F32 if dt == torch.float32 else 0) | (Y_F32 if yt == torch.float32 else 0)
     with _on(dev):
         d_y = torch.empty_like(y_exp)
         d_w = torch.empty_like(topk_w)
-        _call("moe_finalize_routing_backward", _ptr(d_out), _ptr(y_exp), _ptr(row_idx),
-              _ptr(topk_w), T, H, k, flags, d_y.data_ptr(), d_w.data_ptr(), _ptr(status),
-              _stream(dev))
+        _call("moe_finalize_routing_backward", do, y, rows, w, T, H, k, flags, d_y.data_ptr(),
+              d_w.data_ptr(), st, _stream(dev))
     return d_y, d_w
 
 
@@ -526,15 +536,22 @@ def _fp4_empty(rows, K, fmt, scale_exp, groups, dev) -> Fp4Matrix:
                                  device=dev), fmt, int(scale_exp))
 
 
-def _fp4_arg(m: Fp4Matrix, name, groups, dev, rows=None):
+def _fp4_arg(m: Fp4Matrix, name, groups, dev):
     """The C struct of a matrix, its buffers checked against the layout."""
-    _check(m.q, torch.uint8, name + ".q")
-    _check(m.sf, torch.uint8, name + ".sf")
-    n = m.q.numel() // max(m.q.shape[-1], 1) if rows is None else rows
-    if m.sf.numel() < fp4_scales_size(n, m.K, m.fmt, groups):
+    q, sf = m.q, m.sf
+    qp = _arg(q, torch.uint8, dev, None, name)
+    sp = _arg(sf, torch.uint8, dev, None, name)
+    half = q.shape[-1]
+    if sf.numel() < fp4_scales_size(q.numel() // half if half else 0, half * 2, m.fmt, groups):
         raise ValueError(f"{name}.sf is smaller than its scale tiles")
-    _same_device(dev, **{name + ".q": m.q, name + ".sf": m.sf})
-    return ctypes.byref(_Fp4(_ptr(m.q), _ptr(m.sf), _fp4_format(m.fmt), m.scale_exp))
+    return ctypes.byref(_Fp4(qp, sp, FP4_FORMATS[m.fmt], m.scale_exp))
+
+
+def _groups_arg(offsets, dev):
+    """(address, G) of optional group offsets."""
+    if offsets is None:
+        return None, 0
+    return _arg(offsets, torch.int32, dev, None, "offsets"), offsets.numel() - 1
 
 
 def fp4_quantize(x, fmt="mx", scale_exp=0, row_idx=None, k=1, offsets=None,
@@ -543,22 +560,22 @@ def fp4_quantize(x, fmt="mx", scale_exp=0, row_idx=None, k=1, offsets=None,
     ``offsets``, token rows go to their k rows in expert order.  A weight
     [G, N, K] keeps its shape in ``q`` and is quantised ungrouped.  Rows that
     row_idx does not name are not set."""
-    _check(x, torch.bfloat16, "x")
-    _check(row_idx, torch.int32, "row_idx")
-    _check(offsets, torch.int32, "offsets")
+    dev = x.device
+    xp = _arg(x, torch.bfloat16, dev, None, "x")
+    rows = _arg(row_idx, torch.int32, dev, None, "row_idx")
+    off, G = _groups_arg(offsets, dev)
+    st = _status_arg(status, dev)
     K = x.shape[-1]
     T = x.numel() // K if K else 0
-    dev = x.device
-    if row_idx is not None and row_idx.numel() != T * k:
+    if row_idx is None:
+        if k != 1:
+            raise ValueError("k needs row_idx")
+    elif row_idx.numel() != T * k:
         raise ValueError("row_idx must hold T * k rows")
-    if row_idx is None and k != 1:
-        raise ValueError("k needs row_idx")
-    _same_device(dev, row_idx=row_idx, offsets=offsets)
-    G = 0 if offsets is None else offsets.numel() - 1
     with _on(dev):
         m = _fp4_empty(T * k, K, fmt, scale_exp, G, dev)
-        _call("moe_fp4_quantize", _ptr(x), T, K, _ptr(row_idx), k, _ptr(offsets), G,
-              _fp4_arg(m, "out", G, dev), _ptr(status), _stream(dev))
+        _call("moe_fp4_quantize", xp, T, K, rows, k, off, G, _fp4_arg(m, "out", G, dev), st,
+              _stream(dev))
     if x.dim() != 2:
         m.q = m.q.view(*x.shape[:-1], K // 2)
     return m
@@ -567,44 +584,38 @@ def fp4_quantize(x, fmt="mx", scale_exp=0, row_idx=None, k=1, offsets=None,
 def fp4_dequantize(m: Fp4Matrix, offsets=None):
     """-> bf16 values of a 4-bit matrix, exact (``offsets`` as it was made
     with; rows past the last group are not set)."""
-    _check(offsets, torch.int32, "offsets")
     dev = m.q.device
-    _same_device(dev, offsets=offsets)
-    G = 0 if offsets is None else offsets.numel() - 1
-    n = m.q.numel() // max(m.q.shape[-1], 1)
+    off, G = _groups_arg(offsets, dev)
+    K = m.K
+    arg = _fp4_arg(m, "m", G, dev)
     with _on(dev):
-        x = torch.empty((*m.q.shape[:-1], m.K), dtype=torch.bfloat16, device=dev)
-        _call("moe_fp4_dequantize", _fp4_arg(m, "m", G, dev), n, m.K, _ptr(offsets), G, _ptr(x),
+        x = torch.empty((*m.q.shape[:-1], K), dtype=torch.bfloat16, device=dev)
+        _call("moe_fp4_dequantize", arg, x.numel() // K if K else 0, K, off, G, x.data_ptr(),
               _stream(dev))
     return x
 
 
 def _fp4_product(a, offsets, w, name):
-    """(n, K, G, rows of a group's weights) of a grouped 4-bit product."""
-    _check(offsets, torch.int32, "offsets")
-    if a.q.dim() != 2 or w.q.dim() != 3 or a.K != w.K:
+    """(n, K, G, rows of a group's weights, device, offsets' address)."""
+    if a.q.dim() != 2 or w.q.dim() != 3 or a.q.shape[1] != w.q.shape[2]:
         raise ValueError(f"{name}: a [n, K/2] and weights [G, rows, K/2] of the same K")
+    n, half = a.q.shape
     G, rows, _ = w.q.shape
-    if offsets.numel() != G + 1:
-        raise ValueError(f"{name}: offsets must hold G + 1 rows")
-    _same_device(a.q.device, offsets=offsets)
-    return a.q.shape[0], a.K, G, rows
+    dev = a.q.device
+    return n, half * 2, G, rows, dev, _arg(offsets, torch.int32, dev, (G + 1,), "offsets")
 
 
 def fp4_grouped_matmul(a: Fp4Matrix, offsets, w: Fp4Matrix, out_f32=False, out=None, status=None):
     """y = a . w[group]^T -> [n, N] bf16 (fp32 with out_f32).  Rows past the
     last group are left as they were in ``out`` (not set without it)."""
-    n, K, G, N = _fp4_product(a, offsets, w, "fp4_grouped_matmul")
-    dev = a.q.device
+    n, K, G, N, dev, off = _fp4_product(a, offsets, w, "fp4_grouped_matmul")
+    aa, wa, st = _fp4_arg(a, "a", G, dev), _fp4_arg(w, "w", 0, dev), _status_arg(status, dev)
     dt = torch.float32 if out_f32 else torch.bfloat16
     with _on(dev):
         if out is None:
             out = torch.empty((n, N), dtype=dt, device=dev)
-        _check(out, dt, "out")
-        _shape(out, (n, N), "out")
-        _call("moe_fp4_grouped_matmul", _fp4_arg(a, "a", G, dev), _ptr(offsets), G,
-              _fp4_arg(w, "w", 0, dev), n, K, N, Y_F32 if out_f32 else 0, _ptr(out),
-              _ptr(status), _stream(dev))
+        _call("moe_fp4_grouped_matmul", aa, off, G, wa, n, K, N, Y_F32 if out_f32 else 0,
+              _arg(out, dt, dev, (n, N), "out"), st, _stream(dev))
     return out
 
 
@@ -613,41 +624,40 @@ def fp4_grouped_swiglu(a: Fp4Matrix, offsets, w13: Fp4Matrix, quantize=False, sc
     """act = SiLU(gate) * up of the merged w13 [G, 2I, K] -> bf16 [n, I], or
     with ``quantize`` the same values in 4 bits (an Fp4Matrix of a's format,
     grouped by ``offsets``)."""
-    n, K, G, rows = _fp4_product(a, offsets, w13, "fp4_grouped_swiglu")
+    n, K, G, rows, dev, off = _fp4_product(a, offsets, w13, "fp4_grouped_swiglu")
+    if rows % 2:
+        raise ValueError("w13 must hold an even number of rows, gate then up")
     I = rows // 2
-    dev = a.q.device
+    aa, wa, st = _fp4_arg(a, "a", G, dev), _fp4_arg(w13, "w13", 0, dev), _status_arg(status, dev)
     with _on(dev):
         if quantize:
             if out is None:
                 out = _fp4_empty(n, I, a.fmt, scale_exp, G, dev)
-            _shape(out.q, (n, I // 2), "out.q")
+            elif out.q.shape != (n, I // 2):
+                raise ValueError(f"out.q must have shape {(n, I // 2)}")
             bf, q4 = None, _fp4_arg(out, "out", G, dev)
         else:
             if out is None:
                 out = torch.empty((n, I), dtype=torch.bfloat16, device=dev)
-            _check(out, torch.bfloat16, "out")
-            _shape(out, (n, I), "out")
-            bf, q4 = _ptr(out), None
-        _call("moe_fp4_grouped_swiglu", _fp4_arg(a, "a", G, dev), _ptr(offsets), G,
-              _fp4_arg(w13, "w13", 0, dev), n, K, I, bf, q4, _ptr(status), _stream(dev))
+            bf, q4 = _arg(out, torch.bfloat16, dev, (n, I), "out"), None
+        _call("moe_fp4_grouped_swiglu", aa, off, G, wa, n, K, I, bf, q4, st, _stream(dev))
     return out
 
 
 def fp4_grouped_mlp(expanded_x: Fp4Matrix, offsets, w13: Fp4Matrix, w2: Fp4Matrix, y_f32=False,
                     act_exp=0, status=None):
     """-> (act Fp4Matrix [n, I], y bf16 [n, H], fp32 with y_f32)."""
-    n, H, G, rows = _fp4_product(expanded_x, offsets, w13, "fp4_grouped_mlp")
+    n, H, G, rows, dev, off = _fp4_product(expanded_x, offsets, w13, "fp4_grouped_mlp")
     I = rows // 2
-    if tuple(w2.q.shape) != (G, H, I // 2):
-        raise ValueError("w2 must be [G, H, I/2]")
-    dev = expanded_x.q.device
+    if rows % 2 or w2.q.shape != (G, H, I // 2):
+        raise ValueError("w13 must be [G, 2I, H/2] and w2 [G, H, I/2]")
+    xa, wa = _fp4_arg(expanded_x, "expanded_x", G, dev), _fp4_arg(w13, "w13", 0, dev)
+    w2a, st = _fp4_arg(w2, "w2", 0, dev), _status_arg(status, dev)
     with _on(dev):
         act = _fp4_empty(n, I, expanded_x.fmt, act_exp, G, dev)
         y = torch.empty((n, H), dtype=torch.float32 if y_f32 else torch.bfloat16, device=dev)
-        _call("moe_fp4_grouped_mlp", _fp4_arg(expanded_x, "expanded_x", G, dev), _ptr(offsets), G,
-              _fp4_arg(w13, "w13", 0, dev), _fp4_arg(w2, "w2", 0, dev), n, H, I,
-              Y_F32 if y_f32 else 0, _fp4_arg(act, "act", G, dev), _ptr(y), _ptr(status),
-              _stream(dev))
+        _call("moe_fp4_grouped_mlp", xa, off, G, wa, w2a, n, H, I, Y_F32 if y_f32 else 0,
+              _fp4_arg(act, "act", G, dev), y.data_ptr(), st, _stream(dev))
     return act, y
 
 
