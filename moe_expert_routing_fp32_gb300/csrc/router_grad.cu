@@ -89,15 +89,19 @@ __device__ __forceinline__ float group_sum(float v) {
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
-// exp(z - m); the difference first, so that the lowest values and -inf work.
-__device__ __forceinline__ float exp_from(float z, float m) {
+__device__ __forceinline__ float exp2_approx(float x) {
     float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"((z - m) * kLog2e));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+// exp(z - m), the difference first.
+__device__ __forceinline__ float exp_from(float z, float m) { return exp2_approx((z - m) * kLog2e); }
 
-// z -> p in place for U rows; returns (max, 1 / sum) of each.  A row with
-// no finite logit gives zeros.
+// z -> e = exp(z - m) in place for U rows; mr = (m, 1 / sum of e), so that the
+// probabilities are e * mr.y.  A row with no finite logit has mr.y = 0.
+// exp(z - m) is taken as 2^(z log2e - m log2e) in one fused step; what the
+// rounded m log2e is off by is a factor of the whole row and leaves e * mr.y.
+// Rows near the type's limits, where those products overflow, subtract first.
 template <int LPT, int U, int N>
 __device__ __forceinline__ void softmax_rows(float (&z)[U][N], float2 (&mr)[U]) {
     float s[U];
@@ -107,11 +111,18 @@ __device__ __forceinline__ void softmax_rows(float (&z)[U][N], float2 (&mr)[U]) 
 #pragma unroll
         for (int i = 0; i < N; ++i) m = fmaxf(m, z[u][i]);
         m = group_max<LPT>(m);
-        mr[u].x = m == kNegInf ? 0.0f : m;
+        if (m == kNegInf) m = 0.0f;
+        mr[u].x = m;
+        if (__any_sync(0xffffffffu, fabsf(m) > 1e37f)) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) z[u][i] -= m;
+            m = 0.0f;
+        }
+        const float shift = m * kLog2e;
         s[u] = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            z[u][i] = exp_from(z[u][i], mr[u].x);
+            z[u][i] = exp2_approx(__fmaf_rn(z[u][i], kLog2e, -shift));
             s[u] += z[u][i];
         }
     }
@@ -120,11 +131,7 @@ __device__ __forceinline__ void softmax_rows(float (&z)[U][N], float2 (&mr)[U]) 
 #pragma unroll
         for (int u = 0; u < U; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        mr[u].y = s[u] > 0.0f ? __fdividef(1.0f, s[u]) : 0.0f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) z[u][i] *= mr[u].y;
-    }
+    for (int u = 0; u < U; ++u) mr[u].y = s[u] > 0.0f ? __fdividef(1.0f, s[u]) : 0.0f;
 }
 
 // Rows that a group of lanes takes at a time, the next ones being loaded
@@ -228,7 +235,7 @@ balance_partial_kernel(const float *__restrict__ logits, const int32_t *__restri
 #pragma unroll
             for (int v = 0; v < U; ++v) {
 #pragma unroll
-                for (int i = 0; i < R::N; ++i) acc[i] += z[v][i];
+                for (int i = 0; i < R::N; ++i) acc[i] = __fmaf_rn(z[v][i], mr[v].y, acc[i]);
                 if (!on[v]) continue;
                 n += l == 0;
 #pragma unroll
@@ -497,8 +504,8 @@ topk_backward_kernel(const float *__restrict__ logits, const int32_t *__restrict
             }
             float dot = 0.0f;
 #pragma unroll
-            for (int i = 0; i < R::N; ++i) dot += p[v][i] * cnt[i];
-            dot = group_sum<LPT>(dot);
+            for (int i = 0; i < R::N; ++i) dot = __fmaf_rn(p[v][i], cnt[i], dot);
+            dot = group_sum<LPT>(dot) * mr[v].y;
             float sub = 0.0f;                  // sum_l p_l dw_l without renormalisation
             if (d_topk_w) {
                 float w[SPL], ws = 0.0f, wd = 0.0f, m = mr[v].x;
@@ -529,8 +536,10 @@ topk_backward_kernel(const float *__restrict__ logits, const int32_t *__restrict
                     for (int u = 0; u < SPL; ++u) g[v][u] *= w[u];
                 }
             }
+            // p (scale (c - dot) - sub), p = e * mr.y
+            const float rs = scale * mr[v].y, rsub = sub * mr[v].y;
 #pragma unroll
-            for (int i = 0; i < R::N; ++i) p[v][i] *= scale * (cnt[i] - dot) - sub;
+            for (int i = 0; i < R::N; ++i) p[v][i] *= __fmaf_rn(rs, cnt[i] - dot, -rsub);
             if (d_topk_w) {
                 // Each slot's term goes to the lane of its column through the
                 // group's row of shared memory (zeros between tokens).  A slot
@@ -696,13 +705,15 @@ finalize_backward_kernel(const void *__restrict__ d_out, const void *__restrict_
 inline bool a16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
-// Chunks of the forward pass and their tokens: about four CTAs per SM, at
-// least 32 tokens each (two passes of a CTA's sixteen groups).
+// Chunks and their tokens: `per_sm` CTAs per SM, at least 32 tokens each.  The
+// forward pass takes the four that are resident at once, since its chunks'
+// partial sums are joined afterwards; the backward pass three times as many,
+// so that the last round of its three or four resident ones is short.
 struct Chunks {
     int count, per;
 };
-Chunks chunks_of(int T) {
-    const int64_t most = static_cast<int64_t>(num_sms()) * 4;
+Chunks chunks_of(int T, int per_sm = 4) {
+    const int64_t most = static_cast<int64_t>(num_sms()) * per_sm;
     const int64_t want = std::max<int64_t>(1, std::min<int64_t>(most, ceil_div(T, 32)));
     const int per = static_cast<int>(std::max<int64_t>(1, ceil_div(T, want)));
     return {static_cast<int>(std::max<int64_t>(1, ceil_div(T, per))), per};
@@ -817,7 +828,7 @@ extern "C" moe_status_t moe_gate_topk_backward(
     if (!logits || !d_logits || (d_topk_w && !topk_idx)) return MOE_ERR_INVALID_ARG;
     if (!current_device_ok()) return MOE_ERR_NO_DEVICE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const Chunks ch = chunks_of(T);
+    const Chunks ch = chunks_of(T, 12);
     with_row_shape(E, whole_vectors(E, logits, d_logits), [&](auto v, auto l, auto n) {
         // a row of columns per group: at most 32 KB
         const size_t smem = static_cast<size_t>(R_THREADS) * v.value * n.value * 4;
