@@ -858,7 +858,7 @@ extern "C" moe_status_t moe_finalize_routing_backward(const void *d_out, const v
     // few tokens: a CTA per slot, so that the rows spread over the SMs
     const bool few = static_cast<int64_t>(T) < 2 * num_sms();
     const int64_t units = few ? static_cast<int64_t>(T) * k : static_cast<int64_t>(T) * ceil_div(k, 8);
-    const int grid = static_cast<int>(std::min<int64_t>(units, static_cast<int64_t>(num_sms()) * 16));
+    const int grid = static_cast<int>(std::min<int64_t>(units, static_cast<int64_t>(num_sms()) * 64));
 #define MOE_FB(U, YF, DF)                                                                     \
     finalize_backward_kernel<U, YF, DF><<<grid, R_THREADS, 0, s>>>(                           \
         d_out, y_exp, expanded_row_idx, topk_w, T, H, k, T * k, d_y_exp, d_topk_w, dev_status)
