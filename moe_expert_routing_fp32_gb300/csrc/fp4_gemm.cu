@@ -394,8 +394,18 @@ __device__ __forceinline__ void fp4_gemm(const Params &p) {
     const int first_tile = static_cast<int>(blockIdx.x) / CG;
     const int step = static_cast<int>(gridDim.x) / CG;
 
-    if (tid == 0) *s_abort = 0;
-    if (tid == 32) {
+    // Barriers, tensor memory and descriptors are made ready while the group
+    // offsets are on their way.
+    if (warp == 1) {
+        if (CG == 1) {
+            tmem_alloc(s_tmem, TMEM_COLS);
+            tmem_relinquish();
+        } else {
+            tmem_alloc_pair(s_tmem, TMEM_COLS);
+            tmem_relinquish_pair();
+        }
+    } else if (warp == 2 && elect_one()) {
+        *s_abort = 0;
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 2);          // each producer arms its share
             mbar_init(&empty[s], 2);         // both issuers' MMAs have read it
@@ -407,22 +417,16 @@ __device__ __forceinline__ void fp4_gemm(const Params &p) {
         mbar_init(&drain[0], 1);
         mbar_init(&drain[1], 1);
         fence_barrier_init();
+    } else if (warp == 3 && elect_one()) {
+        tma_prefetch_desc(&p.tmA);
+        tma_prefetch_desc(&p.tmB);
+        tma_prefetch_desc(&p.tmSA);
+        tma_prefetch_desc(&p.tmSB);
     }
-    // both CTAs of a pair read the same offsets, so both leave here together
-    if (!list_tiles<BM * CG>(p, s_off, s_prefix, s_bad)) {
-        if (tid == 0 && blockIdx.x == 0) report(p.dev_status, MOE_DEV_BAD_OFFSETS);
-        return;
-    }
-    const int total = s_prefix[p.G];
-    if (warp == 1) {
-        if (CG == 1) {
-            tmem_alloc(s_tmem, TMEM_COLS);
-            tmem_relinquish();
-        } else {
-            tmem_alloc_pair(s_tmem, TMEM_COLS);
-            tmem_relinquish_pair();
-        }
-    }
+    // Bad offsets leave no tiles; both CTAs of a pair read the same ones.
+    const bool good = list_tiles<BM * CG>(p, s_off, s_prefix, s_bad);
+    if (!good && tid == 0 && blockIdx.x == 0) report(p.dev_status, MOE_DEV_BAD_OFFSETS);
+    const int total = good ? s_prefix[p.G] : 0;
     tc_fence_before();
     __syncthreads();
     if (CG == 2) cluster_sync_all();         // barriers and TMEM of both CTAs are ready
@@ -437,8 +441,6 @@ __device__ __forceinline__ void fp4_gemm(const Params &p) {
         // ================= TMA producers: warp 0 A, warp 3 B, each with its scales
         if (elect_one()) {
             const bool is_a = warp == 0;
-            tma_prefetch_desc(is_a ? &p.tmA : &p.tmB);
-            tma_prefetch_desc(is_a ? &p.tmSA : &p.tmSB);
             int stage = 0;
             uint32_t phase = 0;
             int armed[STAGES];
