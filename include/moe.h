@@ -414,11 +414,13 @@ moe_status_t moe_local_finalize_rerouting(const moe_bf16_t *local_y, const int32
  *               every sequence take no part.  NULL (with S = 1): all tokens.
  *   loss [1] fp32, counts [S, E] int32, prob_mean [S, E] fp32,
  *   n_tokens [S] int32: out
- * S <= 65536.  Sums are fp32 in a fixed order: the result is deterministic.
+ * S <= 65536, T <= 2^30.  Sums are fp32 in a fixed order: the result is
+ * deterministic.
  * Expert ids outside [0, E) set MOE_DEV_BAD_EXPERT_ID and are not counted;
  * bad bounds set MOE_DEV_BAD_OFFSETS.  T may be 0.  Workspace:
  * moe_balance_loss_workspace_size() bytes, 256-byte aligned; its contents are
- * scratch, every byte a call reads it has written.
+ * scratch, every byte a call reads it has written.  Calls that may overlap in
+ * time (also as replayed graphs) need one each.
  */
 moe_status_t moe_balance_loss_workspace_size(int32_t T, int32_t E, int32_t S, size_t *bytes);
 moe_status_t moe_balance_loss(const float *logits, const int32_t *topk_idx,
@@ -457,8 +459,9 @@ moe_status_t moe_gate_topk_backward(const float *logits, const int32_t *topk_idx
  *   d_out [T, H] bf16 (fp32 with MOE_OUT_F32); y_exp, d_y_exp [T*k, H] bf16
  *   (fp32 with MOE_Y_F32), d_y_exp not overlapping an input; topk_w,
  *   d_topk_w [T, k] fp32, the dot products summed in fp32 in a fixed order.
- * A slot whose row is negative has d_topk_w = 0; rows that no slot names are
- * left untouched.  A row >= T*k sets MOE_DEV_BAD_OFFSETS and is left out.
+ * expanded_row_idx as moe_init_routing gives it: no row twice.  A slot whose
+ * row is negative has d_topk_w = 0; rows that no slot names are left
+ * untouched.  A row >= T*k sets MOE_DEV_BAD_OFFSETS and is left out.
  * H % 8 == 0, k <= 32.
  */
 moe_status_t moe_finalize_routing_backward(const void *d_out, const void *y_exp,
@@ -504,9 +507,9 @@ moe_status_t moe_fp4_scales_size(int32_t rows, int32_t K, int32_t G, int32_t for
  *       most 448.  Elements: nearest e2m1 of value / scale, ties to even,
  *       beyond 6 to 6; zeros where the scale is zero.
  *   offsets [G+1]: groups of the rows (fixes the scale layout); NULL with G = 0
- * Rows that no slot names, negative rows and rows past offsets[G] are left
- * untouched; a row >= T*k sets MOE_DEV_BAD_OFFSETS and is left out.
- * k <= 32, G <= 1024.
+ * No row may be named twice.  Rows that no slot names, negative rows and rows
+ * past offsets[G] are left untouched; a row >= T*k sets MOE_DEV_BAD_OFFSETS and
+ * is left out.  k <= 32, G <= 1024.  x finite.
  * moe_fp4_dequantize gives the values back: x [n, K] bf16 out, exact (rows
  * past offsets[G] are left untouched).
  */

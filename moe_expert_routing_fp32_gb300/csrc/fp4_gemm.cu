@@ -865,7 +865,9 @@ moe_status_t check_product(const Product &d) {
     moe_status_t st = fp4_check(d.a->format, d.a->scale_exp);
     if (st == MOE_OK) st = fp4_check(d.w->format, d.w->scale_exp);
     if (st != MOE_OK) return st;
-    if (d.G > MAX_GROUPS || d.K % 128 != 0 || d.N % 128 != 0) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (d.G > MAX_GROUPS || d.K % 128 != 0 || d.N % 128 != 0 || d.K > (1 << 20) ||
+        d.n > INT32_MAX - 1024)
+        return MOE_ERR_UNSUPPORTED_SHAPE;
     // tile coordinates and scale tiles are 32-bit
     const int64_t tile_rows = (static_cast<int64_t>(d.n) / 128 + d.G) * (d.K / 64);
     const int64_t w_tiles = static_cast<int64_t>(d.G) * (2 * static_cast<int64_t>(d.N) / 128) * (d.K / 64);

@@ -756,7 +756,7 @@ using namespace moe;
 extern "C" moe_status_t moe_balance_loss_workspace_size(int32_t T, int32_t E, int32_t S,
                                                         size_t *bytes) {
     if (!bytes || T < 0 || E <= 0 || S <= 0) return MOE_ERR_INVALID_ARG;
-    if (E > 1024 || S > 65536) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (E > 1024 || S > 65536 || T > (1 << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
     const size_t P = static_cast<size_t>(chunks_of(T).count) + S;
     // the partials, the shares of the loss and their counter
     *bytes = 2 * align256(P * E * 4) + align256(P * 4) +
@@ -820,10 +820,11 @@ extern "C" moe_status_t moe_gate_topk_backward(
     const float *d_loss, float coef, int32_t T, int32_t E, int32_t k, uint32_t flags,
     float *d_logits, int32_t *dev_status, moe_stream_t stream) {
     if (T < 0 || E <= 0 || k <= 0) return MOE_ERR_INVALID_ARG;
-    if (E > 1024 || k > 32 || k > E) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (E > 1024 || k > 32 || k > E || T > (1 << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (static_cast<int64_t>(T) * k >= (int64_t{1} << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (!counts != !n_tokens) return MOE_ERR_INVALID_ARG;
     if (counts && (S <= 0 || (!seq_offsets && S != 1))) return MOE_ERR_INVALID_ARG;
+    if (counts && S > 65536) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (T == 0) return MOE_OK;
     if (!logits || !d_logits || (d_topk_w && !topk_idx)) return MOE_ERR_INVALID_ARG;
     if (!current_device_ok()) return MOE_ERR_NO_DEVICE;

@@ -106,7 +106,8 @@ def test_refusals_of_the_products(L):
     assert m(n=0, y=None, a=mat(q=None, sf=None)) == 0         # nothing to do
     assert mm(None, FAKE, 2, mat(), 4, 128, 128, 0, FAKE, None, None) == 1
     # sizes whose tile numbers pass 32 bits
-    assert m(n=2 ** 31 - 1, K=1 << 19, N=128) == 2
+    assert m(n=2 ** 30, K=1 << 19, N=128) == 2
+    assert m(n=2 ** 31 - 1) == 2 and m(K=1 << 21) == 2
     # swiglu: exactly one form of the result
     assert sw(mat(), FAKE, 2, mat(), 4, 128, 128, None, None, None, None) == 1
     assert sw(mat(), FAKE, 2, mat(), 4, 128, 128, FAKE, mat(), None, None) == 1
@@ -149,6 +150,7 @@ def test_refusals_of_the_router_operators(L):
     assert L.moe_balance_loss_workspace_size(100, 2000, 1, ctypes.byref(n)) == 2
     assert L.moe_balance_loss_workspace_size(100, 8, 0, ctypes.byref(n)) == 1
     assert L.moe_balance_loss_workspace_size(100, 8, 65537, ctypes.byref(n)) == 2
+    assert L.moe_balance_loss_workspace_size(2 ** 30 + 1, 8, 1, ctypes.byref(n)) == 2
     L.moe_balance_loss_workspace_size(100, 8, 2, ctypes.byref(n))
     bl = L.moe_balance_loss
 
@@ -162,7 +164,8 @@ def test_refusals_of_the_router_operators(L):
 
     def b(lg=FAKE, idx=FAKE, dw=FAKE, seq=None, S=1, c=FAKE, nt=FAKE, T=4, E=8, k=2, d=FAKE):
         return tb(lg, idx, dw, None, seq, S, c, nt, None, 1.0, T, E, k, 0, d, None, None)
-    assert b(k=9) == 2 and b(E=1025) == 2 and b(T=-1) == 1
+    assert b(k=9) == 2 and b(E=1025) == 2 and b(T=-1) == 1 and b(T=2 ** 30 + 1, k=1) == 2
+    assert b(S=65537, seq=FAKE) == 2
     assert b(c=None) == 1 and b(nt=None) == 1                  # both or neither
     assert b(S=2) == 1 and b(S=0) == 1
     assert b(lg=None) == 1 and b(d=None) == 1 and b(idx=None) == 1

@@ -281,6 +281,51 @@ def test_many_rows_per_group(fmt, groups, rows):
     assert np.array_equal(q.sf.cpu().numpy()[pos], byte)
 
 
+def test_offsets_past_32_bits():
+    """More than 2^31 bytes of codes and 2^32 of rows in and values out: the
+    rows of a repeated block give that block's bytes everywhere."""
+    K, block = 4096, 4096
+    n = 2 ** 20 + block + 257
+    G = 2
+    x = _rows(block, K, 91).to(DEV)
+    big = x.repeat(n // block + 1, 1)[:n].contiguous()
+    m = moe.fp4_quantize(big, "nv")
+    one = moe.fp4_quantize(x, "nv")
+    assert torch.equal(m.q[-257:], one.q[:257]) and torch.equal(m.q[2 ** 20:2 ** 20 + block], one.q)
+    v = moe.fp4_dequantize(m)
+    assert torch.equal(v[-257:], moe.fp4_dequantize(one)[:257])
+    del v
+    # the same rows in two groups, the second one far behind
+    off = torch.tensor([0, block, n], dtype=torch.int32, device=DEV)
+    ident = torch.arange(n, dtype=torch.int32, device=DEV)
+    a = moe.fp4_quantize(big, "nv", row_idx=ident, offsets=off)
+    del big
+    w = moe.fp4_quantize(_rows(128, K, 92, 0.02).to(DEV).repeat(G * 8, 1).view(G, 1024, K), "nv", -6)
+    st = moe.new_status(DEV)
+    y = moe.fp4_grouped_matmul(a, off, w, out_f32=True, status=st)
+    assert int(st.item()) == 0 and y.numel() * 4 > 2 ** 32
+    assert torch.equal(y[:block, :128], y[2 ** 20:2 ** 20 + block, 896:])
+    assert torch.equal(y[-257:], y[:257])
+    ex = moe.fp4_dequantize(one).double() @ moe.fp4_dequantize(w)[0, :128].double().T
+    s = moe.fp4_dequantize(one).double().abs() @ moe.fp4_dequantize(w)[0, :128].double().abs().T
+    assert ((y[:block, :128].double() - ex).abs() <= (K + 8) * 2.0 ** -23 * s).all()
+
+
+def test_more_groups_than_a_pair_kernel_lists():
+    """1024 groups of more than 128 rows each: the one-CTA tiles take them."""
+    G, rows, K, N = 1024, 130, 128, 128
+    off = np.arange(G + 1, dtype=np.int32) * rows
+    offc = _cuda(off)
+    ident = torch.arange(G * rows, dtype=torch.int32, device=DEV)
+    a = moe.fp4_quantize(_rows(G * rows, K, 95).to(DEV), "mx", row_idx=ident, offsets=offc)
+    w = moe.fp4_quantize(_rows(G * N, K, 96).to(DEV).view(G, N, K), "mx")
+    y = moe.fp4_grouped_matmul(a, offc, w, out_f32=True)
+    av = moe.fp4_dequantize(a, offc).double().view(G, rows, K)
+    wv = moe.fp4_dequantize(w).double()
+    ex, s = av @ wv.transpose(1, 2), av.abs() @ wv.abs().transpose(1, 2)
+    assert ((y.double().view(G, rows, N) - ex).abs() <= (K + 8) * 2.0 ** -23 * s).all()
+
+
 def test_bad_offsets_are_reported_and_nothing_written():
     off, n, a, av, w, wv = _problem([64, 64], 128, 128, "mx", 0, 0, 61)
     for bad in ([0, 80, 64], [0, 64, 1000], [-1, 64, 128]):
