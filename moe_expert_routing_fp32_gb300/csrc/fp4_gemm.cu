@@ -15,17 +15,27 @@
 // has), and the scale tiles, which are copied into tensor memory ahead of the
 // MMAs that use them.
 //
-// What bounds it.  An MMA of 256 x 256 x 64 takes 128 cycles (measured; 9.5
+// What bounds it.  An MMA of 256 x 256 x 64 takes 128 cycles (measured; 10
 // PFLOP/s at 2.07 GHz), and issuing one, or one of the scale copies, takes its
-// thread some 40, so a slice of 256 columns (512 cycles of MMAs, 4 MMAs and 6
-// to 12 copies) does not leave one thread room for anything else; and tensor
+// thread some 30 to 40, so a slice of 256 columns (512 cycles of MMAs; 4 of them
+// and 6 to 12 copies) leaves one thread no room for anything else; and tensor
 // memory holds no two 256-column accumulators beside the scales, so with one
-// accumulator per tile the MMAs stop while it is drained (some 2,000 of 8,192
-// cycles at K = 4096).  Both go away by halves: a tile is two half tiles of 128
-// columns, each with an issuing thread of its own, and the half tiles take
-// three 128-column accumulators in turn.  The thread of half 0 runs ahead on
-// the staged slices while half 1 waits for an accumulator, from then on stays
-// ahead, and half 0 is drained while half 1 still computes.
+// accumulator per tile the MMAs stop while it is drained.  Both go away by
+// halves: a tile is two half tiles of 128 columns, each with an issuing thread
+// of its own, and the half tiles take three 128-column accumulators in turn.
+// The thread of half 0 runs ahead on the staged slices while half 1 waits for an
+// accumulator, from then on stays ahead, and half 0 is drained while half 1
+// still computes.  (One thread with 256-column MMAs on two accumulators that
+// share 64 columns, drained first: 690 us where this takes 658, SwiGLU 131072 x
+// 4096 x 4096.)  What is left then is the operands' way into shared memory: 70
+// bytes an SM and cycle at the MMAs' full rate, of which about 57 come (118 GB/s
+// an SM), and, in long runs, the power cap.
+//
+// Measured (one GB300, in a loop): SwiGLU 131072 x 4096 x 4096 (MX) 655 us, 6.7
+// PFLOP/s, 2.07 GHz; 720-750 us, 5.9-6.1 PFLOP/s, at the power cap's 1.68 GHz.
+// 131072 x 2048 x 4096 to fp32 (NV) 545 us: 2.6 GB at 4.8 TB/s, the epilogue's
+// boxes and the operands sharing shared memory's bandwidth.  Weights of 41
+// experts for 64 rows (365 MB) 62 us, 5.9 TB/s.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
