@@ -404,8 +404,7 @@ __device__ __forceinline__ void fp4_gemm(const Params &p) {
     const int first_tile = static_cast<int>(blockIdx.x) / CG;
     const int step = static_cast<int>(gridDim.x) / CG;
 
-    // Barriers, tensor memory and descriptors are made ready while the group
-    // offsets are on their way.
+    // Barriers, tensor memory and descriptors are made ready.
     if (warp == 1) {
         if (CG == 1) {
             tmem_alloc(s_tmem, TMEM_COLS);
@@ -433,6 +432,10 @@ __device__ __forceinline__ void fp4_gemm(const Params &p) {
         tma_prefetch_desc(&p.tmSA);
         tma_prefetch_desc(&p.tmSB);
     }
+    // Up to here nothing but shared and tensor memory is touched: launched as a
+    // programmatic dependent, this part runs while the stream's last kernel ends.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // Bad offsets leave no tiles; both CTAs of a pair read the same ones.
     const bool good = list_tiles<BM * CG>(p, s_off, s_prefix, s_bad);
     if (!good && tid == 0 && blockIdx.x == 0) report(p.dev_status, MOE_DEV_BAD_OFFSETS);
@@ -747,6 +750,24 @@ bool use_pair(int n, int G) {
            G <= std::min(Cfg<MOE_FP4_MX, 2>::MAX_G, Cfg<MOE_FP4_NV, 2>::MAX_G);
 }
 
+// Launched as a programmatic dependent of the stream's last kernel (the kernels
+// wait for its end before they read or write memory): 62.2 -> 60.5 us for the
+// weights of 41 experts, one product after another.
+cudaError_t start(void (*kernel)(const Params), int grid, int smem, const Params &p,
+                  cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 template <int FMT, int MODE>
 cudaError_t launch_pair(const Params &p, cudaStream_t stream) {
     using C = Cfg<FMT, 2>;
@@ -783,8 +804,7 @@ cudaError_t launch_pair(const Params &p, cudaStream_t stream) {
     }
     const int64_t tiles = (static_cast<int64_t>(p.n / (2 * BM)) + p.G) * p.nt;
     const int clusters = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(limit, tiles)));
-    fp4_gemm_pair_kernel<FMT, MODE><<<2 * clusters, THREADS, C::smem(p.G), stream>>>(p);
-    return cudaGetLastError();
+    return start(fp4_gemm_pair_kernel<FMT, MODE>, 2 * clusters, C::smem(p.G), p, stream);
 }
 
 template <int FMT, int MODE>
@@ -811,8 +831,7 @@ cudaError_t launch(Params &p, cudaStream_t stream) {
     // at most this many tiles: ceil(rows / 128) summed over the groups
     const int64_t tiles = (static_cast<int64_t>(p.n / BM) + p.G) * p.nt;
     const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms(), tiles)));
-    fp4_gemm_kernel<FMT, MODE><<<grid, THREADS, C::smem(p.G), stream>>>(p);
-    return cudaGetLastError();
+    return start(fp4_gemm_kernel<FMT, MODE>, grid, C::smem(p.G), p, stream);
 }
 
 struct Product {
