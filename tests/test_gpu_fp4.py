@@ -326,15 +326,22 @@ def test_more_groups_than_a_pair_kernel_lists():
     assert ((y.double().view(G, rows, N) - ex).abs() <= (K + 8) * 2.0 ** -23 * s).all()
 
 
-def test_bad_offsets_are_reported_and_nothing_written():
-    off, n, a, av, w, wv = _problem([64, 64], 128, 128, "mx", 0, 0, 61)
-    for bad in ([0, 80, 64], [0, 64, 1000], [-1, 64, 128]):
+@pytest.mark.parametrize("sizes", [[64, 64], [1500, 600]])      # one CTA, CTA pairs
+def test_bad_offsets_are_reported_and_nothing_written(sizes):
+    off, n, a, av, w, wv = _problem(sizes, 128, 128, "mx", 0, 0, 61)
+    x, y = sizes
+    for bad in ([0, n + 16, n], [0, x, n + 1000], [-1, x, n], [x, 0, n]):
         st = moe.new_status(DEV)
         out = torch.full((n, 128), 3.0, device=DEV)
-        moe.fp4_grouped_matmul(a, torch.tensor(bad, dtype=torch.int32, device=DEV), w, out_f32=True,
-                               out=out, status=st)
+        offc = torch.tensor(bad, dtype=torch.int32, device=DEV)
+        moe.fp4_grouped_matmul(a, offc, w, out_f32=True, out=out, status=st)
         assert int(st.item()) == moe.DEV_BAD_OFFSETS
         assert (out == 3.0).all()
+    st = moe.new_status(DEV)
+    moe.fp4_grouped_matmul(a, _cuda(off), w, out_f32=True, out=out, status=st)
+    ex, s = _sums(off, av, wv, n)
+    assert int(st.item()) == 0
+    assert (np.abs(_f64(out) - ex) <= 136 * 2.0 ** -23 * s).all()
 
 
 def test_streams_graphs_and_repeats_give_the_same_bytes():

@@ -246,6 +246,31 @@ def test_gradient_against_differences():
             assert abs(num - d[t, e]) <= 1e-6
 
 
+@pytest.mark.parametrize("E", [64, 200])
+def test_rows_off_the_vector_alignment(E):
+    """Logits that start 4 bytes behind a 16-byte boundary give the results of
+    aligned ones, within the sums' rounding (their lanes hold other columns)."""
+    rng, lg, idx, keep, seq = case(500, E, 6, 3, 0.1, 21)
+    dw = cu(rng.standard_normal((500, 6)).astype(np.float32))
+    buf = torch.zeros(500 * E + 1, device=DEV)
+    off = buf[1:].view(500, E)
+    off.copy_(cu(lg))
+    assert off.data_ptr() % 16 == 4 and off.is_contiguous()
+    res = []
+    for z in (cu(lg), off):
+        b = moe.balance_loss(z, cu(idx), 1.0, token_mask=cu(keep), seq_offsets=cu(seq))
+        d = moe.gate_topk_backward(z, cu(idx), dw, balance=b, token_mask=cu(keep),
+                                   seq_offsets=cu(seq))
+        res.append((b, d.cpu().numpy().astype(np.float64)))
+    loss, c, P, n = ref_balance(lg.astype(np.float64), idx, 1.0, keep, seq)
+    ex, sc = ref_grad(lg.astype(np.float64), idx, dw.cpu().numpy().astype(np.float64), True, keep,
+                      1.0, seq, c, n, 1.0)
+    for b, d in res:
+        assert np.array_equal(b["counts"].cpu().numpy(), c)
+        assert (np.abs(b["prob_mean"].cpu().numpy() - P) <= (1100 + E / 4) * U * P).all()
+        assert (np.abs(d - ex) <= (E + 64) * U * sc + 1e-38).all()
+
+
 def test_long_sequences_and_offsets_past_32_bits():
     """T E beyond 2^31 elements: the last rows are reached (the values of a
     block of rows repeat, so the means are those of the block)."""
