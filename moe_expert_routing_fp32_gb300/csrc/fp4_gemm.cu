@@ -27,15 +27,17 @@
 // accumulator, from then on stays ahead, and half 0 is drained while half 1
 // still computes.  (One thread with 256-column MMAs on two accumulators that
 // share 64 columns, drained first: 690 us where this takes 658, SwiGLU 131072 x
-// 4096 x 4096.)  What is left then is the operands' way into shared memory: 70
-// bytes an SM and cycle at the MMAs' full rate, of which about 57 come (118 GB/s
-// an SM), and, in long runs, the power cap.
+// 4096 x 4096.)  What is left, in cycles a tile of K = 4096 with a quarter of the
+// SMs running (so without the power cap): MMAs and hand-overs alone 9,470 (8,192
+// ideal), with the operands' loads 9,930 (they alone 6,870, 83 bytes a cycle), and
+// with the output 11,130: an SM's loads and stores add up.  In long runs on all
+// SMs the power cap takes a fifth of the clock.
 //
 // Measured (one GB300, in a loop): SwiGLU 131072 x 4096 x 4096 (MX) 655 us, 6.7
 // PFLOP/s, 2.07 GHz; 720-750 us, 5.9-6.1 PFLOP/s, at the power cap's 1.68 GHz.
-// 131072 x 2048 x 4096 to fp32 (NV) 545 us: 2.6 GB at 4.8 TB/s, the epilogue's
-// boxes and the operands sharing shared memory's bandwidth.  Weights of 41
-// experts for 64 rows (365 MB) 62 us, 5.9 TB/s.
+// 131072 x 2048 x 4096 to fp32 (NV) 545 us, 2.6 GB at 4.8 TB/s: of 8,520 cycles a
+// tile (a quarter of the SMs) the loads alone take 3,420 and with the stores
+// 7,260.  Weights of 41 experts for 64 rows (365 MB) 60.5 us, 6.0 TB/s.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
