@@ -197,8 +197,8 @@ __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint
 
 // One 512-byte scale tile (32 rows of 16 bytes) into four columns of tensor
 // memory, repeated in its four lane quarters (CG = 2: in both CTAs, each from
-// its own shared memory).  Ordered before the MMAs this thread issues
-// afterwards, and behind those it issued before.
+// its own shared memory).  The tensor pipe takes one thread's copies and MMAs in
+// the order they were issued.
 template <int CG>
 __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
     uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
@@ -306,10 +306,13 @@ __device__ __forceinline__ Tile decode_tile(const Params &p, int tile, int &g, c
     return t;
 }
 
+// Hardware exponential and division: a few 2^-22 relative, far below the 2^-9
+// that act is rounded by.
 __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
 
 // 64 act columns of one row (bf16 pairs, from column col on): codes and scale
-// bytes, as moe_fp4_quantize forms them.
+// bytes, as moe_fp4_quantize forms them.  act is rounded to bf16 before, as the
+// unquantised form is, so that both forms hold the same values.
 template <int FMT>
 __device__ __forceinline__ void emit_quantized(const Params &p, const uint32_t (&pk)[32], int g,
                                                int start, int row, int col) {

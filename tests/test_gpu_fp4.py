@@ -168,7 +168,7 @@ def _sums(off, av, wv, n):
     return y, s
 
 
-SHAPES = [("ragged", 128, 128), ("ragged", 384, 256), ("one", 256, 384), ("single-tokens", 1152, 128),
+SHAPES = [("ragged", 128, 128), ("one", 128, 128), ("ragged", 384, 256), ("one", 256, 384), ("single-tokens", 1152, 128),
           ("none", 128, 128), ("big", 640, 512), ("ragged", 2048, 640)]
 
 
