@@ -171,18 +171,28 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volat
     return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort, dev_status);
 }
 
+// Shared-memory descriptors are kept as their low words, whose address field
+// steps by plain additions; the high words are constants.  It leaves the issuing
+// threads, which share their schedulers with the epilogue's arithmetic, fewer
+// instructions: 246 cycles a slice of four MMAs and four copies against 315.
+//   operands: 128-byte swizzled K-major rows, 1 KB between groups of eight
+//   scales:   rows of 16 bytes, 128 bytes between groups of eight, no swizzle
+constexpr uint32_t OPERAND_LO = 1u << 16, OPERAND_HI = 0x40004040u;
+constexpr uint32_t SCALES_LO = 8u << 16, SCALES_HI = 0x00004008u;
+
 // D (+)= A * B^T with the scales at sa (rows of A) and sb (rows of B).
 // CG = 2: M = 256 over a CTA pair, each CTA holding its 128 rows of A (and
 // their scales), half the rows of B and the scales of all of them.
 #define MOE_MMA_FP4(GROUP, KIND)                                                              \
-    asm volatile("{\n\t.reg .pred p;\n\t"                                                     \
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"                               \
+                 "mov.b64 da, {%1, %7};\n\tmov.b64 db, {%2, %7};\n\t"                       \
                  "setp.ne.b32 p, %6, 0;\n\t"                                                  \
                  "tcgen05.mma.cta_group::" GROUP ".kind::" KIND                               \
-                 " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),                           \
-                 "l"(a), "l"(b), "r"(id), "r"(sa), "r"(sb), "r"(accumulate)                   \
+                 " [%0], da, db, %3, [%4], [%5], p;\n\t}" ::"r"(d),                           \
+                 "r"(a), "r"(b), "r"(id), "r"(sa), "r"(sb), "r"(accumulate), "n"(OPERAND_HI)  \
                  : "memory")
 template <int FMT, int CG>
-__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t id,
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint32_t a, uint32_t b, uint32_t id,
                                         uint32_t sa, uint32_t sb, uint32_t accumulate) {
     if (FMT == MOE_FP4_MX && CG == 1)
         MOE_MMA_FP4("1", "mxf4.block_scale.scale_vec::2X");
@@ -200,22 +210,22 @@ __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint
 // its own shared memory).  The tensor pipe takes one thread's copies and MMAs in
 // the order they were issued.
 template <int CG>
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
-    uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>(128u >> 4) << 16;
-    d |= static_cast<uint64_t>(128u >> 4) << 32;      // 8-row groups of 16-byte rows
-    d |= static_cast<uint64_t>(1u) << 46;
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t lo) {
     if (CG == 1)
-        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d)
+        asm volatile("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
+                     "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr),
+                     "r"(lo), "n"(SCALES_HI)
                      : "memory");
     else
-        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d)
+        asm volatile("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
+                     "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr),
+                     "r"(lo), "n"(SCALES_HI)
                      : "memory");
 }
 
 // One half tile's MMAs over STEPS * 64 columns of K of a stage (4, or 2 in a
-// last slice of 128 columns): operand tiles at a and b, scale tiles at sa and
-// sb in shared memory.  Two scale tiles of A and two of B at a time go to one
+// last slice of 128 columns): operand tiles a and b, scale tiles sa and sb
+// (descriptors' low words).  Two scale tiles of A and two of B at a time go to one
 // of this thread's two sets of columns, in turn, so that a set is not rewritten
 // while the MMAs just in front still read it.
 template <int FMT, int CG, int STEPS>
@@ -229,15 +239,15 @@ __device__ __forceinline__ void issue_slice(uint32_t d, uint32_t a, uint32_t b, 
         const uint32_t sa_t = sf_col + set * SF_SET, sb_t = sa_t + 8;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            copy_scales<CG>(sa_t + 4 * i, sa + (2 * h + i) * kScaleTile);
-            copy_scales<CG>(sb_t + 4 * i, sb + (2 * h + i) * kScaleTile);
+            copy_scales<CG>(sa_t + 4 * i, sa + (2 * h + i) * (kScaleTile / 16));
+            copy_scales<CG>(sb_t + 4 * i, sb + (2 * h + i) * (kScaleTile / 16));
         }
         set ^= 1;
 #pragma unroll
         for (int j = 0; j < (STEPS < PER ? STEPS : PER); ++j) {
             const int kk = h * PER + j;
             const int i = FMT == MOE_FP4_MX ? j / 2 : j;
-            mma_fp4<FMT, CG>(d, sdesc_kmajor_sw128(a + kk * 32), sdesc_kmajor_sw128(b + kk * 32),
+            mma_fp4<FMT, CG>(d, a + kk * 2, b + kk * 2,          // 32 bytes further along K
                              FMT == MOE_FP4_MX && (j & 1) ? ID2 : ID0, sa_t + 4 * i, sb_t + 4 * i,
                              (kk > 0 || accumulate) ? 1u : 0u);
         }
@@ -532,6 +542,11 @@ __device__ __forceinline__ void fp4_gemm(const Params &p) {
             uint32_t set = 0;
             const uint32_t sf_col = tmem + SF_COL + static_cast<uint32_t>(h) * 2 * SF_SET;
             const bool tail = p.K % BK != 0;                // the last slice holds 128 columns
+            // in units of 16 bytes
+            const uint32_t base = smem_u32(smem) >> 4;
+            const uint32_t b_off = (A_BYTES + static_cast<uint32_t>(h) * C::B_HALF) / 16;
+            const uint32_t sa_off = (A_BYTES + 2 * C::B_HALF) / 16 + SCALES_LO;
+            const uint32_t sb_off = (1 + static_cast<uint32_t>(h)) * C::SF_BYTES / 16;
             bool issued = false;
             for (int tile = first_tile; tile < total && !*s_abort; tile += step) {
                 if (!wait_acc(tempty, u, true, s_abort, p.dev_status)) break;
@@ -544,10 +559,9 @@ __device__ __forceinline__ void fp4_gemm(const Params &p) {
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a = smem_u32(smem + stage * C::STAGE);
-                    const uint32_t b = a + A_BYTES + h * C::B_HALF;
-                    const uint32_t sa = a + A_BYTES + 2 * C::B_HALF;
-                    const uint32_t sb = sa + (1 + h) * C::SF_BYTES;
+                    const uint32_t at = base + static_cast<uint32_t>(stage) * (C::STAGE / 16);
+                    const uint32_t a = at + OPERAND_LO, b = a + b_off;
+                    const uint32_t sa = at + sa_off, sb = sa + sb_off;
                     if (kb + 1 < kblocks || !tail)
                         issue_slice<FMT, CG, 4>(d, a, b, sa, sb, sf_col, set, kb != 0);
                     else
