@@ -529,7 +529,8 @@ moe_status_t moe_fp4_dequantize(const moe_fp4_t *m, int32_t n, int32_t K, const 
  *   swiglu:  act[r, :] = bf16(SiLU(gate) * up), gate = a[r] . w13[g, 0..I-1]^T,
  *            up = a[r] . w13[g, I..2I-1]^T     w13 [G, 2I, K]
  *            act [n, I] bf16, or act4: the same bf16 values quantised as
- *            moe_fp4_quantize does (exactly one of the two, the other NULL)
+ *            moe_fp4_quantize does (exactly one of the two, the other NULL);
+ *            a's and w13's scale_exp add up to -60..60
  *   mlp:     act = swiglu(expanded_x, w13) in 4 bits, y = matmul(act, w2);
  *            w13 [G, 2I, H], w2 [G, H, I], act [n, I] written
  * All matrices of a call have one format; `a` and `act` are grouped by

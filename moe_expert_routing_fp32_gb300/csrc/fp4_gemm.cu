@@ -316,9 +316,46 @@ __device__ __forceinline__ Tile decode_tile(const Params &p, int tile, int &g, c
     return t;
 }
 
-// Hardware exponential and division: a few 2^-22 relative, far below the 2^-9
-// that act is rounded by.
-__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+// Two fp32 values in a 64-bit register, for the packed arithmetic.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// SiLU(alpha g) / alpha of two gate sums, g / (1 + 2^(c g)) with c = -alpha log2 e:
+// hardware exponential and reciprocal, a few 2^-22 relative, far below the 2^-9
+// that act is rounded by; 1 / inf = 0 where the exponential overflows.
+__device__ __forceinline__ uint64_t silu2(float x, float y, uint64_t c) {
+    const uint64_t g = pair(x, y);
+    const float2 t = unpair(mul2(g, c));
+    const float2 d = unpair(add2(pair(ex2(t.x), ex2(t.y)), pair(1.0f, 1.0f)));
+    return mul2(g, pair(rcp(d.x), rcp(d.y)));
+}
 
 // 64 act columns of one row (bf16 pairs, from column col on): codes and scale
 // bytes, as moe_fp4_quantize forms them.  act is rounded to bf16 before, as the
@@ -616,6 +653,9 @@ __device__ __forceinline__ void fp4_gemm(const Params &p) {
             ++u;
             return true;
         };
+        // act = SiLU(alpha g) (alpha u) = alpha^2 (g / (1 + e^(-alpha g))) u
+        const float c = -1.4426950408889634f * p.alpha, a2 = p.alpha * p.alpha;
+        const uint64_t gate_c = pair(c, c), alpha2 = pair(a2, a2);
         int g = 0;
         for (int tile = first_tile; tile < total; tile += step) {
             const Tile t = decode_tile<BM * CG>(p, tile, g, s_off, s_prefix);
@@ -624,22 +664,22 @@ __device__ __forceinline__ void fp4_gemm(const Params &p) {
             const bool boxed = C::BOXES > 0 && row0 + 32 <= t.row_end;
             if (MODE != MODE_STORE) {
                 // half 0 is the gate, half 1 the same columns of up
-                float g0[32], g1[32], u0[32], u1[32];
-                if (!drain_half(g0, g1)) break;
+                float x[32], y[32];
+                uint64_t sg[32];
+                if (!drain_half(x, y)) break;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    g0[i] = silu(g0[i] * p.alpha);
-                    g1[i] = silu(g1[i] * p.alpha);
+                for (int i = 0; i < 16; ++i) {
+                    sg[i] = silu2(x[2 * i], x[2 * i + 1], gate_c);
+                    sg[16 + i] = silu2(y[2 * i], y[2 * i + 1], gate_c);
                 }
-                if (!drain_half(u0, u1)) break;
+                if (!drain_half(x, y)) break;
                 const int col = t.n_blk * HN + c0;
                 uint32_t w[32];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    w[i] = bf16x2(g0[2 * i] * (u0[2 * i] * p.alpha),
-                                       g0[2 * i + 1] * (u0[2 * i + 1] * p.alpha));
-                    w[16 + i] = bf16x2(g1[2 * i] * (u1[2 * i] * p.alpha),
-                                            g1[2 * i + 1] * (u1[2 * i + 1] * p.alpha));
+                for (int i = 0; i < 32; ++i) {
+                    const float *v = i < 16 ? x + 2 * i : y + 2 * (i - 16);
+                    const float2 a = unpair(mul2(mul2(sg[i], pair(v[0], v[1])), alpha2));
+                    w[i] = bf16x2(a.x, a.y);
                 }
                 if (MODE != MODE_SWIGLU_Q)
                     emit_words<uint16_t>(p, box, lane, boxed, ok, w, col, row0);
@@ -930,6 +970,12 @@ moe_status_t check_product(const Product &d) {
     return MOE_OK;
 }
 
+// The square of the matrices' common factor stays a normal fp32 number.
+bool swiglu_range(const Product &d) {
+    const int e = d.a->scale_exp + d.w->scale_exp;
+    return e >= -60 && e <= 60;
+}
+
 moe_status_t run_product(const Product &d, int mode, void *out, bool out_f32, const moe_fp4_t *act,
                          int32_t *dev_status, moe_stream_t stream) {
     if (!current_device_ok()) return MOE_ERR_NO_DEVICE;
@@ -965,6 +1011,7 @@ extern "C" moe_status_t moe_fp4_grouped_swiglu(const moe_fp4_t *a, const int32_t
     moe_status_t st = check_product(d);
     if (st != MOE_OK) return st;
     if (!act == !act4) return MOE_ERR_INVALID_ARG;     // one form of the result
+    if (!swiglu_range(d)) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (act4) {
         st = fp4_check(act4->format, act4->scale_exp);
         if (st != MOE_OK) return st;
@@ -986,6 +1033,7 @@ extern "C" moe_status_t moe_fp4_grouped_mlp(const moe_fp4_t *expanded_x, const i
     if (st == MOE_OK) st = check_product(down);
     if (st != MOE_OK) return st;
     if (act->format != expanded_x->format) return MOE_ERR_INVALID_ARG;
+    if (!swiglu_range(up)) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (n == 0) return MOE_OK;
     if (!y || !a16(y)) return MOE_ERR_INVALID_ARG;
     st = run_product(up, MODE_SWIGLU_Q, nullptr, false, act, dev_status, stream);

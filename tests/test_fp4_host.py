@@ -114,6 +114,11 @@ def test_refusals_of_the_products(L):
     assert sw(mat(), FAKE, 2, mat(), 4, 128, 128, None, mat(fmt=1), None, None) == 1
     assert sw(mat(), FAKE, 2, mat(), 4, 128, 128, None, mat(q=None), None, None) == 1
     assert sw(mat(), FAKE, 2, mat(), 4, 128, 96, FAKE, None, None, None) == 2
+    # the factors of swiglu's two operands together
+    assert sw(mat(fmt=1, exp=40), FAKE, 2, mat(fmt=1, exp=30), 4, 128, 128, FAKE, None, None,
+              None) == 2
+    assert mlp(mat(fmt=1, exp=-40), FAKE, 2, mat(fmt=1, exp=-30), mat(fmt=1), 4, 128, 128, 0,
+               mat(fmt=1), FAKE, None, None) == 2
     # mlp
     assert mlp(mat(), FAKE, 2, mat(), mat(), 4, 128, 128, 0, None, FAKE, None, None) == 1
     assert mlp(mat(), FAKE, 2, mat(), mat(fmt=1), 4, 128, 128, 0, mat(), FAKE, None, None) == 1
