@@ -33,11 +33,11 @@
 // with the output 11,130: an SM's loads and stores add up.  In long runs on all
 // SMs the power cap takes a fifth of the clock.
 //
-// Measured (one GB300, in a loop): SwiGLU 131072 x 4096 x 4096 (MX) 655 us, 6.7
-// PFLOP/s, 2.07 GHz; 720-750 us, 5.9-6.1 PFLOP/s, at the power cap's 1.68 GHz.
+// Measured (one GB300): SwiGLU 131072 x 4096 x 4096 (MX) 650 us, 6.8 PFLOP/s at
+// 2.07 GHz; in a loop 694-720 us, 6.1-6.3 PFLOP/s, at the power cap's 1.68 GHz.
 // 131072 x 2048 x 4096 to fp32 (NV) 545 us, 2.6 GB at 4.8 TB/s: of 8,520 cycles a
 // tile (a quarter of the SMs) the loads alone take 3,420 and with the stores
-// 7,260.  Weights of 41 experts for 64 rows (365 MB) 60.5 us, 6.0 TB/s.
+// 7,260.  Weights of 41 experts for 64 rows (365 MB) 60 us, 6.1 TB/s.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
