@@ -476,7 +476,8 @@ moe_status_t moe_finalize_routing_backward(const void *d_out, const void *y_exp,
  *   MOE_FP4_MX  blocks of 32; value = element * 2^(byte - 127)
  *   MOE_FP4_NV  blocks of 16; value = element * e4m3(byte) * 2^scale_exp
  * scale_exp (-60..60; 0 with MOE_FP4_MX) belongs to the whole matrix: it moves
- * the range of the e4m3 scales (2^-9 .. 448) to that of the data.
+ * the range of the e4m3 scales (2^-9 .. 448) to that of the data.  The byte 255
+ * (MX) or 127 (NV) is NaN, and so is every value of its block.
  *   q   [rows, K/2] bytes, the lower column of a pair in the low four bits
  *   sf  the scale bytes in 512-byte tiles of 128 rows x 4 blocks (the form the
  *       tensor cores take): row r, block b of a tile at (r % 32) * 16 +

@@ -126,6 +126,15 @@ __device__ __forceinline__ uint32_t dequantize2(uint32_t byte, float s) {
     return bf16x2(lo * s, hi * s);
 }
 
+// What a scale byte stands for.  The formats' NaN bytes are NaN here as they
+// are to the tensor cores.
+template <int FMT>
+__device__ __forceinline__ float scale_value(uint32_t b, float unit) {
+    if ((FMT == MOE_FP4_MX ? b : b & 0x7Fu) == kScaleNaN<FMT>) return __uint_as_float(0x7FFFFFFFu);
+    if (FMT == MOE_FP4_MX) return __uint_as_float(b == 0 ? 1u << 22 : b << 23);
+    return e4m3_value(b) * unit;
+}
+
 // A warp takes 1024 columns of the rows r, r + 32, r + 64 and r + 96 of a
 // 128-row scale block: their scale bytes share 16 bytes of every tile, loaded
 // once.  A row's eight passes of 128 columns write 8 bytes a lane.
@@ -189,11 +198,7 @@ fp4_dequantize_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__
                 const int cl = i * 256 + lane * 8;
                 const uint32_t b = __shfl_sync(0xffffffffu, words[j], cl / TK) >>
                                        (8 * (cl / Fp4<FMT>::BLOCK % 4)) & 0xFFu;
-                float s;
-                if (FMT == MOE_FP4_MX)
-                    s = b == 0 ? __uint_as_float(1u << 22) : __uint_as_float(b << 23);
-                else
-                    s = e4m3_value(b) * unit;
+                const float s = scale_value<FMT>(b, unit);
                 if (c0 + cl < K)
                     *reinterpret_cast<uint4 *>(dst + c0 + cl) =
                         make_uint4(dequantize2(w[i] & 0xFFu, s), dequantize2(w[i] >> 8 & 0xFFu, s),

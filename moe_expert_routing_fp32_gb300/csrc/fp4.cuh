@@ -29,6 +29,10 @@ struct Fp4 {
 
 constexpr int kScaleTile = 512;   // bytes: 128 rows x 4 blocks
 
+// The scale byte that makes its block NaN.
+template <int FMT>
+constexpr uint32_t kScaleNaN = FMT == MOE_FP4_MX ? 255u : 127u;
+
 // Row block (128 rows) of row `r` of a matrix whose group g starts at `start`.
 __host__ __device__ __forceinline__ int64_t scale_row_block(int g, int start, int r) {
     return static_cast<int64_t>(start / 128) + g + (r - start) / 128;
@@ -74,7 +78,7 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
     return r;
 }
 
-// e4m3 byte of f >= 0 (nearest even, beyond 448 to 448) and back.
+// e4m3 byte of f >= 0 (nearest even, beyond 448 to 448) and back (not of NaN).
 __device__ __forceinline__ uint32_t e4m3_bits(float f) {
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(f));
