@@ -507,10 +507,12 @@ moe_status_t moe_fp4_scales_size(int32_t rows, int32_t K, int32_t G, int32_t for
  *       not below 2^-127;  NV: e4m3(amax / 6 / 2^scale_exp), nearest even, at
  *       most 448.  Elements: nearest e2m1 of value / scale, ties to even,
  *       beyond 6 to 6; zeros where the scale is zero.
+ *   A block that holds an infinity or a NaN gets the NaN scale byte (its codes
+ *       are unspecified).
  *   offsets [G+1]: groups of the rows (fixes the scale layout); NULL with G = 0
  * No row may be named twice.  Rows that no slot names, negative rows and rows
  * past offsets[G] are left untouched; a row >= T*k sets MOE_DEV_BAD_OFFSETS and
- * is left out.  k <= 32, G <= 1024.  x finite.
+ * is left out.  k <= 32, G <= 1024.
  * moe_fp4_dequantize gives the values back: x [n, K] bf16 out, exact (rows
  * past offsets[G] are left untouched).
  */
@@ -530,7 +532,8 @@ moe_status_t moe_fp4_dequantize(const moe_fp4_t *m, int32_t n, int32_t K, const 
  *   swiglu:  act[r, :] = bf16(SiLU(gate) * up), gate = a[r] . w13[g, 0..I-1]^T,
  *            up = a[r] . w13[g, I..2I-1]^T     w13 [G, 2I, K]
  *            act [n, I] bf16, or act4: the same bf16 values quantised as
- *            moe_fp4_quantize does (exactly one of the two, the other NULL);
+ *            moe_fp4_quantize does (exactly one of the two, the other NULL),
+ *            a block with a value beyond bf16's range as NaN;
  *            a's and w13's scale_exp add up to -60..60
  *   mlp:     act = swiglu(expanded_x, w13) in 4 bits, y = matmul(act, w2);
  *            w13 [G, 2I, H], w2 [G, H, I], act [n, I] written

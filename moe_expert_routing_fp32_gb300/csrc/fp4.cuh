@@ -95,9 +95,15 @@ __device__ __forceinline__ float e4m3_value(uint32_t b) {
 //   MX: 2^(floor(log2 amax) - 2), exact; below 2^-125 the byte is 0.
 //   NV: e4m3(amax / 6) in units of 2^scale_exp; a block whose scale rounds to
 //       zero is held as zeros (factor 0).
+// A block with an infinity or a NaN gets the NaN byte: its codes, which know
+// neither, would make them 6 times a finite scale.
 template <int FMT>
 __device__ __forceinline__ uint32_t block_scale(uint32_t amax, float inv_unit, float unit,
                                                 float &factor) {
+    if (amax >= 0x7F80u) {
+        factor = 0.0f;
+        return kScaleNaN<FMT>;
+    }
     if (FMT == MOE_FP4_MX) {
         const int e = static_cast<int>(amax >> 7);
         const uint32_t b = static_cast<uint32_t>(e > 2 ? e - 2 : 0);
