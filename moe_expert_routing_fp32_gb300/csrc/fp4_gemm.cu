@@ -347,9 +347,12 @@ __device__ __forceinline__ float rcp(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-// SiLU(alpha g) / alpha of two gate sums, g / (1 + 2^(c g)) with c = -alpha log2 e:
-// hardware exponential and reciprocal, a few 2^-22 relative, far below the 2^-9
-// that act is rounded by; 1 / inf = 0 where the exponential overflows.
+// SiLU(alpha g) / alpha of two gate sums, g / (1 + 2^(c g)) with c = -alpha log2 e.
+// With G = alpha g, the product c g is rounded before the exponential: for
+// negative gates that is 2.3 |G| 2^-24 of the result (2^-17 at G = -60), beside
+// which the hardware exponential and reciprocal are a few 2^-22; act's own
+// rounding is 2^-9.  Below G = -87.3 the sum passes 2^126, the reciprocal is
+// flushed and the result is zero, |G| 2^-126 at most from the true one.
 __device__ __forceinline__ uint64_t silu2(float x, float y, uint64_t c) {
     const uint64_t g = pair(x, y);
     const float2 t = unpair(mul2(g, c));
