@@ -417,7 +417,8 @@ moe_status_t moe_local_finalize_rerouting(const moe_bf16_t *local_y, const int32
  * S <= 65536, T <= 2^30.  Sums are fp32 in a fixed order: the result is
  * deterministic.
  * Expert ids outside [0, E) set MOE_DEV_BAD_EXPERT_ID and are not counted;
- * bad bounds set MOE_DEV_BAD_OFFSETS.  T may be 0.  Workspace:
+ * bad bounds set MOE_DEV_BAD_OFFSETS and nothing is written then.  T may be 0.
+ * A sequence's sums add T / 4864 + 100 terms in a row at most.  Workspace:
  * moe_balance_loss_workspace_size() bytes, 256-byte aligned; its contents are
  * scratch, every byte a call reads it has written.  Calls that may overlap in
  * time (also as replayed graphs) need one each.
@@ -442,7 +443,8 @@ moe_status_t moe_balance_loss(const float *logits, const int32_t *topk_idx,
  *   d_logits [T, E] fp32 out; a masked token's row is zero, whatever its
  *            logits, indices and d_topk_w hold.
  * Of a slot list that names an expert twice every slot counts; ids outside
- * [0, E) set MOE_DEV_BAD_EXPERT_ID and those slots are left out.
+ * [0, E) set MOE_DEV_BAD_EXPERT_ID and those slots are left out.  Bad bounds
+ * (with a balance term) set MOE_DEV_BAD_OFFSETS and nothing is written then.
  */
 moe_status_t moe_gate_topk_backward(const float *logits, const int32_t *topk_idx,
                                     const float *d_topk_w, const uint8_t *token_mask,

@@ -169,7 +169,9 @@ __device__ __forceinline__ int sequence_at(const int32_t *seq, int S, int lo, in
 
 // Workspace of the forward pass: chunk c of the tokens (`per` of them) meets
 // sequence s in partial c + s, which no other pair has (both only ascend
-// along the tokens), so a partial is written by one CTA and summed in order:
+// along the tokens), so a partial is written by one CTA and summed in order
+// (terms added in a row: a lane's tokens of a chunk, T / 19456 with 8 lanes a
+// token and T / 4864 with 32; then 8 warps, chunks / 32 partials and two trees):
 //   psum [P, E] fp32, pcnt [P, E] int32, pn [P] int32,  P = chunks + S - 1.
 // Pairs without a common token have no partial.
 struct Joint {
