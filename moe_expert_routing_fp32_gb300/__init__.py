@@ -559,7 +559,8 @@ def fp4_quantize(x, fmt="mx", scale_exp=0, row_idx=None, k=1, offsets=None,
     """bf16 rows to 4 bits.  With ``row_idx`` (init_routing's, int32 [T*k]) and
     ``offsets``, token rows go to their k rows in expert order.  A weight
     [G, N, K] keeps its shape in ``q`` and is quantised ungrouped.  Rows that
-    row_idx does not name are not set."""
+    row_idx does not name are not set.  A block that holds an infinity or a NaN
+    becomes NaN."""
     dev = x.device
     xp = _arg(x, torch.bfloat16, dev, None, "x")
     rows = _arg(row_idx, torch.int32, dev, None, "row_idx")
@@ -623,7 +624,7 @@ def fp4_grouped_swiglu(a: Fp4Matrix, offsets, w13: Fp4Matrix, quantize=False, sc
                        out=None, status=None):
     """act = SiLU(gate) * up of the merged w13 [G, 2I, K] -> bf16 [n, I], or
     with ``quantize`` the same values in 4 bits (an Fp4Matrix of a's format,
-    grouped by ``offsets``)."""
+    grouped by ``offsets``; blocks with values beyond bf16's range are NaN)."""
     n, K, G, rows, dev, off = _fp4_product(a, offsets, w13, "fp4_grouped_swiglu")
     if rows % 2:
         raise ValueError("w13 must hold an even number of rows, gate then up")

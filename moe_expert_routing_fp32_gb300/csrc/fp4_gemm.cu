@@ -16,7 +16,8 @@
 // MMAs that use them.
 //
 // What bounds it.  An MMA of 256 x 256 x 64 takes 128 cycles (measured; 10
-// PFLOP/s at 2.07 GHz), and issuing one, or one of the scale copies, takes its
+// PFLOP/s at 2.07 GHz, the rate of the K = 64 form that is used throughout; the
+// chip's published dense 4-bit rate is 13.5), and issuing one, or one of the scale copies, takes its
 // thread some 30 to 40, so a slice of 256 columns (512 cycles of MMAs; 4 of them
 // and 6 to 12 copies) leaves one thread no room for anything else; and tensor
 // memory holds no two 256-column accumulators beside the scales, so with one
@@ -26,16 +27,16 @@
 // The thread of half 0 runs ahead on the staged slices while half 1 waits for an
 // accumulator, from then on stays ahead, and half 0 is drained while half 1
 // still computes.  (One thread with 256-column MMAs on two accumulators that
-// share 64 columns, drained first: 690 us where this takes 658, SwiGLU 131072 x
-// 4096 x 4096.)  What is left, in cycles a tile of K = 4096 with a quarter of the
+// share 64 columns, drained first, against the halves as they then were: 690 us
+// to 658, SwiGLU 131072 x 4096 x 4096.)  What is left, in cycles a tile of K = 4096 with a quarter of the
 // SMs running (so without the power cap): MMAs and hand-overs alone 9,470 (8,192
 // ideal), with the operands' loads 9,930 (they alone 6,870, 83 bytes a cycle), and
 // with the output 11,130: an SM's loads and stores add up.  In long runs on all
 // SMs the power cap takes a fifth of the clock.
 //
 // Measured (one GB300): SwiGLU 131072 x 4096 x 4096 (MX) 650 us, 6.8 PFLOP/s at
-// 2.07 GHz; in a loop 694-720 us, 6.1-6.3 PFLOP/s, at the power cap's 1.68 GHz.
-// 131072 x 2048 x 4096 to fp32 (NV) 545 us, 2.6 GB at 4.8 TB/s: of 8,520 cycles a
+// 2.07 GHz; in a loop 694-735 us, 6.0-6.3 PFLOP/s, at the power cap's 1.68 GHz.
+// 131072 x 2048 x 4096 to fp32 (NV) 545-572 us, 2.6 GB at 4.5-4.8 TB/s: of 8,520 cycles a
 // tile (a quarter of the SMs) the loads alone take 3,420 and with the stores
 // 7,260.  Weights of 41 experts for 64 rows (365 MB) 60 us, 6.1 TB/s.
 #include <cuda.h>

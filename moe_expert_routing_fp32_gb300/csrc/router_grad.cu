@@ -16,8 +16,8 @@
 // 8, 16 or 32 lanes holds a token's row in registers, as few lanes as leave
 // each up to 16 values: a reduction over 8 lanes takes three shuffles for four
 // tokens, one over 32 takes five for one.  Measured at T = 250007, E = 160, nine
-// sequences: partial sums 33 us (160 MB, 4.9 TB/s; 95 instructions a token, the
-// issue slots 60% busy), joining them 7 us, gradient 52 us (320 MB, 6.2 TB/s).
+// sequences: partial sums 33 us (160 MB, 4.9 TB/s; 98 instructions a token, the
+// issue slots 70% busy), joining them 7 us, gradient 52 us (320 MB, 6.2 TB/s).
 #include <cuda_runtime.h>
 
 #include <algorithm>
