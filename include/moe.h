@@ -71,7 +71,7 @@ enum {
     MOE_Y_F32 = 1u << 6,           /* layer: keep the routed expert outputs y_exp in
                                       fp32, the down matmul's accumulator, instead of
                                       rounding them to bf16 (finalize: y_exp is fp32) */
-    MOE_GATHER_A = 1u << 7         /* layer: no permute pass; the routed w13 matmul
+    MOE_GATHER_A = 1u << 7,        /* layer: no permute pass; the routed w13 matmul
                                       reads each expanded row from the (normalised)
                                       input by its source token, and the workspace
                                       holds no expanded_x.  Takes effect only where
@@ -81,6 +81,9 @@ enum {
                                       bit for bit: the rows are copies either way.
                                       Off by default: the in-kernel row copies make
                                       the matmul slower than the permute pass costs. */
+    MOE_DW_F32 = 1u << 8,          /* grouped MLP backward: the weights' gradients in
+                                      fp32 (else bf16) */
+    MOE_DW_ACCUMULATE = 1u << 9    /* ... added to what their buffers hold (fp32 only) */
 };
 
 typedef struct {
@@ -471,6 +474,48 @@ moe_status_t moe_finalize_routing_backward(const void *d_out, const void *y_exp,
                                            int32_t T, int32_t H, int32_t k, uint32_t flags,
                                            void *d_y_exp, float *d_topk_w, int32_t *dev_status,
                                            moe_stream_t stream);
+
+/*
+ * The expert FFN's training passes (the page has no counterpart: it describes
+ * inference).  Group g owns rows [offsets[g], offsets[g+1]), as in
+ * moe_grouped_mlp; a dense block (the shared expert) is one group.
+ *
+ * Forward, keeping what the backward pass needs:
+ *   h [n, 2I] = [gate up] = expanded_x w13[g]^T       (bf16)
+ *   act [n, I], y [n, H]: as moe_grouped_mlp
+ * Backward, with s = sigmoid(gate) of the h that was kept:
+ *   d_act = d_y w2[g],  d_up = d_act gate s,  d_gate = d_act up s (1 + gate (1 - s))
+ *   d_x      [n, H]     = [d_gate d_up] w13[g]         (bf16)
+ *   d_w13    [G, 2I, H] = [d_gate d_up]^T expanded_x   over the group's rows
+ *   d_w2     [G, H, I]  = d_y^T act
+ * Each of the three may be NULL (not computed).  d_gate, d_up and act are
+ * rounded to bf16 before they enter products, which accumulate in fp32.  Below
+ * a gate of -87.3 sigmoid is taken as zero.
+ *   flags MOE_DW_F32         d_w13 and d_w2 are fp32 (else bf16)
+ *         MOE_DW_ACCUMULATE  they are added to what the buffers hold (fp32 only)
+ * Groups without rows have zero gradients.  Rows past offsets[G] are neither
+ * read into a result nor written; rows of other groups, whatever they hold, do
+ * not enter a group's gradients.  Bad offsets set MOE_DEV_BAD_OFFSETS and
+ * nothing is written.  Results do not depend on the launch (no atomics in
+ * unordered sums).  H and I multiples of 128, G <= 1024; no output may overlap an
+ * input or the workspace.  Workspace:
+ * moe_grouped_mlp_backward_workspace_size() bytes, 256-byte aligned (none for
+ * n = 0); its contents are scratch.  Calls that may overlap in time (also as
+ * replayed graphs) need one each.
+ */
+moe_status_t moe_grouped_mlp_train(const moe_bf16_t *expanded_x, const int32_t *offsets, int32_t G,
+                                   const moe_bf16_t *w13, const moe_bf16_t *w2, int32_t n, int32_t H,
+                                   int32_t I, moe_bf16_t *h, moe_bf16_t *act, moe_bf16_t *y,
+                                   int32_t *dev_status, moe_stream_t stream);
+moe_status_t moe_grouped_mlp_backward_workspace_size(int32_t n, int32_t I, int32_t G,
+                                                     size_t *bytes);
+moe_status_t moe_grouped_mlp_backward(const moe_bf16_t *d_y, const moe_bf16_t *expanded_x,
+                                      const int32_t *offsets, int32_t G, const moe_bf16_t *h,
+                                      const moe_bf16_t *w13, const moe_bf16_t *w2, int32_t n,
+                                      int32_t H, int32_t I, uint32_t flags, moe_bf16_t *d_x,
+                                      void *d_w13, void *d_w2, void *workspace,
+                                      size_t workspace_bytes, int32_t *dev_status,
+                                      moe_stream_t stream);
 
 /*
  * Microscaled 4-bit matrices: e2m1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and

@@ -35,7 +35,7 @@ STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED_S
                 3: "MOE_ERR_WORKSPACE_TOO_SMALL", 4: "MOE_ERR_CUDA", 5: "MOE_ERR_NO_DEVICE"}
 DEV_BAD_EXPERT_ID, DEV_TIMEOUT, DEV_BAD_OFFSETS, DEV_UNSORTED = 1, 2, 4, 8
 RENORM, RMSNORM, SHARED, OUT_F32, SHARED_F32, GATE_SEQUENTIAL, Y_F32 = 1, 2, 4, 8, 16, 32, 64
-GATHER_A = 128
+GATHER_A, DW_F32, DW_ACCUMULATE = 128, 256, 512
 
 # every symbol include/moe.h declares
 EXPORTS = ("moe_status_string", "moe_rmsnorm_gate", "moe_rmsnorm_sumsq",
@@ -50,7 +50,8 @@ EXPORTS = ("moe_status_string", "moe_rmsnorm_gate", "moe_rmsnorm_sumsq",
            "moe_balance_loss_workspace_size", "moe_balance_loss", "moe_gate_topk_backward",
            "moe_finalize_routing_backward", "moe_fp4_scales_size", "moe_fp4_quantize",
            "moe_fp4_dequantize", "moe_fp4_grouped_matmul", "moe_fp4_grouped_swiglu",
-           "moe_fp4_grouped_mlp")
+           "moe_fp4_grouped_mlp", "moe_grouped_mlp_train",
+           "moe_grouped_mlp_backward_workspace_size", "moe_grouped_mlp_backward")
 NUM_STAGES = 6
 STAGE_NAMES = ("router", "route_scan_scatter", "permute", "gemm_w13_swiglu", "gemm_down",
                "finalize")
@@ -129,6 +130,10 @@ def lib() -> ctypes.CDLL:
                 "moe_fp4_grouped_matmul": [P, P, I32, P, I32, I32, I32, U32, P, P, P],
                 "moe_fp4_grouped_swiglu": [P, P, I32, P, I32, I32, I32, P, P, P, P],
                 "moe_fp4_grouped_mlp": [P, P, I32, P, P, I32, I32, I32, U32, P, P, P, P],
+                "moe_grouped_mlp_train": [P, P, I32, P, P, I32, I32, I32, P, P, P, P, P],
+                "moe_grouped_mlp_backward_workspace_size": [I32, I32, I32, PSZ],
+                "moe_grouped_mlp_backward": [P, P, P, I32, P, P, P, I32, I32, I32, U32, P, P, P, P,
+                                             SZ, P, P],
             }
             for name, args in sigs.items():
                 fn = getattr(L, name)
@@ -497,6 +502,89 @@ def finalize_routing_backward(d_out, y_exp, row_idx, topk_w, status=None):
         _call("moe_finalize_routing_backward", do, y, rows, w, T, H, k, flags, d_y.data_ptr(),
               d_w.data_ptr(), st, _stream(dev))
     return d_y, d_w
+
+
+# --------------------------------------------------- training the expert FFN
+def _mlp_shapes(x, offsets, w13, w2):
+    """(n, H, I, G, device, the four addresses) of the FFN's operands."""
+    if x.dim() != 2 or w13.dim() != 3 or w2.dim() != 3:
+        raise ValueError("rows [n, H], w13 [G, 2I, H] and w2 [G, H, I]")
+    n, H = x.shape
+    G, _, I = w2.shape
+    dev = x.device
+    xp = _arg(x, torch.bfloat16, dev, None, "expanded_x")
+    off = _arg(offsets, torch.int32, dev, (G + 1,), "offsets")
+    wp = _arg(w13, torch.bfloat16, dev, (G, 2 * I, H), "w13")
+    w2p = _arg(w2, torch.bfloat16, dev, (G, H, I), "w2")
+    return n, H, I, G, dev, (xp, off, wp, w2p)
+
+
+def grouped_mlp_train(expanded_x, offsets, w13, w2, status=None):
+    """The FFN of grouped_mlp, keeping what its backward pass needs.
+    -> (h bf16 [n, 2I] = gate and up sums, y bf16 [n, H]).  Rows past the last
+    group are not set."""
+    n, H, I, G, dev, (xp, off, wp, w2p) = _mlp_shapes(expanded_x, offsets, w13, w2)
+    st = _status_arg(status, dev)
+    with _on(dev):
+        h = torch.empty((n, 2 * I), dtype=torch.bfloat16, device=dev)
+        y = torch.empty((n, H), dtype=torch.bfloat16, device=dev)
+        act = torch.empty((n, I), dtype=torch.bfloat16, device=dev)
+        _call("moe_grouped_mlp_train", xp, off, G, wp, w2p, n, H, I, h.data_ptr(), act.data_ptr(),
+              y.data_ptr(), st, _stream(dev))
+    return h, y
+
+
+@functools.lru_cache(maxsize=256)
+def grouped_mlp_backward_workspace_size(n, I, G) -> int:
+    b = ctypes.c_size_t(0)
+    _call("moe_grouped_mlp_backward_workspace_size", n, I, G, ctypes.byref(b))
+    return b.value
+
+
+def grouped_mlp_backward(d_y, expanded_x, offsets, h, w13, w2, need=("x", "w13", "w2"),
+                         w_f32=False, d_w13=None, d_w2=None, accumulate=False, workspace=None,
+                         status=None):
+    """Gradients of grouped_mlp_train from that of y (bf16 [n, H]) and the h it
+    kept -> (d_x bf16 [n, H], d_w13, d_w2 like the weights, fp32 with ``w_f32``);
+    None for those not in ``need``.  ``d_w13`` and ``d_w2``: buffers to write,
+    or with ``accumulate`` (fp32 only) to add to.  Rows of d_x past the last
+    group are not set.  ``workspace``: uint8, at least
+    grouped_mlp_backward_workspace_size(n, I, G)."""
+    n, H, I, G, dev, (xp, off, wp, w2p) = _mlp_shapes(expanded_x, offsets, w13, w2)
+    dyp = _arg(d_y, torch.bfloat16, dev, (n, H), "d_y")
+    hp = _arg(h, torch.bfloat16, dev, (n, 2 * I), "h")
+    st = _status_arg(status, dev)
+    unknown = set(need) - {"x", "w13", "w2"}
+    if unknown:
+        raise ValueError(f"need: unknown {sorted(unknown)}")
+    dt = torch.float32 if w_f32 else torch.bfloat16
+    p13 = _arg(d_w13, dt, dev, (G, 2 * I, H), "d_w13")
+    p2 = _arg(d_w2, dt, dev, (G, H, I), "d_w2")
+    if accumulate and not (w_f32 and all(b is not None for k, b in (("w13", d_w13), ("w2", d_w2))
+                                         if k in need)):
+        raise ValueError("accumulate adds to given fp32 buffers (w_f32=True, d_w13, d_w2)")
+    wsp = _arg(workspace, torch.uint8, dev, None, "workspace")
+    flags = (DW_F32 if w_f32 else 0) | (DW_ACCUMULATE if accumulate else 0)
+    with _on(dev):
+        d_x = torch.empty((n, H), dtype=torch.bfloat16, device=dev) if "x" in need else None
+        if "w13" not in need:
+            d_w13, p13 = None, None
+        elif d_w13 is None:
+            d_w13 = torch.empty((G, 2 * I, H), dtype=dt, device=dev)
+            p13 = d_w13.data_ptr()
+        if "w2" not in need:
+            d_w2, p2 = None, None
+        elif d_w2 is None:
+            d_w2 = torch.empty((G, H, I), dtype=dt, device=dev)
+            p2 = d_w2.data_ptr()
+        nbytes = grouped_mlp_backward_workspace_size(n, I, G)
+        if workspace is None:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            wsp = workspace.data_ptr()
+        _call("moe_grouped_mlp_backward", dyp, xp, off, G, hp, wp, w2p, n, H, I, flags,
+              d_x.data_ptr() if d_x is not None else None, p13, p2, wsp, workspace.numel(), st,
+              _stream(dev))
+    return d_x, d_w13, d_w2
 
 
 # ------------------------------------------------------------ 4-bit operands

@@ -1,0 +1,1024 @@
+// mlp_train.cu -- the expert FFN's training passes on the tensor cores.
+//
+// For the rows r of group g, [gate up] = x[r] W13[g]^T, act = SiLU(gate) up,
+// y = act W2[g]^T.  With s = sigmoid(gate) the gradients are
+//   d_act = d_y W2[g],  d_up = d_act gate s,  d_gate = d_act up s (1 + gate (1 - s)),
+//   d_x = [d_gate d_up] W13[g],  d_W13[g] = [d_gate d_up]^T x,  d_W2[g] = d_y^T act.
+// Four products, one kernel body each:
+//   FWD   x W13^T, epilogue: h = [gate up] and act, rounded to bf16 once each
+//         (act from the fp32 sums, as the forward pass without gradients has it)
+//   DACT  d_y W2, epilogue: reads h, writes d_h = [d_gate d_up] and act again
+//         (from h: keeping act for the backward pass would cost half of h's
+//         memory more, making it again costs n I stores beside a product)
+//   DX    d_h W13
+//   DW    d_h^T x and d_y^T act over each group's rows, one launch for both
+// d_h and act are operands of the next products, hence bf16; everything is
+// accumulated in fp32 by the MMAs.
+//
+// Operand layouts.  Nothing is transposed in memory: the tensor cores take an
+// operand whose rows run along K (K-major, as x, d_y, d_h in the first three
+// and W13 in FWD) or across it (MN-major: the weights in DACT and DX, both
+// operands of DW).  A K-major slice is 128-byte rows of 64 K values, an MN-major
+// one 128-byte rows of 64 M or N values, one row per K; both in the 128-byte
+// swizzle TMA writes.
+//
+// Ragged groups.  A row tile may read rows of the next group; only the group's
+// own are stored.  In DW the rows are the contraction: what a group's last slice
+// reads past its end has to be zero, so each group has tensor maps of its own
+// whose row count is the group's end, made by DACT's spare warp (tensormap.replace
+// in shared memory), and TMA fills in the zeros.
+//
+// Roles (12 warps): 0 TMA of A, 3 TMA of B, 1 MMA, 2 setup (DACT: the maps),
+// 4-11 epilogue.  Tiles are CG * 128 rows x 256 columns on one CTA or a pair
+// (tcgen05 cta_group::2, half of B in each CTA), two accumulators in turn.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int BN = 256;                     // columns of a tile
+constexpr int MAX_GROUPS = 1024;
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 128 + 32 * EPI_WARPS;
+constexpr int EPI_BYTES = 32 * 64;          // an output box: 32 rows of 64 bytes
+constexpr int SLICE = 128 * 128;            // bytes of 128 rows (K-major) x 64 K
+constexpr int NMAPS = 4;                    // DW's tensor maps of a group
+
+enum { FWD = 0, DACT = 1, DX = 2, DW = 3 };
+
+struct Params {
+    CUtensorMap tmA, tmB;      // operands (DW: none, it takes the groups' maps)
+    CUtensorMap tmO0, tmO1;    // FWD: h, act; DACT: d_h, act; DX: d_x; DW: d_W13, d_W2
+    CUtensorMap tmG[NMAPS];    // DACT: d_h, x, d_y, act, to be cut at each group's end
+    CUtensorMap *maps;         // [G][NMAPS] in the workspace
+    const int32_t *offsets;
+    int32_t G, n;
+    int32_t K;                 // contraction (not DW)
+    int32_t N;                 // FWD, DACT: I; DX: H
+    int32_t nt;                // column tiles of a row block
+    int32_t wrows;             // rows a group's weights would have as an operand like A
+    const uint16_t *h;         // DACT
+    uint16_t *out0, *out1;
+    int32_t ld0, ld1;
+    // DW: product 0 is d_W13 (M = 2I, N = H), 1 is d_W2 (M = H, N = I)
+    int32_t mt0, nt0, mt1, nt1;
+    int32_t H, I;
+    int32_t w_f32, accumulate;
+    int32_t *dev_status;
+};
+
+template <int MODE, int CG>
+struct Cfg {
+    static constexpr int KSUB = CG == 2 ? 2 : 1;       // 64-wide slices of K per stage
+    static constexpr int STAGES = CG == 2 ? 3 : 4;
+    static constexpr int A_STAGE = SLICE * KSUB;
+    static constexpr int B_SLICE = BN / CG * 128;
+    static constexpr int B_STAGE = B_SLICE * KSUB;
+    static constexpr int STAGE = A_STAGE + B_STAGE;
+    static constexpr int BOXES = MODE == DW ? 2 : 1;    // per epilogue warp
+    static constexpr int EPI_OFF = STAGES * STAGE;
+    static constexpr int MAP_OFF = EPI_OFF + EPI_WARPS * BOXES * EPI_BYTES;
+    static constexpr int BAR_OFF = MAP_OFF + (MODE == DACT ? NMAPS * 128 : 0);
+    static constexpr int NBARS = 2 * STAGES + 5;        // full, empty, tfull, tempty, drain
+    static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
+    static constexpr int OFFS_OFF = MISC_OFF + 16;
+    static constexpr int smem(int G) { return 1024 + OFFS_OFF + (MODE == DW ? 0 : (2 * G + 2) * 4); }
+    static constexpr bool A_MN = MODE == DW, B_MN = MODE != FWD;
+    // shared-memory descriptors: the high word is the same for both layouts (1 KB
+    // between groups of eight 128-byte rows, 128-byte swizzle); the low word's
+    // leading offset, between 64-element blocks of M or N, is used by MN-major ones
+    static constexpr uint32_t MN_LO = static_cast<uint32_t>(64 * KSUB * 128 / 16) << 16;
+    static constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | (A_MN ? 1u << 15 : 0u) |
+                                      (B_MN ? 1u << 16 : 0u) |
+                                      (static_cast<uint32_t>(BN >> 3) << 17) |
+                                      (static_cast<uint32_t>(CG * 128 >> 4) << 24);
+    static_assert(smem(MAX_GROUPS) <= 227 * 1024, "shared memory");
+    static_assert(STAGE % 1024 == 0 && MAP_OFF % 128 == 0, "alignment");
+};
+
+// One lane of a converged warp, known to the compiler to be one.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
+// Bounded wait whose first 64 polls read no timer.
+__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                       int32_t *dev_status) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 63u) == 0u) {
+            if (*abort) return false;
+            const uint64_t t = global_timer_ns();
+            if (t0 == 0) t0 = t;
+            if (t - t0 > kWaitLimitNs || it > (1u << 30)) {
+                *abort = 1;
+                report(dev_status, MOE_DEV_TIMEOUT);
+                return false;
+            }
+        }
+    }
+}
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                           int32_t *dev_status) {
+    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort, dev_status);
+}
+
+// Arrive on a barrier of the pair's even CTA once this warp's tensor memory
+// loads have ended.
+__device__ __forceinline__ void arrive_drained(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// D (+)= A B^T with the descriptors' low words a and b.
+template <int CG>
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                    uint32_t accumulate) {
+    constexpr uint32_t HI = 0x40004040u;
+    if (CG == 1)
+        asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+                     "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+                     "setp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+                     "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(HI)
+                     : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+                     "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+                     "setp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+                     "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(HI)
+                     : "memory");
+}
+
+// A tensor map of the whole rows, copied by one warp with its row count set to
+// `rows`: dst (global, 128-byte aligned) by way of `stage` (shared).
+__device__ __forceinline__ void cut_map(CUtensorMap *dst, uint8_t *stage, const CUtensorMap *src,
+                                        int rows, int lane) {
+    const uint32_t s = smem_u32(stage);
+    reinterpret_cast<uint32_t *>(stage)[lane] = reinterpret_cast<const uint32_t *>(src)[lane];
+    __syncwarp();
+    if (lane == 0)
+        asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(s),
+                     "r"(rows)
+                     : "memory");
+    __syncwarp();
+    asm volatile("tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync"
+                 ".aligned [%0], [%1], 128;" ::"l"(reinterpret_cast<uint64_t>(dst)),
+                 "r"(s)
+                 : "memory");
+}
+__device__ __forceinline__ void acquire_map(const CUtensorMap *m) {
+    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(
+                     reinterpret_cast<uint64_t>(m))
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_store_3d(const void *tmap, const void *src, int c0, int c1,
+                                             int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+            reinterpret_cast<uint64_t>(tmap)),
+        "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(src))
+        : "memory");
+}
+__device__ __forceinline__ void tma_add_3d(const void *tmap, const void *src, int c0, int c1,
+                                           int c2) {
+    asm volatile(
+        "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], "
+        "[%4];" ::"l"(reinterpret_cast<uint64_t>(tmap)),
+        "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(src))
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+struct Tile {
+    int g;
+    int row0, row_end;     // row modes: rows of the tile; DW: rows of the group (the contraction)
+    int n_blk;             // row modes: column tile
+    int prod, m0, n0;      // DW
+};
+
+// Row modes: the group offsets and the tiles of the groups before each;
+// returns the number of tiles, -1 for bad offsets.  All threads.
+template <int BMT>
+__device__ int list_tiles(const Params &p, int *s_off, int *s_prefix, volatile int *s_bad) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    for (int g = tid; g <= p.G; g += THREADS) s_off[g] = p.offsets[g];
+    if (tid == 0) *s_bad = 0;
+    __syncthreads();
+    if (tid < 32) {
+        int run = 0;
+        bool bad = false;
+        for (int g0 = 0; g0 < p.G; g0 += 32) {
+            const int g = g0 + lane;
+            int tiles = 0;
+            if (g < p.G) {
+                const int a = s_off[g], b = s_off[g + 1];
+                if (a < 0 || b < a || b > p.n) bad = true;
+                tiles = b > a ? ((b - a + BMT - 1) / BMT) * p.nt : 0;
+            }
+            int inc = tiles;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, inc, off);
+                if (lane >= off) inc += o;
+            }
+            if (g < p.G) s_prefix[g] = run + inc - tiles;
+            run += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        if (lane == 0) s_prefix[p.G] = run;
+        if (__any_sync(0xffffffffu, bad) && lane == 0) *s_bad = 1;
+    }
+    __syncthreads();
+    return *s_bad ? -1 : s_prefix[p.G];
+}
+
+// Tiles of a group: rows fastest while the group has fewer rows than its
+// weights, columns fastest otherwise (what is shared is read from L2).  DW: the
+// rows of the gradient fastest, both products of a group one after the other.
+template <int MODE, int BMT>
+__device__ __forceinline__ Tile decode_tile(const Params &p, int tile, int &g, const int *s_off,
+                                            const int *s_prefix) {
+    Tile t;
+    if (MODE == DW) {
+        const int t0 = p.mt0 * p.nt0, per = t0 + p.mt1 * p.nt1;
+        t.g = tile / per;
+        int local = tile - t.g * per;
+        t.prod = local >= t0;
+        if (t.prod) local -= t0;
+        const int mt = t.prod ? p.mt1 : p.mt0;
+        const int n = local / mt;
+        t.m0 = (local - n * mt) * 256;
+        t.n0 = n * BN;
+        t.row0 = __ldg(p.offsets + t.g);
+        t.row_end = __ldg(p.offsets + t.g + 1);
+        t.n_blk = 0;
+    } else {
+        while (s_prefix[g + 1] <= tile) ++g;
+        const int start = s_off[g], end = s_off[g + 1], cnt = end - start;
+        const int local = tile - s_prefix[g];
+        const bool nfast = cnt > p.wrows;
+        const int inner = nfast ? p.nt : (cnt + BMT - 1) / BMT;
+        const int hi = static_cast<int>(static_cast<unsigned>(local) / static_cast<unsigned>(inner));
+        const int lo = local - hi * inner;
+        t.g = g;
+        t.n_blk = nfast ? lo : hi;
+        t.row0 = start + (nfast ? hi : lo) * BMT;
+        t.row_end = end;
+        t.prod = t.m0 = t.n0 = 0;
+    }
+    return t;
+}
+
+// 64 bytes of each of a warp's 32 rows (lane i: row row0 + i) into a box in the
+// 64-byte swizzle of the output maps; the caller stores it.
+template <int BOXES>
+__device__ __forceinline__ uint8_t *fill_box(uint8_t *boxes, int &b, int lane,
+                                             const uint32_t (&w)[16]) {
+    uint8_t *box = boxes + b * EPI_BYTES;
+    if (BOXES == 2) b ^= 1;
+    if (lane == 0) bulk_wait_read<BOXES - 1>();     // the store that last used it has read it
+    __syncwarp();
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch)
+        *reinterpret_cast<uint4 *>(box + lane * 64 + ((ch ^ ((lane >> 1) & 3)) << 4)) =
+            make_uint4(w[4 * ch], w[4 * ch + 1], w[4 * ch + 2], w[4 * ch + 3]);
+    fence_proxy_async();
+    __syncwarp();
+    return box;
+}
+
+// 32 bf16 columns of a warp's rows: through a box where all 32 rows belong to
+// the group, else each lane its own row.
+__device__ __forceinline__ void emit_rows(uint8_t *boxes, int &b, int lane, bool boxed, bool ok,
+                                          const uint32_t (&w)[16], const CUtensorMap *map,
+                                          uint16_t *out, int ld, int row0, int col) {
+    if (boxed) {
+        const uint8_t *box = fill_box<1>(boxes, b, lane, w);
+        if (lane == 0) {
+            tma_store_2d(map, box, col, row0);
+            bulk_commit();
+        }
+    } else if (ok) {
+        uint4 *dst = reinterpret_cast<uint4 *>(out + static_cast<int64_t>(row0 + lane) * ld + col);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    }
+}
+
+template <int MODE, int CG>
+__device__ __forceinline__ void train_gemm(const Params &p) {
+    using C = Cfg<MODE, CG>;
+    constexpr int STAGES = C::STAGES, KSUB = C::KSUB, BK = 64 * KSUB;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    // a pair's MMAs are issued by its even CTA: full, tempty are used there
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);
+    uint64_t *empty = full + STAGES;
+    uint64_t *tfull = empty + STAGES;       // [2]
+    uint64_t *tempty = tfull + 2;           // [2]
+    uint64_t *drain = tempty + 2;
+    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF);
+    volatile int *s_abort = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 4);
+    volatile int *s_bad = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 8);
+    int *s_off = reinterpret_cast<int *>(smem + C::OFFS_OFF);
+    int *s_prefix = s_off + p.G + 1;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = CG == 2 ? static_cast<int>(cluster_ctarank()) : 0;
+    const bool leader = rank == 0;
+    const int first_tile = static_cast<int>(blockIdx.x) / CG;
+    const int step = static_cast<int>(gridDim.x) / CG;
+
+    if (warp == 1) {
+        if (CG == 1) {
+            tmem_alloc(s_tmem, 512);
+            tmem_relinquish();
+        } else {
+            tmem_alloc_pair(s_tmem, 512);
+            tmem_relinquish_pair();
+        }
+    } else if (warp == 2 && elect_one()) {
+        *s_abort = 0;
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 2);          // each producer arms its share
+            mbar_init(&empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], CG * EPI_WARPS);
+        }
+        mbar_init(drain, 1);
+        fence_barrier_init();
+    } else if (warp == 3 && MODE != DW && elect_one()) {
+        tma_prefetch_desc(&p.tmA);
+        tma_prefetch_desc(&p.tmB);
+    }
+    // Up to here nothing but shared and tensor memory is touched: launched as a
+    // programmatic dependent, this part runs while the stream's last kernel ends.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    int total;
+    if (MODE == DW) {
+        int bad = 0;
+        for (int g = tid; g < p.G; g += THREADS) {
+            const int a = p.offsets[g], b = p.offsets[g + 1];
+            bad |= a < 0 || b < a || b > p.n;
+        }
+        total = __syncthreads_or(bad) ? -1 : p.G * (p.mt0 * p.nt0 + p.mt1 * p.nt1);
+    } else {
+        total = list_tiles<128 * CG>(p, s_off, s_prefix, s_bad);
+    }
+    if (total < 0) {                         // both CTAs of a pair read the same offsets
+        if (tid == 0 && blockIdx.x == 0) report(p.dev_status, MOE_DEV_BAD_OFFSETS);
+        total = 0;
+    } else if (MODE == DACT && warp == 2) {
+        // the groups' maps of the weight gradients' operands
+        for (int g = blockIdx.x; g < p.G; g += gridDim.x) {
+            if (s_off[g + 1] == s_off[g]) continue;          // never loaded
+#pragma unroll
+            for (int m = 0; m < NMAPS; ++m)
+                cut_map(p.maps + g * NMAPS + m, smem + C::MAP_OFF + m * 128, &p.tmG[m],
+                        s_off[g + 1], lane);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (CG == 2) cluster_sync_all();         // barriers and TMEM of both CTAs are ready
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    const uint32_t lead_full = mapa_shared(smem_u32(full), 0);
+    const uint32_t lead_tempty = mapa_shared(smem_u32(tempty), 0);
+    auto kblocks = [&](const Tile &t) {
+        return MODE == DW ? (t.row_end - t.row0 + BK - 1) / BK : (p.K + BK - 1) / BK;
+    };
+
+    if (warp == 0 || warp == 3) {
+        // ================= TMA producers: warp 0 A, warp 3 B
+        if (elect_one()) {
+            const bool is_a = warp == 0;
+            int stage = 0;
+            uint32_t phase = 0;
+            int armed[STAGES];
+            for (int s = 0; s < STAGES; ++s) armed[s] = -1;
+            auto load2 = [&](void *dst, const CUtensorMap *m, int s, int c0, int c1) {
+                if (CG == 1)
+                    tma_load_2d(dst, m, &full[s], c0, c1);
+                else
+                    tma_load_2d_pair(dst, m, lead_full + 8u * static_cast<uint32_t>(s), c0, c1);
+            };
+            auto load3 = [&](void *dst, const CUtensorMap *m, int s, int c0, int c1, int c2) {
+                if (CG == 1)
+                    tma_load_3d(dst, m, &full[s], c0, c1, c2);
+                else
+                    tma_load_3d_pair(dst, m, lead_full + 8u * static_cast<uint32_t>(s), c0, c1, c2);
+            };
+            int g = 0;
+            for (int tile = first_tile; tile < total && !*s_abort; tile += step) {
+                const Tile t = decode_tile<MODE, 128 * CG>(p, tile, g, s_off, s_prefix);
+                const CUtensorMap *m = is_a ? &p.tmA : &p.tmB;
+                const int nkb = kblocks(t);
+                if (MODE == DW && nkb > 0) {
+                    m = p.maps + t.g * NMAPS + 2 * t.prod + (is_a ? 0 : 1);
+                    acquire_map(m);
+                }
+                bool ok = true;
+                for (int kb = 0; kb < nkb; ++kb) {
+                    if (!wait_phase(&empty[stage], phase ^ 1, s_abort, p.dev_status)) {
+                        ok = false;
+                        break;
+                    }
+                    armed[stage] = static_cast<int>(phase);
+                    uint8_t *dst = smem + stage * C::STAGE + (is_a ? 0 : C::A_STAGE);
+                    if (leader)
+                        mbar_arrive_expect_tx(&full[stage], CG * (is_a ? C::A_STAGE : C::B_STAGE));
+                    const int k0 = kb * BK;
+                    if (MODE == DW) {
+                        const int c = (is_a ? t.m0 : t.n0) + 128 * rank;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            load2(dst + j * (64 * BK * 2), m, stage, c + 64 * j, t.row0 + k0);
+                    } else if (is_a) {
+#pragma unroll
+                        for (int s = 0; s < KSUB; ++s)
+                            load2(dst + s * SLICE, m, stage, k0 + 64 * s, t.row0 + 128 * rank);
+                    } else if (MODE == FWD) {
+                        // gate rows, then the same of up: one half per CTA of a pair
+#pragma unroll
+                        for (int s = 0; s < KSUB; ++s)
+#pragma unroll
+                            for (int j = 0; j < 2 / CG; ++j)
+                                load3(dst + s * C::B_SLICE + j * SLICE, m, stage, k0 + 64 * s,
+                                      (j + rank) * p.N + t.n_blk * 128, t.g);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4 / CG; ++j)
+                            load3(dst + j * (64 * BK * 2), m, stage,
+                                  t.n_blk * BN + BN / CG * rank + 64 * j, k0, t.g);
+                    }
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (!ok) break;
+            }
+            if (*s_abort && leader) {
+                for (int s = 0; s < STAGES; ++s)
+                    if (armed[s] >= 0) mbar_wait_drain(&full[s], static_cast<uint32_t>(armed[s]));
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ================= MMA issuer (even CTA only)
+        if (leader && elect_one()) {
+            int stage = 0;
+            uint32_t phase = 0, u = 0;              // u: tile count, accumulator u & 1
+            const uint32_t base = smem_u32(smem) >> 4;
+            bool issued = false;
+            int g = 0;
+            for (int tile = first_tile; tile < total && !*s_abort; tile += step) {
+                const Tile t = decode_tile<MODE, 128 * CG>(p, tile, g, s_off, s_prefix);
+                const int nkb = kblocks(t);
+                // DW: the 16-row steps of the last slice that hold rows of the group
+                const int last =
+                    MODE == DW ? (t.row_end - t.row0 - (nkb - 1) * BK + 15) / 16 : BK / 16;
+                if (!wait_phase(&tempty[u & 1], ((u >> 1) & 1) ^ 1, s_abort, p.dev_status)) break;
+                tc_fence_after();
+                const uint32_t d = tmem + (u & 1) * BN;
+                bool ok = true;
+                for (int kb = 0; kb < nkb; ++kb) {
+                    if (!wait_phase(&full[stage], phase, s_abort, p.dev_status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t at = base + static_cast<uint32_t>(stage) * (C::STAGE / 16);
+                    const uint32_t a = at + (C::A_MN ? C::MN_LO : 1u << 16);
+                    const uint32_t b = at + C::A_STAGE / 16 + (C::B_MN ? C::MN_LO : 1u << 16);
+                    const int steps = kb + 1 < nkb ? BK / 16 : last;
+#pragma unroll
+                    for (int s = 0; s < BK / 16; ++s) {
+                        if (MODE == DW && s >= steps) break;
+                        // 16 K further: 32 bytes of each row, or 16 rows of 128 bytes
+                        const uint32_t ka = C::A_MN ? s * 128 : s / 4 * (SLICE / 16) + s % 4 * 2;
+                        const uint32_t kbb =
+                            C::B_MN ? s * 128 : s / 4 * (C::B_SLICE / 16) + s % 4 * 2;
+                        mma<CG>(d, a + ka, b + kbb, C::IDESC, (kb | s) != 0 ? 1u : 0u);
+                    }
+                    issued = true;
+                    if (CG == 1)
+                        tc_commit(&empty[stage]);
+                    else
+                        tc_commit_pair_mc(&empty[stage], 0x3);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (!ok) break;
+                if (CG == 1)
+                    tc_commit(&tfull[u & 1]);
+                else
+                    tc_commit_pair_mc(&tfull[u & 1], 0x3);
+                ++u;
+            }
+            if (*s_abort && issued) {
+                // unwinding: every MMA issued so far ends before TMEM is freed
+                if (CG == 1)
+                    tc_commit(drain);
+                else
+                    tc_commit_pair_mc(drain, 0x1);
+                mbar_wait_drain(drain, 0);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ================= epilogue: two warps share a TMEM lane quarter
+        const int quarter = warp & 3, part = (warp - 4) >> 2;
+        uint8_t *boxes = smem + C::EPI_OFF + (warp - 4) * C::BOXES * EPI_BYTES;
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        int bx = 0, g = 0;
+        uint32_t u = 0;
+        for (int tile = first_tile; tile < total; tile += step) {
+            const Tile t = decode_tile<MODE, 128 * CG>(p, tile, g, s_off, s_prefix);
+            const int row0 = (MODE == DW ? t.m0 : t.row0) + 128 * rank + quarter * 32;
+            const bool ok = row0 + lane < t.row_end;
+            const bool boxed = row0 + 32 <= t.row_end;
+            const uint32_t acc = tmem + lanes + (u & 1) * BN;
+            if (!wait_phase(&tfull[u & 1], (u >> 1) & 1, s_abort, p.dev_status)) break;
+            tc_fence_after();
+            if (MODE == FWD) {
+                // columns [0, 128) gate, [128, 256) up; this warp 64 of each
+#pragma unroll 1
+                for (int c = 64 * part; c < 64 * part + 64; c += 32) {
+                    float x[32], y[32];
+                    __syncwarp();
+                    tmem_ld32(acc + c, x);
+                    tmem_ld32(acc + 128 + c, y);
+                    tmem_ld_wait();
+                    const int col = t.n_blk * 128 + c;
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) w[i] = bf16x2(x[2 * i], x[2 * i + 1]);
+                    emit_rows(boxes, bx, lane, boxed, ok, w, &p.tmO0, p.out0, p.ld0, row0, col);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) w[i] = bf16x2(y[2 * i], y[2 * i + 1]);
+                    emit_rows(boxes, bx, lane, boxed, ok, w, &p.tmO0, p.out0, p.ld0, row0,
+                              p.N + col);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float a[2];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const float v = x[2 * i + j];
+                            a[j] = __fdividef(v, 1.0f + __expf(-v)) * y[2 * i + j];
+                        }
+                        w[i] = bf16x2(a[0], a[1]);
+                    }
+                    emit_rows(boxes, bx, lane, boxed, ok, w, &p.tmO1, p.out1, p.ld1, row0, col);
+                }
+            } else if (MODE == DACT) {
+#pragma unroll 1
+                for (int c = 128 * part; c < 128 * part + 128; c += 32) {
+                    const int col = t.n_blk * BN + c;
+                    if (col >= p.N) break;               // N = 128 mod 256: no such columns
+                    uint4 hq[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) hq[j] = make_uint4(0u, 0u, 0u, 0u);
+                    if (ok) {
+                        const uint16_t *src =
+                            p.h + static_cast<int64_t>(row0 + lane) * (2 * p.N) + col;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            hq[j] = __ldg(reinterpret_cast<const uint4 *>(src) + j);
+                            hq[4 + j] = __ldg(reinterpret_cast<const uint4 *>(src + p.N) + j);
+                        }
+                    }
+                    const uint32_t *hg = reinterpret_cast<const uint32_t *>(hq), *hu = hg + 16;
+                    float d[32];
+                    __syncwarp();
+                    tmem_ld32(acc + c, d);
+                    tmem_ld_wait();
+                    uint32_t wg[16], wu[16], wa[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float vg[2], vu[2], va[2];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const float gt = __uint_as_float(j ? hg[i] & 0xFFFF0000u : hg[i] << 16);
+                            const float up = __uint_as_float(j ? hu[i] & 0xFFFF0000u : hu[i] << 16);
+                            const float s = __fdividef(1.0f, 1.0f + __expf(-gt));
+                            const float gs = gt * s;                    // SiLU(gate)
+                            va[j] = gs * up;
+                            vu[j] = d[2 * i + j] * gs;
+                            // s (1 + gate (1 - s)) = s + gs (1 - s)
+                            vg[j] = d[2 * i + j] * up * (s + gs * (1.0f - s));
+                        }
+                        wg[i] = bf16x2(vg[0], vg[1]);
+                        wu[i] = bf16x2(vu[0], vu[1]);
+                        wa[i] = bf16x2(va[0], va[1]);
+                    }
+                    emit_rows(boxes, bx, lane, boxed, ok, wg, &p.tmO0, p.out0, p.ld0, row0, col);
+                    emit_rows(boxes, bx, lane, boxed, ok, wu, &p.tmO0, p.out0, p.ld0, row0,
+                              p.N + col);
+                    emit_rows(boxes, bx, lane, boxed, ok, wa, &p.tmO1, p.out1, p.ld1, row0, col);
+                }
+            } else if (MODE == DX) {
+#pragma unroll 1
+                for (int c = 128 * part; c < 128 * part + 128; c += 32) {
+                    const int col = t.n_blk * BN + c;
+                    if (col >= p.N) break;
+                    float v[32];
+                    __syncwarp();
+                    tmem_ld32(acc + c, v);
+                    tmem_ld_wait();
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) w[i] = bf16x2(v[2 * i], v[2 * i + 1]);
+                    emit_rows(boxes, bx, lane, boxed, ok, w, &p.tmO0, p.out0, p.ld0, row0, col);
+                }
+            } else {
+                const CUtensorMap *om = t.prod ? &p.tmO1 : &p.tmO0;
+                const bool none = t.row_end == t.row0;      // an idle expert: zeros
+                // sizes of 128 mod 256: a tile's second half may be off the gradient
+                const int M = t.prod ? p.H : 2 * p.I, N = t.prod ? p.I : p.H;
+#pragma unroll 1
+                for (int c = 128 * part; c < 128 * part + 128; c += 32) {
+                    if (row0 >= M || t.n0 + c >= N) break;
+                    float v[32];
+                    if (none) {
+                        if (p.accumulate) break;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+                    } else {
+                        __syncwarp();
+                        tmem_ld32(acc + c, v);
+                        tmem_ld_wait();
+                    }
+                    const int col = t.n0 + c;
+                    uint32_t w[16];
+                    if (p.w_f32) {
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[16 * hf + i]);
+                            const uint8_t *box = fill_box<2>(boxes, bx, lane, w);
+                            if (lane == 0) {
+                                if (p.accumulate)
+                                    tma_add_3d(om, box, col + 16 * hf, row0, t.g);
+                                else
+                                    tma_store_3d(om, box, col + 16 * hf, row0, t.g);
+                                bulk_commit();
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) w[i] = bf16x2(v[2 * i], v[2 * i + 1]);
+                        const uint8_t *box = fill_box<2>(boxes, bx, lane, w);
+                        if (lane == 0) {
+                            tma_store_3d(om, box, col, row0, t.g);
+                            bulk_commit();
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_drained(lead_tempty + 8u * (u & 1));
+            ++u;
+        }
+        if (lane == 0) bulk_wait<0>();       // every output box written
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (CG == 2) cluster_sync_all();     // no CTA leaves while its peer may still signal or read it
+    if (warp == 1) {
+        tc_fence_after();
+        if (CG == 1)
+            tmem_dealloc(tmem, 512);
+        else
+            tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(THREADS, 1) train_gemm_kernel(const __grid_constant__ Params p) {
+    train_gemm<MODE, 1>(p);
+}
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    train_gemm_pair_kernel(const __grid_constant__ Params p) {
+    train_gemm<MODE, 2>(p);
+}
+
+// ------------------------------------------------------------------ host side
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static std::once_flag once;
+    static EncodeTiledFn fn = nullptr;
+    std::call_once(once, [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
+                                             cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(ptr);
+    });
+    return fn;
+}
+
+// bf16 [groups][rows][cols] as boxes of 64 columns x box_rows rows, 128-byte
+// swizzle: K-major operands (columns are K) and MN-major ones (rows are K).
+bool operand_map(CUtensorMap *m, const void *ptr, int groups, int64_t rows, int64_t cols,
+                 int box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dim[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                         static_cast<cuuint64_t>(std::max(groups, 1))};
+    cuuint64_t stride[2] = {dim[0] * 2, dim[0] * dim[1] * 2};
+    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1}, es[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, groups > 0 ? 3 : 2, const_cast<void *>(ptr), dim,
+              stride, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Output [groups][rows][cols] as 32-row x 64-byte boxes, 64-byte swizzle.
+bool out_map(CUtensorMap *m, void *ptr, int groups, int64_t rows, int64_t cols, bool f32) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t esz = f32 ? 4 : 2;
+    cuuint64_t dim[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                         static_cast<cuuint64_t>(std::max(groups, 1))};
+    cuuint64_t stride[2] = {dim[0] * esz, dim[0] * dim[1] * esz};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(64 / esz), 32, 1}, es[3] = {1, 1, 1};
+    return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+              groups > 0 ? 3 : 2, ptr, dim, stride, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Row products: pairs where groups have more than one 128-row block on average.
+bool use_pair(int n, int G) { return n > 128ll * G; }
+
+template <int MODE, int CG>
+cudaError_t launch(const Params &p, int64_t tiles, cudaStream_t stream) {
+    using C = Cfg<MODE, CG>;
+    void (*kernel)(const Params);
+    if constexpr (CG == 2)
+        kernel = train_gemm_pair_kernel<MODE>;
+    else
+        kernel = train_gemm_kernel<MODE>;
+    static std::mutex mu;
+    static int resident[64] = {};        // CTAs or pairs that can run at once, by device
+    int dev = 0;
+    cudaGetDevice(&dev);
+    int limit = num_sms() / CG;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (dev >= 64 || resident[dev] == 0) {
+            const cudaError_t e = cudaFuncSetAttribute(
+                kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(MAX_GROUPS));
+            if (e != cudaSuccess) return e;
+            if (CG == 2) {
+                cudaLaunchConfig_t cfg = {};
+                cfg.gridDim = dim3(static_cast<unsigned>(num_sms()), 1, 1);
+                cfg.blockDim = dim3(THREADS, 1, 1);
+                cfg.dynamicSmemBytes = C::smem(MAX_GROUPS);
+                cfg.stream = stream;
+                int n = 0;
+                if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
+                    cudaGetLastError();
+                    n = limit;
+                }
+                limit = std::min(n, limit);
+            }
+            if (dev < 64) resident[dev] = limit;
+        } else {
+            limit = resident[dev];
+        }
+    }
+    const int64_t units = std::max<int64_t>(1, std::min<int64_t>(limit, tiles));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(CG * units), 1, 1);
+    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(C::smem(p.G));
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <int MODE>
+cudaError_t launch_rows(Params &p, cudaStream_t stream) {
+    const bool pair = use_pair(p.n, p.G);
+    const int bm = pair ? 256 : 128;
+    const int64_t tiles = (static_cast<int64_t>(p.n / bm) + std::min(p.G, p.n)) * p.nt;
+    return pair ? launch<MODE, 2>(p, tiles, stream) : launch<MODE, 1>(p, tiles, stream);
+}
+
+inline bool a16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+struct BwdWs {
+    size_t d_h, act, maps, total;
+};
+BwdWs bwd_layout(int n, int I, int G) {
+    BwdWs w;
+    auto up = [](size_t v) { return (v + 255) & ~static_cast<size_t>(255); };
+    w.d_h = 0;
+    w.act = up(static_cast<size_t>(n) * 2 * I * 2);
+    w.maps = w.act + up(static_cast<size_t>(n) * I * 2);
+    w.total = w.maps + up(static_cast<size_t>(G) * NMAPS * sizeof(CUtensorMap));
+    return w;
+}
+
+moe_status_t check_sizes(int32_t G, int32_t n, int32_t H, int32_t I) {
+    if (G <= 0 || n < 0 || H <= 0 || I <= 0) return MOE_ERR_INVALID_ARG;
+    if (G > MAX_GROUPS || H % 128 != 0 || I % 128 != 0 || H > (1 << 20) || I > (1 << 19) ||
+        n > INT32_MAX - 1024)
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    // tile numbers are 32-bit
+    const int64_t w = std::max(2 * static_cast<int64_t>(I), static_cast<int64_t>(H)) / 128;
+    const int64_t row_tiles = (n / 128 + static_cast<int64_t>(G)) * w;
+    const int64_t w_tiles = static_cast<int64_t>(G) * 2 * ceil_div(2 * static_cast<int64_t>(I), 256) *
+                            ceil_div(H, 256);
+    if (row_tiles >= (int64_t{1} << 31) || w_tiles >= (int64_t{1} << 31))
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+#define TRY_CUDA(x)                                     \
+    do {                                                \
+        if ((x) != cudaSuccess) return MOE_ERR_CUDA;    \
+    } while (0)
+
+extern "C" moe_status_t moe_grouped_mlp_train(const moe_bf16_t *expanded_x, const int32_t *offsets,
+                                              int32_t G, const moe_bf16_t *w13, const moe_bf16_t *w2,
+                                              int32_t n, int32_t H, int32_t I, moe_bf16_t *h,
+                                              moe_bf16_t *act, moe_bf16_t *y, int32_t *dev_status,
+                                              moe_stream_t stream) {
+    const moe_status_t st = check_sizes(G, n, H, I);
+    if (st != MOE_OK) return st;
+    if (!offsets || !w13 || !w2) return MOE_ERR_INVALID_ARG;
+    if (n == 0) return MOE_OK;
+    if (!expanded_x || !h || !act || !y) return MOE_ERR_INVALID_ARG;
+    if (!a16(expanded_x) || !a16(w13) || !a16(w2) || !a16(h) || !a16(act) || !a16(y))
+        return MOE_ERR_INVALID_ARG;
+    if (!current_device_ok()) return MOE_ERR_NO_DEVICE;
+    if (!encode_fn()) return MOE_ERR_CUDA;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    Params p{};
+    if (!operand_map(&p.tmA, expanded_x, 0, n, H, 128) ||
+        !operand_map(&p.tmB, w13, G, 2 * static_cast<int64_t>(I), H, 128) ||
+        !out_map(&p.tmO0, h, 0, n, 2 * static_cast<int64_t>(I), false) ||
+        !out_map(&p.tmO1, act, 0, n, I, false))
+        return MOE_ERR_CUDA;
+    p.offsets = offsets;
+    p.G = G;
+    p.n = n;
+    p.K = H;
+    p.N = I;
+    p.nt = I / 128;
+    p.wrows = 2 * I;
+    p.out0 = h;
+    p.ld0 = 2 * I;
+    p.out1 = act;
+    p.ld1 = I;
+    p.dev_status = dev_status;
+    TRY_CUDA(launch_rows<FWD>(p, s));
+    const GemmSegment1 none{};
+    TRY_CUDA(launch_gemm_store(act, offsets, G, n, I, w2, H, y, none, dev_status, s));
+    return MOE_OK;
+}
+
+extern "C" moe_status_t moe_grouped_mlp_backward_workspace_size(int32_t n, int32_t I, int32_t G,
+                                                                size_t *bytes) {
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    const moe_status_t st = check_sizes(G, n, 128, I);
+    if (st != MOE_OK) return st;
+    *bytes = bwd_layout(n, I, G).total;
+    return MOE_OK;
+}
+
+extern "C" moe_status_t moe_grouped_mlp_backward(
+    const moe_bf16_t *d_y, const moe_bf16_t *expanded_x, const int32_t *offsets, int32_t G,
+    const moe_bf16_t *h, const moe_bf16_t *w13, const moe_bf16_t *w2, int32_t n, int32_t H,
+    int32_t I, uint32_t flags, moe_bf16_t *d_x, void *d_w13, void *d_w2, void *workspace,
+    size_t workspace_bytes, int32_t *dev_status, moe_stream_t stream) {
+    const moe_status_t st = check_sizes(G, n, H, I);
+    if (st != MOE_OK) return st;
+    const bool f32 = (flags & MOE_DW_F32) != 0, add = (flags & MOE_DW_ACCUMULATE) != 0;
+    if (add && !f32) return MOE_ERR_INVALID_ARG;
+    if (!offsets || !w13 || !w2) return MOE_ERR_INVALID_ARG;
+    if ((d_x && !a16(d_x)) || (d_w13 && !a16(d_w13)) || (d_w2 && !a16(d_w2)))
+        return MOE_ERR_INVALID_ARG;
+    if (!d_x && !d_w13 && !d_w2) return MOE_OK;
+    if (n > 0) {
+        if (!d_y || !expanded_x || !h) return MOE_ERR_INVALID_ARG;
+        if (!a16(d_y) || !a16(expanded_x) || !a16(h) || !a16(w13) || !a16(w2))
+            return MOE_ERR_INVALID_ARG;
+        if (!workspace || workspace_bytes < bwd_layout(n, I, G).total ||
+            (reinterpret_cast<uintptr_t>(workspace) & 255))
+            return MOE_ERR_WORKSPACE_TOO_SMALL;
+    }
+    if (!current_device_ok()) return MOE_ERR_NO_DEVICE;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int64_t I2 = 2 * static_cast<int64_t>(I);
+    if (n == 0) {
+        const size_t bytes = static_cast<size_t>(G) * I * H * (f32 ? 4 : 2);
+        if (!add && d_w13) TRY_CUDA(cudaMemsetAsync(d_w13, 0, 2 * bytes, s));
+        if (!add && d_w2) TRY_CUDA(cudaMemsetAsync(d_w2, 0, bytes, s));
+        return MOE_OK;
+    }
+    if (!encode_fn()) return MOE_ERR_CUDA;
+    const BwdWs L = bwd_layout(n, I, G);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    uint16_t *d_h = reinterpret_cast<uint16_t *>(ws + L.d_h);
+    uint16_t *act = reinterpret_cast<uint16_t *>(ws + L.act);
+    const int box_k = use_pair(n, G) ? 128 : 64;     // K rows of an MN-major box: a stage's
+
+    Params p{};
+    p.offsets = offsets;
+    p.G = G;
+    p.n = n;
+    p.dev_status = dev_status;
+    p.maps = reinterpret_cast<CUtensorMap *>(ws + L.maps);
+    // d_act and what follows from it
+    if (!operand_map(&p.tmA, d_y, 0, n, H, 128) || !operand_map(&p.tmB, w2, G, H, I, box_k) ||
+        !out_map(&p.tmO0, d_h, 0, n, I2, false) || !out_map(&p.tmO1, act, 0, n, I, false) ||
+        !operand_map(&p.tmG[0], d_h, 0, n, I2, 128) ||
+        !operand_map(&p.tmG[1], expanded_x, 0, n, H, 128) ||
+        !operand_map(&p.tmG[2], d_y, 0, n, H, 128) || !operand_map(&p.tmG[3], act, 0, n, I, 128))
+        return MOE_ERR_CUDA;
+    p.K = H;
+    p.N = I;
+    p.nt = static_cast<int>(ceil_div(I, BN));
+    p.wrows = I;
+    p.h = h;
+    p.out0 = d_h;
+    p.ld0 = 2 * I;
+    p.out1 = act;
+    p.ld1 = I;
+    TRY_CUDA(launch_rows<DACT>(p, s));
+    if (d_x) {
+        if (!operand_map(&p.tmA, d_h, 0, n, I2, 128) || !operand_map(&p.tmB, w13, G, I2, H, box_k) ||
+            !out_map(&p.tmO0, d_x, 0, n, H, false))
+            return MOE_ERR_CUDA;
+        p.K = 2 * I;
+        p.N = H;
+        p.nt = static_cast<int>(ceil_div(H, BN));
+        p.wrows = H;
+        p.out0 = d_x;
+        p.ld0 = H;
+        TRY_CUDA(launch_rows<DX>(p, s));
+    }
+    if (d_w13 || d_w2) {
+        if ((d_w13 && !out_map(&p.tmO0, d_w13, G, I2, H, f32)) ||
+            (d_w2 && !out_map(&p.tmO1, d_w2, G, H, I, f32)))
+            return MOE_ERR_CUDA;
+        p.mt0 = d_w13 ? static_cast<int>(ceil_div(I2, 256)) : 0;
+        p.nt0 = d_w13 ? static_cast<int>(ceil_div(H, BN)) : 0;
+        p.mt1 = d_w2 ? static_cast<int>(ceil_div(H, 256)) : 0;
+        p.nt1 = d_w2 ? static_cast<int>(ceil_div(I, BN)) : 0;
+        p.H = H;
+        p.I = I;
+        p.w_f32 = f32;
+        p.accumulate = add;
+        const int64_t tiles =
+            static_cast<int64_t>(G) * (p.mt0 * p.nt0 + static_cast<int64_t>(p.mt1) * p.nt1);
+        TRY_CUDA((launch<DW, 2>(p, tiles, s)));
+    }
+    return MOE_OK;
+}
