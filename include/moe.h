@@ -603,6 +603,44 @@ moe_status_t moe_fp4_grouped_mlp(const moe_fp4_t *expanded_x, const int32_t *off
                                  int32_t *dev_status, moe_stream_t stream);
 
 /*
+ * bf16 rows times 4-bit weights, for the few rows per group of a decoding step
+ * (the rows are not quantised; the weights are those of moe_fp4_grouped_*):
+ *   matmul:  y[r, :] = x[r] . w[g]^T      x [n, K] bf16, w [G, N, K]
+ *   swiglu:  act[r, :] = SiLU(gate) * up of w13 [G, 2I, K], as above
+ *            y [n, N], act [n, I]: bf16, or fp32 with MOE_Y_F32
+ *   mlp:     act (bf16) = swiglu(expanded_x, w13), y = matmul(act, w2)
+ * Any number of rows is allowed; a group's weights are read once for up to 8
+ * rows (16 where groups have more than two on average) and again for the next,
+ * so that beyond some 32 rows a group moe_fp4_grouped_* on quantised rows is
+ * the faster form.
+ * Rounding: sums in fp32.  A row is taken into f16 under a power of two of its
+ * own: exact for magnitudes down to 2^-30 of its largest finite one, off by at
+ * most 2^-40 of that one below.  Weights' magnitudes stay below 2^90.
+ * Infinities and NaN in a row and NaN scales give what the products give.
+ * Rows past offsets[G] are left untouched.  K, N, I multiples of 128, G <= 1024.
+ * Bad offsets set MOE_DEV_BAD_OFFSETS and no result is written then.
+ * Workspace: moe_fp4_weight_workspace_size(n, K) bytes (mlp: the larger of H and
+ * I for K), 256-byte aligned, scratch; calls that may overlap in time (also as
+ * replayed graphs) need one each.
+ */
+moe_status_t moe_fp4_weight_workspace_size(int32_t n, int32_t K, size_t *bytes);
+moe_status_t moe_fp4_weight_matmul(const moe_bf16_t *x, const int32_t *offsets, int32_t G,
+                                   const moe_fp4_t *w, int32_t n, int32_t K, int32_t N,
+                                   uint32_t flags, void *y, void *workspace,
+                                   size_t workspace_bytes, int32_t *dev_status,
+                                   moe_stream_t stream);
+moe_status_t moe_fp4_weight_swiglu(const moe_bf16_t *x, const int32_t *offsets, int32_t G,
+                                   const moe_fp4_t *w13, int32_t n, int32_t K, int32_t I,
+                                   uint32_t flags, void *act, void *workspace,
+                                   size_t workspace_bytes, int32_t *dev_status,
+                                   moe_stream_t stream);
+moe_status_t moe_fp4_weight_mlp(const moe_bf16_t *expanded_x, const int32_t *offsets, int32_t G,
+                                const moe_fp4_t *w13, const moe_fp4_t *w2, int32_t n, int32_t H,
+                                int32_t I, uint32_t flags, moe_bf16_t *act, void *y,
+                                void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                                moe_stream_t stream);
+
+/*
  * Diagnostics (the page has no counterpart): enqueue a kernel that waits,
  * through the same bounded wait every pipeline here uses, on a barrier that
  * nothing completes.  After about one second it ORs MOE_DEV_TIMEOUT into

@@ -51,7 +51,9 @@ EXPORTS = ("moe_status_string", "moe_rmsnorm_gate", "moe_rmsnorm_sumsq",
            "moe_finalize_routing_backward", "moe_fp4_scales_size", "moe_fp4_quantize",
            "moe_fp4_dequantize", "moe_fp4_grouped_matmul", "moe_fp4_grouped_swiglu",
            "moe_fp4_grouped_mlp", "moe_grouped_mlp_train",
-           "moe_grouped_mlp_backward_workspace_size", "moe_grouped_mlp_backward")
+           "moe_grouped_mlp_backward_workspace_size", "moe_grouped_mlp_backward",
+           "moe_fp4_weight_workspace_size", "moe_fp4_weight_matmul", "moe_fp4_weight_swiglu",
+           "moe_fp4_weight_mlp")
 NUM_STAGES = 6
 STAGE_NAMES = ("router", "route_scan_scatter", "permute", "gemm_w13_swiglu", "gemm_down",
                "finalize")
@@ -134,6 +136,10 @@ def lib() -> ctypes.CDLL:
                 "moe_grouped_mlp_backward_workspace_size": [I32, I32, I32, PSZ],
                 "moe_grouped_mlp_backward": [P, P, P, I32, P, P, P, I32, I32, I32, U32, P, P, P, P,
                                              SZ, P, P],
+                "moe_fp4_weight_workspace_size": [I32, I32, PSZ],
+                "moe_fp4_weight_matmul": [P, P, I32, P, I32, I32, I32, U32, P, P, SZ, P, P],
+                "moe_fp4_weight_swiglu": [P, P, I32, P, I32, I32, I32, U32, P, P, SZ, P, P],
+                "moe_fp4_weight_mlp": [P, P, I32, P, P, I32, I32, I32, U32, P, P, P, SZ, P, P],
             }
             for name, args in sigs.items():
                 fn = getattr(L, name)
@@ -747,6 +753,79 @@ def fp4_grouped_mlp(expanded_x: Fp4Matrix, offsets, w13: Fp4Matrix, w2: Fp4Matri
         y = torch.empty((n, H), dtype=torch.float32 if y_f32 else torch.bfloat16, device=dev)
         _call("moe_fp4_grouped_mlp", xa, off, G, wa, w2a, n, H, I, Y_F32 if y_f32 else 0,
               _fp4_arg(act, "act", G, dev), y.data_ptr(), st, _stream(dev))
+    return act, y
+
+
+# ------------------------------------------- 4-bit weights under bf16 rows
+@functools.lru_cache(maxsize=256)
+def fp4_weight_workspace_size(n, K) -> int:
+    b = ctypes.c_size_t(0)
+    _call("moe_fp4_weight_workspace_size", n, K, ctypes.byref(b))
+    return b.value
+
+
+def _fp4_weight_args(x, offsets, w, name):
+    """(n, K, G, rows of a group's weights, device, the rows' and offsets'
+    addresses, the weights' struct)."""
+    if x.dim() != 2 or w.q.dim() != 3 or x.shape[1] != w.K:
+        raise ValueError(f"{name}: rows [n, K] and weights [G, rows, K/2] of the same K")
+    n, K = x.shape
+    G, rows, _ = w.q.shape
+    dev = x.device
+    xp = _arg(x, torch.bfloat16, dev, None, "rows")
+    off = _arg(offsets, torch.int32, dev, (G + 1,), "offsets")
+    return n, K, G, rows, dev, xp, off, _fp4_arg(w, name, 0, dev)
+
+
+def _fp4_weight_product(fn, x, offsets, w, name, per, out_f32, out, status):
+    n, K, G, rows, dev, xp, off, wa = _fp4_weight_args(x, offsets, w, name)
+    if rows % per:
+        raise ValueError(f"{name} must hold an even number of rows, gate then up")
+    N = rows // per
+    dt = torch.float32 if out_f32 else torch.bfloat16
+    op = _arg(out, dt, dev, (n, N), "out")
+    st = _status_arg(status, dev)
+    with _on(dev):
+        if out is None:
+            out = torch.empty((n, N), dtype=dt, device=dev)
+            op = out.data_ptr()
+        nbytes = fp4_weight_workspace_size(n, K)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        _call(fn, xp, off, G, wa, n, K, N, Y_F32 if out_f32 else 0, op, ws.data_ptr(), nbytes, st,
+              _stream(dev))
+    return out
+
+
+def fp4_weight_matmul(x, offsets, w: Fp4Matrix, out_f32=False, out=None, status=None):
+    """y = x . w[group]^T of bf16 rows [n, K] and 4-bit weights -> [n, N] bf16
+    (fp32 with out_f32), for few rows per group.  Rows past the last group are
+    left as they were in ``out`` (not set without it)."""
+    return _fp4_weight_product("moe_fp4_weight_matmul", x, offsets, w, "w", 1, out_f32, out,
+                               status)
+
+
+def fp4_weight_swiglu(x, offsets, w13: Fp4Matrix, out_f32=False, out=None, status=None):
+    """act = SiLU(gate) * up of bf16 rows and the merged 4-bit w13 [G, 2I, K]
+    -> [n, I] bf16 (fp32 with out_f32), for few rows per group."""
+    return _fp4_weight_product("moe_fp4_weight_swiglu", x, offsets, w13, "w13", 2, out_f32, out,
+                               status)
+
+
+def fp4_weight_mlp(expanded_x, offsets, w13: Fp4Matrix, w2: Fp4Matrix, y_f32=False, status=None):
+    """The FFN of bf16 rows on 4-bit experts, for few rows per expert -> (act
+    bf16 [n, I], y bf16 [n, H], fp32 with y_f32)."""
+    n, H, G, rows, dev, xp, off, wa = _fp4_weight_args(expanded_x, offsets, w13, "w13")
+    I = rows // 2
+    if rows % 2 or w2.q.shape != (G, H, I // 2):
+        raise ValueError("w13 must be [G, 2I, H/2] and w2 [G, H, I/2]")
+    w2a, st = _fp4_arg(w2, "w2", 0, dev), _status_arg(status, dev)
+    with _on(dev):
+        act = torch.empty((n, I), dtype=torch.bfloat16, device=dev)
+        y = torch.empty((n, H), dtype=torch.float32 if y_f32 else torch.bfloat16, device=dev)
+        nbytes = fp4_weight_workspace_size(n, max(H, I))
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        _call("moe_fp4_weight_mlp", xp, off, G, wa, w2a, n, H, I, Y_F32 if y_f32 else 0,
+              act.data_ptr(), y.data_ptr(), ws.data_ptr(), nbytes, st, _stream(dev))
     return act, y
 
 
