@@ -83,7 +83,9 @@ enum {
                                       the matmul slower than the permute pass costs. */
     MOE_DW_F32 = 1u << 8,          /* grouped MLP backward: the weights' gradients in
                                       fp32 (else bf16) */
-    MOE_DW_ACCUMULATE = 1u << 9    /* ... added to what their buffers hold (fp32 only) */
+    MOE_DW_ACCUMULATE = 1u << 9,   /* ... added to what their buffers hold (fp32 only) */
+    MOE_RES_F32 = 1u << 10,        /* norm_residual: the residual stream is fp32 (else bf16) */
+    MOE_POST_NORM = 1u << 11       /* norm_residual: RMSNorm of the block's output */
 };
 
 typedef struct {
@@ -516,6 +518,55 @@ moe_status_t moe_grouped_mlp_backward(const moe_bf16_t *d_y, const moe_bf16_t *e
                                       void *d_w13, void *d_w2, void *workspace,
                                       size_t workspace_bytes, int32_t *dev_status,
                                       moe_stream_t stream);
+
+/*
+ * Between two blocks of a residual stream: the norm after a block with its gate
+ * and residual scale, the addition, and the norm before the next block.  With
+ * N(v; gamma) = gamma v / sqrt(mean(v^2) + eps) over a row,
+ *   r[t]  = x[t] + scale * gate[s] * N(y[t]; gamma_post)    for t in sequence s
+ *   xn[t] = N(r[t]; gamma_next)
+ *   x, r [T, H] bf16 (fp32 with MOE_RES_F32); y [T, H] bf16 (fp32 with MOE_Y_F32)
+ *   gate [S, H] bf16, or NULL = ones (S and seq_offsets are then ignored)
+ *   seq_offsets [S+1] int32 device, ascending inside [0, T]; NULL with S = 1: all
+ *               tokens.  Rows outside every sequence are left untouched.
+ *   gamma_post, gamma_next [H] bf16, or NULL = ones
+ *   MOE_POST_NORM: as above; without it y itself is gated and added
+ *               (gamma_post NULL)
+ *   xn [T, H] bf16, or NULL = no norm before the next block (gamma_next and
+ *               rstd_next NULL)
+ *   rstd_post, rstd_next [T] fp32: 1 / sqrt(mean + eps) of y and r, which the
+ *               backward pass takes; NULL = not kept
+ * xn is the norm of r as it is stored.  Sums are fp32 (moe_rmsnorm_gate's is the
+ * exact sum: its xn may differ in a last bit); a row's sum of squares stays
+ * below fp32's range.
+ *
+ * Backward, from the gradients d_r (like r; NULL = none) and d_xn (bf16; NULL as
+ * xn was) with what the forward pass kept:
+ *   d_x (like x), d_y (like y), d_gamma_post [H], d_gate [S, H], d_gamma_next [H]
+ *   fp32; each may be NULL (not computed).
+ * Sequences without tokens have a zero d_gate.  The sums over tokens are taken in
+ * fp32 in a fixed order.  Bad bounds set MOE_DEV_BAD_OFFSETS and nothing is
+ * written.  H % 8 == 0, H <= 8192, S <= 65536, T <= 2^30.  d_x may be d_r, d_y may
+ * be y, r may be x; otherwise no output overlaps an input.  Workspace (needed for
+ * the last three): moe_norm_residual_backward_workspace_size(T, H, S) bytes (S = 1
+ * without a gate), 256-byte aligned, scratch; calls that may overlap in time
+ * (also as replayed graphs) need one each.
+ */
+moe_status_t moe_norm_residual(const void *x, const void *y, const moe_bf16_t *gamma_post,
+                               const moe_bf16_t *gate, const int32_t *seq_offsets, int32_t S,
+                               const moe_bf16_t *gamma_next, int32_t T, int32_t H, float scale,
+                               float eps, uint32_t flags, void *r, moe_bf16_t *xn,
+                               float *rstd_post, float *rstd_next, int32_t *dev_status,
+                               moe_stream_t stream);
+moe_status_t moe_norm_residual_backward_workspace_size(int32_t T, int32_t H, int32_t S,
+                                                       size_t *bytes);
+moe_status_t moe_norm_residual_backward(
+    const void *d_r, const moe_bf16_t *d_xn, const void *y, const void *r, const float *rstd_post,
+    const float *rstd_next, const moe_bf16_t *gamma_post, const moe_bf16_t *gate,
+    const int32_t *seq_offsets, int32_t S, const moe_bf16_t *gamma_next, int32_t T, int32_t H,
+    float scale, uint32_t flags, void *d_x, void *d_y, float *d_gamma_post, float *d_gate,
+    float *d_gamma_next, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+    moe_stream_t stream);
 
 /*
  * Microscaled 4-bit matrices: e2m1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and

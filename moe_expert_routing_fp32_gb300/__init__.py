@@ -35,7 +35,7 @@ STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED_S
                 3: "MOE_ERR_WORKSPACE_TOO_SMALL", 4: "MOE_ERR_CUDA", 5: "MOE_ERR_NO_DEVICE"}
 DEV_BAD_EXPERT_ID, DEV_TIMEOUT, DEV_BAD_OFFSETS, DEV_UNSORTED = 1, 2, 4, 8
 RENORM, RMSNORM, SHARED, OUT_F32, SHARED_F32, GATE_SEQUENTIAL, Y_F32 = 1, 2, 4, 8, 16, 32, 64
-GATHER_A, DW_F32, DW_ACCUMULATE = 128, 256, 512
+GATHER_A, DW_F32, DW_ACCUMULATE, RES_F32, POST_NORM = 128, 256, 512, 1024, 2048
 
 # every symbol include/moe.h declares
 EXPORTS = ("moe_status_string", "moe_rmsnorm_gate", "moe_rmsnorm_sumsq",
@@ -53,7 +53,8 @@ EXPORTS = ("moe_status_string", "moe_rmsnorm_gate", "moe_rmsnorm_sumsq",
            "moe_fp4_grouped_mlp", "moe_grouped_mlp_train",
            "moe_grouped_mlp_backward_workspace_size", "moe_grouped_mlp_backward",
            "moe_fp4_weight_workspace_size", "moe_fp4_weight_matmul", "moe_fp4_weight_swiglu",
-           "moe_fp4_weight_mlp")
+           "moe_fp4_weight_mlp", "moe_norm_residual",
+           "moe_norm_residual_backward_workspace_size", "moe_norm_residual_backward")
 NUM_STAGES = 6
 STAGE_NAMES = ("router", "route_scan_scatter", "permute", "gemm_w13_swiglu", "gemm_down",
                "finalize")
@@ -140,6 +141,10 @@ def lib() -> ctypes.CDLL:
                 "moe_fp4_weight_matmul": [P, P, I32, P, I32, I32, I32, U32, P, P, SZ, P, P],
                 "moe_fp4_weight_swiglu": [P, P, I32, P, I32, I32, I32, U32, P, P, SZ, P, P],
                 "moe_fp4_weight_mlp": [P, P, I32, P, P, I32, I32, I32, U32, P, P, P, SZ, P, P],
+                "moe_norm_residual": [P, P, P, P, P, I32, P, I32, I32, F, F, U32, P, P, P, P, P, P],
+                "moe_norm_residual_backward_workspace_size": [I32, I32, I32, PSZ],
+                "moe_norm_residual_backward": [P, P, P, P, P, P, P, P, P, I32, P, I32, I32, F, U32,
+                                               P, P, P, P, P, P, SZ, P, P],
             }
             for name, args in sigs.items():
                 fn = getattr(L, name)
@@ -591,6 +596,102 @@ def grouped_mlp_backward(d_y, expanded_x, offsets, h, w13, w2, need=("x", "w13",
               d_x.data_ptr() if d_x is not None else None, p13, p2, wsp, workspace.numel(), st,
               _stream(dev))
     return d_x, d_w13, d_w2
+
+
+# ------------------------------------------------- between two blocks
+def _norm_args(y, res, name, gamma_post, gate, gamma_next, seq_offsets, post_norm, next_norm):
+    """(T, H, S, flags, device, the four addresses) of norm_residual's
+    arguments; ``res`` has the residual stream's type."""
+    if y.dim() != 2:
+        raise ValueError("rows [T, H]")
+    T, H = y.shape
+    dev = y.device
+    flags = (RES_F32 if _bf16_or_f32(res, name) == torch.float32 else 0) | \
+        (Y_F32 if _bf16_or_f32(y, "y") == torch.float32 else 0) | (POST_NORM if post_norm else 0)
+    if gamma_post is not None and not post_norm:
+        raise ValueError("gamma_post belongs to the norm after the block (post_norm)")
+    if gamma_next is not None and not next_norm:
+        raise ValueError("gamma_next belongs to the norm before the next block (next_norm)")
+    gp = _arg(gamma_post, torch.bfloat16, dev, (H,), "gamma_post")
+    gn = _arg(gamma_next, torch.bfloat16, dev, (H,), "gamma_next")
+    S, gt, seq = 1, None, None
+    if gate is not None:
+        S = seq_offsets.numel() - 1 if seq_offsets is not None else 1
+        if S < 1:
+            raise ValueError("seq_offsets: [S + 1] with S >= 1")
+        gt = _arg(gate, torch.bfloat16, dev, (S, H), "gate")
+        seq = _arg(seq_offsets, torch.int32, dev, (S + 1,), "seq_offsets")
+    return T, H, S, flags, dev, (gp, gt, seq, gn)
+
+
+def norm_residual(x, y, gamma_post=None, gate=None, scale=1.0, gamma_next=None, post_norm=True,
+                  next_norm=True, eps=1e-6, seq_offsets=None, status=None):
+    """Between two blocks: r = x + scale * gate * RMSNorm(y) and xn =
+    RMSNorm(r).  ``x`` is the residual stream (bf16 or fp32 [T, H]), ``y`` the
+    block's output (bf16 or fp32), ``gate`` [S, H] bf16 one row per sequence of
+    ``seq_offsets`` (int32 [S+1]; without them one sequence of all tokens).
+    -> dict(r like x, xn bf16 or None, rstd_post, rstd_next fp32 [T] or None);
+    norm_residual_backward takes the dict.  Rows outside every sequence are not
+    set."""
+    T, H, S, flags, dev, (gp, gt, seq, gn) = _norm_args(y, x, "x", gamma_post, gate, gamma_next,
+                                                        seq_offsets, post_norm, next_norm)
+    xp = _arg(x, x.dtype, dev, (T, H), "x")
+    yp = _arg(y, y.dtype, dev, None, "y")
+    st = _status_arg(status, dev)
+    with _on(dev):
+        r = torch.empty_like(x)
+        xn = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if next_norm else None
+        kp = torch.empty(T, dtype=torch.float32, device=dev) if post_norm else None
+        kn = torch.empty(T, dtype=torch.float32, device=dev) if next_norm else None
+        ptr = lambda t: None if t is None else t.data_ptr()               # noqa: E731
+        _call("moe_norm_residual", xp, yp, gp, gt, seq, S, gn, T, H, float(scale), float(eps), flags,
+              r.data_ptr(), ptr(xn), ptr(kp), ptr(kn), st, _stream(dev))
+    return dict(r=r, xn=xn, rstd_post=kp, rstd_next=kn)
+
+
+@functools.lru_cache(maxsize=256)
+def norm_residual_backward_workspace_size(T, H, S=1) -> int:
+    b = ctypes.c_size_t(0)
+    _call("moe_norm_residual_backward_workspace_size", T, H, S, ctypes.byref(b))
+    return b.value
+
+
+def norm_residual_backward(d_r, d_xn, y, saved, gamma_post=None, gate=None, scale=1.0,
+                           gamma_next=None, post_norm=True, seq_offsets=None, status=None):
+    """Gradients of norm_residual from those of r (like r, or None) and xn
+    (bf16, or None: as if it had not been used), the block's output and what the
+    forward pass returned (``saved``: r, rstd_post, rstd_next) -> dict(d_x like
+    x, d_y like y, d_gamma_post, d_gamma_next fp32 [H], d_gate fp32 [S, H]; None
+    where there is no such norm or gate).  Rows of d_x and d_y outside every
+    sequence are not set."""
+    r = saved["r"]
+    next_norm = d_xn is not None
+    T, H, S, flags, dev, (gp, gt, seq, gn) = _norm_args(
+        y, r, "r", gamma_post, gate, gamma_next if next_norm else None, seq_offsets, post_norm,
+        next_norm)
+    if d_r is None and d_xn is None:
+        raise ValueError("one of d_r and d_xn")
+    yp = _arg(y, y.dtype, dev, None, "y")
+    rp = _arg(r, r.dtype, dev, (T, H), "r")
+    drp = _arg(d_r, r.dtype, dev, (T, H), "d_r")
+    dnp = _arg(d_xn, torch.bfloat16, dev, (T, H), "d_xn")
+    kp = _arg(saved["rstd_post"], torch.float32, dev, (T,), "rstd_post") if post_norm else None
+    kn = _arg(saved["rstd_next"], torch.float32, dev, (T,), "rstd_next") if next_norm else None
+    st = _status_arg(status, dev)
+    with _on(dev):
+        d_x = torch.empty_like(r)
+        d_y = torch.empty_like(y)
+        new = lambda *s: torch.empty(s, dtype=torch.float32, device=dev)  # noqa: E731
+        dgp = new(H) if post_norm else None
+        dgt = new(S, H) if gate is not None else None
+        dgn = new(H) if next_norm else None
+        ptr = lambda t: None if t is None else t.data_ptr()               # noqa: E731
+        nbytes = norm_residual_backward_workspace_size(T, H, S)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        _call("moe_norm_residual_backward", drp, dnp, yp, rp, kp, kn, gp, gt, seq, S, gn, T, H,
+              float(scale), flags, d_x.data_ptr(), d_y.data_ptr(), ptr(dgp), ptr(dgt), ptr(dgn),
+              ws.data_ptr(), nbytes, st, _stream(dev))
+    return dict(d_x=d_x, d_y=d_y, d_gamma_post=dgp, d_gate=dgt, d_gamma_next=dgn)
 
 
 # ------------------------------------------------------------ 4-bit operands
