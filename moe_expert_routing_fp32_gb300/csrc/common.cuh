@@ -32,6 +32,14 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
            (static_cast<uint32_t>(float_to_bf16_bits(hi)) << 16);
 }
 
+// Two fp32 values to packed bf16 (nearest even) in one conversion; two single
+// conversions and a merge take four times as long in a kernel's epilogue.
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 __device__ __forceinline__ void report(int32_t *dev_status, int bits) {
     if (dev_status) atomicOr(dev_status, bits);
 }
@@ -110,6 +118,55 @@ __device__ __forceinline__ bool mbar_wait_drain(uint64_t *bar, uint32_t parity) 
         if ((it & 63u) == 63u && (global_timer_ns() - t0 > kWaitLimitNs || it > (1u << 30)))
             return false;
     }
+}
+
+// One lane of a converged warp.  Loops that issue TMA and tcgen05
+// instructions run under this test and not under `lane == 0`: the compiler then
+// knows that one lane is active and feeds the instructions' uniform operands
+// directly.  Measured: 43 cycles an MMA or scale copy to issue against 80,
+// where an MMA of 256 x 256 x 64 takes 128 and a slice of four needs six to
+// twelve copies besides.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
+// Bounded wait (as mbar_wait_bounded) whose first 64 polls read no timer: a
+// %globaltimer read takes far longer than a hand-over between two roles, and
+// here one sits on the path from a finished accumulator to the next tile's
+// first MMA.  No wait here publishes ordinary memory between CTAs (operands
+// come by TMA, accumulators through tensor memory, each with its own ordering),
+// so CTA scope is enough.
+static __device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                              int32_t *dev_status) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 63u) == 0u) {
+            if (*abort) return false;
+            const uint64_t t = global_timer_ns();
+            if (t0 == 0) t0 = t;
+            if (t - t0 > kWaitLimitNs || it > (1u << 30)) {
+                *abort = 1;
+                report(dev_status, MOE_DEV_TIMEOUT);
+                return false;
+            }
+        }
+    }
+}
+
+// Arrive on a barrier of the pair's even CTA once this warp's tensor memory
+// loads have ended (tcgen05.wait::ld and the fence before it order those; a
+// cluster-scope release would also wait for its output stores).
+__device__ __forceinline__ void arrive_drained(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                           int32_t *dev_status) {
+    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort, dev_status);
 }
 
 __device__ __forceinline__ void fence_barrier_init() {

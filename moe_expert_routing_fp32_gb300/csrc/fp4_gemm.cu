@@ -45,7 +45,7 @@
 #include <algorithm>
 #include <mutex>
 
-#include "fp4.cuh"
+#include "fp4_mma.cuh"
 #include "internal.h"
 
 namespace moe {
@@ -112,117 +112,6 @@ struct Cfg {
     static_assert(STAGE % 1024 == 0, "swizzled tiles need 1 KB alignment");
     static_assert(SF_COL + 2 * 2 * SF_SET <= TMEM_COLS, "scale columns");
 };
-
-// Instruction descriptor of the block-scaled MMA: e2m1 operands, both K-major,
-// fp32 accumulator; scale type e8m0 (MX) or e4m3 (NV); the scales of a K = 64
-// step start at byte `id` of their 32-bit column entries.
-template <int FMT>
-__host__ __device__ constexpr uint32_t idesc(int M, int N, int id) {
-    return (static_cast<uint32_t>(id) << 4) | (1u << 7) | (1u << 10) |
-           (static_cast<uint32_t>(N >> 3) << 17) |
-           (static_cast<uint32_t>(FMT == MOE_FP4_MX ? 1 : 0) << 23) |
-           (static_cast<uint32_t>(M >> 7) << 27) | (static_cast<uint32_t>(id) << 29);
-}
-
-// One lane of a converged warp.  The loops below that issue TMA and tcgen05
-// instructions run under this test and not under `lane == 0`: the compiler then
-// knows that one lane is active and feeds the instructions' uniform operands
-// directly.  Measured: 43 cycles an MMA or scale copy to issue against 80,
-// where an MMA of 256 x 256 x 64 takes 128 and a slice of four needs six to
-// twelve copies besides.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(p));
-    return p != 0;
-}
-
-// Bounded wait (as mbar_wait_bounded) whose first 64 polls read no timer: a
-// %globaltimer read takes far longer than a hand-over between two roles, and
-// here one sits on the path from a finished accumulator to the next tile's
-// first MMA.  No wait here publishes ordinary memory between CTAs (operands
-// come by TMA, accumulators through tensor memory, each with its own ordering),
-// so CTA scope is enough.
-__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort,
-                                       int32_t *dev_status) {
-    uint64_t t0 = 0;
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((it & 63u) == 0u) {
-            if (*abort) return false;
-            const uint64_t t = global_timer_ns();
-            if (t0 == 0) t0 = t;
-            if (t - t0 > kWaitLimitNs || it > (1u << 30)) {
-                *abort = 1;
-                report(dev_status, MOE_DEV_TIMEOUT);
-                return false;
-            }
-        }
-    }
-}
-// Arrive on a barrier of the pair's even CTA once this warp's tensor memory
-// loads have ended (tcgen05.wait::ld and the fence before it order those; a
-// cluster-scope release would also wait for its output stores).
-__device__ __forceinline__ void arrive_drained(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volatile int *abort,
-                                           int32_t *dev_status) {
-    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort, dev_status);
-}
-
-// Shared-memory descriptors are kept as their low words, whose address field
-// steps by plain additions; the high words are constants.  It leaves the issuing
-// threads, which share their schedulers with the epilogue's arithmetic, fewer
-// instructions: 246 cycles a slice of four MMAs and four copies against 315.
-//   operands: 128-byte swizzled K-major rows, 1 KB between groups of eight
-//   scales:   rows of 16 bytes, 128 bytes between groups of eight, no swizzle
-constexpr uint32_t OPERAND_LO = 1u << 16, OPERAND_HI = 0x40004040u;
-constexpr uint32_t SCALES_LO = 8u << 16, SCALES_HI = 0x00004008u;
-
-// D (+)= A * B^T with the scales at sa (rows of A) and sb (rows of B).
-// CG = 2: M = 256 over a CTA pair, each CTA holding its 128 rows of A (and
-// their scales), half the rows of B and the scales of all of them.
-#define MOE_MMA_FP4(GROUP, KIND)                                                              \
-    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"                               \
-                 "mov.b64 da, {%1, %7};\n\tmov.b64 db, {%2, %7};\n\t"                       \
-                 "setp.ne.b32 p, %6, 0;\n\t"                                                  \
-                 "tcgen05.mma.cta_group::" GROUP ".kind::" KIND                               \
-                 " [%0], da, db, %3, [%4], [%5], p;\n\t}" ::"r"(d),                           \
-                 "r"(a), "r"(b), "r"(id), "r"(sa), "r"(sb), "r"(accumulate), "n"(OPERAND_HI)  \
-                 : "memory")
-template <int FMT, int CG>
-__device__ __forceinline__ void mma_fp4(uint32_t d, uint32_t a, uint32_t b, uint32_t id,
-                                        uint32_t sa, uint32_t sb, uint32_t accumulate) {
-    if (FMT == MOE_FP4_MX && CG == 1)
-        MOE_MMA_FP4("1", "mxf4.block_scale.scale_vec::2X");
-    else if (FMT == MOE_FP4_MX)
-        MOE_MMA_FP4("2", "mxf4.block_scale.scale_vec::2X");
-    else if (CG == 1)
-        MOE_MMA_FP4("1", "mxf4nvf4.block_scale.scale_vec::4X");
-    else
-        MOE_MMA_FP4("2", "mxf4nvf4.block_scale.scale_vec::4X");
-}
-#undef MOE_MMA_FP4
-
-// One 512-byte scale tile (32 rows of 16 bytes) into four columns of tensor
-// memory, repeated in its four lane quarters (CG = 2: in both CTAs, each from
-// its own shared memory).  The tensor pipe takes one thread's copies and MMAs in
-// the order they were issued.
-template <int CG>
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t lo) {
-    if (CG == 1)
-        asm volatile("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
-                     "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr),
-                     "r"(lo), "n"(SCALES_HI)
-                     : "memory");
-    else
-        asm volatile("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
-                     "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr),
-                     "r"(lo), "n"(SCALES_HI)
-                     : "memory");
-}
 
 // One half tile's MMAs over STEPS * 64 columns of K of a stage (4, or 2 in a
 // last slice of 128 columns): operand tiles a and b, scale tiles sa and sb
@@ -744,51 +633,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 }
 
 // ------------------------------------------------------------------ host side
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static std::once_flag once;
-    static EncodeTiledFn fn = nullptr;
-    std::call_once(once, [] {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
-                                             cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(ptr);
-    });
-    return fn;
-}
-
-// Codes [groups][rows][K / 2 bytes] as boxes of `box` rows x 128 bytes, swizzled.
-bool code_map(CUtensorMap *m, const uint8_t *q, int rank, int64_t groups, int64_t rows, int K,
-              int box) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    const cuuint64_t row_bytes = static_cast<cuuint64_t>(K) / 2;
-    cuuint64_t dim[3] = {row_bytes, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(groups)};
-    cuuint64_t stride[2] = {row_bytes, row_bytes * static_cast<cuuint64_t>(rows)};
-    cuuint32_t boxd[3] = {BK / 2, static_cast<cuuint32_t>(box), 1}, es[3] = {1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<uint8_t *>(q), dim, stride, boxd,
-              es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Scale tiles as rows of 128 words, `box` of them at a time.
-bool scale_map(CUtensorMap *m, const uint8_t *sf, int64_t tiles, int box) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dim[2] = {kScaleTile / 4, static_cast<cuuint64_t>(tiles)};
-    cuuint64_t stride[1] = {kScaleTile};
-    cuuint32_t boxd[2] = {kScaleTile / 4, static_cast<cuuint32_t>(box)}, es[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint8_t *>(sf), dim, stride, boxd, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Output [rows, cols] as 32-row x 128-byte boxes, swizzled.
 bool out_map(CUtensorMap *m, void *out, int64_t rows, int64_t cols, bool f32) {
     EncodeTiledFn fn = encode_fn();

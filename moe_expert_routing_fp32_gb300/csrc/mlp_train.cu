@@ -103,44 +103,6 @@ struct Cfg {
     static_assert(STAGE % 1024 == 0 && MAP_OFF % 128 == 0, "alignment");
 };
 
-// One lane of a converged warp, known to the compiler to be one.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(p));
-    return p != 0;
-}
-
-// Bounded wait whose first 64 polls read no timer.
-__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort,
-                                       int32_t *dev_status) {
-    uint64_t t0 = 0;
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((it & 63u) == 0u) {
-            if (*abort) return false;
-            const uint64_t t = global_timer_ns();
-            if (t0 == 0) t0 = t;
-            if (t - t0 > kWaitLimitNs || it > (1u << 30)) {
-                *abort = 1;
-                report(dev_status, MOE_DEV_TIMEOUT);
-                return false;
-            }
-        }
-    }
-}
-__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volatile int *abort,
-                                           int32_t *dev_status) {
-    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort, dev_status);
-}
-
-// Arrive on a barrier of the pair's even CTA once this warp's tensor memory
-// loads have ended.
-__device__ __forceinline__ void arrive_drained(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
 // D (+)= A B^T with the descriptors' low words a and b.
 template <int CG>
 __device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
@@ -200,12 +162,6 @@ __device__ __forceinline__ void tma_add_3d(const void *tmap, const void *src, in
         "[%4];" ::"l"(reinterpret_cast<uint64_t>(tmap)),
         "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(src))
         : "memory");
-}
-
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
 }
 
 struct Tile {
