@@ -660,21 +660,24 @@ moe_status_t moe_fp4_grouped_mlp(const moe_fp4_t *expanded_x, const int32_t *off
  *   swiglu:  act[r, :] = SiLU(gate) * up of w13 [G, 2I, K], as above
  *            y [n, N], act [n, I]: bf16, or fp32 with MOE_Y_F32
  *   mlp:     act (bf16) = swiglu(expanded_x, w13), y = matmul(act, w2)
- * Any number of rows is allowed; a group's weights are read once for up to 8
- * rows (16 where groups have more than two on average) and again for the next,
- * so that beyond some 32 rows a group moe_fp4_grouped_* on quantised rows is
- * the faster form.
- * Rounding: sums in fp32.  A row is taken into f16 under a power of two of its
- * own: exact for magnitudes down to 2^-30 of its largest finite one, off by at
- * most 2^-40 of that one below.  Weights' magnitudes stay below 2^90.
- * Infinities and NaN in a row and NaN scales give what the products give.
- * Rows past offsets[G] are left untouched.  K, N, I multiples of 128, G <= 1024.
- * Bad offsets set MOE_DEV_BAD_OFFSETS and no result is written then.
- * Workspace: moe_fp4_weight_workspace_size(n, K) bytes (mlp: the larger of H and
- * I for K), 256-byte aligned, scratch; calls that may overlap in time (also as
- * replayed graphs) need one each.
+ * Any number of rows is allowed; a group's weights are read once for every 8
+ * rows, so that beyond some 32 rows a group moe_fp4_grouped_* on quantised rows
+ * is the faster form.
+ * Rounding: a row is written exactly in 4-bit digits, 36 bits below the largest
+ * magnitude of its block (32 columns, MX; 16, NV): values down to 2^-27 of it are
+ * exact, smaller ones off by 2^-35 of it at most (and none by more than 2^-96,
+ * MX, or 2^-52, NV, of the row's largest).  Products are exact, sums fp32.
+ * Weights' magnitudes stay below 2^90.  Infinities and NaN in a row and NaN
+ * scales give what the products give; a row that holds any takes much longer.
+ * Rows past offsets[G] are left untouched.  K, N, I multiples of 128, at most
+ * 2^20, G <= 1024.  Bad offsets set MOE_DEV_BAD_OFFSETS and no result is written
+ * then.  Results do not depend on the launch.
+ * Workspace: moe_fp4_weight_workspace_size(n, K, N, G) bytes (mlp: the larger of
+ * (n, H, I, G) and (n, I, H, G)), 256-byte aligned, scratch; calls that may
+ * overlap in time (also as replayed graphs) need one each.
  */
-moe_status_t moe_fp4_weight_workspace_size(int32_t n, int32_t K, size_t *bytes);
+moe_status_t moe_fp4_weight_workspace_size(int32_t n, int32_t K, int32_t N, int32_t G,
+                                           size_t *bytes);
 moe_status_t moe_fp4_weight_matmul(const moe_bf16_t *x, const int32_t *offsets, int32_t G,
                                    const moe_fp4_t *w, int32_t n, int32_t K, int32_t N,
                                    uint32_t flags, void *y, void *workspace,

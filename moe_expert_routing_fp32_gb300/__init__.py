@@ -137,7 +137,7 @@ def lib() -> ctypes.CDLL:
                 "moe_grouped_mlp_backward_workspace_size": [I32, I32, I32, PSZ],
                 "moe_grouped_mlp_backward": [P, P, P, I32, P, P, P, I32, I32, I32, U32, P, P, P, P,
                                              SZ, P, P],
-                "moe_fp4_weight_workspace_size": [I32, I32, PSZ],
+                "moe_fp4_weight_workspace_size": [I32, I32, I32, I32, PSZ],
                 "moe_fp4_weight_matmul": [P, P, I32, P, I32, I32, I32, U32, P, P, SZ, P, P],
                 "moe_fp4_weight_swiglu": [P, P, I32, P, I32, I32, I32, U32, P, P, SZ, P, P],
                 "moe_fp4_weight_mlp": [P, P, I32, P, P, I32, I32, I32, U32, P, P, P, SZ, P, P],
@@ -859,9 +859,9 @@ def fp4_grouped_mlp(expanded_x: Fp4Matrix, offsets, w13: Fp4Matrix, w2: Fp4Matri
 
 # ------------------------------------------- 4-bit weights under bf16 rows
 @functools.lru_cache(maxsize=256)
-def fp4_weight_workspace_size(n, K) -> int:
+def fp4_weight_workspace_size(n, K, N, G) -> int:
     b = ctypes.c_size_t(0)
-    _call("moe_fp4_weight_workspace_size", n, K, ctypes.byref(b))
+    _call("moe_fp4_weight_workspace_size", n, K, N, G, ctypes.byref(b))
     return b.value
 
 
@@ -890,7 +890,7 @@ def _fp4_weight_product(fn, x, offsets, w, name, per, out_f32, out, status):
         if out is None:
             out = torch.empty((n, N), dtype=dt, device=dev)
             op = out.data_ptr()
-        nbytes = fp4_weight_workspace_size(n, K)
+        nbytes = fp4_weight_workspace_size(n, K, N, G)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         _call(fn, xp, off, G, wa, n, K, N, Y_F32 if out_f32 else 0, op, ws.data_ptr(), nbytes, st,
               _stream(dev))
@@ -923,7 +923,7 @@ def fp4_weight_mlp(expanded_x, offsets, w13: Fp4Matrix, w2: Fp4Matrix, y_f32=Fal
     with _on(dev):
         act = torch.empty((n, I), dtype=torch.bfloat16, device=dev)
         y = torch.empty((n, H), dtype=torch.float32 if y_f32 else torch.bfloat16, device=dev)
-        nbytes = fp4_weight_workspace_size(n, max(H, I))
+        nbytes = max(fp4_weight_workspace_size(n, H, I, G), fp4_weight_workspace_size(n, I, H, G))
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         _call("moe_fp4_weight_mlp", xp, off, G, wa, w2a, n, H, I, Y_F32 if y_f32 else 0,
               act.data_ptr(), y.data_ptr(), ws.data_ptr(), nbytes, st, _stream(dev))

@@ -5,38 +5,44 @@
 //   SWIGLU:  act[r, n] = SiLU(x[r] . W[g, n]) (x[r] . W[g, I + n])
 // for the rows r of group g, W[g, n, k] = e2m1 code * block scale.
 //
-// What bounds it is reading the weights: K (1/2 + 1/block) bytes a weight row,
-// each used for a handful of rows.  So the weights stream through shared memory
-// in 16-byte asynchronous copies (two CTAs a multiprocessor, 3 or 4 stages of 128
-// rows x 256 columns each), and what is done with them has to fit beside: at
-// full bandwidth a multiprocessor has about three issue slots a weight.
+// What bounds it is reading the weights, K (1/2 + 1/block) bytes a weight row,
+// each used for a handful of rows.  A multiprocessor gets about 45 weights a
+// cycle from memory: three instruction issues a weight for everything.  (mma.sync
+// with the weights taken to f16 in registers needs 2.8 to 3.5 and ran at half the
+// memory's rate: 22 us where the weights of 8 experts, K = N = 4096, take 10.5.)
+// So the block-scaled tensor cores take the codes as they are, and the rows
+// become 4-bit operands without loss:
 //
-// The arithmetic.  The weights are the 16-row operand of mma.sync m16n8k16, the
-// rows the 8-column one, so one instruction multiplies 256 weights with up to 8
-// rows.  In f16 a pair of codes takes one conversion (cvt.f16x2.e2m1x2, exact;
-// there is none to bf16, and picking the bits apart takes 4 to 5 instructions a
-// pair).  So the rows go to f16, too, after a scaling by a power of two that puts
-// a row's largest finite magnitude into [2^15, 2^16): a bf16 value fits f16's 11
-// bits and is exact down to 2^-30 of that maximum; below it is rounded by at
-// most 2^-40 of the maximum.  The scaling comes off the fp32 sums at the end.
-//   MX: the sum over a block of 32 columns is made apart and added to the fp32
-//       total times the block's power of two.
-//   NV: code * e4m3 scale has at most 6 significant bits and lies within
-//       [2^-10, 2688], exact in f16, so the scale goes onto the weight and the
-//       MMAs accumulate throughout (post-scaling would cost 4 FMAs per 16 columns).
-// Lane (g, t) of an MMA takes, of each 32 columns, columns 8t .. 8t + 7 of its
-// rows: 4 bytes of codes and 16 bytes of a token, in an order of K of its own
-// that both operands share.
+// Digits.  With u = 2^(e - 1) for a block whose largest magnitude has the exponent
+// e, x / u lies in (-4, 4) and is written to the base 8 in DIGITS digits of -4..4,
+//   x = u sum_d digit_d 8^-d,
+// all of them e2m1 values.  A row becomes DIGITS rows of codes under one scale
+// per block, u relative to the row's largest; a product's columns of one row's
+// digits are added up as sum_d 8^-d by the epilogue, which multiplies the row's
+// own power of two on.  The digits hold 36 bits: magnitudes down to 2^-27 of their
+// block's largest are exact, smaller ones off by at most 2^-35 of it.  (NV scales
+// reach over 2^17 only: a block below 2^-17 of its row's largest counts as if it
+// were there.)  Products and sums are those of the tensor cores, exact and fp32.
 //
-// A cluster of CTAs may share a tile along K (few tiles, long K); their sums meet
-// through distributed shared memory in a fixed order.
-#include <cuda_fp16.h>
+// Weights are the MMA's 128-row operand, two of them side by side (gate and up,
+// or 256 columns of y); up to 8 rows are its 96 columns.  A stage holds 256
+// columns of K.  The work is the list of (tile, stage) steps, cut into equal
+// runs, one per CTA: a tile that two or more CTAs share is added up from its
+// parts by the one that comes last (an atomic counter finds it; the parts are
+// added in the order of K, so the result does not depend on who that is).
+//
+// A row with infinities or NaN has them left out of its digits and added by the
+// epilogue, weight by weight: slow, but what the products give.
+//
+// Roles (8 warps): 0 TMA of the weights (which start before the rows' digits are
+// ready), 3 TMA of the digits, 1 MMA, 2 setup, 4-7 epilogue.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <mutex>
 
-#include "fp4.cuh"
+#include "fp4_mma.cuh"
 #include "internal.h"
 
 namespace moe {
@@ -47,170 +53,306 @@ namespace {
 
 constexpr int MAX_GROUPS = 1024;
 constexpr int THREADS = 256;
-constexpr int ROWS = 128;                    // weight rows of a tile
-constexpr int KC = 256;                      // columns of a stage
-constexpr int W_BYTES = ROWS * KC / 2;
-constexpr int P_LD = ROWS + 4;               // row stride of the partial sums, in floats
+constexpr int TOK = 8;                       // rows of a tile
+constexpr int DIGITS = 12;
+constexpr int NB = TOK * DIGITS;             // 96 columns of an MMA
+constexpr int BK = 256;                      // elements of K per stage: 128 bytes
+constexpr int A_BYTES = 128 * BK / 2;        // of one of the two weight operands
+constexpr int B_BYTES = NB * BK / 2;
+constexpr int STAGES = 4;
+constexpr int SF_COL = 4 * NB;               // two accumulators of two operands, then scales
+constexpr int SF_SET = 24;                   // two scale tiles of each of three operands
+constexpr int TMEM_COLS = 512;
+constexpr int PART = TOK * 256;              // floats of a tile's partial sums
+
+template <int FMT>
+struct Cfg {
+    static constexpr int TILES = BK / Fp4<FMT>::TILE_K;          // scale tiles per stage along K
+    static constexpr int SF_BYTES = TILES * kScaleTile;
+    static constexpr int W_LOAD = 2 * (A_BYTES + SF_BYTES), X_LOAD = B_BYTES + SF_BYTES;
+    static constexpr int STAGE = W_LOAD + X_LOAD;
+    static constexpr int BAR_OFF = STAGES * STAGE;
+    static constexpr int NBARS = 2 * STAGES + 5;                 // full, empty, tfull, tempty, drain
+    static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
+    static constexpr int OFFS_OFF = MISC_OFF + 16;
+    static constexpr int smem(int G) { return 1024 + OFFS_OFF + (2 * G + 2) * 4; }
+    // block scale of a row's largest block: 2^TOP; and how far below it others go
+    static constexpr int TOP = FMT == MOE_FP4_MX ? 20 : 8, RANGE = FMT == MOE_FP4_MX ? 60 : 17;
+    static_assert(STAGE % 1024 == 0, "swizzled tiles need 1 KB alignment");
+    static_assert(smem(MAX_GROUPS) <= 227 * 1024, "shared memory");
+    static_assert(SF_COL + 2 * SF_SET <= TMEM_COLS, "scale columns");
+};
+constexpr int MIN_E = 27;                    // biased exponent a row's largest counts as at least
+
+// Workspace: digits [n * DIGITS, K / 2] bytes, their scale tiles, row factors
+// (negative: the row holds infinities or NaN), counters of shared tiles, parts.
+struct Ws {
+    size_t q, sf, scale, counter, part, total;
+};
 
 struct Params {
-    const uint8_t *q, *sf;
-    const uint16_t *xh;                      // f16 rows [n, K]
-    const float *xscale;                     // what takes their scaling off again
+    CUtensorMap tmA, tmSA;     // weights' codes [G, rows, K / 2] and scale tiles
+    CUtensorMap tmB, tmSB;     // digits
+    const uint16_t *x;
+    const uint8_t *q, *sf;     // weights, for rows with infinities or NaN
+    const float *row_scale;
+    unsigned int *counter;     // [tiles]
+    float *part;               // [2 * CTAs][TOK][256]
     const int32_t *offsets;
-    int32_t G, n, K, N;                      // N: output columns
-    int32_t wrows;                           // rows of a group's weights
-    int32_t split;                           // CTAs that share a tile along K
-    float alpha;                             // 2^scale_exp
+    int32_t G, n, K, N;        // N: output columns
+    int32_t wrows;             // rows of a group's weights
+    int32_t nt;                // column tiles
+    float alpha;               // 2^scale_exp
     void *out;
     int32_t out_f32;
     int32_t *dev_status;
 };
 
-template <int FMT, bool SWIGLU, int MAXT>
-struct Cfg {
-    static constexpr int STAGES = MAXT == 8 ? 4 : 3;
-    static constexpr int KTILES = KC / Fp4<FMT>::TILE_K;              // scale tiles along K
-    static constexpr int S_TILES = KTILES * (SWIGLU ? 2 : 1);
-    static constexpr int S_BYTES = S_TILES * kScaleTile;
-    static constexpr int X_BYTES = MAXT * KC * 2;
-    static constexpr int STAGE = W_BYTES + S_BYTES + X_BYTES;
-    static constexpr int P_OFF = STAGES * STAGE;
-    static constexpr int P_BYTES = MAXT * P_LD * 4;                   // one of two buffers
-    static constexpr int OFFS_OFF = P_OFF + 2 * P_BYTES;
-    static constexpr int smem(int G) { return OFFS_OFF + (2 * G + 3) * 4; }
-    // two CTAs a multiprocessor, 1 KB of each taken by the system
-    static_assert(2 * (smem(MAX_GROUPS) + 1024) <= 228 * 1024, "shared memory");
+// ------------------------------------------------------------------ digits
+constexpr int PREP_THREADS = 256;
+struct PrepParams {
+    const uint16_t *x;
+    const int32_t *offsets;
+    int32_t G, n, K;
+    uint8_t *q, *sf;
+    float *row_scale;
+    unsigned int *counter;
+    int32_t n_counter;
 };
 
-// 16 bytes, or zeros.
-__device__ __forceinline__ void copy16(void *dst, const void *src, bool read) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)),
-                 "l"(reinterpret_cast<uint64_t>(src)), "r"(read ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// Eight codes to four pairs of f16 values.
-__device__ __forceinline__ void decode8(uint32_t w, uint32_t (&v)[4]) {
-    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-        : "r"(w));
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-// Byte `i` of w as an e4m3 value, twice.
-__device__ __forceinline__ uint32_t e4m3_f16x2(uint32_t w, uint32_t i) {
-    uint32_t r;
-    const uint16_t b = static_cast<uint16_t>(__byte_perm(w, 0, i * 0x11u));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(b));
-    return r;
-}
-// Four scale bytes 2^(b - 127) as fp32 (255: NaN).
-__device__ __forceinline__ void e8m0x4(uint32_t w, float (&s)[4]) {
-    uint32_t lo, hi;
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-        "cvt.rn.bf16x2.ue8m0x2 %0, a;\n\tcvt.rn.bf16x2.ue8m0x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
-    s[0] = __uint_as_float(lo << 16);
-    s[1] = __uint_as_float(lo & 0xFFFF0000u);
-    s[2] = __uint_as_float(hi << 16);
-    s[3] = __uint_as_float(hi & 0xFFFF0000u);
-}
-
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
-
-// Rows to f16 under a power of two of their own; one CTA per row.
-constexpr int PREP_THREADS = 256;
-__global__ void __launch_bounds__(PREP_THREADS)
-    prep_kernel(const uint16_t *__restrict__ x, int K, uint16_t *__restrict__ xh,
-                float *__restrict__ xscale) {
+// One CTA per row.
+template <int FMT>
+__global__ void __launch_bounds__(PREP_THREADS) digits_kernel(const PrepParams p) {
+    using C = Cfg<FMT>;
+    constexpr int LANES = Fp4<FMT>::BLOCK / 8;         // lanes that share a block
     __shared__ uint32_t s_max[PREP_THREADS / 32];
+    __shared__ int s_bad[PREP_THREADS / 32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // from here on everything before this call has ended: the products may start
-    // on the weights and the offsets, and wait for the rows
+    // on the weights and the offsets, and wait for the digits
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int64_t base = static_cast<int64_t>(blockIdx.x) * K;
-    const uint4 *row = reinterpret_cast<const uint4 *>(x + base);
-    const int nv = K / 8;
+    const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int i = row * PREP_THREADS + tid; i < p.n_counter; i += gridDim.x * PREP_THREADS)
+        p.counter[i] = 0u;
+    const uint4 *src = reinterpret_cast<const uint4 *>(p.x + static_cast<int64_t>(row) * p.K);
+    const int nv = p.K / 8;
     uint32_t m = 0;
-    for (int i = threadIdx.x; i < nv; i += PREP_THREADS) {
-        const uint4 v = row[i];
+    int bad = 0;
+    for (int i = tid; i < nv; i += PREP_THREADS) {
+        const uint4 v = __ldg(src + i);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const uint32_t a = w[j] & 0x7FFFu, b = (w[j] >> 16) & 0x7FFFu;
-            if (a < 0x7F80u) m = max(m, a);
-            if (b < 0x7F80u) m = max(m, b);
+            if (a < 0x7F80u) m = max(m, a); else bad = 1;
+            if (b < 0x7F80u) m = max(m, b); else bad = 1;
         }
     }
+    // the row's group: the last one that starts at or in front of it
+    int g = -1;
+    for (int g0 = 0; g0 < p.G; g0 += PREP_THREADS)
+        g += __syncthreads_count(g0 + tid < p.G && __ldg(p.offsets + min(g0 + tid, p.G - 1)) <= row);
     m = __reduce_max_sync(0xffffffffu, m);
-    if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
+    bad = __any_sync(0xffffffffu, bad);
+    if (lane == 0) {
+        s_max[warp] = m;
+        s_bad[warp] = bad;
+    }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < PREP_THREADS / 32; ++i) m = max(m, s_max[i]);
-    // 2^(142 - e) of the maximum's exponent field e, at most 2^127
-    const int e = max(static_cast<int>(m >> 7), 15);
-    const float up = pow2f(142 - e);
-    if (threadIdx.x == 0)   // 2^(e - 142), which may be subnormal
-        xscale[blockIdx.x] = e >= 16 ? pow2f(e - 142) : __uint_as_float(1u << 22);
-    uint4 *dst = reinterpret_cast<uint4 *>(xh + base);
-    for (int i = threadIdx.x; i < nv; i += PREP_THREADS) {
-        const uint4 v = row[i];
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t o[4];
+    for (int i = 0; i < PREP_THREADS / 32; ++i) {
+        m = max(m, s_max[i]);
+        bad |= s_bad[i];
+    }
+    const int e_row = max(static_cast<int>(m >> 7), MIN_E);
+    // 1 / u of a block is 2^(127 - e_row) 2^(1 - rel), both within fp32's exponents
+    const float inv_row = pow2f(max(127 - e_row, -126));
+    const int one = e_row == 254 ? 0 : 1;
+    // u * 2^-TOP of the largest block
+    if (tid == 0) {
+        const float f = pow2f(e_row - 127 - 1 - C::TOP);
+        p.row_scale[row] = bad ? -f : f;
+    }
+    const int start = g >= 0 ? __ldg(p.offsets + g) : -1;
+    const bool owned = start >= 0 && start <= row && row < __ldg(p.offsets + g + 1);
+    const int local = row - start;
+    uint8_t *sf = p.sf + (static_cast<int64_t>(start / TOK) + g + local / TOK) *
+                             (p.K / Fp4<FMT>::TILE_K) * kScaleTile;
+    const int digit_row = (local % TOK) * DIGITS;
+    uint8_t *dst = p.q + static_cast<int64_t>(row) * DIGITS * (p.K / 2);
+    for (int i0 = warp * 32; i0 < nv; i0 += PREP_THREADS) {
+        const int i = i0 + lane;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (i < nv) v = __ldg(src + i);
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const __half2 h = __floats2half2_rn(__uint_as_float(w[j] << 16) * up,
-                                                __uint_as_float(w[j] & 0xFFFF0000u) * up);
-            o[j] = *reinterpret_cast<const uint32_t *>(&h);
+        for (int j = 0; j < 4; ++j) {                  // infinities and NaN count as zero
+            if ((w[j] & 0x7F80u) == 0x7F80u) w[j] &= 0xFFFF0000u;
+            if ((w[j] & 0x7F800000u) == 0x7F800000u) w[j] &= 0xFFFFu;
         }
-        dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
+        uint32_t am = amax8(w);
+#pragma unroll
+        for (int o = 1; o < LANES; o <<= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
+        const int rel = max(static_cast<int>(am >> 7) - e_row, -C::RANGE);      // <= 0
+        const float inv = pow2f(one - rel);
+        float t[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {                  // x / u: two exact products
+            t[2 * j] = __uint_as_float(w[j] << 16) * inv_row * inv;
+            t[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u) * inv_row * inv;
+        }
+#pragma unroll
+        for (int d = 0; d < DIGITS; ++d) {
+            float r[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                r[j] = rintf(t[j]);
+                t[j] = (t[j] - r[j]) * 8.0f;
+            }
+            if (i < nv)
+                *reinterpret_cast<uint32_t *>(dst + static_cast<int64_t>(d) * (p.K / 2) + i * 4) = e2m1x8(r);
+        }
+        if (i < nv && owned) {
+            const int e = C::TOP + rel;
+            const uint32_t byte = FMT == MOE_FP4_MX ? static_cast<uint32_t>(127 + e)
+                                  : e >= -6         ? static_cast<uint32_t>((e + 7) << 3)
+                                                    : 1u << (e + 9);
+            const int b = i / LANES;                   // block: its lanes share the digits' rows
+            uint8_t *at = sf + (b >> 2) * kScaleTile + (b & 3);
+            for (int d = lane % LANES; d < DIGITS; d += LANES)
+                at[scale_row_offset(digit_row + d)] = static_cast<uint8_t>(byte);
+        }
     }
 }
 
-struct Item {
-    int g, tok0, cnt, n0;      // group, first row and number of rows, first output column
-};
+// ------------------------------------------------------------------ products
+__device__ __forceinline__ void tmem_ld12(uint32_t taddr, float (&v)[DIGITS]) {
+    uint32_t r[DIGITS];
+#pragma unroll
+    for (int i = 0; i < DIGITS; i += 4)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3])
+                     : "r"(taddr + static_cast<uint32_t>(i))
+                     : "memory");
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < DIGITS; ++i) v[i] = __uint_as_float(r[i]);
+}
+// sum_d 8^-d v_d
+__device__ __forceinline__ float add_digits(const float (&v)[DIGITS]) {
+    float s = v[DIGITS - 1];
+#pragma unroll
+    for (int d = DIGITS - 2; d >= 0; --d) s = fmaf(s, 0.125f, v[d]);
+    return s;
+}
 
-template <int FMT, bool SWIGLU, int MAXT>
-__global__ void __launch_bounds__(THREADS, 2) weight_kernel(const Params p) {
-    using C = Cfg<FMT, SWIGLU, MAXT>;
-    constexpr int STAGES = C::STAGES, NT = MAXT / 8, OUT = SWIGLU ? ROWS / 2 : ROWS;
-    extern __shared__ __align__(128) uint8_t smem[];
+// Half a stage of NV (or all of MX): two scale tiles of each operand to one of
+// two sets of columns in turn, then the MMAs that use them.
+template <int FMT>
+__device__ __forceinline__ void issue_tiles(uint32_t d, uint32_t a, uint32_t b, uint32_t sa, uint32_t sb,
+                                            uint32_t sf_col, int steps, bool accumulate) {
+    constexpr uint32_t ID0 = idesc<FMT>(128, NB, 0), ID2 = idesc<FMT>(128, NB, 2);
+    constexpr uint32_t S1 = Cfg<FMT>::SF_BYTES / 16, A1 = A_BYTES / 16;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        copy_scales<1>(sf_col + 4 * i, sa + i * (kScaleTile / 16));
+        copy_scales<1>(sf_col + 8 + 4 * i, sa + S1 + i * (kScaleTile / 16));
+        copy_scales<1>(sf_col + 16 + 4 * i, sb + i * (kScaleTile / 16));
+    }
+    constexpr int PER = FMT == MOE_FP4_MX ? 4 : 2;       // MMAs of 64 columns of K
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        if (j >= steps) break;
+        const int i = FMT == MOE_FP4_MX ? j / 2 : j;
+        const uint32_t id = FMT == MOE_FP4_MX && (j & 1) ? ID2 : ID0;
+        const uint32_t acc = j > 0 || accumulate ? 1u : 0u;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            mma_fp4<FMT, 1>(d + h * NB, a + h * A1 + j * 2, b + j * 2, id, sf_col + 8 * h + 4 * i,
+                            sf_col + 16 + 4 * i, acc);
+    }
+}
+
+struct Tile {
+    int g, row0, cnt, n_blk;
+};
+// A CTA's run of (tile, stage) steps.
+struct Run {
+    int64_t at, end;
+};
+__device__ __forceinline__ Run run_of(int64_t steps, int ctas, int i) {
+    return Run{steps * i / ctas, steps * (i + 1) / ctas};
+}
+
+// What a row's infinities and NaN add to its product with weight row `wr`.
+template <int FMT>
+__device__ __noinline__ float odd_terms(const Params &p, int row, int64_t wr) {
+    const uint16_t *x = p.x + static_cast<int64_t>(row) * p.K;
+    const uint8_t *q = p.q + wr * (p.K / 2);
+    const uint8_t *sf = p.sf + wr / 128 * (p.K / Fp4<FMT>::TILE_K) * kScaleTile +
+                        scale_row_offset(static_cast<int>(wr % 128));
+    float s = 0.0f;
+    for (int k = 0; k < p.K; ++k) {
+        const uint16_t b = __ldg(x + k);
+        if ((b & 0x7F80u) != 0x7F80u) continue;
+        const uint32_t c = __ldg(q + k / 2) >> (4 * (k & 1)) & 15u;
+        const int blk = k / Fp4<FMT>::BLOCK;
+        const uint32_t sb = __ldg(sf + (blk >> 2) * kScaleTile + (blk & 3));
+        const uint32_t e = c >> 1 & 3u, m = c & 1u;
+        const float mag = e == 0 ? 0.5f * m : static_cast<float>(2u + m) * 0.25f * (1u << e);
+        float scale;
+        if (FMT == MOE_FP4_MX)
+            scale = sb == 255u ? __uint_as_float(0x7FC00000u)
+                               : (sb == 0 ? __uint_as_float(1u << 22) : pow2f(static_cast<int>(sb) - 127));
+        else
+            scale = (sb & 127u) == 127u ? __uint_as_float(0x7FC00000u) : e4m3_value(sb);
+        s += bf16_bits_to_float(b) * ((c & 8u ? -mag : mag) * scale);
+    }
+    return s;
+}
+
+template <int FMT, bool SWIGLU>
+__global__ void __launch_bounds__(THREADS, 1) weight_kernel(const __grid_constant__ Params p) {
+    using C = Cfg<FMT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);
+    uint64_t *empty = full + STAGES;
+    uint64_t *tfull = empty + STAGES;       // [2]
+    uint64_t *tempty = tfull + 2;           // [2]
+    uint64_t *drain = tempty + 2;
+    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF);
+    volatile int *s_abort = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 4);
+    volatile int *s_bad = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 8);
+    volatile int *s_last = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 12);
     int *s_off = reinterpret_cast<int *>(smem + C::OFFS_OFF);
     int *s_prefix = s_off + p.G + 1;
-    int *s_bad = s_prefix + p.G + 1;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rank = static_cast<int>(blockIdx.x) % p.split;
-    const int unit = static_cast<int>(blockIdx.x) / p.split;
-    const int units = static_cast<int>(gridDim.x) / p.split;
-    const int rtiles = p.N / OUT;
 
-    // items of the groups before each
-    for (int g = tid; g <= p.G; g += THREADS) s_off[g] = p.offsets[g];
+    if (warp == 1) {
+        tmem_alloc(s_tmem, TMEM_COLS);
+        tmem_relinquish();
+    } else if (warp == 2 && elect_one()) {
+        *s_abort = 0;
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 2);          // each producer arms its share
+            mbar_init(&empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], 4);
+        }
+        mbar_init(drain, 1);
+        fence_barrier_init();
+    } else if (warp == 3 && elect_one()) {
+        tma_prefetch_desc(&p.tmA);
+        tma_prefetch_desc(&p.tmB);
+        tma_prefetch_desc(&p.tmSA);
+        tma_prefetch_desc(&p.tmSB);
+    }
+    // tiles of the groups before each (the offsets are not the digits' kernel's)
+    for (int g = tid; g <= p.G; g += THREADS) s_off[g] = __ldg(p.offsets + g);
     if (tid == 0) *s_bad = 0;
     __syncthreads();
     if (warp == 0) {
@@ -218,262 +360,334 @@ __global__ void __launch_bounds__(THREADS, 2) weight_kernel(const Params p) {
         bool bad = false;
         for (int g0 = 0; g0 < p.G; g0 += 32) {
             const int g = g0 + lane;
-            int items = 0;
+            int tiles = 0;
             if (g < p.G) {
                 const int a = s_off[g], b = s_off[g + 1];
                 if (a < 0 || b < a || b > p.n) bad = true;
-                items = b > a ? ((b - a + MAXT - 1) / MAXT) * rtiles : 0;
+                tiles = b > a ? ((b - a + TOK - 1) / TOK) * p.nt : 0;
             }
-            int inc = items;
+            int inc = tiles;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const int o = __shfl_up_sync(0xffffffffu, inc, off);
                 if (lane >= off) inc += o;
             }
-            if (g < p.G) s_prefix[g] = run + inc - items;
+            if (g < p.G) s_prefix[g] = run + inc - tiles;
             run += __shfl_sync(0xffffffffu, inc, 31);
         }
         if (lane == 0) s_prefix[p.G] = run;
         if (__any_sync(0xffffffffu, bad) && lane == 0) *s_bad = 1;
     }
+    tc_fence_before();
     __syncthreads();
-    if (*s_bad && tid == 0 && blockIdx.x == 0) report(p.dev_status, MOE_DEV_BAD_OFFSETS);
-    const int total = *s_bad ? 0 : s_prefix[p.G];
-
-    auto decode = [&](int item, int &g) {
-        while (s_prefix[g + 1] <= item) ++g;
-        const int start = s_off[g], cnt = s_off[g + 1] - start;
-        const int local = item - s_prefix[g];
-        const int chunks = (cnt + MAXT - 1) / MAXT;      // next to each other: they share weights
-        const int tile = local / chunks, c = local - tile * chunks;
-        return Item{g, start + c * MAXT, min(MAXT, cnt - c * MAXT), tile * OUT};
-    };
-    const int stages_k = (p.K + KC - 1) / KC;
-    const int k_begin = rank * stages_k / p.split, k_end = (rank + 1) * stages_k / p.split;
-    const int64_t ktiles = p.K / Fp4<FMT>::TILE_K;       // scale tiles along K
-
-    // The copies run ahead of the products by STAGES - 1 stages, across items.
-    int ld_item = unit, ld_k = k_begin, ld_slot = 0, ld_g = 0;
-    Item ld{};
-    if (ld_item < total) ld = decode(ld_item, ld_g);
-    auto copy_weights = [&](int slot, const Item &it, int ks) {
-        uint8_t *w = smem + slot * C::STAGE, *s = w + W_BYTES;
-        const int64_t half = p.K / 2;
-        // row r's 16-byte piece c lies at c ^ (r & 7)
-#pragma unroll
-        for (int i = 0; i < W_BYTES / 16 / THREADS; ++i) {
-            const int e = i * THREADS + tid, r = e >> 3, c = e & 7;
-            const int64_t wr = static_cast<int64_t>(it.g) * p.wrows + it.n0 +
-                               (SWIGLU && r >= 64 ? p.N + r - 64 : r);
-            const int col = ks * (KC / 2) + c * 16;
-            const bool in = col < half;
-            copy16(w + r * (KC / 2) + ((c ^ (r & 7)) << 4), p.q + wr * half + (in ? col : 0), in);
-        }
-        for (int e = tid; e < C::S_BYTES / 16; e += THREADS) {
-            const int t = e >> 5, c = e & 31;            // scale tile, 16-byte piece
-            const int part = t / C::KTILES, kt = ks * C::KTILES + t % C::KTILES;
-            const int64_t blk = (static_cast<int64_t>(it.g) * p.wrows + it.n0 +
-                                 (part ? p.N : 0)) / 128;
-            const bool in = kt < ktiles;
-            copy16(s + t * kScaleTile + c * 16,
-                   p.sf + (blk * ktiles + (in ? kt : 0)) * kScaleTile + c * 16, in);
-        }
-    };
-    auto copy_rows = [&](int slot, const Item &it, int ks) {
-        uint8_t *x = smem + slot * C::STAGE + W_BYTES + C::S_BYTES;
-        // token j's 16-byte piece c lies at c ^ (4 (j & 1))
-#pragma unroll
-        for (int i = 0; i < C::X_BYTES / 16 / THREADS; ++i) {
-            const int e = i * THREADS + tid, j = e >> 5, c = e & 31;
-            const int col = ks * KC + c * 8;
-            const bool in = j < it.cnt && col < p.K;
-            copy16(x + j * (KC * 2) + ((c ^ ((j & 1) << 2)) << 4),
-                   p.xh + (in ? static_cast<int64_t>(it.tok0 + j) * p.K + col : 0), in);
-        }
-    };
-    auto advance = [&]() {
-        if (++ld_slot == STAGES) ld_slot = 0;
-        if (++ld_k == k_end) {
-            ld_k = k_begin;
-            ld_item += units;
-            if (ld_item < total) ld = decode(ld_item, ld_g);
-        }
-    };
-    {
-        // weights first: they do not wait for the rows' conversion
-        const int item0 = ld_item, k0 = ld_k, g0 = ld_g;
-        const Item it0 = ld;
-        for (int s = 0; s < STAGES - 1; ++s) {
-            if (ld_item < total) copy_weights(s, ld, ld_k);
-            advance();
-        }
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        ld_item = item0;
-        ld_k = k0;
-        ld_g = g0;
-        ld = it0;
-        ld_slot = 0;
-        for (int s = 0; s < STAGES - 1; ++s) {
-            if (ld_item < total) copy_rows(s, ld, ld_k);
-            copy_commit();
-            advance();
-        }
-    }
+    tc_fence_after();
+    // a kernel that follows may start to get ready (it waits for this one's end)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (*s_bad && tid == 0 && blockIdx.x == 0) report(p.dev_status, MOE_DEV_BAD_OFFSETS);
+    const int kst = (p.K + BK - 1) / BK;
+    const int64_t steps = *s_bad ? 0 : static_cast<int64_t>(s_prefix[p.G]) * kst;
+    // two steps each at least, as far as they go
+    const int ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), (steps + 1) / 2));
+    const int me = static_cast<int>(blockIdx.x);
+    const Run run = me < ctas ? run_of(steps, ctas, me) : Run{0, 0};
+    const uint32_t tmem = *s_tmem;
+    const int64_t ktiles = p.K / Fp4<FMT>::TILE_K;
 
-    const int wr = (warp & 3) * 32, khalf = warp >> 2;   // this warp's rows, and its half of a stage
-    const int g8 = lane >> 2, t4 = lane & 3;
-    int slot = 0, g = 0, parity = 0;
-    for (int item = unit; item < total; item += units) {
-        const Item it = decode(item, g);
-        const int nt = (it.cnt + 7) >> 3;
-        // where this warp's rows have their scales: tile part and row in it
-        const int s_part = SWIGLU && wr >= 64 ? 1 : 0;
-        const int s_row = (SWIGLU ? it.n0 & 64 : 0) + (SWIGLU ? wr & 63 : wr);
-        float acc[2][NT][4];
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
-        for (int ks = k_begin; ks < k_end; ++ks) {
-            copy_wait<STAGES - 2>();
-            __syncthreads();
-            if (ld_item < total) {
-                copy_weights(ld_slot, ld, ld_k);
-                copy_rows(ld_slot, ld, ld_k);
+    auto decode = [&](int tile, int &g) {
+        while (s_prefix[g + 1] <= tile) ++g;
+        const int start = s_off[g], cnt = s_off[g + 1] - start;
+        const int local = tile - s_prefix[g], chunks = (cnt + TOK - 1) / TOK;
+        const int n_blk = local / chunks, c = local - n_blk * chunks;    // chunks side by side:
+        return Tile{g, start + c * TOK, min(TOK, cnt - c * TOK), n_blk};  // they share weights
+    };
+
+    if (warp == 0 || warp == 3) {
+        // ================= TMA producers: warp 0 the weights, warp 3 the digits
+        if (elect_one()) {
+            const bool weights = warp == 0;
+            if (!weights) asm volatile("griddepcontrol.wait;" ::: "memory");
+            int stage = 0, g = 0;
+            uint32_t phase = 0;
+            int armed[STAGES];
+            for (int s = 0; s < STAGES; ++s) armed[s] = -1;
+            bool ok = true;
+            for (int64_t u = run.at; u < run.end && ok && !*s_abort;) {
+                const int tile = static_cast<int>(u / kst), k0 = static_cast<int>(u % kst);
+                const int k1 = static_cast<int>(min(static_cast<int64_t>(kst), k0 + (run.end - u)));
+                const Tile t = decode(tile, g);
+                const int n0 = t.n_blk * (SWIGLU ? 128 : 256), n1 = SWIGLU ? p.N + n0 : n0 + 128;
+                const int64_t blk = static_cast<int64_t>(t.g) * (p.wrows / 128);
+                const int sa0 = static_cast<int>((blk + n0 / 128) * ktiles);
+                const int sa1 = static_cast<int>((blk + n1 / 128) * ktiles);
+                const int start = s_off[t.g];
+                const int sb = static_cast<int>(
+                    (static_cast<int64_t>(start / TOK) + t.g + (t.row0 - start) / TOK) * ktiles);
+                for (int kb = k0; kb < k1; ++kb) {
+                    if (!wait_phase(&empty[stage], phase ^ 1, s_abort, p.dev_status)) {
+                        ok = false;
+                        break;
+                    }
+                    armed[stage] = static_cast<int>(phase);
+                    uint8_t *s = smem + stage * C::STAGE;
+                    uint8_t *b = s + 2 * A_BYTES, *sf = b + B_BYTES;
+                    const int c = kb * (BK / 2), kt = kb * C::TILES;
+                    mbar_arrive_expect_tx(&full[stage], weights ? C::W_LOAD : C::X_LOAD);
+                    if (weights) {
+                        tma_load_3d(s, &p.tmA, &full[stage], c, n0, t.g);
+                        tma_load_3d(s + A_BYTES, &p.tmA, &full[stage], c, n1, t.g);
+                        tma_load_2d(sf, &p.tmSA, &full[stage], 0, sa0 + kt);
+                        tma_load_2d(sf + C::SF_BYTES, &p.tmSA, &full[stage], 0, sa1 + kt);
+                    } else {
+                        tma_load_2d(b, &p.tmB, &full[stage], c, t.row0 * DIGITS);
+                        tma_load_2d(sf + 2 * C::SF_BYTES, &p.tmSB, &full[stage], 0, sb + kt);
+                    }
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                u += k1 - k0;
             }
-            copy_commit();
-            advance();
-            const uint8_t *w = smem + slot * C::STAGE;
-            const uint8_t *s = w + W_BYTES + s_part * C::KTILES * kScaleTile;
-            const uint8_t *x = w + W_BYTES + C::S_BYTES;
-            if (++slot == STAGES) slot = 0;
-            // scales of rows g8 and g8 + 8 of both 16-row parts
-            uint32_t sw[2][2][C::KTILES / 2];
+            if (*s_abort)
+                for (int s = 0; s < STAGES; ++s)
+                    if (armed[s] >= 0) mbar_wait_drain(&full[s], static_cast<uint32_t>(armed[s]));
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ================= MMA issuer
+        if (elect_one()) {
+            int stage = 0;
+            uint32_t phase = 0, n = 0, set = 0;
+            const uint32_t base = smem_u32(smem) >> 4;
+            bool issued = false, ok = true;
+            for (int64_t u = run.at; u < run.end && ok && !*s_abort; ++n) {
+                const int k0 = static_cast<int>(u % kst);
+                const int k1 = static_cast<int>(min(static_cast<int64_t>(kst), k0 + (run.end - u)));
+                if (!wait_phase(&tempty[n & 1], ((n >> 1) & 1) ^ 1, s_abort, p.dev_status)) break;
+                tc_fence_after();
+                const uint32_t d = tmem + (n & 1) * (2 * NB);
+                for (int kb = k0; kb < k1; ++kb) {
+                    if (!wait_phase(&full[stage], phase, s_abort, p.dev_status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t at = base + static_cast<uint32_t>(stage) * (C::STAGE / 16);
+                    const uint32_t a = at + OPERAND_LO, b = a + 2 * A_BYTES / 16;
+                    const uint32_t sa = at + (2 * A_BYTES + B_BYTES) / 16 + SCALES_LO;
+                    const uint32_t sb = sa + 2 * C::SF_BYTES / 16;
+                    const int left = (p.K - kb * BK) / 64;       // MMA steps of this slice (2 or more)
+                    constexpr int PER = FMT == MOE_FP4_MX ? 4 : 2;
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int k = 0; k < C::KTILES / 2; ++k)
-                        sw[m][h][k] = *reinterpret_cast<const uint32_t *>(
-                            s + (khalf * (C::KTILES / 2) + k) * kScaleTile +
-                            scale_row_offset(s_row + 16 * m + 8 * h + g8)) &
-                            (FMT == MOE_FP4_NV ? 0x7F7F7F7Fu : 0xFFFFFFFFu);
-            float sc[2][2][4];
-            if (FMT == MOE_FP4_MX) {
-#pragma unroll
-                for (int m = 0; m < 2; ++m)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) e8m0x4(sw[m][h][0], sc[m][h]);
+                    for (int h = 0; h < 4 / PER; ++h) {
+                        if (h * PER >= left) break;
+                        issue_tiles<FMT>(d, a + h * PER * 2, b + h * PER * 2,
+                                         sa + h * 2 * (kScaleTile / 16), sb + h * 2 * (kScaleTile / 16),
+                                         tmem + SF_COL + set * SF_SET, left - h * PER, kb > k0 || h > 0);
+                        set ^= 1;
+                    }
+                    issued = true;
+                    tc_commit(&empty[stage]);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (!ok) break;
+                tc_commit(&tfull[n & 1]);
+                u += k1 - k0;
             }
+            if (*s_abort && issued) {
+                // unwinding: every MMA issued so far ends before TMEM is freed
+                tc_commit(drain);
+                mbar_wait_drain(drain, 0);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ================= epilogue: thread = weight row `r` of both operands
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        const int r = (warp & 3) * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        uint32_t n = 0;
+        int g = 0;
+        for (int64_t u = run.at; u < run.end; ++n) {
+            const int tile = static_cast<int>(u / kst), k0 = static_cast<int>(u % kst);
+            const int k1 = static_cast<int>(min(static_cast<int64_t>(kst), k0 + (run.end - u)));
+            u += k1 - k0;
+            const Tile t = decode(tile, g);
+            if (!wait_phase(&tfull[n & 1], (n >> 1) & 1, s_abort, p.dev_status)) break;
+            tc_fence_after();
+            float v[2][TOK];
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {                 // 32 columns at a time
-                const int kb = khalf * 4 + b;
-                uint4 xb[NT];
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    if (j < nt)
-                        xb[j] = *reinterpret_cast<const uint4 *>(
-                            x + (8 * j + g8) * (KC * 2) +
-                            (((kb * 4 + t4) ^ ((g8 & 1) << 2)) << 4));
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    uint32_t a[2][4];
+            for (int j = 0; j < TOK; ++j) {
+                v[0][j] = v[1][j] = 0.0f;
+                if (j < t.cnt) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const int r = wr + 16 * m + 8 * h + g8;
-                        decode8(*reinterpret_cast<const uint32_t *>(
-                                    w + r * (KC / 2) + ((kb ^ (r & 7)) << 4) + t4 * 4),
-                                a[h]);
-                        if (FMT == MOE_FP4_NV) {
-                            // blocks 2b and 2b + 1: this lane's bytes lie in one of them
-                            const uint32_t f = e4m3_f16x2(sw[m][h][b / 2],
-                                                          (2 * b & 3) + (t4 >> 1));
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) a[h][i] = mul_f16x2(a[h][i], f);
-                        }
-                    }
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        if (j >= nt) break;
-                        if (FMT == MOE_FP4_NV) {
-                            mma16816(acc[m][j], a[0][0], a[1][0], a[0][1], a[1][1], xb[j].x, xb[j].y);
-                            mma16816(acc[m][j], a[0][2], a[1][2], a[0][3], a[1][3], xb[j].z, xb[j].w);
-                        } else {
-                            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                            mma16816(d, a[0][0], a[1][0], a[0][1], a[1][1], xb[j].x, xb[j].y);
-                            mma16816(d, a[0][2], a[1][2], a[0][3], a[1][3], xb[j].z, xb[j].w);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                acc[m][j][i] = fmaf(d[i], sc[m][i >> 1][b], acc[m][j][i]);
-                        }
+                        float d[DIGITS];
+                        __syncwarp();
+                        tmem_ld12(tmem + lanes + (n & 1) * (2 * NB) + h * NB + j * DIGITS, d);
+                        v[h][j] = add_digits(d);
                     }
                 }
             }
-        }
-        // The halves of the stages are added, then the CTAs' sums: [token][row].
-        float *P = reinterpret_cast<float *>(smem + C::P_OFF + parity * C::P_BYTES);
-        auto at = [&](int m, int j, int i) -> float & {
-            return P[(8 * j + 2 * t4 + (i & 1)) * P_LD + wr + 16 * m + g8 + 8 * (i >> 1)];
-        };
-        if (khalf == 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tempty[n & 1]);
+            if (k1 - k0 < kst) {
+                // part of a tile: the last of its CTAs adds the parts up
+                const int64_t first = static_cast<int64_t>(tile) * kst, last = first + kst - 1;
+                // the run that holds step s: i with steps i / ctas <= s, the largest
+                auto owner = [&](int64_t s) {
+                    int i = static_cast<int>(s * ctas / steps);
+                    while (i + 1 < ctas && run_of(steps, ctas, i + 1).at <= s) ++i;
+                    while (run_of(steps, ctas, i).at > s) --i;
+                    return i;
+                };
+                const int c0 = owner(first), c1 = owner(last);
+                // a CTA writes parts of its first and of its last tile
+                auto part_of = [&](int c) {
+                    return p.part + (2 * static_cast<int64_t>(c) + (c == c0 && run_of(steps, ctas, c).at < first)) *
+                                        PART;
+                };
+                float *mine = part_of(me);
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+                for (int j = 0; j < TOK; ++j)
+                    if (j < t.cnt) {
+                        __stcg(mine + j * 256 + r, v[0][j]);
+                        __stcg(mine + j * 256 + 128 + r, v[1][j]);
+                    }
+                __threadfence();
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                if (tid == 128)
+                    *s_last = atomicAdd(p.counter + tile, 1u) == static_cast<unsigned>(c1 - c0);
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                const bool done = *s_last != 0;
+                asm volatile("bar.sync 1, 128;" ::: "memory");     // s_last is free again
+                if (!done) continue;
+                __threadfence();
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
+                for (int j = 0; j < TOK; ++j) v[0][j] = v[1][j] = 0.0f;
+                for (int c = c0; c <= c1; ++c) {
+                    const float *q = part_of(c);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) at(m, j, i) = acc[m][j][i];
-        }
-        __syncthreads();
-        if (khalf == 0) {
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) at(m, j, i) += acc[m][j][i];
-        }
-        if (p.split > 1)
-            cluster_sync_all();      // two buffers: the next but one item's sync is behind every read
-        else
-            __syncthreads();
-        const uint32_t mine = smem_u32(P);
-        auto sum = [&](int tok, int row) {
-            const uint32_t off = static_cast<uint32_t>(tok * P_LD + row) * 4;
-            if (p.split == 1) return P[tok * P_LD + row];
-            float v = 0.0f;
-            for (int c = 0; c < p.split; ++c)
-                v += ld_cluster_f32(mapa_shared(mine, static_cast<uint32_t>(c)) + off);
-            return v;
-        };
-        for (int e = rank * THREADS + tid; e < it.cnt * OUT; e += p.split * THREADS) {
-            const int tok = e / OUT, row = e % OUT;
-            const float f = __ldg(p.xscale + it.tok0 + tok);
-            float v = sum(tok, row) * f * p.alpha;
-            if (SWIGLU) {
-                const float u = sum(tok, 64 + row) * f * p.alpha;
-                v = __fdividef(v, 1.0f + __expf(-v)) * u;
+                    for (int j = 0; j < TOK; ++j)
+                        if (j < t.cnt) {
+                            v[0][j] += __ldcg(q + j * 256 + r);
+                            v[1][j] += __ldcg(q + j * 256 + 128 + r);
+                        }
+                }
             }
-            const int64_t o = static_cast<int64_t>(it.tok0 + tok) * p.N + it.n0 + row;
-            if (p.out_f32)
-                static_cast<float *>(p.out)[o] = v;
-            else
-                static_cast<uint16_t *>(p.out)[o] = float_to_bf16_bits(v);
+            const int n0 = t.n_blk * (SWIGLU ? 128 : 256);
+            const int64_t w0 = static_cast<int64_t>(t.g) * p.wrows + n0 + r;
+            const bool second = SWIGLU || n0 + 128 < p.N;          // N = 128 mod 256: no such columns
+#pragma unroll
+            for (int j = 0; j < TOK; ++j) {
+                if (j >= t.cnt) break;
+                const int row = t.row0 + j;
+                const float f = __ldg(p.row_scale + row);
+                float a = v[0][j] * fabsf(f) * p.alpha, b = v[1][j] * fabsf(f) * p.alpha;
+                if (f < 0.0f) {
+                    a += odd_terms<FMT>(p, row, w0) * p.alpha;
+                    if (second) b += odd_terms<FMT>(p, row, w0 + (SWIGLU ? p.N : 128)) * p.alpha;
+                }
+                if (SWIGLU) a = __fdividef(a, 1.0f + __expf(-a)) * b;
+                const int64_t o = static_cast<int64_t>(row) * p.N + n0 + r;
+                if (p.out_f32) {
+                    float *out = static_cast<float *>(p.out) + o;
+                    out[0] = a;
+                    if (!SWIGLU && second) out[128] = b;
+                } else {
+                    uint16_t *out = static_cast<uint16_t *>(p.out) + o;
+                    out[0] = float_to_bf16_bits(a);
+                    if (!SWIGLU && second) out[128] = float_to_bf16_bits(b);
+                }
+            }
         }
-        parity ^= 1;
     }
-    copy_wait<0>();
-    if (p.split > 1) cluster_sync_all();     // no CTA leaves while its sums may be read
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TMEM_COLS);
+    }
 }
 
 // ------------------------------------------------------------------ host side
-template <int FMT, bool SWIGLU, int MAXT>
-cudaError_t launch(Params &p, cudaStream_t stream) {
-    using C = Cfg<FMT, SWIGLU, MAXT>;
-    auto kernel = weight_kernel<FMT, SWIGLU, MAXT>;
+template <typename K, typename P>
+cudaError_t start(K kernel, int64_t grid, int block, int smem, const P &p, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(block), 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+inline bool a16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+constexpr int MAX_CTAS = 256;          // at least the multiprocessors of the GPUs this runs on
+
+Ws layout(int64_t n, int64_t K, int64_t G) {
+    auto up = [](size_t v) { return (v + 255) & ~static_cast<size_t>(255); };
+    Ws w;
+    const size_t blocks = static_cast<size_t>(n / TOK + G);       // 128-row blocks of scales
+    w.q = 0;
+    w.sf = up(static_cast<size_t>(n) * DIGITS * (K / 2));
+    w.scale = w.sf + up(blocks * (K / 64) * kScaleTile);          // NV's, MX takes half
+    w.part = w.scale + up(static_cast<size_t>(n) * 4);
+    w.counter = w.part + static_cast<size_t>(2 * MAX_CTAS) * PART * 4;
+    w.total = w.counter;                                          // + the counters
+    return w;
+}
+size_t workspace_of(int64_t n, int64_t K, int64_t N, int64_t G) {
+    return layout(n, K, G).total +
+           static_cast<size_t>((n / TOK + std::min(n, G)) * ceil_div(N, 128)) * 4;
+}
+
+struct Product {
+    const moe_bf16_t *x;
+    const int32_t *offsets;
+    int G;
+    const moe_fp4_t *w;
+    int n, K, N;
+    bool swiglu;
+};
+
+moe_status_t check_sizes(int64_t n, int64_t K, int64_t N, int64_t G) {
+    if (G <= 0 || n < 0 || K <= 0 || N <= 0) return MOE_ERR_INVALID_ARG;
+    if (G > MAX_GROUPS || K % 128 != 0 || N % 128 != 0 || K > (1 << 20) || N > (1 << 20))
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    // digit rows, tiles and scale tiles are numbered in 32 bits
+    const int64_t lim = int64_t{1} << 31;
+    if (n * DIGITS >= lim - 1024 || (n / TOK + G) * (N / 128) >= lim || (n / TOK + G) * (K / 64) >= lim ||
+        G * (2 * N / 128) * (K / 64) >= lim)
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    return MOE_OK;
+}
+
+moe_status_t check(const Product &d) {
+    if (!d.w) return MOE_ERR_INVALID_ARG;
+    moe_status_t st = check_sizes(d.n, d.K, d.N, d.G);
+    if (st == MOE_OK) st = fp4_check(d.w->format, d.w->scale_exp);
+    if (st != MOE_OK) return st;
+    if (!d.offsets || !d.w->q || !d.w->sf || !a16(d.w->q) || !a16(d.w->sf))
+        return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+template <int FMT, bool SWIGLU>
+cudaError_t launch(const Product &d, uint32_t flags, void *out, uint8_t *ws, int32_t *dev_status,
+                   cudaStream_t stream) {
+    using C = Cfg<FMT>;
+    constexpr int TK = Fp4<FMT>::TILE_K;
+    auto kernel = weight_kernel<FMT, SWIGLU>;
     static std::mutex mu;
     static bool attr_done[64] = {};
     int dev = 0;
@@ -487,120 +701,54 @@ cudaError_t launch(Params &p, cudaStream_t stream) {
             if (dev < 64) attr_done[dev] = true;
         }
     }
-    // As many groups as may have rows decide how far a tile is split along K: the
-    // split with the least time on the fullest multiprocessor.
-    const int slots = 2 * num_sms();
-    const int64_t groups = std::min(p.n, p.G);
-    const int64_t chunks = std::max<int64_t>(groups, ceil_div(p.n, MAXT));
-    const int64_t tiles = chunks * (p.N / (SWIGLU ? ROWS / 2 : ROWS));
-    const int stages_k = static_cast<int>(ceil_div(p.K, KC));
-    double best = 1e30;
-    p.split = 1;
-    for (int s = 1; s <= 8 && s <= stages_k; s *= 2) {
-        const int64_t rounds = ceil_div(tiles, slots / s);
-        // a tile's own time in stages: its share of K, and 1 for the join
-        const double t = static_cast<double>(rounds) * (static_cast<double>(ceil_div(stages_k, s)) + (s > 1 ? 1.0 : 0.5));
-        if (t < best) {
-            best = t;
-            p.split = s;
-        }
-    }
-    const int64_t units = std::max<int64_t>(1, std::min<int64_t>(slots / p.split, tiles));
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(units * p.split), 1, 1);
-    cfg.blockDim = dim3(THREADS, 1, 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>(C::smem(p.G));
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(p.split);
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = p.split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
-}
-
-template <int FMT, bool SWIGLU>
-cudaError_t launch_rows(Params &p, cudaStream_t stream) {
-    // rows per pass over a group's weights: a group with more reads them again
-    // (from L2, its passes run side by side)
-    return p.n <= std::max(8, 2 * p.G) ? launch<FMT, SWIGLU, 8>(p, stream)
-                                       : launch<FMT, SWIGLU, 16>(p, stream);
-}
-
-cudaError_t launch_prep(const uint16_t *x, int n, int K, uint16_t *xh, float *xscale,
-                        cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(n), 1, 1);
-    cfg.blockDim = dim3(PREP_THREADS, 1, 1);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, prep_kernel, x, K, xh, xscale);
-}
-
-inline bool a16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-size_t workspace_bytes_of(int n, int K) {
-    return ((static_cast<size_t>(n) * K * 2 + 255) & ~static_cast<size_t>(255)) +
-           static_cast<size_t>(n) * 4;
-}
-
-struct Product {
-    const moe_bf16_t *x;
-    const int32_t *offsets;
-    int G;
-    const moe_fp4_t *w;
-    int n, K, N;
-    bool swiglu;
-};
-
-moe_status_t check(const Product &d) {
-    if (!d.w || d.G <= 0 || d.n < 0 || d.K <= 0 || d.N <= 0) return MOE_ERR_INVALID_ARG;
-    const moe_status_t st = fp4_check(d.w->format, d.w->scale_exp);
-    if (st != MOE_OK) return st;
-    if (d.G > MAX_GROUPS || d.K % 128 != 0 || d.N % 128 != 0 || d.K > (1 << 20) || d.N > (1 << 24) ||
-        (static_cast<int64_t>(d.n) / 8 + d.G) * (d.N / 64) >= (int64_t{1} << 30))
-        return MOE_ERR_UNSUPPORTED_SHAPE;
-    if (!d.offsets || !d.w->q || !d.w->sf || !a16(d.w->q) || !a16(d.w->sf))
-        return MOE_ERR_INVALID_ARG;
-    return MOE_OK;
-}
-
-moe_status_t run(const Product &d, uint32_t flags, void *out, void *workspace, int32_t *dev_status,
-                 cudaStream_t s) {
-    uint8_t *ws = static_cast<uint8_t *>(workspace);
-    uint16_t *xh = reinterpret_cast<uint16_t *>(ws);
-    float *xscale = reinterpret_cast<float *>(
-        ws + ((static_cast<size_t>(d.n) * d.K * 2 + 255) & ~static_cast<size_t>(255)));
-    if (launch_prep(d.x, d.n, d.K, xh, xscale, s) != cudaSuccess) return MOE_ERR_CUDA;
+    const Ws L = layout(d.n, d.K, d.G);
+    const int64_t ktiles = d.K / TK, blocks = d.n / TOK + d.G;
     Params p{};
+    p.wrows = SWIGLU ? 2 * d.N : d.N;
+    if (!code_map(&p.tmA, d.w->q, 3, d.G, p.wrows, d.K, 128) ||
+        !scale_map(&p.tmSA, d.w->sf, static_cast<int64_t>(d.G) * (p.wrows / 128) * ktiles, C::TILES) ||
+        !code_map(&p.tmB, ws + L.q, 2, 1, static_cast<int64_t>(d.n) * DIGITS, d.K, NB) ||
+        !scale_map(&p.tmSB, ws + L.sf, blocks * ktiles, C::TILES))
+        return cudaErrorInvalidValue;
+    p.x = d.x;
     p.q = d.w->q;
     p.sf = d.w->sf;
-    p.xh = xh;
-    p.xscale = xscale;
+    p.row_scale = reinterpret_cast<float *>(ws + L.scale);
+    p.counter = reinterpret_cast<unsigned int *>(ws + L.counter);
+    p.part = reinterpret_cast<float *>(ws + L.part);
     p.offsets = d.offsets;
     p.G = d.G;
     p.n = d.n;
     p.K = d.K;
     p.N = d.N;
-    p.wrows = d.swiglu ? 2 * d.N : d.N;
+    p.nt = static_cast<int>(ceil_div(d.N, SWIGLU ? 128 : 256));
     p.alpha = pow2f(d.w->scale_exp);
     p.out = out;
     p.out_f32 = (flags & MOE_Y_F32) != 0;
     p.dev_status = dev_status;
+    const int64_t tiles = (d.n / TOK + std::min(d.n, d.G)) * static_cast<int64_t>(p.nt);
+    const PrepParams q{d.x, d.offsets, d.G, d.n, d.K, ws + L.q, ws + L.sf,
+                       reinterpret_cast<float *>(ws + L.scale),
+                       reinterpret_cast<unsigned int *>(ws + L.counter), static_cast<int32_t>(tiles)};
+    const cudaError_t e = start(digits_kernel<FMT>, d.n, PREP_THREADS, 0, q, stream);
+    if (e != cudaSuccess) return e;
+    const int64_t steps = tiles * ceil_div(d.K, BK);
+    const int64_t grid = std::max<int64_t>(
+        1, std::min<int64_t>(std::min(num_sms(), MAX_CTAS), (steps + 1) / 2));
+    return start(kernel, grid, THREADS, C::smem(d.G), p, stream);
+}
+
+moe_status_t run(const Product &d, uint32_t flags, void *out, void *workspace, int32_t *dev_status,
+                 cudaStream_t s) {
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
     const bool mx = d.w->format == MOE_FP4_MX;
     cudaError_t e;
     if (d.swiglu)
-        e = mx ? launch_rows<MOE_FP4_MX, true>(p, s) : launch_rows<MOE_FP4_NV, true>(p, s);
+        e = mx ? launch<MOE_FP4_MX, true>(d, flags, out, ws, dev_status, s)
+               : launch<MOE_FP4_NV, true>(d, flags, out, ws, dev_status, s);
     else
-        e = mx ? launch_rows<MOE_FP4_MX, false>(p, s) : launch_rows<MOE_FP4_NV, false>(p, s);
+        e = mx ? launch<MOE_FP4_MX, false>(d, flags, out, ws, dev_status, s)
+               : launch<MOE_FP4_NV, false>(d, flags, out, ws, dev_status, s);
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -613,10 +761,12 @@ bool bad_workspace(void *ws, size_t have, size_t need) {
 
 using namespace moe;
 
-extern "C" moe_status_t moe_fp4_weight_workspace_size(int32_t n, int32_t K, size_t *bytes) {
-    if (!bytes || n < 0 || K <= 0) return MOE_ERR_INVALID_ARG;
-    if (K % 128 != 0 || K > (1 << 20)) return MOE_ERR_UNSUPPORTED_SHAPE;
-    *bytes = workspace_bytes_of(n, K);
+extern "C" moe_status_t moe_fp4_weight_workspace_size(int32_t n, int32_t K, int32_t N, int32_t G,
+                                                      size_t *bytes) {
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    const moe_status_t st = check_sizes(n, K, N, G);
+    if (st != MOE_OK) return st;
+    *bytes = workspace_of(n, K, N, G);
     return MOE_OK;
 }
 
@@ -626,9 +776,10 @@ static moe_status_t product(const Product &d, uint32_t flags, void *out, void *w
     if (st != MOE_OK) return st;
     if (d.n == 0) return MOE_OK;
     if (!d.x || !a16(d.x) || !out || !a16(out)) return MOE_ERR_INVALID_ARG;
-    if (bad_workspace(workspace, workspace_bytes, workspace_bytes_of(d.n, d.K)))
+    if (bad_workspace(workspace, workspace_bytes, workspace_of(d.n, d.K, d.N, d.G)))
         return MOE_ERR_WORKSPACE_TOO_SMALL;
     if (!current_device_ok()) return MOE_ERR_NO_DEVICE;
+    if (!encode_fn()) return MOE_ERR_CUDA;
     return run(d, flags, out, workspace, dev_status, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -646,8 +797,8 @@ extern "C" moe_status_t moe_fp4_weight_swiglu(const moe_bf16_t *x, const int32_t
                                               uint32_t flags, void *act, void *workspace,
                                               size_t workspace_bytes, int32_t *dev_status,
                                               moe_stream_t stream) {
-    return product(Product{x, offsets, G, w13, n, K, I, true}, flags, act, workspace,
-                   workspace_bytes, dev_status, stream);
+    return product(Product{x, offsets, G, w13, n, K, I, true}, flags, act, workspace, workspace_bytes,
+                   dev_status, stream);
 }
 
 extern "C" moe_status_t moe_fp4_weight_mlp(const moe_bf16_t *expanded_x, const int32_t *offsets,
@@ -656,17 +807,18 @@ extern "C" moe_status_t moe_fp4_weight_mlp(const moe_bf16_t *expanded_x, const i
                                            moe_bf16_t *act, void *y, void *workspace,
                                            size_t workspace_bytes, int32_t *dev_status,
                                            moe_stream_t stream) {
-    const Product up{expanded_x, offsets, G, w13, n, H, I, true}, down{act, offsets, G, w2, n, I, H,
-                                                                       false};
+    const Product up{expanded_x, offsets, G, w13, n, H, I, true}, down{act, offsets, G, w2, n, I, H, false};
     moe_status_t st = check(up);
     if (st == MOE_OK) st = check(down);
     if (st != MOE_OK) return st;
     if (n == 0) return MOE_OK;
     if (!expanded_x || !a16(expanded_x) || !act || !a16(act) || !y || !a16(y))
         return MOE_ERR_INVALID_ARG;
-    if (bad_workspace(workspace, workspace_bytes, workspace_bytes_of(n, std::max(H, I))))
+    if (bad_workspace(workspace, workspace_bytes,
+                      std::max(workspace_of(n, H, I, G), workspace_of(n, I, H, G))))
         return MOE_ERR_WORKSPACE_TOO_SMALL;
     if (!current_device_ok()) return MOE_ERR_NO_DEVICE;
+    if (!encode_fn()) return MOE_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     st = run(up, 0, act, workspace, dev_status, s);
     if (st != MOE_OK) return st;

@@ -20,9 +20,9 @@ def mat(q=0x1000, sf=0x1000, fmt=0, exp=0):
     return ctypes.byref(moe._Fp4(q, sf, fmt, exp))
 
 
-def need(L, n, K):
+def need(L, n, K, N=128, G=4):
     b = ctypes.c_size_t(0)
-    assert L.moe_fp4_weight_workspace_size(n, K, ctypes.byref(b)) == 0
+    assert L.moe_fp4_weight_workspace_size(n, K, N, G, ctypes.byref(b)) == 0
     return b.value
 
 
@@ -51,20 +51,23 @@ def test_products_refuse(L, which):
 def test_mlp_refuses(L):
     def c(x=fake, n=10, H=128, I=256, w13=None, w2=None, act=fake, y=fake, nbytes=None):
         return L.moe_fp4_weight_mlp(x, fake, 4, w13 or mat(), w2 or mat(), n, H, I, 0, act, y, fake,
-                                    need(L, 10, 256) if nbytes is None else nbytes, None, None)
+                                    max(need(L, 10, 256), need(L, 10, 128, 256))
+                                    if nbytes is None else nbytes, None, None)
     assert c(H=100) == 2 and c(I=100) == 2
     assert c(w2=mat(fmt=3)) == 1 and c(w13=mat(exp=2)) == 1
     assert c(x=None) == 1 and c(act=None) == 1 and c(y=odd) == 1
-    assert c(nbytes=need(L, 10, 256) - 1) == 3      # the larger of H and I counts
+    assert c(nbytes=max(need(L, 10, 256), need(L, 10, 128, 256)) - 1) == 3    # the larger one counts
     assert c(n=0, x=None, act=None, y=None) == 0
 
 
 def test_workspace_size(L):
     b = ctypes.c_size_t(0)
-    assert L.moe_fp4_weight_workspace_size(3, 100, ctypes.byref(b)) == 2
-    assert L.moe_fp4_weight_workspace_size(-1, 128, ctypes.byref(b)) == 1
-    assert L.moe_fp4_weight_workspace_size(3, 128, None) == 1
-    assert need(L, 3, 128) >= 3 * 128 * 2 + 3 * 4
+    assert L.moe_fp4_weight_workspace_size(3, 100, 128, 1, ctypes.byref(b)) == 2
+    assert L.moe_fp4_weight_workspace_size(3, 128, 100, 1, ctypes.byref(b)) == 2
+    assert L.moe_fp4_weight_workspace_size(-1, 128, 128, 1, ctypes.byref(b)) == 1
+    assert L.moe_fp4_weight_workspace_size(3, 128, 128, 0, ctypes.byref(b)) == 1
+    assert L.moe_fp4_weight_workspace_size(3, 128, 128, 1, None) == 1
+    assert need(L, 3, 128) >= 12 * 3 * 64 + 3 * 4
 
 
 def test_binding_refuses():

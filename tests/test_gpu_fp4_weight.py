@@ -1,9 +1,9 @@
 """bf16 rows times 4-bit weights against float64.
 
 Tolerance of a sum of K terms: 2 K 2^-24 sum|terms| for the fp32 accumulation
-(the tensor cores may truncate; the join of partial sums and the scalings are
-within that), 2^-40 max|row| sum|w| for the row's conversion to f16, and the
-result's own rounding (bf16: 2^-8).  SwiGLU propagates both sums' errors with
+(the tensor cores may truncate; the joins of digits and partial sums are within
+that), 2^-35 of a row's largest (a block's at most) times sum|w| for the row's
+digits, and the result's own rounding (bf16: 2^-8).  SwiGLU propagates both sums' errors with
 |SiLU'| <= 1.1 and adds 2^-18 for the hardware exponential and reciprocal at
 gates down to -20.
 """
@@ -48,7 +48,7 @@ def sums(x, w):
     X = x.to(F64)
     s = X @ w.T
     mag = X.abs() @ w.abs().T
-    e = 2 * X.shape[1] * U * mag + 2.0 ** -40 * X.abs().amax(1, keepdim=True) * w.abs().sum(1)
+    e = 2 * X.shape[1] * U * mag + 2.0 ** -35 * X.abs().amax(1, keepdim=True) * w.abs().sum(1)
     return s, e + 1e-38
 
 
