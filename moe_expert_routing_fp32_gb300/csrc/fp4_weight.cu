@@ -118,29 +118,40 @@ struct PrepParams {
     float *row_scale;
     unsigned int *counter;
     int32_t n_counter;
+    int32_t parts;             // CTAs of a row
 };
 
-// One CTA per row.
+// A CTA takes 1024 columns of a row (and looks the whole row through for its
+// largest value); two threads share 8 columns, one the upper six digits and one
+// the lower.  Rounding to the sixth digit at once gives the same as digit after
+// digit: what the first five take off is an even multiple of the sixth's unit.
+constexpr int PREP_VECS = PREP_THREADS / 2;
 template <int FMT>
 __global__ void __launch_bounds__(PREP_THREADS) digits_kernel(const PrepParams p) {
     using C = Cfg<FMT>;
     constexpr int LANES = Fp4<FMT>::BLOCK / 8;         // lanes that share a block
-    __shared__ uint32_t s_max[PREP_THREADS / 32];
-    __shared__ int s_bad[PREP_THREADS / 32];
+    constexpr int HALF = DIGITS / 2;
+    __shared__ int4 s_max[PREP_THREADS / 32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // from here on everything before this call has ended: the products may start
     // on the weights and the offsets, and wait for the digits
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int i = row * PREP_THREADS + tid; i < p.n_counter; i += gridDim.x * PREP_THREADS)
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int row = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.parts));
+    const int part = static_cast<int>(blockIdx.x) - row * p.parts;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * PREP_THREADS + tid; i < p.n_counter;
+         i += static_cast<int64_t>(gridDim.x) * PREP_THREADS)
         p.counter[i] = 0u;
     const uint4 *src = reinterpret_cast<const uint4 *>(p.x + static_cast<int64_t>(row) * p.K);
     const int nv = p.K / 8;
+    const int i = part * PREP_VECS + (tid & (PREP_VECS - 1)), half = tid / PREP_VECS;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (i < nv) v = __ldg(src + i);
     uint32_t m = 0;
     int bad = 0;
-    for (int i = tid; i < nv; i += PREP_THREADS) {
-        const uint4 v = __ldg(src + i);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    for (int k = tid; k < nv; k += PREP_THREADS) {
+        const uint4 q = __ldg(src + k);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const uint32_t a = w[j] & 0x7FFFu, b = (w[j] >> 16) & 0x7FFFu;
@@ -148,101 +159,105 @@ __global__ void __launch_bounds__(PREP_THREADS) digits_kernel(const PrepParams p
             if (b < 0x7F80u) m = max(m, b); else bad = 1;
         }
     }
-    // the row's group: the last one that starts at or in front of it
-    int g = -1;
-    for (int g0 = 0; g0 < p.G; g0 += PREP_THREADS)
-        g += __syncthreads_count(g0 + tid < p.G && __ldg(p.offsets + min(g0 + tid, p.G - 1)) <= row);
+    // the row's group is the last one that starts at or in front of it: how many do,
+    // and the last of their starts
+    int g = -1, at = -1, end = -1;
+    for (int g0 = 0; g0 <= p.G; g0 += PREP_THREADS) {
+        const int o = g0 + tid <= p.G ? __ldg(p.offsets + g0 + tid) : -1;
+        const bool in = g0 + tid < p.G && o <= row;
+        g += __syncthreads_count(in);
+        if (in) at = max(at, o);
+        end = max(end, o);
+    }
     m = __reduce_max_sync(0xffffffffu, m);
     bad = __any_sync(0xffffffffu, bad);
-    if (lane == 0) {
-        s_max[warp] = m;
-        s_bad[warp] = bad;
-    }
+    at = __reduce_max_sync(0xffffffffu, at);
+    end = __reduce_max_sync(0xffffffffu, end);
+    if (lane == 0) s_max[warp] = make_int4(static_cast<int>(m), bad, at, end);
     __syncthreads();
+    int start = -1;
 #pragma unroll
-    for (int i = 0; i < PREP_THREADS / 32; ++i) {
-        m = max(m, s_max[i]);
-        bad |= s_bad[i];
+    for (int k = 0; k < PREP_THREADS / 32; ++k) {
+        const int4 w = s_max[k];
+        m = max(m, static_cast<uint32_t>(w.x));
+        bad |= w.y;
+        start = max(start, w.z);
+        end = max(end, w.w);
     }
     const int e_row = max(static_cast<int>(m >> 7), MIN_E);
     // 1 / u of a block is 2^(127 - e_row) 2^(1 - rel), both within fp32's exponents
     const float inv_row = pow2f(max(127 - e_row, -126));
     const int one = e_row == 254 ? 0 : 1;
     // u * 2^-TOP of the largest block
-    if (tid == 0) {
+    if (tid == 0 && part == 0) {
         const float f = pow2f(e_row - 127 - 1 - C::TOP);
         p.row_scale[row] = bad ? -f : f;
     }
-    const int start = g >= 0 ? __ldg(p.offsets + g) : -1;
-    const bool owned = start >= 0 && start <= row && row < __ldg(p.offsets + g + 1);
-    const int local = row - start;
-    uint8_t *sf = p.sf + (static_cast<int64_t>(start / TOK) + g + local / TOK) *
-                             (p.K / Fp4<FMT>::TILE_K) * kScaleTile;
-    const int digit_row = (local % TOK) * DIGITS;
-    uint8_t *dst = p.q + static_cast<int64_t>(row) * DIGITS * (p.K / 2);
-    for (int i0 = warp * 32; i0 < nv; i0 += PREP_THREADS) {
-        const int i = i0 + lane;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (i < nv) v = __ldg(src + i);
-        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {                  // infinities and NaN count as zero
-            if ((w[j] & 0x7F80u) == 0x7F80u) w[j] &= 0xFFFF0000u;
-            if ((w[j] & 0x7F800000u) == 0x7F800000u) w[j] &= 0xFFFFu;
-        }
-        uint32_t am = amax8(w);
-#pragma unroll
-        for (int o = 1; o < LANES; o <<= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
-        const int rel = max(static_cast<int>(am >> 7) - e_row, -C::RANGE);      // <= 0
-        const float inv = pow2f(one - rel);
-        float t[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {                  // x / u: two exact products
-            t[2 * j] = __uint_as_float(w[j] << 16) * inv_row * inv;
-            t[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u) * inv_row * inv;
-        }
-#pragma unroll
-        for (int d = 0; d < DIGITS; ++d) {
-            float r[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                r[j] = rintf(t[j]);
-                t[j] = (t[j] - r[j]) * 8.0f;
-            }
-            if (i < nv)
-                *reinterpret_cast<uint32_t *>(dst + static_cast<int64_t>(d) * (p.K / 2) + i * 4) = e2m1x8(r);
-        }
-        if (i < nv && owned) {
-            const int e = C::TOP + rel;
-            const uint32_t byte = FMT == MOE_FP4_MX ? static_cast<uint32_t>(127 + e)
-                                  : e >= -6         ? static_cast<uint32_t>((e + 7) << 3)
-                                                    : 1u << (e + 9);
-            const int b = i / LANES;                   // block: its lanes share the digits' rows
-            uint8_t *at = sf + (b >> 2) * kScaleTile + (b & 3);
-            for (int d = lane % LANES; d < DIGITS; d += LANES)
-                at[scale_row_offset(digit_row + d)] = static_cast<uint8_t>(byte);
-        }
+    for (int j = 0; j < 4; ++j) {                      // infinities and NaN count as zero
+        if ((w[j] & 0x7F80u) == 0x7F80u) w[j] &= 0xFFFF0000u;
+        if ((w[j] & 0x7F800000u) == 0x7F800000u) w[j] &= 0xFFFFu;
     }
+    uint32_t am = amax8(w);
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
+    if (i >= nv) return;
+    const int rel = max(static_cast<int>(am >> 7) - e_row, -C::RANGE);          // <= 0
+    const float inv = pow2f(one - rel);
+    float t[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {                      // x / u: two exact products
+        t[2 * j] = __uint_as_float(w[j] << 16) * inv_row * inv;
+        t[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u) * inv_row * inv;
+    }
+    if (half)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float s = t[j] * 32768.0f;           // 8^(HALF - 1)
+            t[j] = (s - rintf(s)) * 8.0f;
+        }
+    uint8_t *dst = p.q + (static_cast<int64_t>(row) * DIGITS + half * HALF) * (p.K / 2) + i * 4;
+#pragma unroll
+    for (int d = 0; d < HALF; ++d) {
+        float r[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            r[j] = rintf(t[j]);
+            t[j] = (t[j] - r[j]) * 8.0f;
+        }
+        *reinterpret_cast<uint32_t *>(dst) = e2m1x8(r);
+        dst += p.K / 2;
+    }
+    // (bad offsets are the product's to report; what is written stays in bounds)
+    if (start < 0 || g >= p.G || row >= end) return;
+    const int local = row - start;
+    const int e = C::TOP + rel;
+    const uint32_t byte = FMT == MOE_FP4_MX ? static_cast<uint32_t>(127 + e)
+                          : e >= -6         ? static_cast<uint32_t>((e + 7) << 3)
+                                            : 1u << (e + 9);
+    const int b = i / LANES;                           // block: its lanes share the digits' rows
+    uint8_t *sf = p.sf + ((static_cast<int64_t>(start / TOK) + g + local / TOK) *
+                              (p.K / Fp4<FMT>::TILE_K) + (b >> 2)) * kScaleTile + (b & 3);
+    const int digit_row = (local % TOK) * DIGITS + half * HALF;
+    for (int d = lane % LANES; d < HALF; d += LANES)
+        sf[scale_row_offset(digit_row + d)] = static_cast<uint8_t>(byte);
 }
 
 // ------------------------------------------------------------------ products
-__device__ __forceinline__ void tmem_ld12(uint32_t taddr, float (&v)[DIGITS]) {
-    uint32_t r[DIGITS];
+__device__ __forceinline__ void tmem_ld12(uint32_t taddr, uint32_t (&r)[DIGITS]) {
 #pragma unroll
     for (int i = 0; i < DIGITS; i += 4)
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3])
                      : "r"(taddr + static_cast<uint32_t>(i))
                      : "memory");
-    tmem_ld_wait();
-#pragma unroll
-    for (int i = 0; i < DIGITS; ++i) v[i] = __uint_as_float(r[i]);
 }
 // sum_d 8^-d v_d
-__device__ __forceinline__ float add_digits(const float (&v)[DIGITS]) {
-    float s = v[DIGITS - 1];
+__device__ __forceinline__ float add_digits(const uint32_t (&v)[DIGITS]) {
+    float s = __uint_as_float(v[DIGITS - 1]);
 #pragma unroll
-    for (int d = DIGITS - 2; d >= 0; --d) s = fmaf(s, 0.125f, v[d]);
+    for (int d = DIGITS - 2; d >= 0; --d) s = fmaf(s, 0.125f, __uint_as_float(v[d]));
     return s;
 }
 
@@ -276,13 +291,16 @@ __device__ __forceinline__ void issue_tiles(uint32_t d, uint32_t a, uint32_t b, 
 struct Tile {
     int g, row0, cnt, n_blk;
 };
-// A CTA's run of (tile, stage) steps.
-struct Run {
-    int64_t at, end;
+// The (tile, stage) steps in equal runs, the first `extra` one step longer.
+struct Runs {
+    int base, extra;
+    __device__ __forceinline__ Runs(int steps, int ctas) : base(steps / ctas), extra(steps - base * ctas) {}
+    __device__ __forceinline__ int at(int i) const { return base * i + min(i, extra); }
+    __device__ __forceinline__ int owner(int s) const {       // the run that holds step s
+        const int longer = extra * (base + 1);
+        return s < longer ? s / (base + 1) : extra + (s - longer) / base;
+    }
 };
-__device__ __forceinline__ Run run_of(int64_t steps, int ctas, int i) {
-    return Run{steps * i / ctas, steps * (i + 1) / ctas};
-}
 
 // What a row's infinities and NaN add to its product with weight row `wr`.
 template <int FMT>
@@ -385,11 +403,12 @@ __global__ void __launch_bounds__(THREADS, 1) weight_kernel(const __grid_constan
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (*s_bad && tid == 0 && blockIdx.x == 0) report(p.dev_status, MOE_DEV_BAD_OFFSETS);
     const int kst = (p.K + BK - 1) / BK;
-    const int64_t steps = *s_bad ? 0 : static_cast<int64_t>(s_prefix[p.G]) * kst;
+    const int steps = *s_bad ? 0 : s_prefix[p.G] * kst;
     // two steps each at least, as far as they go
-    const int ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), (steps + 1) / 2));
+    const int ctas = max(1, min(static_cast<int>(gridDim.x), (steps + 1) / 2));
     const int me = static_cast<int>(blockIdx.x);
-    const Run run = me < ctas ? run_of(steps, ctas, me) : Run{0, 0};
+    const Runs runs(steps, ctas);
+    const int run_at = me < ctas ? runs.at(me) : 0, run_end = me < ctas ? runs.at(me + 1) : 0;
     const uint32_t tmem = *s_tmem;
     const int64_t ktiles = p.K / Fp4<FMT>::TILE_K;
 
@@ -411,9 +430,8 @@ __global__ void __launch_bounds__(THREADS, 1) weight_kernel(const __grid_constan
             int armed[STAGES];
             for (int s = 0; s < STAGES; ++s) armed[s] = -1;
             bool ok = true;
-            for (int64_t u = run.at; u < run.end && ok && !*s_abort;) {
-                const int tile = static_cast<int>(u / kst), k0 = static_cast<int>(u % kst);
-                const int k1 = static_cast<int>(min(static_cast<int64_t>(kst), k0 + (run.end - u)));
+            for (int u = run_at; u < run_end && ok && !*s_abort;) {
+                const int tile = u / kst, k0 = u - tile * kst, k1 = min(kst, k0 + run_end - u);
                 const Tile t = decode(tile, g);
                 const int n0 = t.n_blk * (SWIGLU ? 128 : 256), n1 = SWIGLU ? p.N + n0 : n0 + 128;
                 const int64_t blk = static_cast<int64_t>(t.g) * (p.wrows / 128);
@@ -460,9 +478,8 @@ __global__ void __launch_bounds__(THREADS, 1) weight_kernel(const __grid_constan
             uint32_t phase = 0, n = 0, set = 0;
             const uint32_t base = smem_u32(smem) >> 4;
             bool issued = false, ok = true;
-            for (int64_t u = run.at; u < run.end && ok && !*s_abort; ++n) {
-                const int k0 = static_cast<int>(u % kst);
-                const int k1 = static_cast<int>(min(static_cast<int64_t>(kst), k0 + (run.end - u)));
+            for (int u = run_at; u < run_end && ok && !*s_abort; ++n) {
+                const int k0 = u % kst, k1 = min(kst, k0 + run_end - u);
                 if (!wait_phase(&tempty[n & 1], ((n >> 1) & 1) ^ 1, s_abort, p.dev_status)) break;
                 tc_fence_after();
                 const uint32_t d = tmem + (n & 1) * (2 * NB);
@@ -511,84 +528,125 @@ __global__ void __launch_bounds__(THREADS, 1) weight_kernel(const __grid_constan
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         uint32_t n = 0;
         int g = 0;
-        for (int64_t u = run.at; u < run.end; ++n) {
-            const int tile = static_cast<int>(u / kst), k0 = static_cast<int>(u % kst);
-            const int k1 = static_cast<int>(min(static_cast<int64_t>(kst), k0 + (run.end - u)));
+        for (int u = run_at; u < run_end; ++n) {
+            const int tile = u / kst, k0 = u - tile * kst, k1 = min(kst, k0 + run_end - u);
             u += k1 - k0;
             const Tile t = decode(tile, g);
+            const uint32_t acc = tmem + lanes + (n & 1) * (2 * NB);
+            const bool whole = k1 - k0 == kst;
+            const int n0 = t.n_blk * (SWIGLU ? 128 : 256);
+            const int64_t w0 = static_cast<int64_t>(t.g) * p.wrows + n0 + r;
+            const bool second = SWIGLU || n0 + 128 < p.N;          // N = 128 mod 256: no such columns
+            float scale[TOK];
+#pragma unroll
+            for (int j = 0; j < TOK; ++j) scale[j] = __ldg(p.row_scale + t.row0 + min(j, t.cnt - 1));
+            // the CTAs of this tile, and where one of them leaves its part: a CTA has
+            // parts of its first and of its last tile
+            const int c0 = runs.owner(tile * kst), c1 = runs.owner(tile * kst + kst - 1);
+            auto part_of = [&](int c) {
+                return p.part + static_cast<int64_t>(2 * c + (c == c0 && runs.at(c) < tile * kst)) * PART + r;
+            };
+            // the parts of c .. c + 3, their loads all at once
+            float w[4][2][TOK];
+            auto load_parts = [&](int c) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float *q = part_of(min(c + k, c1));
+#pragma unroll
+                    for (int j = 0; j < TOK; ++j) {
+                        if (j >= t.cnt) break;
+                        w[k][0][j] = __ldcg(q + j * 256);
+                        w[k][1][j] = __ldcg(q + j * 256 + 128);
+                    }
+                }
+            };
+            // A tile of few parts whose others are all there already (this CTA's is the
+            // last, as a rule the first in K): they are fetched while its own MMAs run,
+            // and its own part needs not be written.
+            bool rest = false;
+            if (!whole && c1 - c0 < 4) {
+                if (tid == 128) {
+                    unsigned int count;
+                    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];"
+                                 : "=r"(count)
+                                 : "l"(p.counter + tile)
+                                 : "memory");
+                    *s_last = count == static_cast<unsigned>(c1 - c0);
+                }
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                rest = *s_last != 0;
+                asm volatile("bar.sync 1, 128;" ::: "memory");     // s_last is free again
+                if (rest) {
+                    __threadfence();
+                    load_parts(c0);
+                }
+            }
             if (!wait_phase(&tfull[n & 1], (n >> 1) & 1, s_abort, p.dev_status)) break;
             tc_fence_after();
             float v[2][TOK];
 #pragma unroll
             for (int j = 0; j < TOK; ++j) {
-                v[0][j] = v[1][j] = 0.0f;
-                if (j < t.cnt) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float d[DIGITS];
-                        __syncwarp();
-                        tmem_ld12(tmem + lanes + (n & 1) * (2 * NB) + h * NB + j * DIGITS, d);
-                        v[h][j] = add_digits(d);
-                    }
-                }
+                if (j >= t.cnt) break;
+                uint32_t a[DIGITS], b[DIGITS];
+                __syncwarp();
+                tmem_ld12(acc + j * DIGITS, a);
+                tmem_ld12(acc + NB + j * DIGITS, b);
+                tmem_ld_wait();
+                v[0][j] = add_digits(a);
+                v[1][j] = add_digits(b);
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&tempty[n & 1]);
-            if (k1 - k0 < kst) {
-                // part of a tile: the last of its CTAs adds the parts up
-                const int64_t first = static_cast<int64_t>(tile) * kst, last = first + kst - 1;
-                // the run that holds step s: i with steps i / ctas <= s, the largest
-                auto owner = [&](int64_t s) {
-                    int i = static_cast<int>(s * ctas / steps);
-                    while (i + 1 < ctas && run_of(steps, ctas, i + 1).at <= s) ++i;
-                    while (run_of(steps, ctas, i).at > s) --i;
-                    return i;
-                };
-                const int c0 = owner(first), c1 = owner(last);
-                // a CTA writes parts of its first and of its last tile
-                auto part_of = [&](int c) {
-                    return p.part + (2 * static_cast<int64_t>(c) + (c == c0 && run_of(steps, ctas, c).at < first)) *
-                                        PART;
-                };
+            if (!whole && !rest) {
+                // the last of the tile's CTAs adds the parts up
                 float *mine = part_of(me);
 #pragma unroll
-                for (int j = 0; j < TOK; ++j)
-                    if (j < t.cnt) {
-                        __stcg(mine + j * 256 + r, v[0][j]);
-                        __stcg(mine + j * 256 + 128 + r, v[1][j]);
-                    }
+                for (int j = 0; j < TOK; ++j) {
+                    if (j >= t.cnt) break;
+                    __stcg(mine + j * 256, v[0][j]);
+                    __stcg(mine + j * 256 + 128, v[1][j]);
+                }
                 __threadfence();
                 asm volatile("bar.sync 1, 128;" ::: "memory");
                 if (tid == 128)
                     *s_last = atomicAdd(p.counter + tile, 1u) == static_cast<unsigned>(c1 - c0);
                 asm volatile("bar.sync 1, 128;" ::: "memory");
-                const bool done = *s_last != 0;
+                const bool last = *s_last != 0;
                 asm volatile("bar.sync 1, 128;" ::: "memory");     // s_last is free again
-                if (!done) continue;
+                if (!last) continue;
                 __threadfence();
+            }
+            if (!whole) {
+                float own[2][TOK];
 #pragma unroll
-                for (int j = 0; j < TOK; ++j) v[0][j] = v[1][j] = 0.0f;
-                for (int c = c0; c <= c1; ++c) {
-                    const float *q = part_of(c);
+                for (int j = 0; j < TOK; ++j) {
+                    own[0][j] = v[0][j];
+                    own[1][j] = v[1][j];
+                    v[0][j] = v[1][j] = 0.0f;
+                }
+                for (int c = c0; c <= c1; c += 4) {
+                    if (!rest) load_parts(c);
 #pragma unroll
-                    for (int j = 0; j < TOK; ++j)
-                        if (j < t.cnt) {
-                            v[0][j] += __ldcg(q + j * 256 + r);
-                            v[1][j] += __ldcg(q + j * 256 + 128 + r);
+                    for (int k = 0; k < 4; ++k) {
+                        if (c + k > c1) break;
+                        const bool is_own = c + k == me;
+#pragma unroll
+                        for (int j = 0; j < TOK; ++j) {
+                            if (j >= t.cnt) break;
+                            v[0][j] += is_own ? own[0][j] : w[k][0][j];
+                            v[1][j] += is_own ? own[1][j] : w[k][1][j];
                         }
+                    }
                 }
             }
-            const int n0 = t.n_blk * (SWIGLU ? 128 : 256);
-            const int64_t w0 = static_cast<int64_t>(t.g) * p.wrows + n0 + r;
-            const bool second = SWIGLU || n0 + 128 < p.N;          // N = 128 mod 256: no such columns
 #pragma unroll
             for (int j = 0; j < TOK; ++j) {
                 if (j >= t.cnt) break;
                 const int row = t.row0 + j;
-                const float f = __ldg(p.row_scale + row);
-                float a = v[0][j] * fabsf(f) * p.alpha, b = v[1][j] * fabsf(f) * p.alpha;
-                if (f < 0.0f) {
+                const float f = fabsf(scale[j]);
+                float a = v[0][j] * f * p.alpha, b = v[1][j] * f * p.alpha;
+                if (scale[j] < 0.0f) {
                     a += odd_terms<FMT>(p, row, w0) * p.alpha;
                     if (second) b += odd_terms<FMT>(p, row, w0 + (SWIGLU ? p.N : 128)) * p.alpha;
                 }
@@ -664,9 +722,9 @@ moe_status_t check_sizes(int64_t n, int64_t K, int64_t N, int64_t G) {
     if (G <= 0 || n < 0 || K <= 0 || N <= 0) return MOE_ERR_INVALID_ARG;
     if (G > MAX_GROUPS || K % 128 != 0 || N % 128 != 0 || K > (1 << 20) || N > (1 << 20))
         return MOE_ERR_UNSUPPORTED_SHAPE;
-    // digit rows, tiles and scale tiles are numbered in 32 bits
+    // digit rows, steps and scale tiles are numbered in 32 bits
     const int64_t lim = int64_t{1} << 31;
-    if (n * DIGITS >= lim - 1024 || (n / TOK + G) * (N / 128) >= lim || (n / TOK + G) * (K / 64) >= lim ||
+    if (n * DIGITS >= lim - 1024 || (n / TOK + G) * (N / 128) * ceil_div(K, BK) >= lim || (n / TOK + G) * (K / 64) >= lim ||
         G * (2 * N / 128) * (K / 64) >= lim)
         return MOE_ERR_UNSUPPORTED_SHAPE;
     return MOE_OK;
@@ -729,8 +787,9 @@ cudaError_t launch(const Product &d, uint32_t flags, void *out, uint8_t *ws, int
     const int64_t tiles = (d.n / TOK + std::min(d.n, d.G)) * static_cast<int64_t>(p.nt);
     const PrepParams q{d.x, d.offsets, d.G, d.n, d.K, ws + L.q, ws + L.sf,
                        reinterpret_cast<float *>(ws + L.scale),
-                       reinterpret_cast<unsigned int *>(ws + L.counter), static_cast<int32_t>(tiles)};
-    const cudaError_t e = start(digits_kernel<FMT>, d.n, PREP_THREADS, 0, q, stream);
+                       reinterpret_cast<unsigned int *>(ws + L.counter), static_cast<int32_t>(tiles),
+                       static_cast<int32_t>(ceil_div(d.K / 8, PREP_VECS))};
+    const cudaError_t e = start(digits_kernel<FMT>, static_cast<int64_t>(d.n) * q.parts, PREP_THREADS, 0, q, stream);
     if (e != cudaSuccess) return e;
     const int64_t steps = tiles * ceil_div(d.K, BK);
     const int64_t grid = std::max<int64_t>(
