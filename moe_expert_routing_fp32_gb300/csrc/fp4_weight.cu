@@ -245,13 +245,27 @@ __global__ void __launch_bounds__(PREP_THREADS) digits_kernel(const PrepParams p
 }
 
 // ------------------------------------------------------------------ products
-__device__ __forceinline__ void tmem_ld12(uint32_t taddr, uint32_t (&r)[DIGITS]) {
-#pragma unroll
-    for (int i = 0; i < DIGITS; i += 4)
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3])
-                     : "r"(taddr + static_cast<uint32_t>(i))
-                     : "memory");
+// The digits' columns at a and at b (one statement: nothing may touch the registers
+// before the wait).
+__device__ __forceinline__ void tmem_read12x2(uint32_t a, uint32_t b, uint32_t (&x)[DIGITS],
+                                              uint32_t (&y)[DIGITS]) {
+    static_assert(DIGITS == 12, "three loads of four columns");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%24];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%4, %5, %6, %7}, [%25];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%8, %9, %10, %11}, [%26];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%12, %13, %14, %15}, [%27];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%16, %17, %18, %19}, [%28];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%20, %21, %22, %23}, [%29];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=&r"(x[0]), "=&r"(x[1]), "=&r"(x[2]), "=&r"(x[3]),
+          "=&r"(x[4]), "=&r"(x[5]), "=&r"(x[6]), "=&r"(x[7]),
+          "=&r"(x[8]), "=&r"(x[9]), "=&r"(x[10]), "=&r"(x[11]),
+          "=&r"(y[0]), "=&r"(y[1]), "=&r"(y[2]), "=&r"(y[3]),
+          "=&r"(y[4]), "=&r"(y[5]), "=&r"(y[6]), "=&r"(y[7]),
+          "=&r"(y[8]), "=&r"(y[9]), "=&r"(y[10]), "=&r"(y[11])
+        : "r"(a), "r"(a + 4), "r"(a + 8), "r"(b), "r"(b + 4), "r"(b + 8)
+        : "memory");
 }
 // sum_d 8^-d v_d
 __device__ __forceinline__ float add_digits(const uint32_t (&v)[DIGITS]) {
@@ -589,9 +603,7 @@ __global__ void __launch_bounds__(THREADS, 1) weight_kernel(const __grid_constan
                 if (j >= t.cnt) break;
                 uint32_t a[DIGITS], b[DIGITS];
                 __syncwarp();
-                tmem_ld12(acc + j * DIGITS, a);
-                tmem_ld12(acc + NB + j * DIGITS, b);
-                tmem_ld_wait();
+                tmem_read12x2(acc + j * DIGITS, acc + NB + j * DIGITS, a, b);
                 v[0][j] = add_digits(a);
                 v[1][j] = add_digits(b);
             }

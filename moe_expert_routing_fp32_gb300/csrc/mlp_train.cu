@@ -64,6 +64,7 @@ struct Params {
     int32_t N;                 // FWD, DACT: I; DX: H
     int32_t nt;                // column tiles of a row block
     int32_t wrows;             // rows a group's weights would have as an operand like A
+    int32_t boxes;             // output boxes per epilogue warp
     const uint16_t *h;         // DACT
     uint16_t *out0, *out1;
     int32_t ld0, ld1;
@@ -82,14 +83,21 @@ struct Cfg {
     static constexpr int B_SLICE = BN / CG * 128;
     static constexpr int B_STAGE = B_SLICE * KSUB;
     static constexpr int STAGE = A_STAGE + B_STAGE;
-    static constexpr int BOXES = MODE == DW ? 2 : 1;    // per epilogue warp
+    // behind the stages: output boxes (one or two per epilogue warp), and what
+    // follows them, counted from there
     static constexpr int EPI_OFF = STAGES * STAGE;
-    static constexpr int MAP_OFF = EPI_OFF + EPI_WARPS * BOXES * EPI_BYTES;
+    static constexpr int BOX_BYTES = EPI_WARPS * EPI_BYTES;
+    static constexpr int MAP_OFF = 0;
     static constexpr int BAR_OFF = MAP_OFF + (MODE == DACT ? NMAPS * 128 : 0);
     static constexpr int NBARS = 2 * STAGES + 5;        // full, empty, tfull, tempty, drain
     static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
     static constexpr int OFFS_OFF = MISC_OFF + 16;
-    static constexpr int smem(int G) { return 1024 + OFFS_OFF + (MODE == DW ? 0 : (2 * G + 2) * 4); }
+    static constexpr int smem(int G, int boxes) {
+        return 1024 + EPI_OFF + boxes * BOX_BYTES + OFFS_OFF + (MODE == DW ? 0 : (2 * G + 2) * 4);
+    }
+    // two boxes where they fit beside the groups' tables: a warp fills one while the
+    // last one's store still reads the other
+    static constexpr int boxes(int G) { return smem(G, 2) <= 227 * 1024 ? 2 : 1; }
     static constexpr bool A_MN = MODE == DW, B_MN = MODE != FWD;
     // shared-memory descriptors: the high word is the same for both layouts (1 KB
     // between groups of eight 128-byte rows, 128-byte swizzle); the low word's
@@ -99,8 +107,8 @@ struct Cfg {
                                       (B_MN ? 1u << 16 : 0u) |
                                       (static_cast<uint32_t>(BN >> 3) << 17) |
                                       (static_cast<uint32_t>(CG * 128 >> 4) << 24);
-    static_assert(smem(MAX_GROUPS) <= 227 * 1024, "shared memory");
-    static_assert(STAGE % 1024 == 0 && MAP_OFF % 128 == 0, "alignment");
+    static_assert(smem(MAX_GROUPS, 1) <= 227 * 1024, "shared memory");
+    static_assert(STAGE % 1024 == 0 && BOX_BYTES % 1024 == 0, "alignment");
 };
 
 // D (+)= A B^T with the descriptors' low words a and b.
@@ -243,42 +251,49 @@ __device__ __forceinline__ Tile decode_tile(const Params &p, int tile, int &g, c
     return t;
 }
 
-// 64 bytes of each of a warp's 32 rows (lane i: row row0 + i) into a box in the
-// 64-byte swizzle of the output maps; the caller stores it.
-template <int BOXES>
-__device__ __forceinline__ uint8_t *fill_box(uint8_t *boxes, int &b, int lane,
-                                             const uint32_t (&w)[16]) {
-    uint8_t *box = boxes + b * EPI_BYTES;
-    if (BOXES == 2) b ^= 1;
-    if (lane == 0) bulk_wait_read<BOXES - 1>();     // the store that last used it has read it
-    __syncwarp();
-#pragma unroll
-    for (int ch = 0; ch < 4; ++ch)
-        *reinterpret_cast<uint4 *>(box + lane * 64 + ((ch ^ ((lane >> 1) & 3)) << 4)) =
-            make_uint4(w[4 * ch], w[4 * ch + 1], w[4 * ch + 2], w[4 * ch + 3]);
-    fence_proxy_async();
-    __syncwarp();
-    return box;
-}
-
-// 32 bf16 columns of a warp's rows: through a box where all 32 rows belong to
-// the group, else each lane its own row.
-__device__ __forceinline__ void emit_rows(uint8_t *boxes, int &b, int lane, bool boxed, bool ok,
-                                          const uint32_t (&w)[16], const CUtensorMap *map,
-                                          uint16_t *out, int ld, int row0, int col) {
-    if (boxed) {
-        const uint8_t *box = fill_box<1>(boxes, b, lane, w);
-        if (lane == 0) {
-            tma_store_2d(map, box, col, row0);
-            bulk_commit();
+// An epilogue warp's output boxes.
+struct Boxes {
+    uint8_t *base;
+    int n, at, lane;           // one or two, the next one
+    // 64 bytes of each of the warp's 32 rows (lane i: row row0 + i) into a box, in the
+    // 64-byte swizzle of the output maps; the caller stores it.
+    __device__ __forceinline__ const uint8_t *fill(const uint32_t (&w)[16]) {
+        uint8_t *box = base + at * EPI_BYTES;
+        if (lane == 0) {                             // the store that last used it has read it
+            if (n == 2)
+                bulk_wait_read<1>();
+            else
+                bulk_wait_read<0>();
         }
-    } else if (ok) {
-        uint4 *dst = reinterpret_cast<uint4 *>(out + static_cast<int64_t>(row0 + lane) * ld + col);
+        if (n == 2) at ^= 1;
+        __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        for (int ch = 0; ch < 4; ++ch)
+            *reinterpret_cast<uint4 *>(box + lane * 64 + ((ch ^ ((lane >> 1) & 3)) << 4)) =
+                make_uint4(w[4 * ch], w[4 * ch + 1], w[4 * ch + 2], w[4 * ch + 3]);
+        fence_proxy_async();
+        __syncwarp();
+        return box;
     }
-}
+    // 32 bf16 columns of the rows: through a box where all 32 rows belong to the
+    // group, else each lane its own row.
+    __device__ __forceinline__ void emit(bool boxed, bool ok, const uint32_t (&w)[16],
+                                         const CUtensorMap *map, uint16_t *out, int ld, int row0,
+                                         int col) {
+        if (boxed) {
+            const uint8_t *box = fill(w);
+            if (lane == 0) {
+                tma_store_2d(map, box, col, row0);
+                bulk_commit();
+            }
+        } else if (ok) {
+            uint4 *dst = reinterpret_cast<uint4 *>(out + static_cast<int64_t>(row0 + lane) * ld + col);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        }
+    }
+};
 
 template <int MODE, int CG>
 __device__ __forceinline__ void train_gemm(const Params &p) {
@@ -288,15 +303,16 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     // a pair's MMAs are issued by its even CTA: full, tempty are used there
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);
+    uint8_t *rest = smem + C::EPI_OFF + p.boxes * C::BOX_BYTES;
+    uint64_t *full = reinterpret_cast<uint64_t *>(rest + C::BAR_OFF);
     uint64_t *empty = full + STAGES;
     uint64_t *tfull = empty + STAGES;       // [2]
     uint64_t *tempty = tfull + 2;           // [2]
     uint64_t *drain = tempty + 2;
-    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF);
-    volatile int *s_abort = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 4);
-    volatile int *s_bad = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 8);
-    int *s_off = reinterpret_cast<int *>(smem + C::OFFS_OFF);
+    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(rest + C::MISC_OFF);
+    volatile int *s_abort = reinterpret_cast<volatile int *>(rest + C::MISC_OFF + 4);
+    volatile int *s_bad = reinterpret_cast<volatile int *>(rest + C::MISC_OFF + 8);
+    int *s_off = reinterpret_cast<int *>(rest + C::OFFS_OFF);
     int *s_prefix = s_off + p.G + 1;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = CG == 2 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -352,7 +368,7 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
             if (s_off[g + 1] == s_off[g]) continue;          // never loaded
 #pragma unroll
             for (int m = 0; m < NMAPS; ++m)
-                cut_map(p.maps + g * NMAPS + m, smem + C::MAP_OFF + m * 128, &p.tmG[m],
+                cut_map(p.maps + g * NMAPS + m, rest + C::MAP_OFF + m * 128, &p.tmG[m],
                         s_off[g + 1], lane);
         }
     }
@@ -510,9 +526,9 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
     } else if (warp >= 4) {
         // ================= epilogue: two warps share a TMEM lane quarter
         const int quarter = warp & 3, part = (warp - 4) >> 2;
-        uint8_t *boxes = smem + C::EPI_OFF + (warp - 4) * C::BOXES * EPI_BYTES;
+        Boxes boxes{smem + C::EPI_OFF + (warp - 4) * p.boxes * EPI_BYTES, p.boxes, 0, lane};
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-        int bx = 0, g = 0;
+        int g = 0;
         uint32_t u = 0;
         for (int tile = first_tile; tile < total; tile += step) {
             const Tile t = decode_tile<MODE, 128 * CG>(p, tile, g, s_off, s_prefix);
@@ -520,6 +536,23 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
             const bool ok = row0 + lane < t.row_end;
             const bool boxed = row0 + 32 <= t.row_end;
             const uint32_t acc = tmem + lanes + (u & 1) * BN;
+            // DACT: this lane's row of h, 32 columns of gate and up at a time, fetched one
+            // step ahead (the first while the tile is still computed)
+            uint4 hq[8];
+            auto fetch_h = [&](int c) {
+                const int col = t.n_blk * BN + c;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) hq[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (ok && col < p.N) {
+                    const uint16_t *src = p.h + static_cast<int64_t>(row0 + lane) * (2 * p.N) + col;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        hq[j] = __ldg(reinterpret_cast<const uint4 *>(src) + j);
+                        hq[4 + j] = __ldg(reinterpret_cast<const uint4 *>(src + p.N) + j);
+                    }
+                }
+            };
+            if (MODE == DACT) fetch_h(128 * part);
             if (!wait_phase(&tfull[u & 1], (u >> 1) & 1, s_abort, p.dev_status)) break;
             tc_fence_after();
             if (MODE == FWD) {
@@ -528,17 +561,16 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                 for (int c = 64 * part; c < 64 * part + 64; c += 32) {
                     float x[32], y[32];
                     __syncwarp();
-                    tmem_ld32(acc + c, x);
-                    tmem_ld32(acc + 128 + c, y);
-                    tmem_ld_wait();
+                    tmem_read32(acc + c, x);
+                    tmem_read32(acc + 128 + c, y);
                     const int col = t.n_blk * 128 + c;
                     uint32_t w[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) w[i] = bf16x2(x[2 * i], x[2 * i + 1]);
-                    emit_rows(boxes, bx, lane, boxed, ok, w, &p.tmO0, p.out0, p.ld0, row0, col);
+                    boxes.emit(boxed, ok, w, &p.tmO0, p.out0, p.ld0, row0, col);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) w[i] = bf16x2(y[2 * i], y[2 * i + 1]);
-                    emit_rows(boxes, bx, lane, boxed, ok, w, &p.tmO0, p.out0, p.ld0, row0,
+                    boxes.emit(boxed, ok, w, &p.tmO0, p.out0, p.ld0, row0,
                               p.N + col);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
@@ -550,30 +582,25 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                         }
                         w[i] = bf16x2(a[0], a[1]);
                     }
-                    emit_rows(boxes, bx, lane, boxed, ok, w, &p.tmO1, p.out1, p.ld1, row0, col);
+                    boxes.emit(boxed, ok, w, &p.tmO1, p.out1, p.ld1, row0, col);
                 }
             } else if (MODE == DACT) {
 #pragma unroll 1
                 for (int c = 128 * part; c < 128 * part + 128; c += 32) {
                     const int col = t.n_blk * BN + c;
                     if (col >= p.N) break;               // N = 128 mod 256: no such columns
-                    uint4 hq[8];
+                    uint32_t hg[16], hu[16];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) hq[j] = make_uint4(0u, 0u, 0u, 0u);
-                    if (ok) {
-                        const uint16_t *src =
-                            p.h + static_cast<int64_t>(row0 + lane) * (2 * p.N) + col;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            hq[j] = __ldg(reinterpret_cast<const uint4 *>(src) + j);
-                            hq[4 + j] = __ldg(reinterpret_cast<const uint4 *>(src + p.N) + j);
-                        }
+                    for (int j = 0; j < 4; ++j) {
+                        hg[4 * j] = hq[j].x, hg[4 * j + 1] = hq[j].y;
+                        hg[4 * j + 2] = hq[j].z, hg[4 * j + 3] = hq[j].w;
+                        hu[4 * j] = hq[4 + j].x, hu[4 * j + 1] = hq[4 + j].y;
+                        hu[4 * j + 2] = hq[4 + j].z, hu[4 * j + 3] = hq[4 + j].w;
                     }
-                    const uint32_t *hg = reinterpret_cast<const uint32_t *>(hq), *hu = hg + 16;
+                    if (c + 32 < 128 * part + 128) fetch_h(c + 32);
                     float d[32];
                     __syncwarp();
-                    tmem_ld32(acc + c, d);
-                    tmem_ld_wait();
+                    tmem_read32(acc + c, d);
                     uint32_t wg[16], wu[16], wa[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
@@ -593,10 +620,10 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                         wu[i] = bf16x2(vu[0], vu[1]);
                         wa[i] = bf16x2(va[0], va[1]);
                     }
-                    emit_rows(boxes, bx, lane, boxed, ok, wg, &p.tmO0, p.out0, p.ld0, row0, col);
-                    emit_rows(boxes, bx, lane, boxed, ok, wu, &p.tmO0, p.out0, p.ld0, row0,
+                    boxes.emit(boxed, ok, wg, &p.tmO0, p.out0, p.ld0, row0, col);
+                    boxes.emit(boxed, ok, wu, &p.tmO0, p.out0, p.ld0, row0,
                               p.N + col);
-                    emit_rows(boxes, bx, lane, boxed, ok, wa, &p.tmO1, p.out1, p.ld1, row0, col);
+                    boxes.emit(boxed, ok, wa, &p.tmO1, p.out1, p.ld1, row0, col);
                 }
             } else if (MODE == DX) {
 #pragma unroll 1
@@ -605,12 +632,11 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                     if (col >= p.N) break;
                     float v[32];
                     __syncwarp();
-                    tmem_ld32(acc + c, v);
-                    tmem_ld_wait();
+                    tmem_read32(acc + c, v);
                     uint32_t w[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) w[i] = bf16x2(v[2 * i], v[2 * i + 1]);
-                    emit_rows(boxes, bx, lane, boxed, ok, w, &p.tmO0, p.out0, p.ld0, row0, col);
+                    boxes.emit(boxed, ok, w, &p.tmO0, p.out0, p.ld0, row0, col);
                 }
             } else {
                 const CUtensorMap *om = t.prod ? &p.tmO1 : &p.tmO0;
@@ -627,8 +653,7 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                         for (int i = 0; i < 32; ++i) v[i] = 0.0f;
                     } else {
                         __syncwarp();
-                        tmem_ld32(acc + c, v);
-                        tmem_ld_wait();
+                        tmem_read32(acc + c, v);
                     }
                     const int col = t.n0 + c;
                     uint32_t w[16];
@@ -637,7 +662,7 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                         for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
                             for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[16 * hf + i]);
-                            const uint8_t *box = fill_box<2>(boxes, bx, lane, w);
+                            const uint8_t *box = boxes.fill(w);
                             if (lane == 0) {
                                 if (p.accumulate)
                                     tma_add_3d(om, box, col + 16 * hf, row0, t.g);
@@ -649,7 +674,7 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                     } else {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) w[i] = bf16x2(v[2 * i], v[2 * i + 1]);
-                        const uint8_t *box = fill_box<2>(boxes, bx, lane, w);
+                        const uint8_t *box = boxes.fill(w);
                         if (lane == 0) {
                             tma_store_3d(om, box, col, row0, t.g);
                             bulk_commit();
@@ -742,8 +767,9 @@ bool out_map(CUtensorMap *m, void *ptr, int groups, int64_t rows, int64_t cols, 
 bool use_pair(int n, int G) { return n > 128ll * G; }
 
 template <int MODE, int CG>
-cudaError_t launch(const Params &p, int64_t tiles, cudaStream_t stream) {
+cudaError_t launch(Params &p, int64_t tiles, cudaStream_t stream) {
     using C = Cfg<MODE, CG>;
+    p.boxes = C::boxes(p.G);
     void (*kernel)(const Params);
     if constexpr (CG == 2)
         kernel = train_gemm_pair_kernel<MODE>;
@@ -758,13 +784,13 @@ cudaError_t launch(const Params &p, int64_t tiles, cudaStream_t stream) {
         std::lock_guard<std::mutex> lock(mu);
         if (dev >= 64 || resident[dev] == 0) {
             const cudaError_t e = cudaFuncSetAttribute(
-                kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(MAX_GROUPS));
+                kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
             if (e != cudaSuccess) return e;
             if (CG == 2) {
                 cudaLaunchConfig_t cfg = {};
                 cfg.gridDim = dim3(static_cast<unsigned>(num_sms()), 1, 1);
                 cfg.blockDim = dim3(THREADS, 1, 1);
-                cfg.dynamicSmemBytes = C::smem(MAX_GROUPS);
+                cfg.dynamicSmemBytes = 227 * 1024;
                 cfg.stream = stream;
                 int n = 0;
                 if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
@@ -782,7 +808,7 @@ cudaError_t launch(const Params &p, int64_t tiles, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(CG * units), 1, 1);
     cfg.blockDim = dim3(THREADS, 1, 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>(C::smem(p.G));
+    cfg.dynamicSmemBytes = static_cast<size_t>(C::smem(p.G, p.boxes));
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
