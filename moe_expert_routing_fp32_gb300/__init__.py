@@ -188,6 +188,11 @@ def _call(name: str, *args):
         raise MoeError(name, st)
 
 
+# the current device's number without torch's check for initialisation (a CUDA
+# tensor is at hand where it is asked for)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 class _Here:
     """Nothing to switch: the tensors' device is the current one."""
 
@@ -204,7 +209,7 @@ _here = _Here()
 def _on(dev):
     """The context in which a call for tensors on ``dev`` is made (entering
     torch.cuda.device costs more than the call where nothing changes)."""
-    if dev.type == "cuda" and dev.index == torch.cuda.current_device():
+    if dev.type == "cuda" and dev.index == _current_device():
         return _here
     return torch.cuda.device(dev)
 
@@ -395,15 +400,20 @@ def _arg(t, dtype, dev, shape, name):
     device (the call's), its shape (None: any) and that it is contiguous."""
     if t is None:
         return None
+    if t.dtype is dtype and t.device == dev and (shape is None or t.shape == shape) and \
+            t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"libmoe takes contiguous tensors only ({name})")
-    return t.data_ptr()
+    raise ValueError(f"libmoe takes contiguous tensors only ({name})")
+
+
+def _ptr_of(t):
+    return None if t is None else t.data_ptr()
 
 
 def _status_arg(status, dev):
@@ -643,9 +653,8 @@ def norm_residual(x, y, gamma_post=None, gate=None, scale=1.0, gamma_next=None, 
         xn = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if next_norm else None
         kp = torch.empty(T, dtype=torch.float32, device=dev) if post_norm else None
         kn = torch.empty(T, dtype=torch.float32, device=dev) if next_norm else None
-        ptr = lambda t: None if t is None else t.data_ptr()               # noqa: E731
         _call("moe_norm_residual", xp, yp, gp, gt, seq, S, gn, T, H, float(scale), float(eps), flags,
-              r.data_ptr(), ptr(xn), ptr(kp), ptr(kn), st, _stream(dev))
+              r.data_ptr(), _ptr_of(xn), _ptr_of(kp), _ptr_of(kn), st, _stream(dev))
     return dict(r=r, xn=xn, rstd_post=kp, rstd_next=kn)
 
 
@@ -685,11 +694,11 @@ def norm_residual_backward(d_r, d_xn, y, saved, gamma_post=None, gate=None, scal
         dgp = new(H) if post_norm else None
         dgt = new(S, H) if gate is not None else None
         dgn = new(H) if next_norm else None
-        ptr = lambda t: None if t is None else t.data_ptr()               # noqa: E731
         nbytes = norm_residual_backward_workspace_size(T, H, S)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         _call("moe_norm_residual_backward", drp, dnp, yp, rp, kp, kn, gp, gt, seq, S, gn, T, H,
-              float(scale), flags, d_x.data_ptr(), d_y.data_ptr(), ptr(dgp), ptr(dgt), ptr(dgn),
+              float(scale), flags, d_x.data_ptr(), d_y.data_ptr(), _ptr_of(dgp), _ptr_of(dgt),
+              _ptr_of(dgn),
               ws.data_ptr(), nbytes, st, _stream(dev))
     return dict(d_x=d_x, d_y=d_y, d_gamma_post=dgp, d_gate=dgt, d_gamma_next=dgn)
 

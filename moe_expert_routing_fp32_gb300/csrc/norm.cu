@@ -36,6 +36,7 @@ constexpr int WARPS = THREADS / 32;
 constexpr int MAX_CTAS = 304;             // two on each of 152 multiprocessors
 constexpr int MAX_SLOTS = 4;
 constexpr int MAX_H = 8192;
+constexpr int MAX_SMEM = 224 * 1024;      // two rows of 8192 columns, all arrays fp32 that can be
 
 // Layout of rows of H columns: warps per team, teams per CTA, vectors per lane.
 struct Shape {
@@ -75,42 +76,74 @@ struct Params {
     int32_t *dev_status;
 };
 
+// Two fp32 values in a 64-bit register: one instruction does the arithmetic of both.
+using f2 = uint64_t;
+__device__ __forceinline__ f2 pack2(float x, float y) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ f2 splat(float x) { return pack2(x, x); }
+__device__ __forceinline__ float2 unpack2(f2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 x, f2 y) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 x, f2 y) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 x, f2 y, f2 z) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+__device__ __forceinline__ f2 from_bf16x2(uint32_t w) {
+    return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint32_t to_bf16x2(f2 v) {
+    const float2 f = unpack2(v);
+    return bf16x2(f.x, f.y);
+}
+// Eight values as four pairs: of a bf16 vector, or the v-th eight of a row.
+__device__ __forceinline__ void widen(const uint4 &q, f2 (&o)[4]) {
+    o[0] = from_bf16x2(q.x), o[1] = from_bf16x2(q.y);
+    o[2] = from_bf16x2(q.z), o[3] = from_bf16x2(q.w);
+}
 template <bool F32>
-__device__ __forceinline__ void load8(const void *base, int v, float (&o)[8]) {
+__device__ __forceinline__ void load8(const void *base, int v, f2 (&o)[4]) {
     if (F32) {
-        const float4 a = reinterpret_cast<const float4 *>(base)[2 * v];
-        const float4 b = reinterpret_cast<const float4 *>(base)[2 * v + 1];
-        o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w;
-        o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
+        const ulonglong2 a = reinterpret_cast<const ulonglong2 *>(base)[2 * v];
+        const ulonglong2 b = reinterpret_cast<const ulonglong2 *>(base)[2 * v + 1];
+        o[0] = a.x, o[1] = a.y, o[2] = b.x, o[3] = b.y;
     } else {
-        const uint4 q = reinterpret_cast<const uint4 *>(base)[v];
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        widen(reinterpret_cast<const uint4 *>(base)[v], o);
+    }
+}
+__device__ __forceinline__ uint4 narrow(const f2 (&o)[4]) {
+    return make_uint4(to_bf16x2(o[0]), to_bf16x2(o[1]), to_bf16x2(o[2]), to_bf16x2(o[3]));
+}
+template <bool F32>
+__device__ __forceinline__ void store8(void *row, int v, const f2 (&o)[4]) {
+    if (F32) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            o[2 * i] = __uint_as_float(w[i] << 16);
-            o[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        for (int i = 0; i < 2; ++i) {
+            const float2 a = unpack2(o[2 * i]), b = unpack2(o[2 * i + 1]);
+            __stcs(reinterpret_cast<float4 *>(row) + 2 * v + i, make_float4(a.x, a.y, b.x, b.y));
         }
-    }
-}
-__device__ __forceinline__ void unpack8(const uint4 &q, float (&o)[8]) {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        o[2 * i] = __uint_as_float(w[i] << 16);
-        o[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-}
-__device__ __forceinline__ uint4 pack8(const float (&o)[8]) {
-    return make_uint4(bf16x2(o[0], o[1]), bf16x2(o[2], o[3]), bf16x2(o[4], o[5]), bf16x2(o[6], o[7]));
-}
-template <bool F32>
-__device__ __forceinline__ void store8(void *row, int v, const float (&o)[8]) {
-    if (F32) {
-        __stcs(reinterpret_cast<float4 *>(row) + 2 * v, make_float4(o[0], o[1], o[2], o[3]));
-        __stcs(reinterpret_cast<float4 *>(row) + 2 * v + 1, make_float4(o[4], o[5], o[6], o[7]));
     } else {
-        __stcs(reinterpret_cast<uint4 *>(row) + v, pack8(o));
+        __stcs(reinterpret_cast<uint4 *>(row) + v, narrow(o));
     }
+}
+__device__ __forceinline__ float total2(f2 v) {
+    const float2 f = unpack2(v);
+    return f.x + f.y;
 }
 
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
@@ -121,22 +154,31 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
         : "memory");
 }
 
-// A team: its threads' sum of a value (each call another of two buffers, so
+// A team: its threads' sums of two values (each call another of two buffers, so
 // one barrier a call is enough).
 struct Team {
     int W, id, lane, warp;      // warps, number in the CTA, lane and warp in the team
-    float *red;                 // [2][WARPS]
+    float2 *red;                // [2][WARPS]
     int parity;
-    __device__ __forceinline__ float sum(float v) {
+    __device__ __forceinline__ float2 sum(float x, float y) {
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-        if (W == 1) return v;
-        float *b = red + parity * WARPS;
+        for (int off = 16; off > 0; off >>= 1) {
+            x += __shfl_xor_sync(0xffffffffu, x, off);
+            y += __shfl_xor_sync(0xffffffffu, y, off);
+        }
+        if (W == 1) {
+            __syncwarp();
+            return make_float2(x, y);
+        }
+        float2 *b = red + parity * WARPS;
         parity ^= 1;
-        if (lane == 0) b[warp] = v;
+        if (lane == 0) b[warp] = make_float2(x, y);
         asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(32 * W) : "memory");
-        float s = 0.0f;
-        for (int i = 0; i < W; ++i) s += b[i];
+        float2 s = make_float2(0.0f, 0.0f);
+        for (int i = 0; i < W; ++i) {
+            s.x += b[i].x;
+            s.y += b[i].y;
+        }
         return s;
     }
 };
@@ -165,14 +207,11 @@ __device__ bool bounds_ok(const Params &p) {
     return !__syncthreads_or(bad);
 }
 
-// The rows of a team, one after the other: body(row, sequence, slot's address).
-// `body` calls the team's barrier at least once after its last read of the slot
-// and then release().
 template <bool BWD, bool XF, bool YF, int VPT>
 __global__ void __launch_bounds__(THREADS, VPT <= 2 ? 2 : 1) norm_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t s_bar[WARPS][MAX_SLOTS];
-    __shared__ float s_red[WARPS][2][WARPS];
+    __shared__ float2 s_red[WARPS][2][WARPS];
     __shared__ int s_abort;
     const Shape sh = shape_of(p.H);
     const int warp = threadIdx.x >> 5;
@@ -227,48 +266,102 @@ __global__ void __launch_bounds__(THREADS, VPT <= 2 ? 2 : 1) norm_kernel(const _
     const float inv_h = 1.0f / static_cast<float>(p.H);
     int seq = p.seq && a < b ? find_sequence(p.seq, p.S, a) : 0;
     int seq_end = p.seq && a < b ? __ldg(p.seq + seq + 1) : p.T;
-    // the gammas and the gate of this lane's columns
-    uint4 gp[VPT], gn[VPT], gt[VPT];
+    // What a lane keeps of its columns: gamma_next, and scale * gate * gamma_post
+    // (without the scale in the backward pass, where it joins a row's factor)
+    uint4 gn[VPT];
+    f2 gf[VPT][4];
     const uint4 ones = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+    auto column = [&](const uint16_t *base, int64_t row, int v) {
+        return base && v < nvec ? __ldg(reinterpret_cast<const uint4 *>(base) + row * nvec + v) : ones;
+    };
     auto gate_row = [&]() {
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int v = me + j * size;
-            gt[j] = p.gate && v < nvec
-                        ? __ldg(reinterpret_cast<const uint4 *>(p.gate) + static_cast<int64_t>(seq) * nvec + v)
-                        : ones;
+            f2 g[4], f[4];
+            widen(column(p.gate, seq, v), g);
+            widen(column(p.gamma_post, 0, v), f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                gf[j][i] = mul2(g[i], f[i]);
+                if (!BWD) gf[j][i] = mul2(gf[j][i], splat(p.scale));
+            }
         }
     };
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const int v = me + j * size;
-        gp[j] = p.gamma_post && v < nvec ? __ldg(reinterpret_cast<const uint4 *>(p.gamma_post) + v) : ones;
-        gn[j] = p.gamma_next && v < nvec ? __ldg(reinterpret_cast<const uint4 *>(p.gamma_next) + v) : ones;
-    }
+    for (int j = 0; j < VPT; ++j) gn[j] = column(p.gamma_next, 0, me + j * size);
     if (a < b) gate_row();
-    float cs[BWD ? VPT : 1][8], ns[BWD ? VPT : 1][8];
-    auto clear = [&](float (&s)[BWD ? VPT : 1][8]) {
+    constexpr int AV = BWD ? VPT : 1;
+    f2 cs[AV][4], ns[AV][4];
+    auto clear = [&](f2 (&s)[AV][4]) {
 #pragma unroll
-        for (int j = 0; j < (BWD ? VPT : 1); ++j)
+        for (int j = 0; j < AV; ++j)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s[j][i] = 0.0f;
+            for (int i = 0; i < 4; ++i) s[j][i] = 0;
     };
-    auto flush = [&](float *part, int64_t slot, const float (&s)[BWD ? VPT : 1][8]) {
+    auto flush = [&](float *part, int64_t slot, const f2 (&s)[AV][4]) {
         if (!part) return;
 #pragma unroll
-        for (int j = 0; j < (BWD ? VPT : 1); ++j) {
+        for (int j = 0; j < AV; ++j) {
             const int v = me + j * size;
             if (v >= nvec) continue;
-            float4 *d = reinterpret_cast<float4 *>(part + slot * p.H) + 2 * v;
-            d[0] = make_float4(s[j][0], s[j][1], s[j][2], s[j][3]);
-            d[1] = make_float4(s[j][4], s[j][5], s[j][6], s[j][7]);
+            ulonglong2 *d = reinterpret_cast<ulonglong2 *>(part + slot * p.H) + 2 * v;
+            d[0] = make_ulonglong2(s[j][0], s[j][1]);
+            d[1] = make_ulonglong2(s[j][2], s[j][3]);
         }
     };
     clear(cs);
     clear(ns);
 
+    // A row's two sums depend on one another, but the second one of a row and the
+    // first one of the next do not: they are taken together, one barrier a row.
     int slot = 0;
     uint32_t phase = 0;
+    const uint8_t *in = ring;
+    bool keep = true;                                // no wait has given up
+    auto arrive = [&]() {                            // the row in `slot` has landed
+        in = ring + slot * p.slot_bytes;
+        mbar_wait_bounded(&bar[slot], phase, abort, p.dev_status);
+        keep = *abort == 0;
+    };
+    const f2 ks2 = splat(p.scale);
+    // first sum of a row: forward of y^2; backward of w r with w = k_r d_xn gamma_next
+    // (and the column sums of d_xn r^)
+    auto first_sum = [&](float k_next) {
+        f2 m = 0;
+        if (BWD ? p.next : p.post) {
+            const f2 kr2 = splat(k_next);
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int v = me + j * size;
+                if (v >= nvec) continue;
+                if (!BWD) {
+                    f2 y[4];
+                    load8<YF>(in + p.off[0], v, y);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) m = fma2(y[i], y[i], m);
+                } else {
+                    f2 d[4], r[4], f[4];
+                    load8<false>(in + p.off[0], v, d);
+                    load8<XF>(in + p.off[1], v, r);
+                    widen(gn[j], f);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const f2 u = mul2(d[i], kr2);
+                        ns[j % AV][i] = fma2(u, r[i], ns[j % AV][i]);
+                        m = fma2(mul2(u, f[i]), r[i], m);
+                    }
+                }
+            }
+        }
+        return total2(m);
+    };
+    float k_next = 0.0f, s1 = 0.0f;
+    if (a < b) {
+        if (BWD && p.next) k_next = __ldg(p.k_next + a);
+        arrive();
+        s1 = team.sum(first_sum(k_next), 0.0f).x;
+    }
     for (int row = a; row < b; ++row) {
         if (row == seq_end) {                        // the next sequence that has rows
             if (BWD) {
@@ -280,141 +373,135 @@ __global__ void __launch_bounds__(THREADS, VPT <= 2 ? 2 : 1) norm_kernel(const _
             while (seq_end == row);
             gate_row();
         }
-        const uint8_t *in = ring + slot * p.slot_bytes;
-        mbar_wait_bounded(&bar[slot], phase, abort, p.dev_status);
-        const bool keep = *abort == 0;
-        auto release = [&]() {
-            if (first && row + p.slots < b && *abort == 0) fetch(row + p.slots, slot);
-        };
+        const bool more = row + 1 < b;
+        const int this_slot = slot;
+        const float k_post = BWD && p.post ? __ldg(p.k_post + row) : 1.0f;
+        const float k_after = BWD && p.next && more ? __ldg(p.k_next + row + 1) : 0.0f;
+        f2 keep_q[VPT][4], m = 0;                    // forward r, backward q
+        uint4 yq[BWD && !YF ? VPT : 1];
+        f2 yf[BWD && YF ? VPT : 1][4];
         if (!BWD) {
-            const void *ys = in + p.off[0], *xs = in + p.off[1];
             float ky = 1.0f;
             if (p.post) {
-                float ss = 0.0f;
-#pragma unroll
-                for (int j = 0; j < VPT; ++j) {
-                    const int v = me + j * size;
-                    if (v >= nvec) continue;
-                    float y[8];
-                    load8<YF>(ys, v, y);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
-                }
-                ky = 1.0f / sqrtf(team.sum(ss) * inv_h + p.eps);
+                ky = 1.0f / sqrtf(s1 * inv_h + p.eps);
                 if (first && keep && p.rstd_post) p.rstd_post[row] = ky;
             }
-            float r[VPT][8], ss = 0.0f;
+            const f2 ky2 = splat(ky);
             uint8_t *ro = static_cast<uint8_t *>(p.out0) + static_cast<int64_t>(row) * p.H * (XF ? 4 : 2);
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
                 const int v = me + j * size;
                 if (v >= nvec) continue;
-                float y[8], x[8], g[8], f[8];
-                load8<YF>(ys, v, y);
-                load8<XF>(xs, v, x);
-                unpack8(gt[j], g);
-                unpack8(gp[j], f);
+                f2 y[4], x[4];
+                load8<YF>(in + p.off[0], v, y);
+                load8<XF>(in + p.off[1], v, x);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    r[j][i] = fmaf(p.scale * g[i], y[i] * ky * f[i], x[i]);
-                if (!XF) unpack8(pack8(r[j]), r[j]);     // the norm of what is stored
-                if (keep) store8<XF>(ro, v, r[j]);
+                for (int i = 0; i < 4; ++i) x[i] = fma2(mul2(y[i], ky2), gf[j][i], x[i]);
+                if (XF) {
+                    if (keep) store8<true>(ro, v, x);
+                } else {                             // the norm is that of what is stored
+                    const uint4 q = narrow(x);
+                    if (keep) __stcs(reinterpret_cast<uint4 *>(ro) + v, q);
+                    widen(q, x);
+                }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ss = fmaf(r[j][i], r[j][i], ss);
-            }
-            const float tot = team.sum(ss);
-            if (team.W == 1) __syncwarp();
-            release();
-            if (p.next) {
-                const float kr = 1.0f / sqrtf(tot * inv_h + p.eps);
-                if (first && keep && p.rstd_next) p.rstd_next[row] = kr;
-                uint8_t *xo = static_cast<uint8_t *>(p.out1) + static_cast<int64_t>(row) * p.H * 2;
-#pragma unroll
-                for (int j = 0; j < VPT; ++j) {
-                    const int v = me + j * size;
-                    if (v >= nvec) continue;
-                    float f[8], o[8];
-                    unpack8(gn[j], f);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i] = r[j][i] * kr * f[i];
-                    if (keep) store8<false>(xo, v, o);
+                for (int i = 0; i < 4; ++i) {
+                    m = fma2(x[i], x[i], m);
+                    keep_q[j][i] = x[i];
                 }
             }
         } else {
-            const void *nx = in + p.off[0], *rs = in + p.off[1], *dr = in + p.off[2], *ys = in + p.off[3];
-            float m1 = 0.0f, kr = 0.0f;
-            if (p.next) {
-                kr = __ldg(p.k_next + row);
-#pragma unroll
-                for (int j = 0; j < VPT; ++j) {
-                    const int v = me + j * size;
-                    if (v >= nvec) continue;
-                    float d[8], r[8], f[8];
-                    load8<false>(nx, v, d);
-                    load8<XF>(rs, v, r);
-                    unpack8(gn[j], f);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float dr_hat = d[i] * (r[i] * kr);
-                        ns[j][i] += dr_hat;
-                        m1 = fmaf(dr_hat, f[i], m1);
-                    }
-                }
-                m1 = team.sum(m1) * inv_h;
-            }
-            const float ky = p.post ? __ldg(p.k_post + row) : 1.0f;
-            float q[VPT][8], yh[VPT][8], m2 = 0.0f;
+            // With the row factors taken out of the sums,
+            //   d = d_r + w - r (k_r^2 mean(w r)),
+            // and, with q = scale k_y d gate gamma_post, d_y = q - y (k_y^2 mean(q y)).
+            const f2 kr2 = splat(k_next), ky2 = mul2(ks2, splat(k_post));
+            const f2 c1 = splat(-k_next * k_next * (s1 * inv_h));
             uint8_t *xo = static_cast<uint8_t *>(p.out0) + static_cast<int64_t>(row) * p.H * (XF ? 4 : 2);
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
                 const int v = me + j * size;
                 if (v >= nvec) continue;
-                float d[8], f[8], g[8];
+                f2 d[4];
                 if (p.src[2])
-                    load8<XF>(dr, v, d);
+                    load8<XF>(in + p.off[2], v, d);
                 else
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) d[i] = 0.0f;
+                    for (int i = 0; i < 4; ++i) d[i] = 0;
                 if (p.next) {
-                    float t[8], r[8];
-                    load8<false>(nx, v, t);
-                    load8<XF>(rs, v, r);
-                    unpack8(gn[j], f);
+                    f2 t[4], r[4], f[4];
+                    load8<false>(in + p.off[0], v, t);
+                    load8<XF>(in + p.off[1], v, r);
+                    widen(gn[j], f);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        d[i] = fmaf(kr, fmaf(-(r[i] * kr), m1, t[i] * f[i]), d[i]);
+                    for (int i = 0; i < 4; ++i)
+                        d[i] = fma2(r[i], c1, fma2(mul2(t[i], kr2), f[i], d[i]));
                 }
                 if (keep && p.out0) store8<XF>(xo, v, d);
-                load8<YF>(ys, v, yh[j]);
-                unpack8(gt[j], g);
-                unpack8(gp[j], f);
+                f2 y[4];
+                if (YF) {
+                    load8<true>(in + p.off[3], v, yf[YF ? j : 0]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    yh[j][i] *= ky;
-                    const float sd = p.scale * d[i];
-                    cs[j][i] = fmaf(sd, yh[j][i], cs[j][i]);
-                    q[j][i] = sd * g[i] * f[i];
-                    m2 = fmaf(q[j][i], yh[j][i], m2);
+                    for (int i = 0; i < 4; ++i) y[i] = yf[YF ? j : 0][i];
+                } else {
+                    yq[YF ? 0 : j] = reinterpret_cast<const uint4 *>(in + p.off[3])[v];
+                    widen(yq[YF ? 0 : j], y);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const f2 e = mul2(d[i], ky2);
+                    cs[j % AV][i] = fma2(e, y[i], cs[j % AV][i]);
+                    keep_q[j][i] = mul2(e, gf[j][i]);
+                    m = fma2(keep_q[j][i], y[i], m);
                 }
             }
-            m2 = team.sum(m2) * inv_h;
-            if (team.W == 1) __syncwarp();
-            release();
-            if (!p.post) m2 = 0.0f;
+        }
+        float ahead = 0.0f;
+        if (more) {
+            if (++slot == p.slots) {
+                slot = 0;
+                phase ^= 1;
+            }
+            arrive();
+            ahead = first_sum(k_after);
+        }
+        const float2 sums = team.sum(total2(m), ahead);
+        // every thread has read this row's slot
+        if (first && row + p.slots < b && *abort == 0) fetch(row + p.slots, this_slot);
+        s1 = sums.y;
+        k_next = k_after;
+        if (!BWD) {
+            if (!p.next) continue;
+            const float kr = 1.0f / sqrtf(sums.x * inv_h + p.eps);
+            if (first && keep && p.rstd_next) p.rstd_next[row] = kr;
+            uint8_t *xo = static_cast<uint8_t *>(p.out1) + static_cast<int64_t>(row) * p.H * 2;
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int v = me + j * size;
+                if (v >= nvec) continue;
+                f2 f[4];
+                widen(gn[j], f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] = mul2(mul2(keep_q[j][i], splat(kr)), f[i]);
+                if (keep) store8<false>(xo, v, f);
+            }
+        } else {
+            const f2 c2 = splat(p.post ? -k_post * k_post * (sums.x * inv_h) : 0.0f);
             uint8_t *yo = static_cast<uint8_t *>(p.out1) + static_cast<int64_t>(row) * p.H * (YF ? 4 : 2);
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
                 const int v = me + j * size;
                 if (v >= nvec) continue;
-                float o[8];
+                f2 y[4];
+                if (YF) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = ky * fmaf(-yh[j][i], m2, q[j][i]);
-                if (keep && p.out1) store8<YF>(yo, v, o);
+                    for (int i = 0; i < 4; ++i) y[i] = yf[YF ? j : 0][i];
+                } else {
+                    widen(yq[YF ? 0 : j], y);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = fma2(y[i], c2, keep_q[j][i]);
+                if (keep && p.out1) store8<YF>(yo, v, y);
             }
-        }
-        if (++slot == p.slots) {
-            slot = 0;
-            phase ^= 1;
         }
     }
     if (BWD) {
@@ -440,15 +527,18 @@ struct SumParams {
 __device__ __forceinline__ float add_slots(const float *part, int64_t slot0, int n, int first, int step,
                                            int H, int col) {
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    int i = first;
-    for (; i + 3 * step < n; i += 4 * step)
+    for (int i = first; i < n; i += 8 * step) {      // eight loads at a time
+        float v[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) s[k] += __ldg(part + (slot0 + i + k * step) * H + col);
-    for (; i < n; i += step) s[0] += __ldg(part + (slot0 + i) * H + col);
+        for (int k = 0; k < 8; ++k)
+            v[k] = i + k * step < n ? __ldg(part + (slot0 + i + k * step) * H + col) : 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s[k & 3] += v[k];
+    }
     return (s[0] + s[1]) + (s[2] + s[3]);
 }
 __global__ void __launch_bounds__(32 * RED_WARPS) norm_sums_kernel(const SumParams p) {
-    __shared__ float s_red[RED_WARPS][33];
+    __shared__ float s_red[RED_WARPS][RED_WARPS][33];   // [sequence][warp][column]
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -463,15 +553,21 @@ __global__ void __launch_bounds__(32 * RED_WARPS) norm_sums_kernel(const SumPara
     const int col = min(h, p.H - 1);
     const bool in = h < p.H;
     auto bf = [&](const uint16_t *v, int64_t i) { return v ? bf16_bits_to_float(__ldg(v + i)) : 1.0f; };
-    auto block_sum = [&](float v) {
-        s_red[warp][lane] = v;
-        __syncthreads();
+    // what the warps left in s_red[i], the first warps' sums first
+    auto add_warps = [&](int i) {
         float s = 0.0f;
 #pragma unroll
-        for (int w = 0; w < RED_WARPS; ++w) s += s_red[w][lane];
-        __syncthreads();
+        for (int w = 0; w < RED_WARPS; ++w) s += s_red[i][w][lane];
         return s;
     };
+    if (blockIdx.y == 0) {
+        if (!p.d_gamma_next) return;
+        s_red[0][warp][lane] = add_slots(p.part_n, 0, p.nteams, warp, RED_WARPS, p.H, col);
+        __syncthreads();
+        if (warp == 0 && in) p.d_gamma_next[h] = add_warps(0);
+        return;
+    }
+    if (!p.d_gamma_post && !p.d_gate) return;
     // the teams that have rows of [a, b): team i owns rows [i T / n, (i + 1) T / n)
     auto team_of = [&](int row) {
         int i = static_cast<int>((static_cast<int64_t>(row) * p.nteams) / p.T);
@@ -479,29 +575,35 @@ __global__ void __launch_bounds__(32 * RED_WARPS) norm_sums_kernel(const SumPara
         while (static_cast<int64_t>(i) * p.T / p.nteams > row) --i;
         return i;
     };
-    if (p.d_gamma_next) {
-        const float v = block_sum(add_slots(p.part_n, 0, p.nteams, warp, RED_WARPS, p.H, col));
-        if (warp == 0 && in) p.d_gamma_next[h] = v;
-    }
-    if (!p.d_gamma_post && !p.d_gate) return;
+    auto part_of = [&](int s, int first, int step) {
+        const int a = p.seq ? __ldg(p.seq + s) : 0, b = p.seq ? __ldg(p.seq + s + 1) : p.T;
+        if (a >= b) return 0.0f;
+        const int t0 = team_of(a), t1 = team_of(b - 1);
+        return add_slots(p.part_c, static_cast<int64_t>(t0) + s, t1 - t0 + 1, first, step, p.H, col);
+    };
     const float gp = bf(p.gamma_post, col);
     float gamma = 0.0f;
-    const bool shared = p.S < RED_WARPS;
-    for (int s = shared ? 0 : warp; s < p.S; s += shared ? 1 : RED_WARPS) {
-        const int a = p.seq ? __ldg(p.seq + s) : 0, b = p.seq ? __ldg(p.seq + s + 1) : p.T;
+    if (p.S < RED_WARPS) {
+        for (int s = 0; s < p.S; ++s) s_red[s][warp][lane] = part_of(s, warp, RED_WARPS);
+        __syncthreads();
         float c = 0.0f;
-        if (a < b) {
-            const int t0 = team_of(a), t1 = team_of(b - 1);
-            c = add_slots(p.part_c, static_cast<int64_t>(t0) + s, t1 - t0 + 1, shared ? warp : 0,
-                          shared ? RED_WARPS : 1, p.H, col);
+        if (warp < p.S) {
+            c = add_warps(warp);
+            if (p.d_gate && in) p.d_gate[static_cast<int64_t>(warp) * p.H + h] = gp * c;
+            gamma = bf(p.gate, static_cast<int64_t>(warp) * p.H + col) * c;
         }
-        if (shared) c = block_sum(c);
-        if (p.d_gate && in && (!shared || warp == 0)) p.d_gate[static_cast<int64_t>(s) * p.H + h] = gp * c;
-        gamma = fmaf(bf(p.gate, static_cast<int64_t>(s) * p.H + col), c, gamma);
+        __syncthreads();
+    } else {
+        for (int s = warp; s < p.S; s += RED_WARPS) {
+            const float c = part_of(s, 0, 1);
+            if (p.d_gate && in) p.d_gate[static_cast<int64_t>(s) * p.H + h] = gp * c;
+            gamma = fmaf(bf(p.gate, static_cast<int64_t>(s) * p.H + col), c, gamma);
+        }
     }
     if (p.d_gamma_post) {
-        if (!shared) gamma = block_sum(gamma);
-        if (warp == 0 && in) p.d_gamma_post[h] = gamma;
+        s_red[0][warp][lane] = gamma;
+        __syncthreads();
+        if (warp == 0 && in) p.d_gamma_post[h] = add_warps(0);
     }
 }
 
@@ -509,9 +611,9 @@ __global__ void __launch_bounds__(32 * RED_WARPS) norm_sums_kernel(const SumPara
 inline bool a16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 template <typename K, typename P>
-cudaError_t start(K kernel, int grid, int block, int smem, const P &p, cudaStream_t stream) {
+cudaError_t start(K kernel, dim3 grid, int block, int smem, const P &p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(static_cast<unsigned>(block), 1, 1);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = stream;
@@ -526,7 +628,6 @@ cudaError_t start(K kernel, int grid, int block, int smem, const P &p, cudaStrea
 template <bool BWD, bool XF, bool YF, int VPT>
 cudaError_t launch_shape(const Params &p, const Shape &sh, cudaStream_t stream) {
     auto kernel = norm_kernel<BWD, XF, YF, VPT>;
-    constexpr int MAX_SMEM = 224 * 1024;
     static std::mutex mu;
     static bool attr_done[64] = {};
     int dev = 0;
@@ -540,7 +641,7 @@ cudaError_t launch_shape(const Params &p, const Shape &sh, cudaStream_t stream) 
             if (dev < 64) attr_done[dev] = true;
         }
     }
-    const int grid = static_cast<int>(ceil_div(p.nteams, sh.teams));
+    const dim3 grid(static_cast<unsigned>(ceil_div(p.nteams, sh.teams)));
     return start(kernel, grid, THREADS, sh.teams * p.slots * p.slot_bytes, p, stream);
 }
 
@@ -554,11 +655,12 @@ cudaError_t launch(Params &p, bool xf, bool yf, cudaStream_t stream) {
         if (p.src[i]) at += p.bytes[i];
     }
     p.slot_bytes = at;
-    // rows ahead: as many as two CTAs a multiprocessor have room for, or one where
-    // that is less than two
+    // rows in the ring: as many as two CTAs a multiprocessor have room for, or one
+    // where that is less than two (a row and the next one are needed at once)
     const int row = sh.teams * at;
     p.slots = std::min(MAX_SLOTS, 104 * 1024 / row);
-    if (p.slots < 2) p.slots = std::max(1, std::min(MAX_SLOTS, 208 * 1024 / row));
+    if (p.slots < 2) p.slots = std::min(MAX_SLOTS, MAX_SMEM / row);
+    if (p.slots < 2) return cudaErrorInvalidValue;
 #define MOE_NORM(X, Y)                                                                        \
     (sh.vpt == 1   ? launch_shape<BWD, X, Y, 1>(p, sh, stream)                               \
      : sh.vpt == 2 ? launch_shape<BWD, X, Y, 2>(p, sh, stream)                               \
@@ -721,7 +823,7 @@ extern "C" moe_status_t moe_norm_residual_backward(
     q.d_gamma_post = d_gamma_post;
     q.d_gate = d_gate;
     q.d_gamma_next = d_gamma_next;
-    if (start(norm_sums_kernel, static_cast<int>(ceil_div(H, 32)), 32 * RED_WARPS, 0, q, s) != cudaSuccess)
+    if (start(norm_sums_kernel, dim3(static_cast<unsigned>(ceil_div(H, 32)), 2), 32 * RED_WARPS, 0, q, s) != cudaSuccess)
         return MOE_ERR_CUDA;
     return MOE_OK;
 }
