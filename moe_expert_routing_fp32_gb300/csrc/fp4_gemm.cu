@@ -206,37 +206,6 @@ __device__ __forceinline__ Tile decode_tile(const Params &p, int tile, int &g, c
     return t;
 }
 
-// Two fp32 values in a 64-bit register, for the packed arithmetic.
-__device__ __forceinline__ uint64_t pair(float x, float y) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-    return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ float rcp(float x) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 // SiLU(alpha g) / alpha of two gate sums, g / (1 + 2^(c g)) with c = -alpha log2 e.
 // With G = alpha g, the product c g is rounded before the exponential: for
 // negative gates that is 2.3 |G| 2^-24 of the result (2^-17 at G = -60), beside
@@ -244,10 +213,10 @@ __device__ __forceinline__ float rcp(float x) {
 // rounding is 2^-9.  Below G = -87.3 the sum passes 2^126, the reciprocal is
 // flushed and the result is zero, |G| 2^-126 at most from the true one.
 __device__ __forceinline__ uint64_t silu2(float x, float y, uint64_t c) {
-    const uint64_t g = pair(x, y);
-    const float2 t = unpair(mul2(g, c));
-    const float2 d = unpair(add2(pair(ex2(t.x), ex2(t.y)), pair(1.0f, 1.0f)));
-    return mul2(g, pair(rcp(d.x), rcp(d.y)));
+    const uint64_t g = pack2(x, y);
+    const float2 t = unpack2(mul2(g, c));
+    const float2 d = unpack2(add2(pack2(ex2(t.x), ex2(t.y)), pack2(1.0f, 1.0f)));
+    return mul2(g, pack2(rcp(d.x), rcp(d.y)));
 }
 
 // 64 act columns of one row (bf16 pairs, from column col on): codes and scale
@@ -548,7 +517,7 @@ __device__ __forceinline__ void fp4_gemm(const Params &p) {
         };
         // act = SiLU(alpha g) (alpha u) = alpha^2 (g / (1 + e^(-alpha g))) u
         const float c = -1.4426950408889634f * p.alpha, a2 = p.alpha * p.alpha;
-        const uint64_t gate_c = pair(c, c), alpha2 = pair(a2, a2);
+        const uint64_t gate_c = pack2(c, c), alpha2 = pack2(a2, a2);
         int g = 0;
         for (int tile = first_tile; tile < total; tile += step) {
             const Tile t = decode_tile<BM * CG>(p, tile, g, s_off, s_prefix);
@@ -571,7 +540,7 @@ __device__ __forceinline__ void fp4_gemm(const Params &p) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     const float *v = i < 16 ? x + 2 * i : y + 2 * (i - 16);
-                    const float2 a = unpair(mul2(mul2(sg[i], pair(v[0], v[1])), alpha2));
+                    const float2 a = unpack2(mul2(mul2(sg[i], pack2(v[0], v[1])), alpha2));
                     w[i] = bf16x2(a.x, a.y);
                 }
                 if (MODE != MODE_SWIGLU_Q)

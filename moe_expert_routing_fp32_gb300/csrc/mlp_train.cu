@@ -604,21 +604,18 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                     uint32_t wg[16], wu[16], wa[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        float vg[2], vu[2], va[2];
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const float gt = __uint_as_float(j ? hg[i] & 0xFFFF0000u : hg[i] << 16);
-                            const float up = __uint_as_float(j ? hu[i] & 0xFFFF0000u : hu[i] << 16);
-                            const float s = __fdividef(1.0f, 1.0f + __expf(-gt));
-                            const float gs = gt * s;                    // SiLU(gate)
-                            va[j] = gs * up;
-                            vu[j] = d[2 * i + j] * gs;
-                            // s (1 + gate (1 - s)) = s + gs (1 - s)
-                            vg[j] = d[2 * i + j] * up * (s + gs * (1.0f - s));
-                        }
-                        wg[i] = bf16x2(vg[0], vg[1]);
-                        wu[i] = bf16x2(vu[0], vu[1]);
-                        wa[i] = bf16x2(va[0], va[1]);
+                        const f2 gt = from_bf16x2(hg[i]), up = from_bf16x2(hu[i]);
+                        const f2 dd = pack2(d[2 * i], d[2 * i + 1]);
+                        // s = 1 / (1 + 2^(-gate log2 e))
+                        const float2 e = unpack2(mul2(gt, splat(-1.4426950408889634f)));
+                        const float2 q = unpack2(add2(pack2(ex2(e.x), ex2(e.y)), splat(1.0f)));
+                        const f2 s = pack2(rcp(q.x), rcp(q.y));
+                        const f2 gs = mul2(gt, s);                  // SiLU(gate)
+                        wa[i] = to_bf16x2(mul2(gs, up));
+                        wu[i] = to_bf16x2(mul2(dd, gs));
+                        // s (1 + gate (1 - s)) = s + gs (1 - s)
+                        const f2 t = fma2(gs, fma2(s, splat(-1.0f), splat(1.0f)), s);
+                        wg[i] = to_bf16x2(mul2(mul2(dd, up), t));
                     }
                     boxes.emit(boxed, ok, wg, &p.tmO0, p.out0, p.ld0, row0, col);
                     boxes.emit(boxed, ok, wu, &p.tmO0, p.out0, p.ld0, row0,

@@ -76,41 +76,6 @@ struct Params {
     int32_t *dev_status;
 };
 
-// Two fp32 values in a 64-bit register: one instruction does the arithmetic of both.
-using f2 = uint64_t;
-__device__ __forceinline__ f2 pack2(float x, float y) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ f2 splat(float x) { return pack2(x, x); }
-__device__ __forceinline__ float2 unpack2(f2 v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ f2 mul2(f2 x, f2 y) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-    return r;
-}
-__device__ __forceinline__ f2 add2(f2 x, f2 y) {
-    f2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-    return r;
-}
-__device__ __forceinline__ f2 fma2(f2 x, f2 y, f2 z) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
-    return r;
-}
-__device__ __forceinline__ f2 from_bf16x2(uint32_t w) {
-    return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-}
-__device__ __forceinline__ uint32_t to_bf16x2(f2 v) {
-    const float2 f = unpack2(v);
-    return bf16x2(f.x, f.y);
-}
 // Eight values as four pairs: of a bf16 vector, or the v-th eight of a row.
 __device__ __forceinline__ void widen(const uint4 &q, f2 (&o)[4]) {
     o[0] = from_bf16x2(q.x), o[1] = from_bf16x2(q.y);
