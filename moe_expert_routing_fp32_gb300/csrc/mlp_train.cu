@@ -56,6 +56,7 @@ enum { FWD = 0, DACT = 1, DX = 2, DW = 3 };
 struct Params {
     CUtensorMap tmA, tmB;      // operands (DW: none, it takes the groups' maps)
     CUtensorMap tmO0, tmO1;    // FWD: h, act; DACT: d_h, act; DX: d_x; DW: d_W13, d_W2
+    CUtensorMap tmAh, tmBh;    // a pair's tiles of at most 128 rows: 64-row boxes of A (FWD: and B)
     CUtensorMap tmG[NMAPS];    // DACT: d_h, x, d_y, act, to be cut at each group's end
     CUtensorMap *maps;         // [G][NMAPS] in the workspace
     const int32_t *offsets;
@@ -91,9 +92,10 @@ struct Cfg {
     static constexpr int BAR_OFF = MAP_OFF + (MODE == DACT ? NMAPS * 128 : 0);
     static constexpr int NBARS = 2 * STAGES + 5;        // full, empty, tfull, tempty, drain
     static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
-    static constexpr int OFFS_OFF = MISC_OFF + 16;
+    static constexpr int W_MISC_OFF = BAR_OFF + 13 * 8;   // the wide kernel has a stage more
+    static constexpr int OFFS_OFF = W_MISC_OFF + 16;
     static constexpr int smem(int G, int boxes) {
-        return 1024 + EPI_OFF + boxes * BOX_BYTES + OFFS_OFF + (MODE == DW ? 0 : (2 * G + 2) * 4);
+        return 1024 + EPI_OFF + boxes * BOX_BYTES + OFFS_OFF + (MODE == DW ? G + 1 : 2 * G + 2) * 4;
     }
     // two boxes where they fit beside the groups' tables: a warp fills one while the
     // last one's store still reads the other
@@ -217,7 +219,7 @@ __device__ int list_tiles(const Params &p, int *s_off, int *s_prefix, volatile i
 // Tiles of a group: rows fastest while the group has fewer rows than its
 // weights, columns fastest otherwise (what is shared is read from L2).  DW: the
 // rows of the gradient fastest, both products of a group one after the other.
-template <int MODE, int BMT>
+template <int MODE, int BMT, int BNT = BN>
 __device__ __forceinline__ Tile decode_tile(const Params &p, int tile, int &g, const int *s_off,
                                             const int *s_prefix) {
     Tile t;
@@ -230,9 +232,9 @@ __device__ __forceinline__ Tile decode_tile(const Params &p, int tile, int &g, c
         const int mt = t.prod ? p.mt1 : p.mt0;
         const int n = local / mt;
         t.m0 = (local - n * mt) * 256;
-        t.n0 = n * BN;
-        t.row0 = __ldg(p.offsets + t.g);
-        t.row_end = __ldg(p.offsets + t.g + 1);
+        t.n0 = n * BNT;
+        t.row0 = s_off[t.g];
+        t.row_end = s_off[t.g + 1];
         t.n_blk = 0;
     } else {
         while (s_prefix[g + 1] <= tile) ++g;
@@ -257,7 +259,7 @@ struct Boxes {
     int n, at, lane;           // one or two, the next one
     // 64 bytes of each of the warp's 32 rows (lane i: row row0 + i) into a box, in the
     // 64-byte swizzle of the output maps; the caller stores it.
-    __device__ __forceinline__ const uint8_t *fill(const uint32_t (&w)[16]) {
+    __device__ __forceinline__ const uint8_t *fill(const uint32_t *w) {
         uint8_t *box = base + at * EPI_BYTES;
         if (lane == 0) {                             // the store that last used it has read it
             if (n == 2)
@@ -274,6 +276,18 @@ struct Boxes {
         fence_proxy_async();
         __syncwarp();
         return box;
+    }
+    // 128 bytes of each row into both boxes as one, in the 128-byte swizzle (DW).
+    __device__ __forceinline__ const uint8_t *fill_wide(const uint32_t (&w)[32]) {
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+#pragma unroll
+        for (int ch = 0; ch < 8; ++ch)
+            *reinterpret_cast<uint4 *>(base + lane * 128 + ((ch ^ (lane & 7)) << 4)) =
+                make_uint4(w[4 * ch], w[4 * ch + 1], w[4 * ch + 2], w[4 * ch + 3]);
+        fence_proxy_async();
+        __syncwarp();
+        return base;
     }
     // 32 bf16 columns of the rows: through a box where all 32 rows belong to the
     // group, else each lane its own row.
@@ -294,6 +308,97 @@ struct Boxes {
         }
     }
 };
+
+// FWD: 32 columns of gate (x) and up (y) sums to h and act.
+__device__ __forceinline__ void emit_forward(const Params &p, Boxes &boxes, bool boxed, bool ok,
+                                             const float (&x)[32], const float (&y)[32], int row0,
+                                             int col) {
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = bf16x2(x[2 * i], x[2 * i + 1]);
+    boxes.emit(boxed, ok, w, &p.tmO0, p.out0, p.ld0, row0, col);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = bf16x2(y[2 * i], y[2 * i + 1]);
+    boxes.emit(boxed, ok, w, &p.tmO0, p.out0, p.ld0, row0, p.N + col);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float a[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float v = x[2 * i + j];
+            a[j] = __fdividef(v, 1.0f + __expf(-v)) * y[2 * i + j];
+        }
+        w[i] = bf16x2(a[0], a[1]);
+    }
+    boxes.emit(boxed, ok, w, &p.tmO1, p.out1, p.ld1, row0, col);
+}
+
+// DW: 64 columns of a gradient from tensor memory at `taddr`; false where they and
+// all further ones are off the gradient (sizes of 128 mod the tile) or nothing has to
+// be written (an idle expert's zeros, added).  They leave as rows of 128 bytes where
+// the boxes have room for those: a store's hand-over to the async proxy costs a warp
+// more than the values it moves.
+__device__ __forceinline__ bool emit_gradient(const Params &p, Boxes &boxes, const Tile &t,
+                                              uint32_t taddr, int row0, int col) {
+    const CUtensorMap *om = t.prod ? &p.tmO1 : &p.tmO0;
+    const int M = t.prod ? p.H : 2 * p.I, N = t.prod ? p.I : p.H;
+    const bool none = t.row_end == t.row0;
+    if (row0 >= M || col >= N || (none && p.accumulate)) return false;
+    auto store = [&](const uint8_t *box, int c) {
+        if (boxes.lane == 0) {
+            if (p.accumulate)
+                tma_add_3d(om, box, c, row0, t.g);
+            else
+                tma_store_3d(om, box, c, row0, t.g);
+            bulk_commit();
+        }
+    };
+    float v[2][32];
+    if (none) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[0][i] = v[1][i] = 0.0f;
+    } else {
+        __syncwarp();
+        tmem_read32(taddr, v[0]);
+        tmem_read32(taddr + 32, v[1]);
+    }
+    if (p.w_f32) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint32_t w[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[k][i]);
+            if (boxes.n == 2) {
+                store(boxes.fill_wide(w), col + 32 * k);
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) store(boxes.fill(w + 16 * h), col + 32 * k + 16 * h);
+            }
+        }
+    } else {
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) w[i] = bf16x2(v[i / 16][2 * (i % 16)], v[i / 16][2 * (i % 16) + 1]);
+        if (boxes.n == 2) {
+            store(boxes.fill_wide(w), col);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) store(boxes.fill(w + 16 * h), col + 32 * h);
+        }
+    }
+    return true;
+}
+
+// DW: the group offsets, and whether they ascend inside the rows.  All threads.
+__device__ __forceinline__ bool load_groups(const Params &p, int *s_off) {
+    int bad = 0;
+    for (int g = threadIdx.x; g <= p.G; g += THREADS) {
+        const int a = p.offsets[g], b = p.offsets[min(g + 1, p.G)];
+        s_off[g] = a;
+        bad |= a < 0 || b < a || b > p.n;
+    }
+    return !__syncthreads_or(bad);
+}
 
 template <int MODE, int CG>
 __device__ __forceinline__ void train_gemm(const Params &p) {
@@ -350,12 +455,7 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int total;
     if (MODE == DW) {
-        int bad = 0;
-        for (int g = tid; g < p.G; g += THREADS) {
-            const int a = p.offsets[g], b = p.offsets[g + 1];
-            bad |= a < 0 || b < a || b > p.n;
-        }
-        total = __syncthreads_or(bad) ? -1 : p.G * (p.mt0 * p.nt0 + p.mt1 * p.nt1);
+        total = load_groups(p, s_off) ? p.G * (p.mt0 * p.nt0 + p.mt1 * p.nt1) : -1;
     } else {
         total = list_tiles<128 * CG>(p, s_off, s_prefix, s_bad);
     }
@@ -379,6 +479,8 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
     const uint32_t tmem = *s_tmem;
     const uint32_t lead_full = mapa_shared(smem_u32(full), 0);
     const uint32_t lead_tempty = mapa_shared(smem_u32(tempty), 0);
+    // a pair's tile of at most 128 rows
+    auto is_half = [&](const Tile &t) { return CG == 2 && MODE != DW && t.row_end - t.row0 <= 128; };
     auto kblocks = [&](const Tile &t) {
         return MODE == DW ? (t.row_end - t.row0 + BK - 1) / BK : (p.K + BK - 1) / BK;
     };
@@ -406,8 +508,11 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
             int g = 0;
             for (int tile = first_tile; tile < total && !*s_abort; tile += step) {
                 const Tile t = decode_tile<MODE, 128 * CG>(p, tile, g, s_off, s_prefix);
-                const CUtensorMap *m = is_a ? &p.tmA : &p.tmB;
+                const bool half = is_half(t);
+                const CUtensorMap *m = is_a ? (half ? &p.tmAh : &p.tmA)
+                                            : (half && MODE == FWD ? &p.tmBh : &p.tmB);
                 const int nkb = kblocks(t);
+                const uint32_t tx = CG * (is_a ? C::A_STAGE / (half ? 2 : 1) : C::B_STAGE);
                 if (MODE == DW && nkb > 0) {
                     m = p.maps + t.g * NMAPS + 2 * t.prod + (is_a ? 0 : 1);
                     acquire_map(m);
@@ -421,7 +526,7 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                     armed[stage] = static_cast<int>(phase);
                     uint8_t *dst = smem + stage * C::STAGE + (is_a ? 0 : C::A_STAGE);
                     if (leader)
-                        mbar_arrive_expect_tx(&full[stage], CG * (is_a ? C::A_STAGE : C::B_STAGE));
+                        mbar_arrive_expect_tx(&full[stage], tx);
                     const int k0 = kb * BK;
                     if (MODE == DW) {
                         const int c = (is_a ? t.m0 : t.n0) + 128 * rank;
@@ -431,7 +536,15 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                     } else if (is_a) {
 #pragma unroll
                         for (int s = 0; s < KSUB; ++s)
-                            load2(dst + s * SLICE, m, stage, k0 + 64 * s, t.row0 + 128 * rank);
+                            load2(dst + s * SLICE, m, stage, k0 + 64 * s, t.row0 + (half ? 64 : 128) * rank);
+                    } else if (MODE == FWD && half) {
+                        // 64 gate rows and the same of up in each CTA
+#pragma unroll
+                        for (int s = 0; s < KSUB; ++s)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+                                load3(dst + s * C::B_SLICE + j * (SLICE / 2), m, stage, k0 + 64 * s,
+                                      j * p.N + t.n_blk * 128 + 64 * rank, t.g);
                     } else if (MODE == FWD) {
                         // gate rows, then the same of up: one half per CTA of a pair
 #pragma unroll
@@ -476,6 +589,7 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                 if (!wait_phase(&tempty[u & 1], ((u >> 1) & 1) ^ 1, s_abort, p.dev_status)) break;
                 tc_fence_after();
                 const uint32_t d = tmem + (u & 1) * BN;
+                const uint32_t idesc = is_half(t) ? C::IDESC - (8u << 24) : C::IDESC;    // M = 128
                 bool ok = true;
                 for (int kb = 0; kb < nkb; ++kb) {
                     if (!wait_phase(&full[stage], phase, s_abort, p.dev_status)) {
@@ -494,7 +608,7 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                         const uint32_t ka = C::A_MN ? s * 128 : s / 4 * (SLICE / 16) + s % 4 * 2;
                         const uint32_t kbb =
                             C::B_MN ? s * 128 : s / 4 * (C::B_SLICE / 16) + s % 4 * 2;
-                        mma<CG>(d, a + ka, b + kbb, C::IDESC, (kb | s) != 0 ? 1u : 0u);
+                        mma<CG>(d, a + ka, b + kbb, idesc, (kb | s) != 0 ? 1u : 0u);
                     }
                     issued = true;
                     if (CG == 1)
@@ -532,72 +646,59 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
         uint32_t u = 0;
         for (int tile = first_tile; tile < total; tile += step) {
             const Tile t = decode_tile<MODE, 128 * CG>(p, tile, g, s_off, s_prefix);
-            const int row0 = (MODE == DW ? t.m0 : t.row0) + 128 * rank + quarter * 32;
+            // half tiles: 64 rows a CTA, N's lower 128 columns in lanes 0-63 and its upper
+            // ones, of the same rows, in lanes 64-127
+            const bool half = is_half(t);
+            const int hq = half ? quarter >> 1 : 0;
+            const int row0 = (MODE == DW ? t.m0 : t.row0) + (half ? 64 : 128) * rank +
+                             32 * (half ? quarter & 1 : quarter);
+            const int span = half ? 64 : 128;       // columns of this warp (FWD: of gate and up)
             const bool ok = row0 + lane < t.row_end;
             const bool boxed = row0 + 32 <= t.row_end;
             const uint32_t acc = tmem + lanes + (u & 1) * BN;
             // DACT: this lane's row of h, 32 columns of gate and up at a time, fetched one
             // step ahead (the first while the tile is still computed)
-            uint4 hq[8];
+            uint4 h8[8];
             auto fetch_h = [&](int c) {
-                const int col = t.n_blk * BN + c;
+                const int col = t.n_blk * BN + 128 * hq + c;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) hq[j] = make_uint4(0u, 0u, 0u, 0u);
+                for (int j = 0; j < 8; ++j) h8[j] = make_uint4(0u, 0u, 0u, 0u);
                 if (ok && col < p.N) {
                     const uint16_t *src = p.h + static_cast<int64_t>(row0 + lane) * (2 * p.N) + col;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        hq[j] = __ldg(reinterpret_cast<const uint4 *>(src) + j);
-                        hq[4 + j] = __ldg(reinterpret_cast<const uint4 *>(src + p.N) + j);
+                        h8[j] = __ldg(reinterpret_cast<const uint4 *>(src) + j);
+                        h8[4 + j] = __ldg(reinterpret_cast<const uint4 *>(src + p.N) + j);
                     }
                 }
             };
-            if (MODE == DACT) fetch_h(128 * part);
+            if (MODE == DACT) fetch_h(span * part);
             if (!wait_phase(&tfull[u & 1], (u >> 1) & 1, s_abort, p.dev_status)) break;
             tc_fence_after();
             if (MODE == FWD) {
-                // columns [0, 128) gate, [128, 256) up; this warp 64 of each
+                // columns [0, span) gate, [span, 2 span) up; this warp takes half of each
 #pragma unroll 1
-                for (int c = 64 * part; c < 64 * part + 64; c += 32) {
+                for (int c = span / 2 * part; c < span / 2 * (part + 1); c += 32) {
                     float x[32], y[32];
                     __syncwarp();
                     tmem_read32(acc + c, x);
-                    tmem_read32(acc + 128 + c, y);
-                    const int col = t.n_blk * 128 + c;
-                    uint32_t w[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) w[i] = bf16x2(x[2 * i], x[2 * i + 1]);
-                    boxes.emit(boxed, ok, w, &p.tmO0, p.out0, p.ld0, row0, col);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) w[i] = bf16x2(y[2 * i], y[2 * i + 1]);
-                    boxes.emit(boxed, ok, w, &p.tmO0, p.out0, p.ld0, row0,
-                              p.N + col);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float a[2];
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const float v = x[2 * i + j];
-                            a[j] = __fdividef(v, 1.0f + __expf(-v)) * y[2 * i + j];
-                        }
-                        w[i] = bf16x2(a[0], a[1]);
-                    }
-                    boxes.emit(boxed, ok, w, &p.tmO1, p.out1, p.ld1, row0, col);
+                    tmem_read32(acc + span + c, y);
+                    emit_forward(p, boxes, boxed, ok, x, y, row0, t.n_blk * 128 + 64 * hq + c);
                 }
             } else if (MODE == DACT) {
 #pragma unroll 1
-                for (int c = 128 * part; c < 128 * part + 128; c += 32) {
-                    const int col = t.n_blk * BN + c;
+                for (int c = span * part; c < span * (part + 1); c += 32) {
+                    const int col = t.n_blk * BN + 128 * hq + c;
                     if (col >= p.N) break;               // N = 128 mod 256: no such columns
                     uint32_t hg[16], hu[16];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        hg[4 * j] = hq[j].x, hg[4 * j + 1] = hq[j].y;
-                        hg[4 * j + 2] = hq[j].z, hg[4 * j + 3] = hq[j].w;
-                        hu[4 * j] = hq[4 + j].x, hu[4 * j + 1] = hq[4 + j].y;
-                        hu[4 * j + 2] = hq[4 + j].z, hu[4 * j + 3] = hq[4 + j].w;
+                        hg[4 * j] = h8[j].x, hg[4 * j + 1] = h8[j].y;
+                        hg[4 * j + 2] = h8[j].z, hg[4 * j + 3] = h8[j].w;
+                        hu[4 * j] = h8[4 + j].x, hu[4 * j + 1] = h8[4 + j].y;
+                        hu[4 * j + 2] = h8[4 + j].z, hu[4 * j + 3] = h8[4 + j].w;
                     }
-                    if (c + 32 < 128 * part + 128) fetch_h(c + 32);
+                    if (c + 32 < span * (part + 1)) fetch_h(c + 32);
                     float d[32];
                     __syncwarp();
                     tmem_read32(acc + c, d);
@@ -624,8 +725,8 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                 }
             } else if (MODE == DX) {
 #pragma unroll 1
-                for (int c = 128 * part; c < 128 * part + 128; c += 32) {
-                    const int col = t.n_blk * BN + c;
+                for (int c = span * part; c < span * (part + 1); c += 32) {
+                    const int col = t.n_blk * BN + 128 * hq + c;
                     if (col >= p.N) break;
                     float v[32];
                     __syncwarp();
@@ -636,48 +737,9 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                     boxes.emit(boxed, ok, w, &p.tmO0, p.out0, p.ld0, row0, col);
                 }
             } else {
-                const CUtensorMap *om = t.prod ? &p.tmO1 : &p.tmO0;
-                const bool none = t.row_end == t.row0;      // an idle expert: zeros
-                // sizes of 128 mod 256: a tile's second half may be off the gradient
-                const int M = t.prod ? p.H : 2 * p.I, N = t.prod ? p.I : p.H;
 #pragma unroll 1
-                for (int c = 128 * part; c < 128 * part + 128; c += 32) {
-                    if (row0 >= M || t.n0 + c >= N) break;
-                    float v[32];
-                    if (none) {
-                        if (p.accumulate) break;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-                    } else {
-                        __syncwarp();
-                        tmem_read32(acc + c, v);
-                    }
-                    const int col = t.n0 + c;
-                    uint32_t w[16];
-                    if (p.w_f32) {
-#pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[16 * hf + i]);
-                            const uint8_t *box = boxes.fill(w);
-                            if (lane == 0) {
-                                if (p.accumulate)
-                                    tma_add_3d(om, box, col + 16 * hf, row0, t.g);
-                                else
-                                    tma_store_3d(om, box, col + 16 * hf, row0, t.g);
-                                bulk_commit();
-                            }
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) w[i] = bf16x2(v[2 * i], v[2 * i + 1]);
-                        const uint8_t *box = boxes.fill(w);
-                        if (lane == 0) {
-                            tma_store_3d(om, box, col, row0, t.g);
-                            bulk_commit();
-                        }
-                    }
-                }
+                for (int c = 128 * part; c < 128 * part + 128; c += 64)
+                    if (!emit_gradient(p, boxes, t, acc + c, row0, t.n0 + c)) break;
             }
             tc_fence_before();
             __syncwarp();
@@ -697,6 +759,250 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
             tmem_dealloc(tmem, 512);
         else
             tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------ wide tiles
+// DW in tiles of 256 rows x 512 columns per CTA pair: half as many hand-overs
+// between the roles, and 48 KB of operands for the MMAs that take 64 KB in 256 x 256
+// tiles.  The accumulator fills tensor memory, so tiles overlap by halves of 256
+// columns: the epilogue drains half 0 and then half 1; the next tile's MMAs start on
+// half 0 as soon as that is free and run ahead on it over the staged slices until
+// half 1 is free, too; and a tile's last W_TAIL slices issue their half-1 MMAs after
+// all of half 0, which is then drained while they run.  CTA r stages columns
+// [256 r, 256 r + 256); column j of half h is column 128 h + j (j < 128) or
+// 256 + 128 h + (j - 128).
+constexpr int BW = 512;
+constexpr int W_STAGES = 4;
+constexpr int W_TAIL = 3;
+constexpr int W_B = 2 * SLICE;                       // 256 columns (or rows) x 64 K
+constexpr int W_STAGE = SLICE + W_B;
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    gradient_wide_kernel(const __grid_constant__ Params p) {
+    using C = Cfg<DW, 2>;
+    static_assert(W_STAGES * W_STAGE == C::EPI_OFF && W_STAGES <= C::STAGES + 1, "shared memory");
+    constexpr int BK = 64;
+    constexpr uint32_t MN_LO = static_cast<uint32_t>(64 * 128 / 16) << 16;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t *rest = smem + C::EPI_OFF + p.boxes * C::BOX_BYTES;
+    uint64_t *full = reinterpret_cast<uint64_t *>(rest + C::BAR_OFF);    // used in the even CTA
+    uint64_t *empty = full + W_STAGES;
+    uint64_t *tfull = empty + W_STAGES;     // [2]: half h is complete
+    uint64_t *tempty = tfull + 2;           // [2], used in the even CTA
+    uint64_t *drain = tempty + 2;
+    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(rest + C::W_MISC_OFF);
+    volatile int *s_abort = reinterpret_cast<volatile int *>(rest + C::W_MISC_OFF + 4);
+    int *s_off = reinterpret_cast<int *>(rest + C::W_MISC_OFF + 16);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = static_cast<int>(cluster_ctarank());
+    const bool leader = rank == 0;
+    const int first_tile = static_cast<int>(blockIdx.x) / 2, step = static_cast<int>(gridDim.x) / 2;
+
+    if (warp == 1) {
+        tmem_alloc_pair(s_tmem, 512);
+        tmem_relinquish_pair();
+    } else if (warp == 2 && elect_one()) {
+        *s_abort = 0;
+        for (int s = 0; s < W_STAGES; ++s) {
+            mbar_init(&full[s], 2);          // each producer arms its share
+            mbar_init(&empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], 2 * EPI_WARPS);
+        }
+        mbar_init(drain, 1);
+        fence_barrier_init();
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    int total = load_groups(p, s_off) ? p.G * (p.mt0 * p.nt0 + p.mt1 * p.nt1) : -1;
+    if (total < 0) {                         // both CTAs of a pair read the same offsets
+        if (tid == 0 && blockIdx.x == 0) report(p.dev_status, MOE_DEV_BAD_OFFSETS);
+        total = 0;
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();                      // barriers and TMEM of both CTAs are ready
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    const uint32_t lead_full = mapa_shared(smem_u32(full), 0);
+    const uint32_t lead_tempty = mapa_shared(smem_u32(tempty), 0);
+    auto slices = [&](const Tile &t) { return (t.row_end - t.row0 + BK - 1) / BK; };
+
+    if (warp == 0 || warp == 3) {
+        // ================= TMA producers: warp 0 A, warp 3 B
+        if (elect_one()) {
+            const bool is_a = warp == 0;
+            int stage = 0;
+            uint32_t phase = 0;
+            int armed[W_STAGES];
+            for (int s = 0; s < W_STAGES; ++s) armed[s] = -1;
+            int g = 0;
+            for (int tile = first_tile; tile < total && !*s_abort; tile += step) {
+                const Tile t = decode_tile<DW, 256, BW>(p, tile, g, s_off, nullptr);
+                const int nkb = slices(t);
+                const CUtensorMap *m = p.maps + t.g * NMAPS + 2 * t.prod + (is_a ? 0 : 1);
+                if (nkb > 0) acquire_map(m);
+                bool ok = true;
+                for (int kb = 0; kb < nkb; ++kb) {
+                    if (!wait_phase(&empty[stage], phase ^ 1, s_abort, p.dev_status)) {
+                        ok = false;
+                        break;
+                    }
+                    armed[stage] = static_cast<int>(phase);
+                    uint8_t *dst = smem + stage * W_STAGE + (is_a ? 0 : SLICE);
+                    const uint32_t fb = lead_full + 8u * static_cast<uint32_t>(stage);
+                    if (leader) mbar_arrive_expect_tx(&full[stage], 2 * (is_a ? SLICE : W_B));
+                    const int c = is_a ? t.m0 + 128 * rank : t.n0 + 256 * rank;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (!is_a || j < 2)
+                            tma_load_2d_pair(dst + j * (SLICE / 2), m, fb, c + 64 * j, t.row0 + kb * BK);
+                    if (++stage == W_STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (!ok) break;
+            }
+            if (*s_abort && leader) {
+                for (int s = 0; s < W_STAGES; ++s)
+                    if (armed[s] >= 0) mbar_wait_drain(&full[s], static_cast<uint32_t>(armed[s]));
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ================= MMA issuer (even CTA only)
+        if (leader && elect_one()) {
+            int stage = 0, g = 0;
+            uint32_t phase = 0, tph = 0;
+            const uint32_t base = smem_u32(smem) >> 4;
+            bool issued = false;
+            for (int tile = first_tile; tile < total && !*s_abort; tile += step) {
+                const Tile t = decode_tile<DW, 256, BW>(p, tile, g, s_off, nullptr);
+                const int nkb = slices(t);
+                // the 16-row steps of the last slice that hold rows of the group
+                const int last = (t.row_end - t.row0 - (nkb - 1) * BK + 15) / 16;
+                // half h of slice kb, staged in st
+                auto mma_half = [&](int st, int kb, int h) {
+                    const uint32_t at = base + static_cast<uint32_t>(st) * (W_STAGE / 16);
+                    const uint32_t a = at + MN_LO;
+                    const uint32_t b = a + (1 + static_cast<uint32_t>(h)) * (SLICE / 16);
+                    const int steps = kb + 1 < nkb ? 4 : last;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (k >= steps) break;
+                        mma<2>(tmem + 256u * static_cast<uint32_t>(h), a + k * 128, b + k * 128, C::IDESC,
+                               (kb | k) != 0 ? 1u : 0u);
+                    }
+                };
+                if (!wait_phase(&tempty[0], tph ^ 1, s_abort, p.dev_status)) break;
+                tc_fence_after();
+                bool h1 = false, ok = true;              // half 1 is free
+                int pend[W_STAGES], npend = 0, pend_kb = 0;
+                auto flush = [&]() {
+                    for (int i = 0; i < npend; ++i) {
+                        mma_half(pend[i], pend_kb + i, 1);
+                        tc_commit_pair_mc(&empty[pend[i]], 0x3);
+                    }
+                    npend = 0;
+                };
+                auto wait_h1 = [&]() {
+                    if (!h1) {
+                        h1 = wait_phase(&tempty[1], tph ^ 1, s_abort, p.dev_status);
+                        tc_fence_after();
+                    }
+                    return h1;
+                };
+                for (int kb = 0; kb < nkb; ++kb) {
+                    if (!wait_phase(&full[stage], phase, s_abort, p.dev_status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    mma_half(stage, kb, 0);
+                    issued = true;
+                    const bool tail = kb >= nkb - W_TAIL;
+                    if (!tail && !h1 && mbar_test_wait_cluster(&tempty[1], tph ^ 1)) {
+                        tc_fence_after();
+                        h1 = true;
+                    }
+                    if (h1 && !tail) {
+                        flush();
+                        mma_half(stage, kb, 1);
+                        tc_commit_pair_mc(&empty[stage], 0x3);
+                    } else {
+                        if (npend == 0) pend_kb = kb;
+                        pend[npend++] = stage;
+                        if (npend == W_STAGES) {         // every stage waits for half 1
+                            if (!wait_h1()) {
+                                ok = false;
+                                break;
+                            }
+                            flush();
+                        }
+                    }
+                    if (++stage == W_STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (!ok) break;
+                tc_commit_pair_mc(&tfull[0], 0x3);
+                if (!wait_h1()) break;
+                flush();
+                tc_commit_pair_mc(&tfull[1], 0x3);
+                tph ^= 1;
+            }
+            if (*s_abort && issued) {
+                // unwinding: every MMA issued so far ends before TMEM is freed
+                tc_commit_pair_mc(drain, 0x1);
+                mbar_wait_drain(drain, 0);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ================= epilogue: two warps share a TMEM lane quarter
+        const int quarter = warp & 3, part = (warp - 4) >> 2;
+        Boxes boxes{smem + C::EPI_OFF + (warp - 4) * p.boxes * EPI_BYTES, p.boxes, 0, lane};
+        int g = 0;
+        uint32_t tph = 0;
+        for (int tile = first_tile; tile < total; tile += step) {
+            const Tile t = decode_tile<DW, 256, BW>(p, tile, g, s_off, nullptr);
+            const int row0 = t.m0 + 128 * rank + 32 * quarter;
+            const uint32_t tq = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+            bool stop = false;
+            for (int h = 0; h < 2; ++h) {
+                if (!wait_phase(&tfull[h], tph, s_abort, p.dev_status)) {
+                    stop = true;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t acc = tq + 256u * static_cast<uint32_t>(h) + 128u * static_cast<uint32_t>(part);
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 64)
+                    if (!emit_gradient(p, boxes, t, acc + c, row0, t.n0 + 128 * h + 256 * part + c)) break;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_drained(lead_tempty + 8u * static_cast<uint32_t>(h));
+            }
+            if (stop) break;
+            tph ^= 1;
+        }
+        if (lane == 0) bulk_wait<0>();       // every output box written
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();                  // no CTA leaves while its peer may still signal or read it
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
     }
 }
 
@@ -745,30 +1051,43 @@ bool operand_map(CUtensorMap *m, const void *ptr, int groups, int64_t rows, int6
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Output [groups][rows][cols] as 32-row x 64-byte boxes, 64-byte swizzle.
-bool out_map(CUtensorMap *m, void *ptr, int groups, int64_t rows, int64_t cols, bool f32) {
+// Output [groups][rows][cols] as boxes of 32 rows x 64 bytes, or 128 (DW), swizzled
+// over as many.
+bool out_map(CUtensorMap *m, void *ptr, int groups, int64_t rows, int64_t cols, bool f32,
+             bool wide = false) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t esz = f32 ? 4 : 2;
     cuuint64_t dim[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                          static_cast<cuuint64_t>(std::max(groups, 1))};
     cuuint64_t stride[2] = {dim[0] * esz, dim[0] * dim[1] * esz};
-    cuuint32_t box[3] = {static_cast<cuuint32_t>(64 / esz), 32, 1}, es[3] = {1, 1, 1};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>((wide ? 128 : 64) / esz), 32, 1}, es[3] = {1, 1, 1};
     return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
               groups > 0 ? 3 : 2, ptr, dim, stride, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Row products: pairs where groups have more than one 128-row block on average.
 bool use_pair(int n, int G) { return n > 128ll * G; }
 
+// DW in wide tiles: with few rows a group, where the gradients' stores decide and
+// fewer hand-overs help, and with very many.  Measured with H = 2048, I = 1024 and 64
+// groups (whole backward pass, us, 256 against 512 columns): 16 rows a group 288 : 272,
+// 64 305 : 295, 256 435 : 433, 512 691 : 707, 1024 1199 : 1248, 2048 2251 : 2298;
+// one group of 16384 rows, H = 4096, I = 2048: 1028 : 1005.
+bool wide_gradient(int n, int G) { return n < 192ll * G || n >= 8192ll * G; }
+
+// CG = 1, 2: the 256-column kernels; 3: the wide one.
 template <int MODE, int CG>
 cudaError_t launch(Params &p, int64_t tiles, cudaStream_t stream) {
-    using C = Cfg<MODE, CG>;
+    constexpr int PAIR = CG == 1 ? 1 : 2;
+    using C = Cfg<MODE, PAIR>;
     p.boxes = C::boxes(p.G);
     void (*kernel)(const Params);
-    if constexpr (CG == 2)
+    if constexpr (CG == 3)          // DW only
+        kernel = gradient_wide_kernel;
+    else if constexpr (CG == 2)
         kernel = train_gemm_pair_kernel<MODE>;
     else
         kernel = train_gemm_kernel<MODE>;
@@ -776,14 +1095,14 @@ cudaError_t launch(Params &p, int64_t tiles, cudaStream_t stream) {
     static int resident[64] = {};        // CTAs or pairs that can run at once, by device
     int dev = 0;
     cudaGetDevice(&dev);
-    int limit = num_sms() / CG;
+    int limit = num_sms() / PAIR;
     {
         std::lock_guard<std::mutex> lock(mu);
         if (dev >= 64 || resident[dev] == 0) {
             const cudaError_t e = cudaFuncSetAttribute(
                 kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
             if (e != cudaSuccess) return e;
-            if (CG == 2) {
+            if (PAIR == 2) {
                 cudaLaunchConfig_t cfg = {};
                 cfg.gridDim = dim3(static_cast<unsigned>(num_sms()), 1, 1);
                 cfg.blockDim = dim3(THREADS, 1, 1);
@@ -803,7 +1122,7 @@ cudaError_t launch(Params &p, int64_t tiles, cudaStream_t stream) {
     }
     const int64_t units = std::max<int64_t>(1, std::min<int64_t>(limit, tiles));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(CG * units), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(PAIR * units), 1, 1);
     cfg.blockDim = dim3(THREADS, 1, 1);
     cfg.dynamicSmemBytes = static_cast<size_t>(C::smem(p.G, p.boxes));
     cfg.stream = stream;
@@ -815,11 +1134,20 @@ cudaError_t launch(Params &p, int64_t tiles, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+// FWD, DACT, DX: A [n, K], B as the mode's weights.
 template <int MODE>
-cudaError_t launch_rows(Params &p, cudaStream_t stream) {
+cudaError_t launch_rows(Params &p, const void *a, const void *w, cudaStream_t stream) {
     const bool pair = use_pair(p.n, p.G);
-    const int bm = pair ? 256 : 128;
-    const int64_t tiles = (static_cast<int64_t>(p.n / bm) + std::min(p.G, p.n)) * p.nt;
+    const int64_t brows = MODE == FWD ? 2 * static_cast<int64_t>(p.N) : p.K;       // of a group's weights
+    const int bcols = MODE == FWD ? p.K : p.N;
+    // rows of B's box: FWD 128 weight rows, else a stage's K
+    const int box = MODE == FWD || pair ? 128 : 64;
+    if (!operand_map(&p.tmA, a, 0, p.n, p.K, 128) || !operand_map(&p.tmB, w, p.G, brows, bcols, box) ||
+        !operand_map(&p.tmAh, a, 0, p.n, p.K, 64) ||
+        (MODE == FWD && !operand_map(&p.tmBh, w, p.G, brows, bcols, 64)))
+        return cudaErrorInvalidValue;
+    p.nt = static_cast<int>(ceil_div(p.N, MODE == FWD ? 128 : 256));
+    const int64_t tiles = (static_cast<int64_t>(p.n / (pair ? 256 : 128)) + std::min(p.G, p.n)) * p.nt;
     return pair ? launch<MODE, 2>(p, tiles, stream) : launch<MODE, 1>(p, tiles, stream);
 }
 
@@ -879,9 +1207,7 @@ extern "C" moe_status_t moe_grouped_mlp_train(const moe_bf16_t *expanded_x, cons
     if (!encode_fn()) return MOE_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     Params p{};
-    if (!operand_map(&p.tmA, expanded_x, 0, n, H, 128) ||
-        !operand_map(&p.tmB, w13, G, 2 * static_cast<int64_t>(I), H, 128) ||
-        !out_map(&p.tmO0, h, 0, n, 2 * static_cast<int64_t>(I), false) ||
+    if (!out_map(&p.tmO0, h, 0, n, 2 * static_cast<int64_t>(I), false) ||
         !out_map(&p.tmO1, act, 0, n, I, false))
         return MOE_ERR_CUDA;
     p.offsets = offsets;
@@ -889,14 +1215,13 @@ extern "C" moe_status_t moe_grouped_mlp_train(const moe_bf16_t *expanded_x, cons
     p.n = n;
     p.K = H;
     p.N = I;
-    p.nt = I / 128;
     p.wrows = 2 * I;
     p.out0 = h;
     p.ld0 = 2 * I;
     p.out1 = act;
     p.ld1 = I;
     p.dev_status = dev_status;
-    TRY_CUDA(launch_rows<FWD>(p, s));
+    TRY_CUDA(launch_rows<FWD>(p, expanded_x, w13, s));
     const GemmSegment1 none{};
     TRY_CUDA(launch_gemm_store(act, offsets, G, n, I, w2, H, y, none, dev_status, s));
     return MOE_OK;
@@ -946,8 +1271,7 @@ extern "C" moe_status_t moe_grouped_mlp_backward(
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     uint16_t *d_h = reinterpret_cast<uint16_t *>(ws + L.d_h);
     uint16_t *act = reinterpret_cast<uint16_t *>(ws + L.act);
-    const int box_k = use_pair(n, G) ? 128 : 64;     // K rows of an MN-major box: a stage's
-
+    const int box_w = wide_gradient(n, G) ? 64 : 128;         // rows of DW's boxes: a stage's
     Params p{};
     p.offsets = offsets;
     p.G = G;
@@ -955,49 +1279,46 @@ extern "C" moe_status_t moe_grouped_mlp_backward(
     p.dev_status = dev_status;
     p.maps = reinterpret_cast<CUtensorMap *>(ws + L.maps);
     // d_act and what follows from it
-    if (!operand_map(&p.tmA, d_y, 0, n, H, 128) || !operand_map(&p.tmB, w2, G, H, I, box_k) ||
-        !out_map(&p.tmO0, d_h, 0, n, I2, false) || !out_map(&p.tmO1, act, 0, n, I, false) ||
-        !operand_map(&p.tmG[0], d_h, 0, n, I2, 128) ||
-        !operand_map(&p.tmG[1], expanded_x, 0, n, H, 128) ||
-        !operand_map(&p.tmG[2], d_y, 0, n, H, 128) || !operand_map(&p.tmG[3], act, 0, n, I, 128))
+    if (!out_map(&p.tmO0, d_h, 0, n, I2, false) || !out_map(&p.tmO1, act, 0, n, I, false) ||
+        !operand_map(&p.tmG[0], d_h, 0, n, I2, box_w) ||
+        !operand_map(&p.tmG[1], expanded_x, 0, n, H, box_w) ||
+        !operand_map(&p.tmG[2], d_y, 0, n, H, box_w) || !operand_map(&p.tmG[3], act, 0, n, I, box_w))
         return MOE_ERR_CUDA;
     p.K = H;
     p.N = I;
-    p.nt = static_cast<int>(ceil_div(I, BN));
     p.wrows = I;
     p.h = h;
     p.out0 = d_h;
     p.ld0 = 2 * I;
     p.out1 = act;
     p.ld1 = I;
-    TRY_CUDA(launch_rows<DACT>(p, s));
+    TRY_CUDA(launch_rows<DACT>(p, d_y, w2, s));
     if (d_x) {
-        if (!operand_map(&p.tmA, d_h, 0, n, I2, 128) || !operand_map(&p.tmB, w13, G, I2, H, box_k) ||
-            !out_map(&p.tmO0, d_x, 0, n, H, false))
-            return MOE_ERR_CUDA;
+        if (!out_map(&p.tmO0, d_x, 0, n, H, false)) return MOE_ERR_CUDA;
         p.K = 2 * I;
         p.N = H;
-        p.nt = static_cast<int>(ceil_div(H, BN));
         p.wrows = H;
         p.out0 = d_x;
         p.ld0 = H;
-        TRY_CUDA(launch_rows<DX>(p, s));
+        TRY_CUDA(launch_rows<DX>(p, d_h, w13, s));
     }
     if (d_w13 || d_w2) {
-        if ((d_w13 && !out_map(&p.tmO0, d_w13, G, I2, H, f32)) ||
-            (d_w2 && !out_map(&p.tmO1, d_w2, G, H, I, f32)))
+        const bool wide_rows = Cfg<DW, 2>::boxes(G) == 2;
+        if ((d_w13 && !out_map(&p.tmO0, d_w13, G, I2, H, f32, wide_rows)) ||
+            (d_w2 && !out_map(&p.tmO1, d_w2, G, H, I, f32, wide_rows)))
             return MOE_ERR_CUDA;
         p.mt0 = d_w13 ? static_cast<int>(ceil_div(I2, 256)) : 0;
-        p.nt0 = d_w13 ? static_cast<int>(ceil_div(H, BN)) : 0;
+        const int bn = wide_gradient(n, G) ? BW : BN;
+        p.nt0 = d_w13 ? static_cast<int>(ceil_div(H, bn)) : 0;
         p.mt1 = d_w2 ? static_cast<int>(ceil_div(H, 256)) : 0;
-        p.nt1 = d_w2 ? static_cast<int>(ceil_div(I, BN)) : 0;
+        p.nt1 = d_w2 ? static_cast<int>(ceil_div(I, bn)) : 0;
         p.H = H;
         p.I = I;
         p.w_f32 = f32;
         p.accumulate = add;
         const int64_t tiles =
             static_cast<int64_t>(G) * (p.mt0 * p.nt0 + static_cast<int64_t>(p.mt1) * p.nt1);
-        TRY_CUDA((launch<DW, 2>(p, tiles, s)));
+        TRY_CUDA((bn == BW ? launch<DW, 3>(p, tiles, s) : launch<DW, 2>(p, tiles, s)));
     }
     return MOE_OK;
 }
