@@ -4,9 +4,10 @@
 // y = act W2[g]^T.  With s = sigmoid(gate) the gradients are
 //   d_act = d_y W2[g],  d_up = d_act gate s,  d_gate = d_act up s (1 + gate (1 - s)),
 //   d_x = [d_gate d_up] W13[g],  d_W13[g] = [d_gate d_up]^T x,  d_W2[g] = d_y^T act.
-// Four products, one kernel body each:
+// Five products on one kernel body:
 //   FWD   x W13^T, epilogue: h = [gate up] and act, rounded to bf16 once each
 //         (act from the fp32 sums, as the forward pass without gradients has it)
+//   DOWN  act W2^T = y
 //   DACT  d_y W2, epilogue: reads h, writes d_h = [d_gate d_up] and act again
 //         (from h: keeping act for the backward pass would cost half of h's
 //         memory more, making it again costs n I stores beside a product)
@@ -16,8 +17,8 @@
 // accumulated in fp32 by the MMAs.
 //
 // Operand layouts.  Nothing is transposed in memory: the tensor cores take an
-// operand whose rows run along K (K-major, as x, d_y, d_h in the first three
-// and W13 in FWD) or across it (MN-major: the weights in DACT and DX, both
+// operand whose rows run along K (K-major, as x, act, d_y, d_h and, in the forward
+// pass, the weights) or across it (MN-major: the weights in DACT and DX, both
 // operands of DW).  A K-major slice is 128-byte rows of 64 K values, an MN-major
 // one 128-byte rows of 64 M or N values, one row per K; both in the 128-byte
 // swizzle TMA writes.
@@ -51,18 +52,18 @@ constexpr int EPI_BYTES = 32 * 64;          // an output box: 32 rows of 64 byte
 constexpr int SLICE = 128 * 128;            // bytes of 128 rows (K-major) x 64 K
 constexpr int NMAPS = 4;                    // DW's tensor maps of a group
 
-enum { FWD = 0, DACT = 1, DX = 2, DW = 3 };
+enum { FWD = 0, DACT = 1, DX = 2, DW = 3, DOWN = 4 };
 
 struct Params {
     CUtensorMap tmA, tmB;      // operands (DW: none, it takes the groups' maps)
-    CUtensorMap tmO0, tmO1;    // FWD: h, act; DACT: d_h, act; DX: d_x; DW: d_W13, d_W2
+    CUtensorMap tmO0, tmO1;    // FWD: h, act; DACT: d_h, act; DX: d_x; DOWN: y; DW: d_W13, d_W2
     CUtensorMap tmAh, tmBh;    // a pair's tiles of at most 128 rows: 64-row boxes of A (FWD: and B)
     CUtensorMap tmG[NMAPS];    // DACT: d_h, x, d_y, act, to be cut at each group's end
     CUtensorMap *maps;         // [G][NMAPS] in the workspace
     const int32_t *offsets;
     int32_t G, n;
     int32_t K;                 // contraction (not DW)
-    int32_t N;                 // FWD, DACT: I; DX: H
+    int32_t N;                 // FWD, DACT: I; DX, DOWN: H
     int32_t nt;                // column tiles of a row block
     int32_t wrows;             // rows a group's weights would have as an operand like A
     int32_t boxes;             // output boxes per epilogue warp
@@ -100,7 +101,7 @@ struct Cfg {
     // two boxes where they fit beside the groups' tables: a warp fills one while the
     // last one's store still reads the other
     static constexpr int boxes(int G) { return smem(G, 2) <= 227 * 1024 ? 2 : 1; }
-    static constexpr bool A_MN = MODE == DW, B_MN = MODE != FWD;
+    static constexpr bool A_MN = MODE == DW, B_MN = MODE != FWD && MODE != DOWN;
     // shared-memory descriptors: the high word is the same for both layouts (1 KB
     // between groups of eight 128-byte rows, 128-byte swizzle); the low word's
     // leading offset, between 64-element blocks of M or N, is used by MN-major ones
@@ -553,6 +554,13 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                             for (int j = 0; j < 2 / CG; ++j)
                                 load3(dst + s * C::B_SLICE + j * SLICE, m, stage, k0 + 64 * s,
                                       (j + rank) * p.N + t.n_blk * 128, t.g);
+                    } else if (MODE == DOWN) {
+#pragma unroll
+                        for (int s = 0; s < KSUB; ++s)
+#pragma unroll
+                            for (int j = 0; j < 2 / CG; ++j)
+                                load3(dst + s * C::B_SLICE + j * SLICE, m, stage, k0 + 64 * s,
+                                      t.n_blk * BN + 128 * (j + rank), t.g);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 4 / CG; ++j)
@@ -723,7 +731,7 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                               p.N + col);
                     boxes.emit(boxed, ok, wa, &p.tmO1, p.out1, p.ld1, row0, col);
                 }
-            } else if (MODE == DX) {
+            } else if (MODE == DX || MODE == DOWN) {
 #pragma unroll 1
                 for (int c = span * part; c < span * (part + 1); c += 32) {
                     const int col = t.n_blk * BN + 128 * hq + c;
@@ -1134,14 +1142,15 @@ cudaError_t launch(Params &p, int64_t tiles, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-// FWD, DACT, DX: A [n, K], B as the mode's weights.
+// All but DW: A [n, K], B as the mode's weights.
 template <int MODE>
 cudaError_t launch_rows(Params &p, const void *a, const void *w, cudaStream_t stream) {
     const bool pair = use_pair(p.n, p.G);
-    const int64_t brows = MODE == FWD ? 2 * static_cast<int64_t>(p.N) : p.K;       // of a group's weights
-    const int bcols = MODE == FWD ? p.K : p.N;
-    // rows of B's box: FWD 128 weight rows, else a stage's K
-    const int box = MODE == FWD || pair ? 128 : 64;
+    constexpr bool K_MAJOR = MODE == FWD || MODE == DOWN;                           // the weights
+    const int64_t brows = MODE == FWD ? 2 * static_cast<int64_t>(p.N) : K_MAJOR ? p.N : p.K;
+    const int bcols = K_MAJOR ? p.K : p.N;
+    // rows of B's box: 128 weight rows, or a stage's K
+    const int box = K_MAJOR || pair ? 128 : 64;
     if (!operand_map(&p.tmA, a, 0, p.n, p.K, 128) || !operand_map(&p.tmB, w, p.G, brows, bcols, box) ||
         !operand_map(&p.tmAh, a, 0, p.n, p.K, 64) ||
         (MODE == FWD && !operand_map(&p.tmBh, w, p.G, brows, bcols, 64)))
@@ -1222,8 +1231,13 @@ extern "C" moe_status_t moe_grouped_mlp_train(const moe_bf16_t *expanded_x, cons
     p.ld1 = I;
     p.dev_status = dev_status;
     TRY_CUDA(launch_rows<FWD>(p, expanded_x, w13, s));
-    const GemmSegment1 none{};
-    TRY_CUDA(launch_gemm_store(act, offsets, G, n, I, w2, H, y, none, dev_status, s));
+    if (!out_map(&p.tmO0, y, 0, n, H, false)) return MOE_ERR_CUDA;
+    p.K = I;
+    p.N = H;
+    p.wrows = H;
+    p.out0 = y;
+    p.ld0 = H;
+    TRY_CUDA(launch_rows<DOWN>(p, act, w2, s));
     return MOE_OK;
 }
 

@@ -131,6 +131,8 @@ def test_forward_and_backward(counts, H, I):
     st = moe.new_status(DEV)
     h, y = moe.grouped_mlp_train(x, off, w13, w2, status=st)
     check_forward(x, off, w13, w2, h, y)
+    _, plain = moe.grouped_mlp(x, off, w13, w2)
+    assert torch.equal(y, plain)
     got = moe.grouped_mlp_backward(d_y, x, off, h, w13, w2, status=st)
     check_backward(x, off, w13, w2, h, d_y, got)
     f32 = moe.grouped_mlp_backward(d_y, x, off, h, w13, w2, w_f32=True, status=st)
