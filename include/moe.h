@@ -501,7 +501,7 @@ moe_status_t moe_finalize_routing_backward(const void *d_out, const void *y_exp,
  * nothing is written.  Results do not depend on the launch (no atomics in
  * unordered sums).  H and I multiples of 128, G <= 1024; no output may overlap an
  * input or the workspace.  Workspace:
- * moe_grouped_mlp_backward_workspace_size() bytes, 256-byte aligned (none for
+ * moe_grouped_mlp_backward_workspace_size(n, I) bytes, 256-byte aligned (none for
  * n = 0); its contents are scratch.  Calls that may overlap in time (also as
  * replayed graphs) need one each.
  */
@@ -509,8 +509,7 @@ moe_status_t moe_grouped_mlp_train(const moe_bf16_t *expanded_x, const int32_t *
                                    const moe_bf16_t *w13, const moe_bf16_t *w2, int32_t n, int32_t H,
                                    int32_t I, moe_bf16_t *h, moe_bf16_t *act, moe_bf16_t *y,
                                    int32_t *dev_status, moe_stream_t stream);
-moe_status_t moe_grouped_mlp_backward_workspace_size(int32_t n, int32_t I, int32_t G,
-                                                     size_t *bytes);
+moe_status_t moe_grouped_mlp_backward_workspace_size(int32_t n, int32_t I, size_t *bytes);
 moe_status_t moe_grouped_mlp_backward(const moe_bf16_t *d_y, const moe_bf16_t *expanded_x,
                                       const int32_t *offsets, int32_t G, const moe_bf16_t *h,
                                       const moe_bf16_t *w13, const moe_bf16_t *w2, int32_t n,

@@ -134,7 +134,7 @@ def lib() -> ctypes.CDLL:
                 "moe_fp4_grouped_swiglu": [P, P, I32, P, I32, I32, I32, P, P, P, P],
                 "moe_fp4_grouped_mlp": [P, P, I32, P, P, I32, I32, I32, U32, P, P, P, P],
                 "moe_grouped_mlp_train": [P, P, I32, P, P, I32, I32, I32, P, P, P, P, P],
-                "moe_grouped_mlp_backward_workspace_size": [I32, I32, I32, PSZ],
+                "moe_grouped_mlp_backward_workspace_size": [I32, I32, PSZ],
                 "moe_grouped_mlp_backward": [P, P, P, I32, P, P, P, I32, I32, I32, U32, P, P, P, P,
                                              SZ, P, P],
                 "moe_fp4_weight_workspace_size": [I32, I32, I32, I32, PSZ],
@@ -556,9 +556,9 @@ def grouped_mlp_train(expanded_x, offsets, w13, w2, status=None):
 
 
 @functools.lru_cache(maxsize=256)
-def grouped_mlp_backward_workspace_size(n, I, G) -> int:
+def grouped_mlp_backward_workspace_size(n, I) -> int:
     b = ctypes.c_size_t(0)
-    _call("moe_grouped_mlp_backward_workspace_size", n, I, G, ctypes.byref(b))
+    _call("moe_grouped_mlp_backward_workspace_size", n, I, ctypes.byref(b))
     return b.value
 
 
@@ -570,7 +570,7 @@ def grouped_mlp_backward(d_y, expanded_x, offsets, h, w13, w2, need=("x", "w13",
     None for those not in ``need``.  ``d_w13`` and ``d_w2``: buffers to write,
     or with ``accumulate`` (fp32 only) to add to.  Rows of d_x past the last
     group are not set.  ``workspace``: uint8, at least
-    grouped_mlp_backward_workspace_size(n, I, G)."""
+    grouped_mlp_backward_workspace_size(n, I)."""
     n, H, I, G, dev, (xp, off, wp, w2p) = _mlp_shapes(expanded_x, offsets, w13, w2)
     dyp = _arg(d_y, torch.bfloat16, dev, (n, H), "d_y")
     hp = _arg(h, torch.bfloat16, dev, (n, 2 * I), "h")
@@ -598,7 +598,7 @@ def grouped_mlp_backward(d_y, expanded_x, offsets, h, w13, w2, need=("x", "w13",
         elif d_w2 is None:
             d_w2 = torch.empty((G, H, I), dtype=dt, device=dev)
             p2 = d_w2.data_ptr()
-        nbytes = grouped_mlp_backward_workspace_size(n, I, G)
+        nbytes = grouped_mlp_backward_workspace_size(n, I)
         if workspace is None:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
             wsp = workspace.data_ptr()

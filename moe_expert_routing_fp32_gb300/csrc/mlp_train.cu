@@ -24,12 +24,13 @@
 // swizzle TMA writes.
 //
 // Ragged groups.  A row tile may read rows of the next group; only the group's
-// own are stored.  In DW the rows are the contraction: what a group's last slice
-// reads past its end has to be zero, so each group has tensor maps of its own
-// whose row count is the group's end, made by DACT's spare warp (tensormap.replace
-// in shared memory), and TMA fills in the zeros.
+// own are stored.  In DW the rows are the contraction, 16 to an MMA: those of the
+// group's last step that belong to the next group (and may hold anything) are
+// zeroed in shared memory, of both operands, before the MMA.  Such a slice is
+// announced on a barrier of each CTA; the CTA's spare warp zeroes the rows and
+// arrives in the producers' place on the barrier that the MMA waits for.
 //
-// Roles (12 warps): 0 TMA of A, 3 TMA of B, 1 MMA, 2 setup (DACT: the maps),
+// Roles (12 warps): 0 TMA of A, 3 TMA of B, 1 MMA, 2 setup (DW: the zeroes),
 // 4-11 epilogue.  Tiles are CG * 128 rows x 256 columns on one CTA or a pair
 // (tcgen05 cta_group::2, half of B in each CTA), two accumulators in turn.
 #include <cuda.h>
@@ -50,16 +51,14 @@ constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 128 + 32 * EPI_WARPS;
 constexpr int EPI_BYTES = 32 * 64;          // an output box: 32 rows of 64 bytes
 constexpr int SLICE = 128 * 128;            // bytes of 128 rows (K-major) x 64 K
-constexpr int NMAPS = 4;                    // DW's tensor maps of a group
 
 enum { FWD = 0, DACT = 1, DX = 2, DW = 3, DOWN = 4 };
 
 struct Params {
-    CUtensorMap tmA, tmB;      // operands (DW: none, it takes the groups' maps)
+    CUtensorMap tmA, tmB;      // operands (not DW)
     CUtensorMap tmO0, tmO1;    // FWD: h, act; DACT: d_h, act; DX: d_x; DOWN: y; DW: d_W13, d_W2
     CUtensorMap tmAh, tmBh;    // a pair's tiles of at most 128 rows: 64-row boxes of A (FWD: and B)
-    CUtensorMap tmG[NMAPS];    // DACT: d_h, x, d_y, act, to be cut at each group's end
-    CUtensorMap *maps;         // [G][NMAPS] in the workspace
+    CUtensorMap tmG[4];        // DW's operands: d_h and x, d_y and act
     const int32_t *offsets;
     int32_t G, n;
     int32_t K;                 // contraction (not DW)
@@ -91,9 +90,8 @@ struct Cfg {
     // follows them, counted from there
     static constexpr int EPI_OFF = STAGES * STAGE;
     static constexpr int BOX_BYTES = EPI_WARPS * EPI_BYTES;
-    static constexpr int MAP_OFF = 0;
-    static constexpr int BAR_OFF = MAP_OFF + (MODE == DACT ? NMAPS * 128 : 0);
-    static constexpr int NBARS = 2 * STAGES + 5;        // full, empty, tfull, tempty, drain
+    static constexpr int BAR_OFF = 0;
+    static constexpr int NBARS = 3 * STAGES + 5;        // full, empty, tail, tfull, tempty, drain
     static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
     static constexpr int OFFS_OFF = MISC_OFF + 16;
     static constexpr int smem(int G, int boxes) {
@@ -134,29 +132,6 @@ __device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t
                      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
                      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(HI)
                      : "memory");
-}
-
-// A tensor map of the whole rows, copied by one warp with its row count set to
-// `rows`: dst (global, 128-byte aligned) by way of `stage` (shared).
-__device__ __forceinline__ void cut_map(CUtensorMap *dst, uint8_t *stage, const CUtensorMap *src,
-                                        int rows, int lane) {
-    const uint32_t s = smem_u32(stage);
-    reinterpret_cast<uint32_t *>(stage)[lane] = reinterpret_cast<const uint32_t *>(src)[lane];
-    __syncwarp();
-    if (lane == 0)
-        asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(s),
-                     "r"(rows)
-                     : "memory");
-    __syncwarp();
-    asm volatile("tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync"
-                 ".aligned [%0], [%1], 128;" ::"l"(reinterpret_cast<uint64_t>(dst)),
-                 "r"(s)
-                 : "memory");
-}
-__device__ __forceinline__ void acquire_map(const CUtensorMap *m) {
-    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(
-                     reinterpret_cast<uint64_t>(m))
-                 : "memory");
 }
 
 __device__ __forceinline__ void tma_store_3d(const void *tmap, const void *src, int c0, int c1,
@@ -402,6 +377,39 @@ __device__ __forceinline__ bool load_groups(const Params &p, int *s_off) {
     return !__syncthreads_or(bad);
 }
 
+// DW: whether the group's last 16-row step has rows of the next group in it.
+__device__ __forceinline__ bool has_tail(const Tile &t) { return ((t.row_end - t.row0) & 15) != 0; }
+// The parities of the stages' tail barriers, which complete a phase per use.
+struct Tails {
+    uint32_t used = 0, parity = 0;      // by stage
+    __device__ __forceinline__ void arm(int s) {
+        used |= 1u << s;
+        parity ^= 1u << s;
+    }
+    __device__ __forceinline__ uint32_t take(int s) {
+        const uint32_t p = (parity >> s) & 1u;
+        parity ^= 1u << s;
+        return p;
+    }
+    // the last loads announced on each barrier land before the CTA leaves
+    __device__ __forceinline__ void drain(uint64_t *tail, int stages) const {
+        for (int s = 0; s < stages; ++s)
+            if ((used >> s) & 1u) mbar_wait_drain(&tail[s], ((parity >> s) & 1u) ^ 1u);
+    }
+};
+// Rows `from` .. the end of its step of 16 in each of a stage's blocks of 64 rows x
+// 128 bytes (a row is 128 bytes in the swizzle, too).  One warp.
+__device__ __forceinline__ void zero_rows(uint8_t *stage, int blocks, int from, int lane) {
+    const int n = (((from + 15) & ~15) - from) * 8;          // 16-byte pieces per block
+    for (int i = lane; i < blocks * n; i += 32) {
+        const int b = i / n, c = i - b * n;
+        *reinterpret_cast<uint4 *>(stage + b * (64 * 128) + from * 128 + c * 16) =
+            make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_proxy_async();
+    __syncwarp();
+}
+
 template <int MODE, int CG>
 __device__ __forceinline__ void train_gemm(const Params &p) {
     using C = Cfg<MODE, CG>;
@@ -413,7 +421,8 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
     uint8_t *rest = smem + C::EPI_OFF + p.boxes * C::BOX_BYTES;
     uint64_t *full = reinterpret_cast<uint64_t *>(rest + C::BAR_OFF);
     uint64_t *empty = full + STAGES;
-    uint64_t *tfull = empty + STAGES;       // [2]
+    uint64_t *tail = empty + STAGES;        // DW: a stage that needs zeroes has landed here
+    uint64_t *tfull = tail + STAGES;        // [2]
     uint64_t *tempty = tfull + 2;           // [2]
     uint64_t *drain = tempty + 2;
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(rest + C::MISC_OFF);
@@ -440,6 +449,7 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 2);          // each producer arms its share
             mbar_init(&empty[s], 1);
+            mbar_init(&tail[s], 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&tfull[i], 1);
@@ -464,15 +474,6 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
     if (total < 0) {                         // both CTAs of a pair read the same offsets
         if (tid == 0 && blockIdx.x == 0) report(p.dev_status, MOE_DEV_BAD_OFFSETS);
         total = 0;
-    } else if (MODE == DACT && warp == 2) {
-        // the groups' maps of the weight gradients' operands
-        for (int g = blockIdx.x; g < p.G; g += gridDim.x) {
-            if (s_off[g + 1] == s_off[g]) continue;          // never loaded
-#pragma unroll
-            for (int m = 0; m < NMAPS; ++m)
-                cut_map(p.maps + g * NMAPS + m, rest + C::MAP_OFF + m * 128, &p.tmG[m],
-                        s_off[g + 1], lane);
-        }
     }
     tc_fence_before();
     __syncthreads();
@@ -495,6 +496,7 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
             uint32_t phase = 0;
             int armed[STAGES];
             for (int s = 0; s < STAGES; ++s) armed[s] = -1;
+            Tails tails;
             auto load2 = [&](void *dst, const CUtensorMap *m, int s, int c0, int c1) {
                 if (CG == 1)
                     tma_load_2d(dst, m, &full[s], c0, c1);
@@ -511,25 +513,37 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
             for (int tile = first_tile; tile < total && !*s_abort; tile += step) {
                 const Tile t = decode_tile<MODE, 128 * CG>(p, tile, g, s_off, s_prefix);
                 const bool half = is_half(t);
-                const CUtensorMap *m = is_a ? (half ? &p.tmAh : &p.tmA)
-                                            : (half && MODE == FWD ? &p.tmBh : &p.tmB);
+                const CUtensorMap *m = MODE == DW ? &p.tmG[2 * t.prod + (is_a ? 0 : 1)]
+                                       : is_a     ? (half ? &p.tmAh : &p.tmA)
+                                                  : (half && MODE == FWD ? &p.tmBh : &p.tmB);
                 const int nkb = kblocks(t);
                 const uint32_t tx = CG * (is_a ? C::A_STAGE / (half ? 2 : 1) : C::B_STAGE);
-                if (MODE == DW && nkb > 0) {
-                    m = p.maps + t.g * NMAPS + 2 * t.prod + (is_a ? 0 : 1);
-                    acquire_map(m);
-                }
                 bool ok = true;
                 for (int kb = 0; kb < nkb; ++kb) {
                     if (!wait_phase(&empty[stage], phase ^ 1, s_abort, p.dev_status)) {
                         ok = false;
                         break;
                     }
-                    armed[stage] = static_cast<int>(phase);
                     uint8_t *dst = smem + stage * C::STAGE + (is_a ? 0 : C::A_STAGE);
+                    const int k0 = kb * BK;
+                    if (MODE == DW && kb + 1 == nkb && has_tail(t)) {
+                        // to this CTA's own barrier, for the warp that zeroes
+                        const int c = (is_a ? t.m0 : t.n0) + 128 * rank;
+                        mbar_arrive_expect_tx(&tail[stage], is_a ? C::A_STAGE : C::B_STAGE);
+                        tails.arm(stage);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            tma_load_2d(dst + j * (64 * BK * 2), m, &tail[stage], c + 64 * j, t.row0 + k0);
+                        armed[stage] = -1;
+                        if (++stage == STAGES) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
+                        continue;
+                    }
+                    armed[stage] = static_cast<int>(phase);
                     if (leader)
                         mbar_arrive_expect_tx(&full[stage], tx);
-                    const int k0 = kb * BK;
                     if (MODE == DW) {
                         const int c = (is_a ? t.m0 : t.n0) + 128 * rank;
 #pragma unroll
@@ -579,8 +593,25 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                 for (int s = 0; s < STAGES; ++s)
                     if (armed[s] >= 0) mbar_wait_drain(&full[s], static_cast<uint32_t>(armed[s]));
             }
+            if (MODE == DW && *s_abort) tails.drain(tail, STAGES);
         }
         __syncwarp();
+    } else if (MODE == DW && warp == 2) {
+        // ================= zeroes: the rows behind a group in its last step
+        int stage = 0, g = 0;
+        Tails tails;
+        for (int tile = first_tile; tile < total; tile += step) {
+            const Tile t = decode_tile<MODE, 128 * CG>(p, tile, g, s_off, s_prefix);
+            const int nkb = kblocks(t);
+            if (nkb == 0) continue;
+            stage = (stage + nkb - 1) % STAGES;
+            if (has_tail(t)) {
+                if (!wait_phase(&tail[stage], tails.take(stage), s_abort, p.dev_status)) break;
+                zero_rows(smem + stage * C::STAGE, C::STAGE / (64 * 128), t.row_end - t.row0 - (nkb - 1) * BK, lane);
+                if (lane == 0) mbar_arrive_cluster(lead_full + 8u * static_cast<uint32_t>(stage));
+            }
+            if (++stage == STAGES) stage = 0;
+        }
     } else if (warp == 1) {
         // ================= MMA issuer (even CTA only)
         if (leader && elect_one()) {
@@ -601,10 +632,14 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                 const uint32_t idesc = is_half(t) ? C::IDESC - (8u << 24) : C::IDESC;    // M = 128
                 bool ok = true;
                 for (int kb = 0; kb < nkb; ++kb) {
-                    if (!wait_phase(&full[stage], phase, s_abort, p.dev_status)) {
+                    // (zeroes are written by the warps of both CTAs, through the generic proxy)
+                    const bool zeroed = MODE == DW && kb + 1 == nkb && has_tail(t);
+                    if (zeroed ? !mbar_wait_bounded_cluster(&full[stage], phase, s_abort, p.dev_status)
+                               : !wait_phase(&full[stage], phase, s_abort, p.dev_status)) {
                         ok = false;
                         break;
                     }
+                    if (zeroed) fence_proxy_async();
                     tc_fence_after();
                     const uint32_t at = base + static_cast<uint32_t>(stage) * (C::STAGE / 16);
                     const uint32_t a = at + (C::A_MN ? C::MN_LO : 1u << 16);
@@ -799,7 +834,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     uint8_t *rest = smem + C::EPI_OFF + p.boxes * C::BOX_BYTES;
     uint64_t *full = reinterpret_cast<uint64_t *>(rest + C::BAR_OFF);    // used in the even CTA
     uint64_t *empty = full + W_STAGES;
-    uint64_t *tfull = empty + W_STAGES;     // [2]: half h is complete
+    uint64_t *tail = empty + W_STAGES;      // a stage that needs zeroes has landed here
+    uint64_t *tfull = tail + W_STAGES;      // [2]: half h is complete
     uint64_t *tempty = tfull + 2;           // [2], used in the even CTA
     uint64_t *drain = tempty + 2;
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(rest + C::MISC_OFF);
@@ -818,6 +854,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         for (int s = 0; s < W_STAGES; ++s) {
             mbar_init(&full[s], 2);          // each producer arms its share
             mbar_init(&empty[s], 1);
+            mbar_init(&tail[s], 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&tfull[i], 1);
@@ -850,27 +887,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             uint32_t phase = 0;
             int armed[W_STAGES];
             for (int s = 0; s < W_STAGES; ++s) armed[s] = -1;
+            Tails tails;
             int g = 0;
             for (int tile = first_tile; tile < total && !*s_abort; tile += step) {
                 const Tile t = decode_tile<DW, 256, BW>(p, tile, g, s_off, nullptr);
                 const int nkb = slices(t);
-                const CUtensorMap *m = p.maps + t.g * NMAPS + 2 * t.prod + (is_a ? 0 : 1);
-                if (nkb > 0) acquire_map(m);
+                const CUtensorMap *m = &p.tmG[2 * t.prod + (is_a ? 0 : 1)];
                 bool ok = true;
                 for (int kb = 0; kb < nkb; ++kb) {
                     if (!wait_phase(&empty[stage], phase ^ 1, s_abort, p.dev_status)) {
                         ok = false;
                         break;
                     }
-                    armed[stage] = static_cast<int>(phase);
                     uint8_t *dst = smem + stage * W_STAGE + (is_a ? 0 : SLICE);
                     const uint32_t fb = lead_full + 8u * static_cast<uint32_t>(stage);
-                    if (leader) mbar_arrive_expect_tx(&full[stage], 2 * (is_a ? SLICE : W_B));
+                    // with zeroes to come: to this CTA's own barrier
+                    const bool last = kb + 1 == nkb && has_tail(t);
+                    if (last) {
+                        mbar_arrive_expect_tx(&tail[stage], is_a ? SLICE : W_B);
+                        tails.arm(stage);
+                    } else if (leader) {
+                        mbar_arrive_expect_tx(&full[stage], 2 * (is_a ? SLICE : W_B));
+                    }
+                    armed[stage] = last ? -1 : static_cast<int>(phase);
                     const int c = is_a ? t.m0 + 128 * rank : t.n0 + 256 * rank;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (!is_a || j < 2)
+                    for (int j = 0; j < 4; ++j) {
+                        if (is_a && j >= 2) break;
+                        if (last)
+                            tma_load_2d(dst + j * (SLICE / 2), m, &tail[stage], c + 64 * j, t.row0 + kb * BK);
+                        else
                             tma_load_2d_pair(dst + j * (SLICE / 2), m, fb, c + 64 * j, t.row0 + kb * BK);
+                    }
                     if (++stage == W_STAGES) {
                         stage = 0;
                         phase ^= 1;
@@ -882,8 +930,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 for (int s = 0; s < W_STAGES; ++s)
                     if (armed[s] >= 0) mbar_wait_drain(&full[s], static_cast<uint32_t>(armed[s]));
             }
+            if (*s_abort) tails.drain(tail, W_STAGES);
         }
         __syncwarp();
+    } else if (warp == 2) {
+        // ================= zeroes: the rows behind a group in its last step
+        int stage = 0, g = 0;
+        Tails tails;
+        for (int tile = first_tile; tile < total; tile += step) {
+            const Tile t = decode_tile<DW, 256, BW>(p, tile, g, s_off, nullptr);
+            const int nkb = slices(t);
+            if (nkb == 0) continue;
+            stage = (stage + nkb - 1) % W_STAGES;
+            if (has_tail(t)) {
+                if (!wait_phase(&tail[stage], tails.take(stage), s_abort, p.dev_status)) break;
+                zero_rows(smem + stage * W_STAGE, W_STAGE / (64 * 128), t.row_end - t.row0 - (nkb - 1) * BK, lane);
+                if (lane == 0) mbar_arrive_cluster(lead_full + 8u * static_cast<uint32_t>(stage));
+            }
+            if (++stage == W_STAGES) stage = 0;
+        }
     } else if (warp == 1) {
         // ================= MMA issuer (even CTA only)
         if (leader && elect_one()) {
@@ -928,10 +993,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     return h1;
                 };
                 for (int kb = 0; kb < nkb; ++kb) {
-                    if (!wait_phase(&full[stage], phase, s_abort, p.dev_status)) {
+                    const bool zeroed = kb + 1 == nkb && has_tail(t);
+                    if (zeroed ? !mbar_wait_bounded_cluster(&full[stage], phase, s_abort, p.dev_status)
+                               : !wait_phase(&full[stage], phase, s_abort, p.dev_status)) {
                         ok = false;
                         break;
                     }
+                    if (zeroed) fence_proxy_async();
                     tc_fence_after();
                     mma_half(stage, kb, 0);
                     issued = true;
@@ -1164,15 +1232,14 @@ cudaError_t launch_rows(Params &p, const void *a, const void *w, cudaStream_t st
 inline bool a16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 struct BwdWs {
-    size_t d_h, act, maps, total;
+    size_t d_h, act, total;
 };
-BwdWs bwd_layout(int n, int I, int G) {
+BwdWs bwd_layout(int n, int I) {
     BwdWs w;
     auto up = [](size_t v) { return (v + 255) & ~static_cast<size_t>(255); };
     w.d_h = 0;
     w.act = up(static_cast<size_t>(n) * 2 * I * 2);
-    w.maps = w.act + up(static_cast<size_t>(n) * I * 2);
-    w.total = w.maps + up(static_cast<size_t>(G) * NMAPS * sizeof(CUtensorMap));
+    w.total = w.act + up(static_cast<size_t>(n) * I * 2);
     return w;
 }
 
@@ -1242,12 +1309,11 @@ extern "C" moe_status_t moe_grouped_mlp_train(const moe_bf16_t *expanded_x, cons
     return MOE_OK;
 }
 
-extern "C" moe_status_t moe_grouped_mlp_backward_workspace_size(int32_t n, int32_t I, int32_t G,
-                                                                size_t *bytes) {
+extern "C" moe_status_t moe_grouped_mlp_backward_workspace_size(int32_t n, int32_t I, size_t *bytes) {
     if (!bytes) return MOE_ERR_INVALID_ARG;
-    const moe_status_t st = check_sizes(G, n, 128, I);
+    const moe_status_t st = check_sizes(1, n, 128, I);
     if (st != MOE_OK) return st;
-    *bytes = bwd_layout(n, I, G).total;
+    *bytes = bwd_layout(n, I).total;
     return MOE_OK;
 }
 
@@ -1268,7 +1334,7 @@ extern "C" moe_status_t moe_grouped_mlp_backward(
         if (!d_y || !expanded_x || !h) return MOE_ERR_INVALID_ARG;
         if (!a16(d_y) || !a16(expanded_x) || !a16(h) || !a16(w13) || !a16(w2))
             return MOE_ERR_INVALID_ARG;
-        if (!workspace || workspace_bytes < bwd_layout(n, I, G).total ||
+        if (!workspace || workspace_bytes < bwd_layout(n, I).total ||
             (reinterpret_cast<uintptr_t>(workspace) & 255))
             return MOE_ERR_WORKSPACE_TOO_SMALL;
     }
@@ -1282,7 +1348,7 @@ extern "C" moe_status_t moe_grouped_mlp_backward(
         return MOE_OK;
     }
     if (!encode_fn()) return MOE_ERR_CUDA;
-    const BwdWs L = bwd_layout(n, I, G);
+    const BwdWs L = bwd_layout(n, I);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     uint16_t *d_h = reinterpret_cast<uint16_t *>(ws + L.d_h);
     uint16_t *act = reinterpret_cast<uint16_t *>(ws + L.act);
@@ -1291,7 +1357,6 @@ extern "C" moe_status_t moe_grouped_mlp_backward(
     p.G = G;
     p.n = n;
     p.dev_status = dev_status;
-    p.maps = reinterpret_cast<CUtensorMap *>(ws + L.maps);
     // d_act and what follows from it
     if (!out_map(&p.tmO0, d_h, 0, n, I2, false) || !out_map(&p.tmO1, act, 0, n, I, false) ||
         !operand_map(&p.tmG[0], d_h, 0, n, I2, 64) ||

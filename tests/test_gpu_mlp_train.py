@@ -169,7 +169,7 @@ def test_rows_behind_the_last_group_are_left():
     s = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
     assert L.moe_grouped_mlp_train(p(x), p(off), 3, p(w13), p(w2), N, H, I, p(h), p(act), p(y),
                                    None, s) == 0
-    ws = torch.empty(moe.grouped_mlp_backward_workspace_size(N, I, 3), dtype=torch.uint8,
+    ws = torch.empty(moe.grouped_mlp_backward_workspace_size(N, I), dtype=torch.uint8,
                      device=DEV)
     assert L.moe_grouped_mlp_backward(p(d_y), p(x), p(off), 3, p(h), p(w13), p(w2), N, H, I, 0,
                                       p(d_x), None, None, p(ws), ws.numel(), None, s) == 0

@@ -25,7 +25,7 @@ def bwd(L, d_y=fake, x=fake, off=fake, G=4, h=fake, w13=fake, w2=fake, n=10, H=1
         d_x=fake, d_w13=fake, d_w2=fake, ws=fake, nbytes=None):
     if nbytes is None:
         b = ctypes.c_size_t(0)
-        L.moe_grouped_mlp_backward_workspace_size(max(n, 0), 128, 4, ctypes.byref(b))
+        L.moe_grouped_mlp_backward_workspace_size(max(n, 0), 128, ctypes.byref(b))
         nbytes = b.value
     return L.moe_grouped_mlp_backward(d_y, x, off, G, h, w13, w2, n, H, I, flags, d_x, d_w13, d_w2,
                                       ws, nbytes, None, None)
@@ -51,10 +51,10 @@ def test_pointers(L):
 
 def test_workspace_and_flags(L):
     b = ctypes.c_size_t(0)
-    assert L.moe_grouped_mlp_backward_workspace_size(10, 128, 4, ctypes.byref(b)) == 0
-    assert b.value >= 10 * 3 * 128 * 2 + 4 * 4 * 128
-    assert L.moe_grouped_mlp_backward_workspace_size(10, 100, 4, ctypes.byref(b)) == 2
-    assert L.moe_grouped_mlp_backward_workspace_size(10, 128, 4, None) == 1
+    assert L.moe_grouped_mlp_backward_workspace_size(10, 128, ctypes.byref(b)) == 0
+    assert b.value >= 10 * 3 * 128 * 2
+    assert L.moe_grouped_mlp_backward_workspace_size(10, 100, ctypes.byref(b)) == 2
+    assert L.moe_grouped_mlp_backward_workspace_size(10, 128, None) == 1
     assert bwd(L, nbytes=b.value - 1) == 3
     assert bwd(L, ws=None) == 3 and bwd(L, ws=P(0x1010)) == 3
     # adding is for fp32 buffers
