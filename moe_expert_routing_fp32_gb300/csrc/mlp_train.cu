@@ -703,16 +703,16 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
             // DACT: this lane's row of h, 32 columns of gate and up at a time, fetched one
             // step ahead (the first while the tile is still computed)
             uint4 h8[8];
+            // (rows behind the group: its last one again, so that the warp stays together)
+            const uint16_t *h_row =
+                MODE == DACT ? p.h + static_cast<int64_t>(min(row0 + lane, t.row_end - 1)) * (2 * p.N) : nullptr;
             auto fetch_h = [&](int c) {
                 const int col = t.n_blk * BN + 128 * hq + c;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) h8[j] = make_uint4(0u, 0u, 0u, 0u);
-                if (ok && col < p.N) {
-                    const uint16_t *src = p.h + static_cast<int64_t>(row0 + lane) * (2 * p.N) + col;
+                if (col < p.N) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        h8[j] = __ldg(reinterpret_cast<const uint4 *>(src) + j);
-                        h8[4 + j] = __ldg(reinterpret_cast<const uint4 *>(src + p.N) + j);
+                        h8[j] = __ldg(reinterpret_cast<const uint4 *>(h_row + col) + j);
+                        h8[4 + j] = __ldg(reinterpret_cast<const uint4 *>(h_row + p.N + col) + j);
                     }
                 }
             };
@@ -787,7 +787,14 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_drained(lead_tempty + 8u * (u & 1));
+            if (lane == 0) {
+                // CG = 1: as an ordinary arrival.  One through the cluster's window could be on
+                // its way when this CTA, for which no peer waits, has left.
+                if (CG == 1)
+                    mbar_arrive(&tempty[u & 1]);
+                else
+                    arrive_drained(lead_tempty + 8u * (u & 1));
+            }
             ++u;
         }
         if (lane == 0) bulk_wait<0>();       // every output box written
