@@ -511,7 +511,14 @@ __device__ __forceinline__ void fp4_gemm(const Params &p) {
             tmem_ld_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_drained(lead_tempty + 8u * (u % NACC));
+            if (lane == 0) {
+                // CG = 1: as an ordinary arrival.  One through the cluster's window could be on
+                // its way when this CTA, for which no peer waits, has left.
+                if (CG == 1)
+                    mbar_arrive(&tempty[u % NACC]);
+                else
+                    arrive_drained(lead_tempty + 8u * (u % NACC));
+            }
             ++u;
             return true;
         };
