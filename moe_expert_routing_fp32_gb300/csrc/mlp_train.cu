@@ -377,6 +377,15 @@ __device__ __forceinline__ bool load_groups(const Params &p, int *s_off) {
     return !__syncthreads_or(bad);
 }
 
+// wait_phase with an acquire that reaches the other CTA of the pair.
+__device__ __forceinline__ bool wait_zeroed(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                            int32_t *dev_status) {
+#pragma unroll 1
+    for (int i = 0; i < 1024; ++i)                       // no timer is read at first
+        if (mbar_try_wait_cluster(bar, parity)) return true;
+    return mbar_wait_bounded_cluster(bar, parity, abort, dev_status);
+}
+
 // DW: whether the group's last 16-row step has rows of the next group in it.
 __device__ __forceinline__ bool has_tail(const Tile &t) { return ((t.row_end - t.row0) & 15) != 0; }
 // The parities of the stages' tail barriers, which complete a phase per use.
@@ -400,12 +409,11 @@ struct Tails {
 // Rows `from` .. the end of its step of 16 in each of a stage's blocks of 64 rows x
 // 128 bytes (a row is 128 bytes in the swizzle, too).  One warp.
 __device__ __forceinline__ void zero_rows(uint8_t *stage, int blocks, int from, int lane) {
-    const int n = (((from + 15) & ~15) - from) * 8;          // 16-byte pieces per block
-    for (int i = lane; i < blocks * n; i += 32) {
-        const int b = i / n, c = i - b * n;
-        *reinterpret_cast<uint4 *>(stage + b * (64 * 128) + from * 128 + c * 16) =
-            make_uint4(0u, 0u, 0u, 0u);
-    }
+    const int to = (from + 15) & ~15;
+    for (int b = 0; b < blocks; ++b)
+        for (int r = from + (lane >> 3); r < to; r += 4)     // eight lanes a row
+            *reinterpret_cast<uint4 *>(stage + b * (64 * 128) + r * 128 + (lane & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async();
     __syncwarp();
 }
@@ -519,7 +527,8 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                 const int nkb = kblocks(t);
                 const uint32_t tx = CG * (is_a ? C::A_STAGE / (half ? 2 : 1) : C::B_STAGE);
                 bool ok = true;
-                for (int kb = 0; kb < nkb; ++kb) {
+                for (int i = 0; i < nkb; ++i) {
+                    const int kb = MODE == DW && has_tail(t) ? (i == 0 ? nkb - 1 : i - 1) : i;
                     if (!wait_phase(&empty[stage], phase ^ 1, s_abort, p.dev_status)) {
                         ok = false;
                         break;
@@ -603,14 +612,12 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
         for (int tile = first_tile; tile < total; tile += step) {
             const Tile t = decode_tile<MODE, 128 * CG>(p, tile, g, s_off, s_prefix);
             const int nkb = kblocks(t);
-            if (nkb == 0) continue;
-            stage = (stage + nkb - 1) % STAGES;
-            if (has_tail(t)) {
+            if (has_tail(t)) {                       // a tile's first stage
                 if (!wait_phase(&tail[stage], tails.take(stage), s_abort, p.dev_status)) break;
                 zero_rows(smem + stage * C::STAGE, C::STAGE / (64 * 128), t.row_end - t.row0 - (nkb - 1) * BK, lane);
                 if (lane == 0) mbar_arrive_cluster(lead_full + 8u * static_cast<uint32_t>(stage));
             }
-            if (++stage == STAGES) stage = 0;
+            stage = (stage + nkb) % STAGES;
         }
     } else if (warp == 1) {
         // ================= MMA issuer (even CTA only)
@@ -631,19 +638,28 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                 const uint32_t d = tmem + (u & 1) * BN;
                 const uint32_t idesc = is_half(t) ? C::IDESC - (8u << 24) : C::IDESC;    // M = 128
                 bool ok = true;
-                for (int kb = 0; kb < nkb; ++kb) {
+                // DW's slice with zeroes is loaded first and taken some slices later (as many as
+                // the ring allows), so that nobody waits for its zeroes
+                const bool early = MODE == DW && nkb > 0 && has_tail(t);
+                const int taken = early ? min(nkb - 1, STAGES - 2) : 0;
+                for (int i = 0; i < nkb; ++i) {
+                    // place in the order of loading, slice, stage
+                    const int at = !early || i > taken ? i : i == taken ? 0 : i + 1;
+                    const int kb = !early ? at : at == 0 ? nkb - 1 : at - 1;
+                    const int ring = stage + at, st = ring % STAGES;
+                    const uint32_t ph = phase ^ (static_cast<uint32_t>(ring / STAGES) & 1u);
                     // (zeroes are written by the warps of both CTAs, through the generic proxy)
-                    const bool zeroed = MODE == DW && kb + 1 == nkb && has_tail(t);
-                    if (zeroed ? !mbar_wait_bounded_cluster(&full[stage], phase, s_abort, p.dev_status)
-                               : !wait_phase(&full[stage], phase, s_abort, p.dev_status)) {
+                    const bool zeroed = early && at == 0;
+                    if (zeroed ? !wait_zeroed(&full[st], ph, s_abort, p.dev_status)
+                               : !wait_phase(&full[st], ph, s_abort, p.dev_status)) {
                         ok = false;
                         break;
                     }
                     if (zeroed) fence_proxy_async();
                     tc_fence_after();
-                    const uint32_t at = base + static_cast<uint32_t>(stage) * (C::STAGE / 16);
-                    const uint32_t a = at + (C::A_MN ? C::MN_LO : 1u << 16);
-                    const uint32_t b = at + C::A_STAGE / 16 + (C::B_MN ? C::MN_LO : 1u << 16);
+                    const uint32_t addr = base + static_cast<uint32_t>(st) * (C::STAGE / 16);
+                    const uint32_t a = addr + (C::A_MN ? C::MN_LO : 1u << 16);
+                    const uint32_t b = addr + C::A_STAGE / 16 + (C::B_MN ? C::MN_LO : 1u << 16);
                     const int steps = kb + 1 < nkb ? BK / 16 : last;
 #pragma unroll
                     for (int s = 0; s < BK / 16; ++s) {
@@ -652,19 +668,18 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                         const uint32_t ka = C::A_MN ? s * 128 : s / 4 * (SLICE / 16) + s % 4 * 2;
                         const uint32_t kbb =
                             C::B_MN ? s * 128 : s / 4 * (C::B_SLICE / 16) + s % 4 * 2;
-                        mma<CG>(d, a + ka, b + kbb, idesc, (kb | s) != 0 ? 1u : 0u);
+                        mma<CG>(d, a + ka, b + kbb, idesc, (i | s) != 0 ? 1u : 0u);
                     }
                     issued = true;
                     if (CG == 1)
-                        tc_commit(&empty[stage]);
+                        tc_commit(&empty[st]);
                     else
-                        tc_commit_pair_mc(&empty[stage], 0x3);
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
+                        tc_commit_pair_mc(&empty[st], 0x3);
                 }
                 if (!ok) break;
+                stage += nkb;
+                phase ^= static_cast<uint32_t>(stage / STAGES) & 1u;
+                stage %= STAGES;
                 if (CG == 1)
                     tc_commit(&tfull[u & 1]);
                 else
@@ -1001,7 +1016,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 };
                 for (int kb = 0; kb < nkb; ++kb) {
                     const bool zeroed = kb + 1 == nkb && has_tail(t);
-                    if (zeroed ? !mbar_wait_bounded_cluster(&full[stage], phase, s_abort, p.dev_status)
+                    if (zeroed ? !wait_zeroed(&full[stage], phase, s_abort, p.dev_status)
                                : !wait_phase(&full[stage], phase, s_abort, p.dev_status)) {
                         ok = false;
                         break;
