@@ -59,6 +59,7 @@ struct Params {
     CUtensorMap tmO0, tmO1;    // FWD: h, act; DACT: d_h, act; DX: d_x; DOWN: y; DW: d_W13, d_W2
     CUtensorMap tmAh, tmBh;    // a pair's tiles of at most 128 rows: 64-row boxes of A (FWD: and B)
     CUtensorMap tmG[4];        // DW's operands: d_h and x, d_y and act
+    CUtensorMap tmH;           // DACT: h
     const int32_t *offsets;
     int32_t G, n;
     int32_t K;                 // contraction (not DW)
@@ -80,8 +81,10 @@ template <int MODE, int CG>
 struct Cfg {
     // 64-wide slices of K per stage: two at a time load a little faster, one wastes
     // less of a group's last rows (DW, 32768 rows of 64 groups: 666 -> 645 us a pass)
-    static constexpr int KSUB = CG == 2 && MODE != DW ? 2 : 1;
-    static constexpr int STAGES = CG == 1 ? 4 : 6 / KSUB;
+    static constexpr int KSUB = CG == 2 && MODE != DW && MODE != DACT ? 2 : 1;
+    // d_act on pairs: h comes by TMA, too, into boxes that take a stage's place
+    static constexpr bool H_BOXES = CG == 2 && MODE == DACT;
+    static constexpr int STAGES = CG == 1 ? 4 : H_BOXES ? 5 : 6 / KSUB;
     static constexpr int A_STAGE = SLICE * KSUB;
     static constexpr int B_SLICE = BN / CG * 128;
     static constexpr int B_STAGE = B_SLICE * KSUB;
@@ -90,12 +93,14 @@ struct Cfg {
     // follows them, counted from there
     static constexpr int EPI_OFF = STAGES * STAGE;
     static constexpr int BOX_BYTES = EPI_WARPS * EPI_BYTES;
+    static constexpr int H_BYTES = H_BOXES ? 2 * BOX_BYTES : 0;     // gate and up of each warp
     static constexpr int BAR_OFF = 0;
-    static constexpr int NBARS = 3 * STAGES + 5;        // full, empty, tail, tfull, tempty, drain
+    // full, empty, tail, tfull, tempty, drain, h
+    static constexpr int NBARS = 3 * STAGES + 5 + (H_BOXES ? EPI_WARPS : 0);
     static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
     static constexpr int OFFS_OFF = MISC_OFF + 16;
     static constexpr int smem(int G, int boxes) {
-        return 1024 + EPI_OFF + boxes * BOX_BYTES + OFFS_OFF + (MODE == DW ? G + 1 : 2 * G + 2) * 4;
+        return 1024 + EPI_OFF + boxes * BOX_BYTES + H_BYTES + OFFS_OFF + (MODE == DW ? G + 1 : 2 * G + 2) * 4;
     }
     // two boxes where they fit beside the groups' tables: a warp fills one while the
     // last one's store still reads the other
@@ -426,13 +431,15 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     // a pair's MMAs are issued by its even CTA: full, tempty are used there
-    uint8_t *rest = smem + C::EPI_OFF + p.boxes * C::BOX_BYTES;
+    uint8_t *h_boxes = smem + C::EPI_OFF + p.boxes * C::BOX_BYTES;
+    uint8_t *rest = h_boxes + C::H_BYTES;
     uint64_t *full = reinterpret_cast<uint64_t *>(rest + C::BAR_OFF);
     uint64_t *empty = full + STAGES;
     uint64_t *tail = empty + STAGES;        // DW: a stage that needs zeroes has landed here
     uint64_t *tfull = tail + STAGES;        // [2]
     uint64_t *tempty = tfull + 2;           // [2]
     uint64_t *drain = tempty + 2;
+    uint64_t *h_full = drain + 1;           // an epilogue warp's boxes of h have landed
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(rest + C::MISC_OFF);
     volatile int *s_abort = reinterpret_cast<volatile int *>(rest + C::MISC_OFF + 4);
     volatile int *s_bad = reinterpret_cast<volatile int *>(rest + C::MISC_OFF + 8);
@@ -464,6 +471,8 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
             mbar_init(&tempty[i], CG * EPI_WARPS);
         }
         mbar_init(drain, 1);
+        if (C::H_BOXES)
+            for (int i = 0; i < EPI_WARPS; ++i) mbar_init(&h_full[i], 1);
         fence_barrier_init();
     } else if (warp == 3 && MODE != DW && elect_one()) {
         tma_prefetch_desc(&p.tmA);
@@ -701,6 +710,9 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
         const int quarter = warp & 3, part = (warp - 4) >> 2;
         Boxes boxes{smem + C::EPI_OFF + (warp - 4) * p.boxes * EPI_BYTES, p.boxes, 0, lane};
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        uint8_t *h_box = h_boxes + (warp - 4) * (2 * EPI_BYTES);
+        uint32_t h_phase = 0;
+        bool h_pending = false, lost = false;
         int g = 0;
         uint32_t u = 0;
         for (int tile = first_tile; tile < total; tile += step) {
@@ -715,15 +727,26 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
             const bool ok = row0 + lane < t.row_end;
             const bool boxed = row0 + 32 <= t.row_end;
             const uint32_t acc = tmem + lanes + (u & 1) * BN;
-            // DACT: this lane's row of h, 32 columns of gate and up at a time, fetched one
-            // step ahead (the first while the tile is still computed)
+            // DACT: 32 columns of gate and up of h, fetched one step ahead (the first while the
+            // tile is still computed): on pairs by TMA into the warp's own boxes, which costs
+            // the other roles nothing (loads of a row per lane keep their instructions
+            // waiting), else this lane's row into registers
             uint4 h8[8];
             // (rows behind the group: its last one again, so that the warp stays together)
-            const uint16_t *h_row =
-                MODE == DACT ? p.h + static_cast<int64_t>(min(row0 + lane, t.row_end - 1)) * (2 * p.N) : nullptr;
+            const uint16_t *h_row = MODE == DACT && !C::H_BOXES
+                                        ? p.h + static_cast<int64_t>(min(row0 + lane, t.row_end - 1)) * (2 * p.N)
+                                        : nullptr;
             auto fetch_h = [&](int c) {
                 const int col = t.n_blk * BN + 128 * hq + c;
-                if (col < p.N) {
+                if (col >= p.N) return;
+                if (C::H_BOXES) {
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&h_full[warp - 4], 2 * EPI_BYTES);
+                        tma_load_2d(h_box, &p.tmH, &h_full[warp - 4], col, row0);
+                        tma_load_2d(h_box + EPI_BYTES, &p.tmH, &h_full[warp - 4], p.N + col, row0);
+                    }
+                    h_pending = true;
+                } else {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         h8[j] = __ldg(reinterpret_cast<const uint4 *>(h_row + col) + j);
@@ -750,6 +773,21 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                     const int col = t.n_blk * BN + 128 * hq + c;
                     if (col >= p.N) break;               // N = 128 mod 256: no such columns
                     uint32_t hg[16], hu[16];
+                    if (C::H_BOXES) {
+                        if (!wait_phase(&h_full[warp - 4], h_phase, s_abort, p.dev_status)) {
+                            lost = true;
+                            break;
+                        }
+                        h_phase ^= 1;
+                        h_pending = false;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int at = lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4);
+                            h8[j] = *reinterpret_cast<const uint4 *>(h_box + at);
+                            h8[4 + j] = *reinterpret_cast<const uint4 *>(h_box + EPI_BYTES + at);
+                        }
+                        __syncwarp();                    // read, before the next ones land there
+                    }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         hg[4 * j] = h8[j].x, hg[4 * j + 1] = h8[j].y;
@@ -782,6 +820,7 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                               p.N + col);
                     boxes.emit(boxed, ok, wa, &p.tmO1, p.out1, p.ld1, row0, col);
                 }
+                if (lost) break;
             } else if (MODE == DX || MODE == DOWN) {
 #pragma unroll 1
                 for (int c = span * part; c < span * (part + 1); c += 32) {
@@ -812,6 +851,7 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
             }
             ++u;
         }
+        if (C::H_BOXES && h_pending) mbar_wait_drain(&h_full[warp - 4], h_phase);    // unwinding
         if (lane == 0) bulk_wait<0>();       // every output box written
         __syncwarp();
     }
@@ -1241,7 +1281,7 @@ cudaError_t launch_rows(Params &p, const void *a, const void *w, cudaStream_t st
     const int64_t brows = MODE == FWD ? 2 * static_cast<int64_t>(p.N) : K_MAJOR ? p.N : p.K;
     const int bcols = K_MAJOR ? p.K : p.N;
     // rows of B's box: 128 weight rows, or a stage's K
-    const int box = K_MAJOR || pair ? 128 : 64;
+    const int box = K_MAJOR ? 128 : 64 * (pair ? Cfg<MODE, 2>::KSUB : 1);
     if (!operand_map(&p.tmA, a, 0, p.n, p.K, 128) || !operand_map(&p.tmB, w, p.G, brows, bcols, box) ||
         !operand_map(&p.tmAh, a, 0, p.n, p.K, 64) ||
         (MODE == FWD && !operand_map(&p.tmBh, w, p.G, brows, bcols, 64)))
@@ -1381,6 +1421,7 @@ extern "C" moe_status_t moe_grouped_mlp_backward(
     p.dev_status = dev_status;
     // d_act and what follows from it
     if (!out_map(&p.tmO0, d_h, 0, n, I2, false) || !out_map(&p.tmO1, act, 0, n, I, false) ||
+        !out_map(&p.tmH, const_cast<uint16_t *>(h), 0, n, I2, false) ||
         !operand_map(&p.tmG[0], d_h, 0, n, I2, 64) ||
         !operand_map(&p.tmG[1], expanded_x, 0, n, H, 64) ||
         !operand_map(&p.tmG[2], d_y, 0, n, H, 64) || !operand_map(&p.tmG[3], act, 0, n, I, 64))
