@@ -66,7 +66,6 @@ struct Params {
     int32_t N;                 // FWD, DACT: I; DX, DOWN: H
     int32_t nt;                // column tiles of a row block
     int32_t wrows;             // rows a group's weights would have as an operand like A
-    int32_t boxes;             // output boxes per epilogue warp
     const uint16_t *h;         // DACT
     uint16_t *out0, *out1;
     int32_t ld0, ld1;
@@ -89,8 +88,9 @@ struct Cfg {
     static constexpr int B_SLICE = BN / CG * 128;
     static constexpr int B_STAGE = B_SLICE * KSUB;
     static constexpr int STAGE = A_STAGE + B_STAGE;
-    // behind the stages: output boxes (one or two per epilogue warp), and what
-    // follows them, counted from there
+    // behind the stages: an output box per epilogue warp (a second one, filled while the
+    // first one's store still reads it, is worth nothing: 655 us a pass of those 32768 rows
+    // against 645 with one), and what follows them, counted from there
     static constexpr int EPI_OFF = STAGES * STAGE;
     static constexpr int BOX_BYTES = EPI_WARPS * EPI_BYTES;
     static constexpr int H_BYTES = H_BOXES ? 2 * BOX_BYTES : 0;     // gate and up of each warp
@@ -99,12 +99,9 @@ struct Cfg {
     static constexpr int NBARS = 3 * STAGES + 5 + (H_BOXES ? EPI_WARPS : 0);
     static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
     static constexpr int OFFS_OFF = MISC_OFF + 16;
-    static constexpr int smem(int G, int boxes) {
-        return 1024 + EPI_OFF + boxes * BOX_BYTES + H_BYTES + OFFS_OFF + (MODE == DW ? G + 1 : 2 * G + 2) * 4;
+    static constexpr int smem(int G) {
+        return 1024 + EPI_OFF + BOX_BYTES + H_BYTES + OFFS_OFF + (MODE == DW ? G + 1 : 2 * G + 2) * 4;
     }
-    // two boxes where they fit beside the groups' tables: a warp fills one while the
-    // last one's store still reads the other
-    static constexpr int boxes(int G) { return smem(G, 2) <= 227 * 1024 ? 2 : 1; }
     static constexpr bool A_MN = MODE == DW, B_MN = MODE != FWD && MODE != DOWN;
     // shared-memory descriptors: the high word is the same for both layouts (1 KB
     // between groups of eight 128-byte rows, 128-byte swizzle); the low word's
@@ -114,7 +111,7 @@ struct Cfg {
                                       (B_MN ? 1u << 16 : 0u) |
                                       (static_cast<uint32_t>(BN >> 3) << 17) |
                                       (static_cast<uint32_t>(CG * 128 >> 4) << 24);
-    static_assert(smem(MAX_GROUPS, 1) <= 227 * 1024, "shared memory");
+    static_assert(smem(MAX_GROUPS) <= 227 * 1024, "shared memory");
     static_assert(STAGE % 1024 == 0 && BOX_BYTES % 1024 == 0, "alignment");
 };
 
@@ -235,51 +232,31 @@ __device__ __forceinline__ Tile decode_tile(const Params &p, int tile, int &g, c
     return t;
 }
 
-// An epilogue warp's output boxes.
-struct Boxes {
-    uint8_t *base;
-    int n, at, lane;           // one or two, the next one
-    // 64 bytes of each of the warp's 32 rows (lane i: row row0 + i) into a box, in the
-    // 64-byte swizzle of the output maps; the caller stores it.
-    __device__ __forceinline__ const uint8_t *fill(const uint32_t *w) {
-        uint8_t *box = base + at * EPI_BYTES;
-        if (lane == 0) {                             // the store that last used it has read it
-            if (n == 2)
-                bulk_wait_read<1>();
-            else
-                bulk_wait_read<0>();
-        }
-        if (n == 2) at ^= 1;
+// An epilogue warp's output box.
+struct Box {
+    uint8_t *at;
+    int lane;
+    // 64 bytes of each of the warp's 32 rows (lane i: row row0 + i), in the 64-byte
+    // swizzle of the output maps; the caller stores it.
+    __device__ __forceinline__ void fill(const uint32_t *w) const {
+        if (lane == 0) bulk_wait_read<0>();          // the last store has read it
         __syncwarp();
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch)
-            *reinterpret_cast<uint4 *>(box + lane * 64 + ((ch ^ ((lane >> 1) & 3)) << 4)) =
+            *reinterpret_cast<uint4 *>(at + lane * 64 + ((ch ^ ((lane >> 1) & 3)) << 4)) =
                 make_uint4(w[4 * ch], w[4 * ch + 1], w[4 * ch + 2], w[4 * ch + 3]);
         fence_proxy_async();
         __syncwarp();
-        return box;
-    }
-    // 128 bytes of each row into both boxes as one, in the 128-byte swizzle (DW).
-    __device__ __forceinline__ const uint8_t *fill_wide(const uint32_t (&w)[32]) {
-        if (lane == 0) bulk_wait_read<0>();
-        __syncwarp();
-#pragma unroll
-        for (int ch = 0; ch < 8; ++ch)
-            *reinterpret_cast<uint4 *>(base + lane * 128 + ((ch ^ (lane & 7)) << 4)) =
-                make_uint4(w[4 * ch], w[4 * ch + 1], w[4 * ch + 2], w[4 * ch + 3]);
-        fence_proxy_async();
-        __syncwarp();
-        return base;
     }
     // 32 bf16 columns of the rows: through a box where all 32 rows belong to the
     // group, else each lane its own row.
     __device__ __forceinline__ void emit(bool boxed, bool ok, const uint32_t (&w)[16],
                                          const CUtensorMap *map, uint16_t *out, int ld, int row0,
-                                         int col) {
+                                         int col) const {
         if (boxed) {
-            const uint8_t *box = fill(w);
+            fill(w);
             if (lane == 0) {
-                tma_store_2d(map, box, col, row0);
+                tma_store_2d(map, at, col, row0);
                 bulk_commit();
             }
         } else if (ok) {
@@ -292,16 +269,16 @@ struct Boxes {
 };
 
 // FWD: 32 columns of gate (x) and up (y) sums to h and act.
-__device__ __forceinline__ void emit_forward(const Params &p, Boxes &boxes, bool boxed, bool ok,
+__device__ __forceinline__ void emit_forward(const Params &p, const Box &box, bool boxed, bool ok,
                                              const float (&x)[32], const float (&y)[32], int row0,
                                              int col) {
     uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) w[i] = bf16x2(x[2 * i], x[2 * i + 1]);
-    boxes.emit(boxed, ok, w, &p.tmO0, p.out0, p.ld0, row0, col);
+    box.emit(boxed, ok, w, &p.tmO0, p.out0, p.ld0, row0, col);
 #pragma unroll
     for (int i = 0; i < 16; ++i) w[i] = bf16x2(y[2 * i], y[2 * i + 1]);
-    boxes.emit(boxed, ok, w, &p.tmO0, p.out0, p.ld0, row0, p.N + col);
+    box.emit(boxed, ok, w, &p.tmO0, p.out0, p.ld0, row0, p.N + col);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         float a[2];
@@ -312,26 +289,25 @@ __device__ __forceinline__ void emit_forward(const Params &p, Boxes &boxes, bool
         }
         w[i] = bf16x2(a[0], a[1]);
     }
-    boxes.emit(boxed, ok, w, &p.tmO1, p.out1, p.ld1, row0, col);
+    box.emit(boxed, ok, w, &p.tmO1, p.out1, p.ld1, row0, col);
 }
 
 // DW: 64 columns of a gradient from tensor memory at `taddr`; false where they and
 // all further ones are off the gradient (sizes of 128 mod the tile) or nothing has to
-// be written (an idle expert's zeros, added).  They leave as rows of 128 bytes where
-// the boxes have room for those: a store's hand-over to the async proxy costs a warp
-// more than the values it moves.
-__device__ __forceinline__ bool emit_gradient(const Params &p, Boxes &boxes, const Tile &t,
+// be written (an idle expert's zeros, added).
+__device__ __forceinline__ bool emit_gradient(const Params &p, const Box &box, const Tile &t,
                                               uint32_t taddr, int row0, int col) {
     const CUtensorMap *om = t.prod ? &p.tmO1 : &p.tmO0;
     const int M = t.prod ? p.H : 2 * p.I, N = t.prod ? p.I : p.H;
     const bool none = t.row_end == t.row0;
     if (row0 >= M || col >= N || (none && p.accumulate)) return false;
-    auto store = [&](const uint8_t *box, int c) {
-        if (boxes.lane == 0) {
+    auto store = [&](const uint32_t *w, int c) {
+        box.fill(w);
+        if (box.lane == 0) {
             if (p.accumulate)
-                tma_add_3d(om, box, c, row0, t.g);
+                tma_add_3d(om, box.at, c, row0, t.g);
             else
-                tma_store_3d(om, box, c, row0, t.g);
+                tma_store_3d(om, box.at, c, row0, t.g);
             bulk_commit();
         }
     };
@@ -344,28 +320,20 @@ __device__ __forceinline__ bool emit_gradient(const Params &p, Boxes &boxes, con
         tmem_read32(taddr, v[0]);
         tmem_read32(taddr + 32, v[1]);
     }
+    uint32_t w[16];
     if (p.w_f32) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            uint32_t w[32];
+        for (int k = 0; k < 4; ++k) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[k][i]);
-            if (boxes.n == 2) {
-                store(boxes.fill_wide(w), col + 32 * k);
-            } else {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) store(boxes.fill(w + 16 * h), col + 32 * k + 16 * h);
-            }
+            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[k / 2][16 * (k % 2) + i]);
+            store(w, col + 16 * k);
         }
     } else {
-        uint32_t w[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) w[i] = bf16x2(v[i / 16][2 * (i % 16)], v[i / 16][2 * (i % 16) + 1]);
-        if (boxes.n == 2) {
-            store(boxes.fill_wide(w), col);
-        } else {
+        for (int k = 0; k < 2; ++k) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) store(boxes.fill(w + 16 * h), col + 32 * h);
+            for (int i = 0; i < 16; ++i) w[i] = bf16x2(v[k][2 * i], v[k][2 * i + 1]);
+            store(w, col + 32 * k);
         }
     }
     return true;
@@ -431,7 +399,7 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     // a pair's MMAs are issued by its even CTA: full, tempty are used there
-    uint8_t *h_boxes = smem + C::EPI_OFF + p.boxes * C::BOX_BYTES;
+    uint8_t *h_boxes = smem + C::EPI_OFF + C::BOX_BYTES;
     uint8_t *rest = h_boxes + C::H_BYTES;
     uint64_t *full = reinterpret_cast<uint64_t *>(rest + C::BAR_OFF);
     uint64_t *empty = full + STAGES;
@@ -499,7 +467,8 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
     const uint32_t tmem = *s_tmem;
     const uint32_t lead_full = mapa_shared(smem_u32(full), 0);
     const uint32_t lead_tempty = mapa_shared(smem_u32(tempty), 0);
-    // a pair's tile of at most 128 rows
+    // a pair's tile of at most 128 rows (256 rows a group: forward 204 -> 197 us, backward
+    // 455 -> 449, 512: 319 -> 307 and no change)
     auto is_half = [&](const Tile &t) { return CG == 2 && MODE != DW && t.row_end - t.row0 <= 128; };
     auto kblocks = [&](const Tile &t) {
         return MODE == DW ? (t.row_end - t.row0 + BK - 1) / BK : (p.K + BK - 1) / BK;
@@ -708,7 +677,7 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
     } else if (warp >= 4) {
         // ================= epilogue: two warps share a TMEM lane quarter
         const int quarter = warp & 3, part = (warp - 4) >> 2;
-        Boxes boxes{smem + C::EPI_OFF + (warp - 4) * p.boxes * EPI_BYTES, p.boxes, 0, lane};
+        const Box box{smem + C::EPI_OFF + (warp - 4) * EPI_BYTES, lane};
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         uint8_t *h_box = h_boxes + (warp - 4) * (2 * EPI_BYTES);
         uint32_t h_phase = 0;
@@ -765,7 +734,7 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                     __syncwarp();
                     tmem_read32(acc + c, x);
                     tmem_read32(acc + span + c, y);
-                    emit_forward(p, boxes, boxed, ok, x, y, row0, t.n_blk * 128 + 64 * hq + c);
+                    emit_forward(p, box, boxed, ok, x, y, row0, t.n_blk * 128 + 64 * hq + c);
                 }
             } else if (MODE == DACT) {
 #pragma unroll 1
@@ -786,7 +755,10 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                             h8[j] = *reinterpret_cast<const uint4 *>(h_box + at);
                             h8[4 + j] = *reinterpret_cast<const uint4 *>(h_box + EPI_BYTES + at);
                         }
-                        __syncwarp();                    // read, before the next ones land there
+                        // the reads are over before the next ones land there (a barrier of the
+                        // warp alone lets them wait in line behind its stores of single rows)
+                        fence_proxy_async();
+                        __syncwarp();
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -815,10 +787,10 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                         const f2 t = fma2(gs, fma2(s, splat(-1.0f), splat(1.0f)), s);
                         wg[i] = to_bf16x2(mul2(mul2(dd, up), t));
                     }
-                    boxes.emit(boxed, ok, wg, &p.tmO0, p.out0, p.ld0, row0, col);
-                    boxes.emit(boxed, ok, wu, &p.tmO0, p.out0, p.ld0, row0,
+                    box.emit(boxed, ok, wg, &p.tmO0, p.out0, p.ld0, row0, col);
+                    box.emit(boxed, ok, wu, &p.tmO0, p.out0, p.ld0, row0,
                               p.N + col);
-                    boxes.emit(boxed, ok, wa, &p.tmO1, p.out1, p.ld1, row0, col);
+                    box.emit(boxed, ok, wa, &p.tmO1, p.out1, p.ld1, row0, col);
                 }
                 if (lost) break;
             } else if (MODE == DX || MODE == DOWN) {
@@ -832,12 +804,12 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                     uint32_t w[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) w[i] = bf16x2(v[2 * i], v[2 * i + 1]);
-                    boxes.emit(boxed, ok, w, &p.tmO0, p.out0, p.ld0, row0, col);
+                    box.emit(boxed, ok, w, &p.tmO0, p.out0, p.ld0, row0, col);
                 }
             } else {
 #pragma unroll 1
                 for (int c = 128 * part; c < 128 * part + 128; c += 64)
-                    if (!emit_gradient(p, boxes, t, acc + c, row0, t.n0 + c)) break;
+                    if (!emit_gradient(p, box, t, acc + c, row0, t.n0 + c)) break;
             }
             tc_fence_before();
             __syncwarp();
@@ -893,7 +865,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint8_t *rest = smem + C::EPI_OFF + p.boxes * C::BOX_BYTES;
+    uint8_t *rest = smem + C::EPI_OFF + C::BOX_BYTES;
     uint64_t *full = reinterpret_cast<uint64_t *>(rest + C::BAR_OFF);    // used in the even CTA
     uint64_t *empty = full + W_STAGES;
     uint64_t *tail = empty + W_STAGES;      // a stage that needs zeroes has landed here
@@ -1107,7 +1079,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     } else if (warp >= 4) {
         // ================= epilogue: two warps share a TMEM lane quarter
         const int quarter = warp & 3, part = (warp - 4) >> 2;
-        Boxes boxes{smem + C::EPI_OFF + (warp - 4) * p.boxes * EPI_BYTES, p.boxes, 0, lane};
+        const Box box{smem + C::EPI_OFF + (warp - 4) * EPI_BYTES, lane};
         int g = 0;
         uint32_t tph = 0;
         for (int tile = first_tile; tile < total; tile += step) {
@@ -1124,7 +1096,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 const uint32_t acc = tq + 256u * static_cast<uint32_t>(h) + 128u * static_cast<uint32_t>(part);
 #pragma unroll 1
                 for (int c = 0; c < 128; c += 64)
-                    if (!emit_gradient(p, boxes, t, acc + c, row0, t.n0 + 128 * h + 256 * part + c)) break;
+                    if (!emit_gradient(p, box, t, acc + c, row0, t.n0 + 128 * h + 256 * part + c)) break;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) arrive_drained(lead_tempty + 8u * static_cast<uint32_t>(h));
@@ -1190,31 +1162,31 @@ bool operand_map(CUtensorMap *m, const void *ptr, int groups, int64_t rows, int6
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Output [groups][rows][cols] as boxes of 32 rows x 64 bytes, or 128 (DW), swizzled
-// over as many.
-bool out_map(CUtensorMap *m, void *ptr, int groups, int64_t rows, int64_t cols, bool f32,
-             bool wide = false) {
+// Output [groups][rows][cols] (and h) as boxes of 32 rows x 64 bytes, swizzled over as many.
+bool out_map(CUtensorMap *m, void *ptr, int groups, int64_t rows, int64_t cols, bool f32) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t esz = f32 ? 4 : 2;
     cuuint64_t dim[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                          static_cast<cuuint64_t>(std::max(groups, 1))};
     cuuint64_t stride[2] = {dim[0] * esz, dim[0] * dim[1] * esz};
-    cuuint32_t box[3] = {static_cast<cuuint32_t>((wide ? 128 : 64) / esz), 32, 1}, es[3] = {1, 1, 1};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(64 / esz), 32, 1}, es[3] = {1, 1, 1};
     return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
               groups > 0 ? 3 : 2, ptr, dim, stride, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Row products: pairs where groups have more than one 128-row block on average.
-bool use_pair(int n, int G) { return n > 128ll * G; }
+// Row products: pairs where groups have a 128-row block or more on average.  Measured
+// as above (forward and backward pass, us, one CTA against a pair): 64 rows a group
+// 146 : 146 and 298 : 297, 128 158 : 156 and 358 : 349, 256 214 : 197 and 475 : 449.  Below,
+// a pair's tile would load 256 rows for a group's few.
+bool use_pair(int n, int G) { return n >= 128ll * G; }
 
 // DW in wide tiles: with few rows a group, where the gradients' stores decide and
 // fewer hand-overs help, and with very many.  Measured with H = 2048, I = 1024 and 64
-// groups (whole backward pass, us, 256 against 512 columns): 16 rows a group 288 : 272,
-// 64 305 : 295, 256 435 : 433, 512 691 : 707, 1024 1199 : 1248, 2048 2251 : 2298;
-// one group of 16384 rows, H = 4096, I = 2048: 1028 : 1005.
+// groups (whole backward pass, us, 256 against 512 columns): 16 rows a group 296 : 280,
+// 64 330 : 295, 128 373 : 360, 256 450 : 456, 512 683 : 713, 1024 1210 : 1245, 2048
+// 2252 : 2278; 16384 rows of H = 4096, I = 2048: one group 1030 : 1006, two 1028 : 1022.
 bool wide_gradient(int n, int G) { return n < 192ll * G || n >= 8192ll * G; }
 
 // CG = 1, 2: the 256-column kernels; 3: the wide one.
@@ -1222,7 +1194,6 @@ template <int MODE, int CG>
 cudaError_t launch(Params &p, int64_t tiles, cudaStream_t stream) {
     constexpr int PAIR = CG == 1 ? 1 : 2;
     using C = Cfg<MODE, PAIR>;
-    p.boxes = C::boxes(p.G);
     void (*kernel)(const Params);
     if constexpr (CG == 3)          // DW only
         kernel = gradient_wide_kernel;
@@ -1263,7 +1234,7 @@ cudaError_t launch(Params &p, int64_t tiles, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(PAIR * units), 1, 1);
     cfg.blockDim = dim3(THREADS, 1, 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>(C::smem(p.G, p.boxes));
+    cfg.dynamicSmemBytes = static_cast<size_t>(C::smem(p.G));
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1445,9 +1416,8 @@ extern "C" moe_status_t moe_grouped_mlp_backward(
         TRY_CUDA(launch_rows<DX>(p, d_h, w13, s));
     }
     if (d_w13 || d_w2) {
-        const bool wide_rows = Cfg<DW, 2>::boxes(G) == 2;
-        if ((d_w13 && !out_map(&p.tmO0, d_w13, G, I2, H, f32, wide_rows)) ||
-            (d_w2 && !out_map(&p.tmO1, d_w2, G, H, I, f32, wide_rows)))
+        if ((d_w13 && !out_map(&p.tmO0, d_w13, G, I2, H, f32)) ||
+            (d_w2 && !out_map(&p.tmO1, d_w2, G, H, I, f32)))
             return MOE_ERR_CUDA;
         p.mt0 = d_w13 ? static_cast<int>(ceil_div(I2, 256)) : 0;
         const int bn = wide_gradient(n, G) ? BW : BN;

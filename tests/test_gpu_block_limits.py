@@ -243,3 +243,18 @@ def test_two_blocks_step():
     for key, v in want.items():
         err = float((got[key].to(F64) - v).norm() / v.norm())
         assert err <= 11 ** 0.5 * nr.B / 3 ** 0.5, (key, err)
+
+
+@pytest.mark.parametrize("H,I", [(256, 256), (512, 384), (128, 128)])
+def test_ragged_groups_again(H, I):
+    """Groups whose last rows are stored row by row (31 and 127 mod 128 of them):
+    pass after pass has the same bits."""
+    x, off, w13, w2, d_y = mlp.make([127, 255, 31, 191] * 20, H, I, I)
+    h, y = moe.grouped_mlp_train(x, off, w13, w2)
+    want = moe.grouped_mlp_backward(d_y, x, off, h, w13, w2)
+    mlp.check_backward(x, off, w13, w2, h, d_y, want)
+    for _ in range(150):
+        h1, y1 = moe.grouped_mlp_train(x, off, w13, w2)
+        got = moe.grouped_mlp_backward(d_y, x, off, h, w13, w2)
+        assert torch.equal(h, h1) and torch.equal(y, y1)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
