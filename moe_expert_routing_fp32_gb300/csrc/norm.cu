@@ -429,6 +429,7 @@ __global__ void __launch_bounds__(THREADS, VPT <= 2 ? 2 : 1) norm_kernel(const _
             arrive();
             ahead = first_sum(k_after);
         }
+        fence_proxy_async();                         // (reads, before the slot is filled again)
         const float2 sums = team.sum(total2(m), ahead);
         // every thread has read this row's slot
         if (first && row + p.slots < b && *abort == 0) fetch(row + p.slots, this_slot);
