@@ -34,6 +34,11 @@
 // A row with infinities or NaN has them left out of its digits and added by the
 // epilogue, weight by weight: slow, but what the products give.
 //
+// 256 rows on 63 experts, K = 2048, N = 4096: 55 us (floor 44.6, 0.82 of the memory's
+// rate; 86 with mma.sync).  One row on 8 experts, K = 4096, I = 2048: 20.6 us with the digits,
+// 17.7 of them the product (floor 10.5; starting, the first loads and the joining of parts take
+// the rest).  Four rows on one expert: 11.3.
+//
 // Roles (8 warps): 0 TMA of the weights (which start before the rows' digits are
 // ready), 3 TMA of the digits, 1 MMA, 2 setup, 4-7 epilogue.
 #include <cuda.h>

@@ -33,6 +33,14 @@
 // Roles (12 warps): 0 TMA of A, 3 TMA of B, 1 MMA, 2 setup (DW: the zeroes),
 // 4-11 epilogue.  Tiles are CG * 128 rows x 256 columns on one CTA or a pair
 // (tcgen05 cta_group::2, half of B in each CTA), two accumulators in turn.
+//
+// What bounds it.  Many rows a group: the MMAs.  A pair's 256 x 256 tile needs 64 bytes
+// a cycle of each multiprocessor for them, all that one gets from L2, so depth of
+// the operands' ring and little else on that way decide.  131072 rows of 64 groups, H = 4096,
+// I = 2048: forward 3.45-3.75 ms (0.94-0.96 of the MMAs' rate), backward 7.0-7.8 (DX 0.96,
+// DW 0.89, DACT 0.83), 8.3 in a loop under the power cap; the flops' floors are 3.5 and
+// 7.0.  Few rows: the weights and their gradients; 509 rows, H = 2048, I = 1024: backward 246
+// us, the bytes' floor 218.  Between, both at once: 32768 rows 644 us, floors 311 and 438.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -79,7 +87,8 @@ struct Params {
 template <int MODE, int CG>
 struct Cfg {
     // 64-wide slices of K per stage: two at a time load a little faster, one wastes
-    // less of a group's last rows (DW, 32768 rows of 64 groups: 666 -> 645 us a pass)
+    // less of a group's last rows (DW, 32768 rows of 64 groups: 645 us a pass, 666 with two)
+    // and lets the ring shrink by half as much (DACT)
     static constexpr int KSUB = CG == 2 && MODE != DW && MODE != DACT ? 2 : 1;
     // d_act on pairs: h comes by TMA, too, into boxes that take a stage's place
     static constexpr bool H_BOXES = CG == 2 && MODE == DACT;

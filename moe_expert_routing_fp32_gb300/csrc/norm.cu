@@ -15,11 +15,13 @@
 // What bounds it is memory: every row is read and written once.  A team of 1 to 8
 // warps takes a row (8 columns a lane and step); rows come through a ring of
 // shared-memory slots filled by bulk copies some rows ahead, so that the copies
-// run on through the two sums a row waits for (one barrier each).  A team takes
+// run on through the sums a row waits for (its second one and the next row's first
+// share a barrier: 144 us backward where two took 211).  A team takes
 // consecutive rows and keeps the column sums in registers; it writes them out
 // when a sequence ends, team i's sums of sequence s to slot i + s (both only
 // grow along the rows, so no two meet), and a second kernel adds the slots in a
-// fixed order.
+// fixed order.  16384 rows of 4096, bf16: 89 us forward (6.0 TB/s), 143 backward (5.6);
+// 50021 of 2048 with an fp32 stream: 308 backward (6.0).  One row: 3.7.
 #include <cuda_runtime.h>
 
 #include <algorithm>
