@@ -31,8 +31,9 @@
 // arrives in the producers' place on the barrier that the MMA waits for.
 //
 // Roles (12 warps): 0 TMA of A, 3 TMA of B, 1 MMA, 2 setup (DW: the zeroes),
-// 4-11 epilogue.  Tiles are CG * 128 rows x 256 columns on one CTA or a pair
-// (tcgen05 cta_group::2, half of B in each CTA), two accumulators in turn.
+// 4-11 epilogue.  Tiles are 256 rows x 256 columns on a pair of CTAs (tcgen05
+// cta_group::2, half of B in each CTA), two accumulators in turn; a group's last rows,
+// if they are at most 128, are a tile of half the MMA time.
 //
 // What bounds it.  Many rows a group: the MMAs.  A pair's 256 x 256 tile needs 64 bytes
 // a cycle of each multiprocessor for them, all that one gets from L2, so depth of
@@ -53,7 +54,7 @@
 namespace moe {
 namespace {
 
-constexpr int BN = 256;                     // columns of a tile
+constexpr int BM = 256, BN = 256;           // rows and columns of a tile
 constexpr int MAX_GROUPS = 1024;
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 128 + 32 * EPI_WARPS;
@@ -74,7 +75,6 @@ struct Params {
     int32_t N;                 // FWD, DACT: I; DX, DOWN: H
     int32_t nt;                // column tiles of a row block
     int32_t wrows;             // rows a group's weights would have as an operand like A
-    const uint16_t *h;         // DACT
     uint16_t *out0, *out1;
     int32_t ld0, ld1;
     // DW: product 0 is d_W13 (M = 2I, N = H), 1 is d_W2 (M = H, N = I)
@@ -84,17 +84,16 @@ struct Params {
     int32_t *dev_status;
 };
 
-template <int MODE, int CG>
+template <int MODE>
 struct Cfg {
     // 64-wide slices of K per stage: two at a time load a little faster, one wastes
     // less of a group's last rows (DW, 32768 rows of 64 groups: 645 us a pass, 666 with two)
     // and lets the ring shrink by half as much (DACT)
-    static constexpr int KSUB = CG == 2 && MODE != DW && MODE != DACT ? 2 : 1;
-    // d_act on pairs: h comes by TMA, too, into boxes that take a stage's place
-    static constexpr bool H_BOXES = CG == 2 && MODE == DACT;
-    static constexpr int STAGES = CG == 1 ? 4 : H_BOXES ? 5 : 6 / KSUB;
+    static constexpr int KSUB = MODE != DW && MODE != DACT ? 2 : 1;
+    // DACT: h comes by TMA, too, into boxes that take a stage's place
+    static constexpr int STAGES = MODE == DACT ? 5 : 6 / KSUB;
     static constexpr int A_STAGE = SLICE * KSUB;
-    static constexpr int B_SLICE = BN / CG * 128;
+    static constexpr int B_SLICE = BN / 2 * 128;
     static constexpr int B_STAGE = B_SLICE * KSUB;
     static constexpr int STAGE = A_STAGE + B_STAGE;
     // behind the stages: an output box per epilogue warp (a second one, filled while the
@@ -102,10 +101,10 @@ struct Cfg {
     // against 645 with one), and what follows them, counted from there
     static constexpr int EPI_OFF = STAGES * STAGE;
     static constexpr int BOX_BYTES = EPI_WARPS * EPI_BYTES;
-    static constexpr int H_BYTES = H_BOXES ? 2 * BOX_BYTES : 0;     // gate and up of each warp
+    static constexpr int H_BYTES = MODE == DACT ? 2 * BOX_BYTES : 0;     // gate and up of each warp
     static constexpr int BAR_OFF = 0;
     // full, empty, tail, tfull, tempty, drain, h
-    static constexpr int NBARS = 3 * STAGES + 5 + (H_BOXES ? EPI_WARPS : 0);
+    static constexpr int NBARS = 3 * STAGES + 5 + (MODE == DACT ? EPI_WARPS : 0);
     static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
     static constexpr int OFFS_OFF = MISC_OFF + 16;
     static constexpr int smem(int G) {
@@ -119,30 +118,20 @@ struct Cfg {
     static constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | (A_MN ? 1u << 15 : 0u) |
                                       (B_MN ? 1u << 16 : 0u) |
                                       (static_cast<uint32_t>(BN >> 3) << 17) |
-                                      (static_cast<uint32_t>(CG * 128 >> 4) << 24);
+                                      (static_cast<uint32_t>(256 >> 4) << 24);
     static_assert(smem(MAX_GROUPS) <= 227 * 1024, "shared memory");
     static_assert(STAGE % 1024 == 0 && BOX_BYTES % 1024 == 0, "alignment");
 };
 
 // D (+)= A B^T with the descriptors' low words a and b.
-template <int CG>
 __device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                     uint32_t accumulate) {
-    constexpr uint32_t HI = 0x40004040u;
-    if (CG == 1)
-        asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
-                     "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
-                     "setp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
-                     "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(HI)
-                     : "memory");
-    else
-        asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
-                     "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
-                     "setp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
-                     "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(HI)
-                     : "memory");
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+                 "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(0x40004040u)
+                 : "memory");
 }
 
 __device__ __forceinline__ void tma_store_3d(const void *tmap, const void *src, int c0, int c1,
@@ -171,7 +160,6 @@ struct Tile {
 
 // Row modes: the group offsets and the tiles of the groups before each;
 // returns the number of tiles, -1 for bad offsets.  All threads.
-template <int BMT>
 __device__ int list_tiles(const Params &p, int *s_off, int *s_prefix, volatile int *s_bad) {
     const int tid = threadIdx.x, lane = tid & 31;
     for (int g = tid; g <= p.G; g += THREADS) s_off[g] = p.offsets[g];
@@ -186,7 +174,7 @@ __device__ int list_tiles(const Params &p, int *s_off, int *s_prefix, volatile i
             if (g < p.G) {
                 const int a = s_off[g], b = s_off[g + 1];
                 if (a < 0 || b < a || b > p.n) bad = true;
-                tiles = b > a ? ((b - a + BMT - 1) / BMT) * p.nt : 0;
+                tiles = b > a ? ((b - a + BM - 1) / BM) * p.nt : 0;
             }
             int inc = tiles;
 #pragma unroll
@@ -207,7 +195,7 @@ __device__ int list_tiles(const Params &p, int *s_off, int *s_prefix, volatile i
 // Tiles of a group: rows fastest while the group has fewer rows than its
 // weights, columns fastest otherwise (what is shared is read from L2).  DW: the
 // rows of the gradient fastest, both products of a group one after the other.
-template <int MODE, int BMT, int BNT = BN>
+template <int MODE, int BNT = BN>
 __device__ __forceinline__ Tile decode_tile(const Params &p, int tile, int &g, const int *s_off,
                                             const int *s_prefix) {
     Tile t;
@@ -229,12 +217,12 @@ __device__ __forceinline__ Tile decode_tile(const Params &p, int tile, int &g, c
         const int start = s_off[g], end = s_off[g + 1], cnt = end - start;
         const int local = tile - s_prefix[g];
         const bool nfast = cnt > p.wrows;
-        const int inner = nfast ? p.nt : (cnt + BMT - 1) / BMT;
+        const int inner = nfast ? p.nt : (cnt + BM - 1) / BM;
         const int hi = static_cast<int>(static_cast<unsigned>(local) / static_cast<unsigned>(inner));
         const int lo = local - hi * inner;
         t.g = g;
         t.n_blk = nfast ? lo : hi;
-        t.row0 = start + (nfast ? hi : lo) * BMT;
+        t.row0 = start + (nfast ? hi : lo) * BM;
         t.row_end = end;
         t.prod = t.m0 = t.n0 = 0;
     }
@@ -400,9 +388,10 @@ __device__ __forceinline__ void zero_rows(uint8_t *stage, int blocks, int from, 
     __syncwarp();
 }
 
-template <int MODE, int CG>
-__device__ __forceinline__ void train_gemm(const Params &p) {
-    using C = Cfg<MODE, CG>;
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    train_gemm_kernel(const __grid_constant__ Params p) {
+    using C = Cfg<MODE>;
     constexpr int STAGES = C::STAGES, KSUB = C::KSUB, BK = 64 * KSUB;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -423,19 +412,13 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
     int *s_off = reinterpret_cast<int *>(rest + C::OFFS_OFF);
     int *s_prefix = s_off + p.G + 1;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rank = CG == 2 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int rank = static_cast<int>(cluster_ctarank());
     const bool leader = rank == 0;
-    const int first_tile = static_cast<int>(blockIdx.x) / CG;
-    const int step = static_cast<int>(gridDim.x) / CG;
+    const int first_tile = static_cast<int>(blockIdx.x) / 2, step = static_cast<int>(gridDim.x) / 2;
 
     if (warp == 1) {
-        if (CG == 1) {
-            tmem_alloc(s_tmem, 512);
-            tmem_relinquish();
-        } else {
-            tmem_alloc_pair(s_tmem, 512);
-            tmem_relinquish_pair();
-        }
+        tmem_alloc_pair(s_tmem, 512);
+        tmem_relinquish_pair();
     } else if (warp == 2 && elect_one()) {
         *s_abort = 0;
         for (int s = 0; s < STAGES; ++s) {
@@ -445,25 +428,21 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&tfull[i], 1);
-            mbar_init(&tempty[i], CG * EPI_WARPS);
+            mbar_init(&tempty[i], 2 * EPI_WARPS);
         }
         mbar_init(drain, 1);
-        if (C::H_BOXES)
+        if (MODE == DACT)
             for (int i = 0; i < EPI_WARPS; ++i) mbar_init(&h_full[i], 1);
         fence_barrier_init();
     } else if (warp == 3 && MODE != DW && elect_one()) {
         tma_prefetch_desc(&p.tmA);
         tma_prefetch_desc(&p.tmB);
     }
-    // Up to here nothing but shared and tensor memory is touched: launched as a
-    // programmatic dependent, this part runs while the stream's last kernel ends.
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int total;
     if (MODE == DW) {
         total = load_groups(p, s_off) ? p.G * (p.mt0 * p.nt0 + p.mt1 * p.nt1) : -1;
     } else {
-        total = list_tiles<128 * CG>(p, s_off, s_prefix, s_bad);
+        total = list_tiles(p, s_off, s_prefix, s_bad);
     }
     if (total < 0) {                         // both CTAs of a pair read the same offsets
         if (tid == 0 && blockIdx.x == 0) report(p.dev_status, MOE_DEV_BAD_OFFSETS);
@@ -471,14 +450,14 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
     }
     tc_fence_before();
     __syncthreads();
-    if (CG == 2) cluster_sync_all();         // barriers and TMEM of both CTAs are ready
+    cluster_sync_all();                      // barriers and TMEM of both CTAs are ready
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
     const uint32_t lead_full = mapa_shared(smem_u32(full), 0);
     const uint32_t lead_tempty = mapa_shared(smem_u32(tempty), 0);
     // a pair's tile of at most 128 rows (256 rows a group: forward 204 -> 197 us, backward
     // 455 -> 449, 512: 319 -> 307 and no change)
-    auto is_half = [&](const Tile &t) { return CG == 2 && MODE != DW && t.row_end - t.row0 <= 128; };
+    auto is_half = [&](const Tile &t) { return MODE != DW && t.row_end - t.row0 <= 128; };
     auto kblocks = [&](const Tile &t) {
         return MODE == DW ? (t.row_end - t.row0 + BK - 1) / BK : (p.K + BK - 1) / BK;
     };
@@ -493,26 +472,20 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
             for (int s = 0; s < STAGES; ++s) armed[s] = -1;
             Tails tails;
             auto load2 = [&](void *dst, const CUtensorMap *m, int s, int c0, int c1) {
-                if (CG == 1)
-                    tma_load_2d(dst, m, &full[s], c0, c1);
-                else
-                    tma_load_2d_pair(dst, m, lead_full + 8u * static_cast<uint32_t>(s), c0, c1);
+                tma_load_2d_pair(dst, m, lead_full + 8u * static_cast<uint32_t>(s), c0, c1);
             };
             auto load3 = [&](void *dst, const CUtensorMap *m, int s, int c0, int c1, int c2) {
-                if (CG == 1)
-                    tma_load_3d(dst, m, &full[s], c0, c1, c2);
-                else
-                    tma_load_3d_pair(dst, m, lead_full + 8u * static_cast<uint32_t>(s), c0, c1, c2);
+                tma_load_3d_pair(dst, m, lead_full + 8u * static_cast<uint32_t>(s), c0, c1, c2);
             };
             int g = 0;
             for (int tile = first_tile; tile < total && !*s_abort; tile += step) {
-                const Tile t = decode_tile<MODE, 128 * CG>(p, tile, g, s_off, s_prefix);
+                const Tile t = decode_tile<MODE>(p, tile, g, s_off, s_prefix);
                 const bool half = is_half(t);
                 const CUtensorMap *m = MODE == DW ? &p.tmG[2 * t.prod + (is_a ? 0 : 1)]
                                        : is_a     ? (half ? &p.tmAh : &p.tmA)
                                                   : (half && MODE == FWD ? &p.tmBh : &p.tmB);
                 const int nkb = kblocks(t);
-                const uint32_t tx = CG * (is_a ? C::A_STAGE / (half ? 2 : 1) : C::B_STAGE);
+                const uint32_t tx = 2 * (is_a ? C::A_STAGE / (half ? 2 : 1) : C::B_STAGE);
                 bool ok = true;
                 for (int i = 0; i < nkb; ++i) {
                     const int kb = MODE == DW && has_tail(t) ? (i == 0 ? nkb - 1 : i - 1) : i;
@@ -558,25 +531,21 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                                 load3(dst + s * C::B_SLICE + j * (SLICE / 2), m, stage, k0 + 64 * s,
                                       j * p.N + t.n_blk * 128 + 64 * rank, t.g);
                     } else if (MODE == FWD) {
-                        // gate rows, then the same of up: one half per CTA of a pair
+                        // gate rows in the even CTA, up's in the odd one
 #pragma unroll
                         for (int s = 0; s < KSUB; ++s)
-#pragma unroll
-                            for (int j = 0; j < 2 / CG; ++j)
-                                load3(dst + s * C::B_SLICE + j * SLICE, m, stage, k0 + 64 * s,
-                                      (j + rank) * p.N + t.n_blk * 128, t.g);
+                            load3(dst + s * C::B_SLICE, m, stage, k0 + 64 * s, rank * p.N + t.n_blk * 128,
+                                  t.g);
                     } else if (MODE == DOWN) {
 #pragma unroll
                         for (int s = 0; s < KSUB; ++s)
-#pragma unroll
-                            for (int j = 0; j < 2 / CG; ++j)
-                                load3(dst + s * C::B_SLICE + j * SLICE, m, stage, k0 + 64 * s,
-                                      t.n_blk * BN + 128 * (j + rank), t.g);
+                            load3(dst + s * C::B_SLICE, m, stage, k0 + 64 * s, t.n_blk * BN + 128 * rank,
+                                  t.g);
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 4 / CG; ++j)
-                            load3(dst + j * (64 * BK * 2), m, stage,
-                                  t.n_blk * BN + BN / CG * rank + 64 * j, k0, t.g);
+                        for (int j = 0; j < 2; ++j)
+                            load3(dst + j * (64 * BK * 2), m, stage, t.n_blk * BN + 128 * rank + 64 * j, k0,
+                                  t.g);
                     }
                     if (++stage == STAGES) {
                         stage = 0;
@@ -597,7 +566,7 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
         int stage = 0, g = 0;
         Tails tails;
         for (int tile = first_tile; tile < total; tile += step) {
-            const Tile t = decode_tile<MODE, 128 * CG>(p, tile, g, s_off, s_prefix);
+            const Tile t = decode_tile<MODE>(p, tile, g, s_off, s_prefix);
             const int nkb = kblocks(t);
             if (has_tail(t)) {                       // a tile's first stage
                 if (!wait_phase(&tail[stage], tails.take(stage), s_abort, p.dev_status)) break;
@@ -615,7 +584,7 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
             bool issued = false;
             int g = 0;
             for (int tile = first_tile; tile < total && !*s_abort; tile += step) {
-                const Tile t = decode_tile<MODE, 128 * CG>(p, tile, g, s_off, s_prefix);
+                const Tile t = decode_tile<MODE>(p, tile, g, s_off, s_prefix);
                 const int nkb = kblocks(t);
                 // DW: the 16-row steps of the last slice that hold rows of the group
                 const int last =
@@ -655,30 +624,21 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                         const uint32_t ka = C::A_MN ? s * 128 : s / 4 * (SLICE / 16) + s % 4 * 2;
                         const uint32_t kbb =
                             C::B_MN ? s * 128 : s / 4 * (C::B_SLICE / 16) + s % 4 * 2;
-                        mma<CG>(d, a + ka, b + kbb, idesc, (i | s) != 0 ? 1u : 0u);
+                        mma(d, a + ka, b + kbb, idesc, (i | s) != 0 ? 1u : 0u);
                     }
                     issued = true;
-                    if (CG == 1)
-                        tc_commit(&empty[st]);
-                    else
-                        tc_commit_pair_mc(&empty[st], 0x3);
+                    tc_commit_pair_mc(&empty[st], 0x3);
                 }
                 if (!ok) break;
                 stage += nkb;
                 phase ^= static_cast<uint32_t>(stage / STAGES) & 1u;
                 stage %= STAGES;
-                if (CG == 1)
-                    tc_commit(&tfull[u & 1]);
-                else
-                    tc_commit_pair_mc(&tfull[u & 1], 0x3);
+                tc_commit_pair_mc(&tfull[u & 1], 0x3);
                 ++u;
             }
             if (*s_abort && issued) {
                 // unwinding: every MMA issued so far ends before TMEM is freed
-                if (CG == 1)
-                    tc_commit(drain);
-                else
-                    tc_commit_pair_mc(drain, 0x1);
+                tc_commit_pair_mc(drain, 0x1);
                 mbar_wait_drain(drain, 0);
             }
         }
@@ -694,7 +654,7 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
         int g = 0;
         uint32_t u = 0;
         for (int tile = first_tile; tile < total; tile += step) {
-            const Tile t = decode_tile<MODE, 128 * CG>(p, tile, g, s_off, s_prefix);
+            const Tile t = decode_tile<MODE>(p, tile, g, s_off, s_prefix);
             // half tiles: 64 rows a CTA, N's lower 128 columns in lanes 0-63 and its upper
             // ones, of the same rows, in lanes 64-127
             const bool half = is_half(t);
@@ -706,31 +666,18 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
             const bool boxed = row0 + 32 <= t.row_end;
             const uint32_t acc = tmem + lanes + (u & 1) * BN;
             // DACT: 32 columns of gate and up of h, fetched one step ahead (the first while the
-            // tile is still computed): on pairs by TMA into the warp's own boxes, which costs
-            // the other roles nothing (loads of a row per lane keep their instructions
-            // waiting), else this lane's row into registers
-            uint4 h8[8];
-            // (rows behind the group: its last one again, so that the warp stays together)
-            const uint16_t *h_row = MODE == DACT && !C::H_BOXES
-                                        ? p.h + static_cast<int64_t>(min(row0 + lane, t.row_end - 1)) * (2 * p.N)
-                                        : nullptr;
+            // tile is still computed) by TMA into the warp's own boxes.  Loads of a row per
+            // lane keep the other roles' instructions waiting: 1,364 cycles a slice of 128
+            // against 1,238 (131072 rows of H = 4096, I = 2048).
             auto fetch_h = [&](int c) {
                 const int col = t.n_blk * BN + 128 * hq + c;
                 if (col >= p.N) return;
-                if (C::H_BOXES) {
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(&h_full[warp - 4], 2 * EPI_BYTES);
-                        tma_load_2d(h_box, &p.tmH, &h_full[warp - 4], col, row0);
-                        tma_load_2d(h_box + EPI_BYTES, &p.tmH, &h_full[warp - 4], p.N + col, row0);
-                    }
-                    h_pending = true;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        h8[j] = __ldg(reinterpret_cast<const uint4 *>(h_row + col) + j);
-                        h8[4 + j] = __ldg(reinterpret_cast<const uint4 *>(h_row + p.N + col) + j);
-                    }
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&h_full[warp - 4], 2 * EPI_BYTES);
+                    tma_load_2d(h_box, &p.tmH, &h_full[warp - 4], col, row0);
+                    tma_load_2d(h_box + EPI_BYTES, &p.tmH, &h_full[warp - 4], p.N + col, row0);
                 }
+                h_pending = true;
             };
             if (MODE == DACT) fetch_h(span * part);
             if (!wait_phase(&tfull[u & 1], (u >> 1) & 1, s_abort, p.dev_status)) break;
@@ -750,32 +697,25 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
                 for (int c = span * part; c < span * (part + 1); c += 32) {
                     const int col = t.n_blk * BN + 128 * hq + c;
                     if (col >= p.N) break;               // N = 128 mod 256: no such columns
-                    uint32_t hg[16], hu[16];
-                    if (C::H_BOXES) {
-                        if (!wait_phase(&h_full[warp - 4], h_phase, s_abort, p.dev_status)) {
-                            lost = true;
-                            break;
-                        }
-                        h_phase ^= 1;
-                        h_pending = false;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int at = lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4);
-                            h8[j] = *reinterpret_cast<const uint4 *>(h_box + at);
-                            h8[4 + j] = *reinterpret_cast<const uint4 *>(h_box + EPI_BYTES + at);
-                        }
-                        // the reads are over before the next ones land there (a barrier of the
-                        // warp alone lets them wait in line behind its stores of single rows)
-                        fence_proxy_async();
-                        __syncwarp();
+                    if (!wait_phase(&h_full[warp - 4], h_phase, s_abort, p.dev_status)) {
+                        lost = true;
+                        break;
                     }
+                    h_phase ^= 1;
+                    h_pending = false;
+                    uint32_t hg[16], hu[16];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        hg[4 * j] = h8[j].x, hg[4 * j + 1] = h8[j].y;
-                        hg[4 * j + 2] = h8[j].z, hg[4 * j + 3] = h8[j].w;
-                        hu[4 * j] = h8[4 + j].x, hu[4 * j + 1] = h8[4 + j].y;
-                        hu[4 * j + 2] = h8[4 + j].z, hu[4 * j + 3] = h8[4 + j].w;
+                        const int at = lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4);
+                        const uint4 g4 = *reinterpret_cast<const uint4 *>(h_box + at);
+                        const uint4 u4 = *reinterpret_cast<const uint4 *>(h_box + EPI_BYTES + at);
+                        hg[4 * j] = g4.x, hg[4 * j + 1] = g4.y, hg[4 * j + 2] = g4.z, hg[4 * j + 3] = g4.w;
+                        hu[4 * j] = u4.x, hu[4 * j + 1] = u4.y, hu[4 * j + 2] = u4.z, hu[4 * j + 3] = u4.w;
                     }
+                    // the reads are over before the next ones land there (a barrier of the
+                    // warp alone lets them wait in line behind its stores of single rows)
+                    fence_proxy_async();
+                    __syncwarp();
                     if (c + 32 < span * (part + 1)) fetch_h(c + 32);
                     float d[32];
                     __syncwarp();
@@ -822,31 +762,23 @@ __device__ __forceinline__ void train_gemm(const Params &p) {
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                // CG = 1: as an ordinary arrival.  One through the cluster's window could be on
-                // its way when this CTA, for which no peer waits, has left.
-                if (CG == 1)
-                    mbar_arrive(&tempty[u & 1]);
-                else
-                    arrive_drained(lead_tempty + 8u * (u & 1));
-            }
+            if (lane == 0) arrive_drained(lead_tempty + 8u * (u & 1));
             ++u;
         }
-        if (C::H_BOXES && h_pending) mbar_wait_drain(&h_full[warp - 4], h_phase);    // unwinding
+        if (MODE == DACT && h_pending) mbar_wait_drain(&h_full[warp - 4], h_phase);    // unwinding
         if (lane == 0) bulk_wait<0>();       // every output box written
         __syncwarp();
     }
 
     tc_fence_before();
     __syncthreads();
-    if (CG == 2) cluster_sync_all();     // no CTA leaves while its peer may still signal or read it
+    cluster_sync_all();                  // no CTA leaves while its peer may still signal or read it
     if (warp == 1) {
         tc_fence_after();
-        if (CG == 1)
-            tmem_dealloc(tmem, 512);
-        else
-            tmem_dealloc_pair(tmem, 512);
+        tmem_dealloc_pair(tmem, 512);
     }
+    __syncwarp();
+    cluster_sync_all();                  // nor before both have given their tensor memory back
 }
 
 // ------------------------------------------------------------------ wide tiles
@@ -867,7 +799,7 @@ constexpr int W_STAGE = SLICE + W_B;
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     gradient_wide_kernel(const __grid_constant__ Params p) {
-    using C = Cfg<DW, 2>;
+    using C = Cfg<DW>;
     static_assert(W_STAGES * W_STAGE == C::EPI_OFF && W_STAGES <= C::STAGES, "shared memory");
     constexpr int BK = 64;
     constexpr uint32_t MN_LO = static_cast<uint32_t>(64 * 128 / 16) << 16;
@@ -906,8 +838,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         mbar_init(drain, 1);
         fence_barrier_init();
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int total = load_groups(p, s_off) ? p.G * (p.mt0 * p.nt0 + p.mt1 * p.nt1) : -1;
     if (total < 0) {                         // both CTAs of a pair read the same offsets
         if (tid == 0 && blockIdx.x == 0) report(p.dev_status, MOE_DEV_BAD_OFFSETS);
@@ -933,7 +863,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             Tails tails;
             int g = 0;
             for (int tile = first_tile; tile < total && !*s_abort; tile += step) {
-                const Tile t = decode_tile<DW, 256, BW>(p, tile, g, s_off, nullptr);
+                const Tile t = decode_tile<DW, BW>(p, tile, g, s_off, nullptr);
                 const int nkb = slices(t);
                 const CUtensorMap *m = &p.tmG[2 * t.prod + (is_a ? 0 : 1)];
                 bool ok = true;
@@ -981,7 +911,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         int stage = 0, g = 0;
         Tails tails;
         for (int tile = first_tile; tile < total; tile += step) {
-            const Tile t = decode_tile<DW, 256, BW>(p, tile, g, s_off, nullptr);
+            const Tile t = decode_tile<DW, BW>(p, tile, g, s_off, nullptr);
             const int nkb = slices(t);
             if (nkb == 0) continue;
             stage = (stage + nkb - 1) % W_STAGES;
@@ -1000,7 +930,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             const uint32_t base = smem_u32(smem) >> 4;
             bool issued = false;
             for (int tile = first_tile; tile < total && !*s_abort; tile += step) {
-                const Tile t = decode_tile<DW, 256, BW>(p, tile, g, s_off, nullptr);
+                const Tile t = decode_tile<DW, BW>(p, tile, g, s_off, nullptr);
                 const int nkb = slices(t);
                 // the 16-row steps of the last slice that hold rows of the group
                 const int last = (t.row_end - t.row0 - (nkb - 1) * BK + 15) / 16;
@@ -1013,7 +943,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         if (k >= steps) break;
-                        mma<2>(tmem + 256u * static_cast<uint32_t>(h), a + k * 128, b + k * 128, C::IDESC,
+                        mma(tmem + 256u * static_cast<uint32_t>(h), a + k * 128, b + k * 128, C::IDESC,
                                (kb | k) != 0 ? 1u : 0u);
                     }
                 };
@@ -1092,7 +1022,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         int g = 0;
         uint32_t tph = 0;
         for (int tile = first_tile; tile < total; tile += step) {
-            const Tile t = decode_tile<DW, 256, BW>(p, tile, g, s_off, nullptr);
+            const Tile t = decode_tile<DW, BW>(p, tile, g, s_off, nullptr);
             const int row0 = t.m0 + 128 * rank + 32 * quarter;
             const uint32_t tq = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
             bool stop = false;
@@ -1124,16 +1054,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         tc_fence_after();
         tmem_dealloc_pair(tmem, 512);
     }
-}
-
-template <int MODE>
-__global__ void __launch_bounds__(THREADS, 1) train_gemm_kernel(const __grid_constant__ Params p) {
-    train_gemm<MODE, 1>(p);
-}
-template <int MODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
-    train_gemm_pair_kernel(const __grid_constant__ Params p) {
-    train_gemm<MODE, 2>(p);
+    __syncwarp();
+    cluster_sync_all();                  // nor before both have given their tensor memory back
 }
 
 // ------------------------------------------------------------------ host side
@@ -1185,12 +1107,6 @@ bool out_map(CUtensorMap *m, void *ptr, int groups, int64_t rows, int64_t cols, 
               CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Row products: pairs where groups have a 128-row block or more on average.  Measured
-// as above (forward and backward pass, us, one CTA against a pair): 64 rows a group
-// 146 : 146 and 298 : 297, 128 158 : 156 and 358 : 349, 256 214 : 197 and 475 : 449.  Below,
-// a pair's tile would load 256 rows for a group's few.
-bool use_pair(int n, int G) { return n >= 128ll * G; }
-
 // DW in wide tiles: with few rows a group, where the gradients' stores decide and
 // fewer hand-overs help, and with very many.  Measured with H = 2048, I = 1024 and 64
 // groups (whole backward pass, us, 256 against 512 columns): 16 rows a group 296 : 280,
@@ -1198,42 +1114,32 @@ bool use_pair(int n, int G) { return n >= 128ll * G; }
 // 2252 : 2278; 16384 rows of H = 4096, I = 2048: one group 1030 : 1006, two 1028 : 1022.
 bool wide_gradient(int n, int G) { return n < 192ll * G || n >= 8192ll * G; }
 
-// CG = 1, 2: the 256-column kernels; 3: the wide one.
-template <int MODE, int CG>
-cudaError_t launch(Params &p, int64_t tiles, cudaStream_t stream) {
-    constexpr int PAIR = CG == 1 ? 1 : 2;
-    using C = Cfg<MODE, PAIR>;
-    void (*kernel)(const Params);
-    if constexpr (CG == 3)          // DW only
-        kernel = gradient_wide_kernel;
-    else if constexpr (CG == 2)
-        kernel = train_gemm_pair_kernel<MODE>;
-    else
-        kernel = train_gemm_kernel<MODE>;
+template <int MODE, bool WIDE = false>
+cudaError_t launch(const Params &p, int64_t tiles, cudaStream_t stream) {
+    void (*kernel)(const Params) = train_gemm_kernel<MODE>;
+    if (WIDE) kernel = gradient_wide_kernel;                 // DW only
     static std::mutex mu;
-    static int resident[64] = {};        // CTAs or pairs that can run at once, by device
+    static int resident[64] = {};        // pairs that can run at once, by device
     int dev = 0;
     cudaGetDevice(&dev);
-    int limit = num_sms() / PAIR;
+    int limit = num_sms() / 2;
     {
         std::lock_guard<std::mutex> lock(mu);
         if (dev >= 64 || resident[dev] == 0) {
             const cudaError_t e = cudaFuncSetAttribute(
                 kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
             if (e != cudaSuccess) return e;
-            if (PAIR == 2) {
-                cudaLaunchConfig_t cfg = {};
-                cfg.gridDim = dim3(static_cast<unsigned>(num_sms()), 1, 1);
-                cfg.blockDim = dim3(THREADS, 1, 1);
-                cfg.dynamicSmemBytes = 227 * 1024;
-                cfg.stream = stream;
-                int n = 0;
-                if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
-                    cudaGetLastError();
-                    n = limit;
-                }
-                limit = std::min(n, limit);
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(static_cast<unsigned>(num_sms()), 1, 1);
+            cfg.blockDim = dim3(THREADS, 1, 1);
+            cfg.dynamicSmemBytes = 227 * 1024;
+            cfg.stream = stream;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
+                cudaGetLastError();
+                n = limit;
             }
+            limit = std::min(n, limit);
             if (dev < 64) resident[dev] = limit;
         } else {
             limit = resident[dev];
@@ -1241,34 +1147,28 @@ cudaError_t launch(Params &p, int64_t tiles, cudaStream_t stream) {
     }
     const int64_t units = std::max<int64_t>(1, std::min<int64_t>(limit, tiles));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(PAIR * units), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * units), 1, 1);
     cfg.blockDim = dim3(THREADS, 1, 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>(C::smem(p.G));
+    cfg.dynamicSmemBytes = static_cast<size_t>(Cfg<MODE>::smem(p.G));
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 // All but DW: A [n, K], B as the mode's weights.
 template <int MODE>
 cudaError_t launch_rows(Params &p, const void *a, const void *w, cudaStream_t stream) {
-    const bool pair = use_pair(p.n, p.G);
     constexpr bool K_MAJOR = MODE == FWD || MODE == DOWN;                           // the weights
     const int64_t brows = MODE == FWD ? 2 * static_cast<int64_t>(p.N) : K_MAJOR ? p.N : p.K;
     const int bcols = K_MAJOR ? p.K : p.N;
     // rows of B's box: 128 weight rows, or a stage's K
-    const int box = K_MAJOR ? 128 : 64 * (pair ? Cfg<MODE, 2>::KSUB : 1);
+    const int box = K_MAJOR ? 128 : 64 * Cfg<MODE>::KSUB;
     if (!operand_map(&p.tmA, a, 0, p.n, p.K, 128) || !operand_map(&p.tmB, w, p.G, brows, bcols, box) ||
         !operand_map(&p.tmAh, a, 0, p.n, p.K, 64) ||
         (MODE == FWD && !operand_map(&p.tmBh, w, p.G, brows, bcols, 64)))
         return cudaErrorInvalidValue;
     p.nt = static_cast<int>(ceil_div(p.N, MODE == FWD ? 128 : 256));
-    const int64_t tiles = (static_cast<int64_t>(p.n / (pair ? 256 : 128)) + std::min(p.G, p.n)) * p.nt;
-    return pair ? launch<MODE, 2>(p, tiles, stream) : launch<MODE, 1>(p, tiles, stream);
+    const int64_t tiles = (static_cast<int64_t>(p.n / BM) + std::min(p.G, p.n)) * p.nt;
+    return launch<MODE>(p, tiles, stream);
 }
 
 inline bool a16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -1409,7 +1309,6 @@ extern "C" moe_status_t moe_grouped_mlp_backward(
     p.K = H;
     p.N = I;
     p.wrows = I;
-    p.h = h;
     p.out0 = d_h;
     p.ld0 = 2 * I;
     p.out1 = act;
@@ -1439,7 +1338,7 @@ extern "C" moe_status_t moe_grouped_mlp_backward(
         p.accumulate = add;
         const int64_t tiles =
             static_cast<int64_t>(G) * (p.mt0 * p.nt0 + static_cast<int64_t>(p.mt1) * p.nt1);
-        TRY_CUDA((bn == BW ? launch<DW, 3>(p, tiles, s) : launch<DW, 2>(p, tiles, s)));
+        TRY_CUDA((bn == BW ? launch<DW, true>(p, tiles, s) : launch<DW>(p, tiles, s)));
     }
     return MOE_OK;
 }
