@@ -38,10 +38,10 @@
 // What bounds it.  Many rows a group: the MMAs.  A pair's 256 x 256 tile needs 64 bytes
 // a cycle of each multiprocessor for them, all that one gets from L2, so depth of
 // the operands' ring and little else on that way decide.  131072 rows of 64 groups, H = 4096,
-// I = 2048: forward 3.45-3.75 ms (0.94-0.96 of the MMAs' rate), backward 7.0-7.8 (DX 0.96,
-// DW 0.89, DACT 0.83), 8.3 in a loop under the power cap; the flops' floors are 3.5 and
-// 7.0.  Few rows: the weights and their gradients; 509 rows, H = 2048, I = 1024: backward 246
-// us, the bytes' floor 218.  Between, both at once: 32768 rows 644 us, floors 311 and 438.
+// I = 2048: forward 3.5-3.75 ms (0.94-0.96 of the MMAs' rate), backward 7.2-7.9 (DX 0.96,
+// DW 0.89, DACT 0.83), 8.5 in a loop under the power cap; the flops' floors are 3.5 and
+// 7.0.  Few rows: the weights and their gradients; 509 rows, H = 2048, I = 1024: backward 250
+// us, the bytes' floor 218.  Between, both at once: 32768 rows 647 us, floors 311 and 438.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
