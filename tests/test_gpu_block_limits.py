@@ -258,3 +258,17 @@ def test_ragged_groups_again(H, I):
         got = moe.grouped_mlp_backward(d_y, x, off, h, w13, w2)
         assert torch.equal(h, h1) and torch.equal(y, y1)
         assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_rows_in_front_of_the_first_group():
+    """Offsets may start behind row 0; what the rows in front hold enters nothing."""
+    x, off, w13, w2, d_y = mlp.make([37, 0, 300, 5], 256, 384, 4)
+    h, y = moe.grouped_mlp_train(x, off, w13, w2)
+    want = moe.grouped_mlp_backward(d_y, x, off, h, w13, w2)
+    nan = torch.full((21, 768), float("nan"), dtype=torch.bfloat16, device=DEV)
+    front = lambda t: torch.cat((nan[:, :t.shape[1]], t))                  # noqa: E731
+    off2 = off + 21
+    h2, y2 = moe.grouped_mlp_train(front(x), off2, w13, w2)
+    got = moe.grouped_mlp_backward(front(d_y), front(x), off2, front(h), w13, w2)
+    assert torch.equal(h2[21:], h) and torch.equal(y2[21:], y) and torch.equal(got[0][21:], want[0])
+    assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
