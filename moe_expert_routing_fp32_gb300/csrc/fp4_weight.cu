@@ -661,8 +661,12 @@ __global__ void __launch_bounds__(THREADS, 1) weight_kernel(const __grid_constan
             for (int j = 0; j < TOK; ++j) {
                 if (j >= t.cnt) break;
                 const int row = t.row0 + j;
+                // The exponent of the weights first: a sum of digits lies within 2^-52 and
+                // 2^42 (NV; alpha is 1 for MX), so alpha's 2^60 either way leaves it in fp32's
+                // range, whatever the row.  The row's own power of two first would not: 2^118
+                // times such a sum is infinite where a small alpha makes it 1e20.
                 const float f = fabsf(scale[j]);
-                float a = v[0][j] * f * p.alpha, b = v[1][j] * f * p.alpha;
+                float a = v[0][j] * p.alpha * f, b = v[1][j] * p.alpha * f;
                 if (scale[j] < 0.0f) {
                     a += odd_terms<FMT>(p, row, w0) * p.alpha;
                     if (second) b += odd_terms<FMT>(p, row, w0 + (SWIGLU ? p.N : 128)) * p.alpha;
