@@ -453,7 +453,9 @@ __global__ void __launch_bounds__(THREADS, VPT <= 2 ? 2 : 1) norm_kernel(const _
                 if (keep) store8<false>(xo, v, f);
             }
         } else {
-            const f2 c2 = splat(p.post ? -k_post * k_post * (sums.x * inv_h) : 0.0f);
+            // (no zero of c2 in front of y without that norm: infinities and NaN of y would
+            // make NaN of a gradient that holds no y)
+            const f2 c2 = splat(-k_post * k_post * (sums.x * inv_h));
             uint8_t *yo = static_cast<uint8_t *>(p.out1) + static_cast<int64_t>(row) * p.H * (YF ? 4 : 2);
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
@@ -467,7 +469,7 @@ __global__ void __launch_bounds__(THREADS, VPT <= 2 ? 2 : 1) norm_kernel(const _
                     widen(yq[YF ? 0 : j], y);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) y[i] = fma2(y[i], c2, keep_q[j][i]);
+                for (int i = 0; i < 4; ++i) y[i] = p.post ? fma2(y[i], c2, keep_q[j][i]) : keep_q[j][i];
                 if (keep && p.out1) store8<YF>(yo, v, y);
             }
         }
