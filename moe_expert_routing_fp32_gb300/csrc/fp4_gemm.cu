@@ -596,6 +596,12 @@ __device__ __forceinline__ void fp4_gemm(const Params &p) {
         else
             tmem_dealloc_pair(tmem, TMEM_COLS);
     }
+    if (CG == 2) {
+        // ... nor before both have given their tensor memory back: the next kernel in the
+        // stream may be one of lone CTAs that is only waiting for a place to allocate its own
+        __syncwarp();
+        cluster_sync_all();
+    }
 }
 
 template <int FMT, int MODE>

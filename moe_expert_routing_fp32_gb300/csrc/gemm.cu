@@ -976,6 +976,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         tc_fence_after();
         tmem_dealloc_pair(tmem_base, TMEM2_COLS);
     }
+    __syncwarp();
+    cluster_sync_all();          // nor before both have given their tensor memory back
 }
 
 // ------------------------------------------------------------------ wide CTA-pair kernel
@@ -1617,11 +1619,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GATHER ? W_THREADS_G
 
     tc_fence_before();
     __syncthreads();
-    cluster_sync_all();
+    cluster_sync_all();          // no CTA leaves while its peer may still signal or read it
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc_pair(tmem_base, TMEM2_COLS);
     }
+    __syncwarp();
+    cluster_sync_all();          // nor before both have given their tensor memory back
 }
 
 // ------------------------------------------------------------------ host side
