@@ -348,6 +348,21 @@ __device__ __noinline__ float odd_terms(const Params &p, int row, int64_t wr) {
     return s;
 }
 
+// Whether a wait succeeded in every thread of the epilogue's four warps, which share
+// barrier 1: they go on or leave their loop together.  A warp that gave up alone would
+// leave the others at a barrier that it never reaches.
+__device__ __forceinline__ bool all_warps(bool ok) {
+    uint32_t all;
+    __syncwarp();
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"(ok ? 1u : 0u)
+        : "memory");
+    return all != 0;
+}
+
 template <int FMT, bool SWIGLU>
 __global__ void __launch_bounds__(THREADS, 1) weight_kernel(const __grid_constant__ Params p) {
     using C = Cfg<FMT>;
@@ -600,7 +615,7 @@ __global__ void __launch_bounds__(THREADS, 1) weight_kernel(const __grid_constan
                     load_parts(c0);
                 }
             }
-            if (!wait_phase(&tfull[n & 1], (n >> 1) & 1, s_abort, p.dev_status)) break;
+            if (!all_warps(wait_phase(&tfull[n & 1], (n >> 1) & 1, s_abort, p.dev_status))) break;
             tc_fence_after();
             float v[2][TOK];
 #pragma unroll
