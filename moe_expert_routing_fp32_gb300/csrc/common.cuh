@@ -217,6 +217,11 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volat
     return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort, dev_status);
 }
 
+// The outcome of a wait for a whole warp, whose lanes each poll by themselves: a
+// lane that gave up must not leave the others to instructions that take all of them
+// (tensor memory loads, shuffles, __syncwarp).
+__device__ __forceinline__ bool whole_warp(bool ok) { return __all_sync(0xffffffffu, ok); }
+
 __device__ __forceinline__ void fence_barrier_init() {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }

@@ -502,7 +502,7 @@ __device__ __forceinline__ void fp4_gemm(const Params &p) {
         uint32_t u = 0;
         // both 32-column parts of this warp's share of half tile u, and release it
         auto drain_half = [&](float (&x)[32], float (&y)[32]) -> bool {
-            if (!wait_acc(tfull, u, false, s_abort, p.dev_status)) return false;
+            if (!whole_warp(wait_acc(tfull, u, false, s_abort, p.dev_status))) return false;
             tc_fence_after();
             const uint32_t taddr = tmem + lanes + (u % NACC) * HN + static_cast<uint32_t>(c0);
             __syncwarp();

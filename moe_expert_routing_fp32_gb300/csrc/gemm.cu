@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_gemm_kernel(const __grid_c
         uint32_t acc_phase = 0;
         for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
             const Tile t = decode_tile(p, tile, s_off, s_prefix, total0);
-            if (!mbar_wait_bounded(&tfull[acc], acc_phase, s_abort, p.dev_status)) break;
+            if (!whole_warp(mbar_wait_bounded(&tfull[acc], acc_phase, s_abort, p.dev_status))) break;
             tc_fence_after();
             const int row = t.row0 + row_in_tile;
             const bool ok = row < t.row_end;
@@ -861,7 +861,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             }
             if (!got || tile >= total) break;
             const Tile t = decode_tile_pair(p, tile, s_off, s_prefix, total0);
-            if (!mbar_wait_bounded(&tfull[acc], acc_phase, s_abort, p.dev_status)) break;
+            if (!whole_warp(mbar_wait_bounded(&tfull[acc], acc_phase, s_abort, p.dev_status))) break;
             tc_fence_after();
             // full tile: this CTA's 128 rows, warp quadrant q = rows 32q..;
             // half tile: this CTA's 64 rows, quadrant q = rows 32(q & 1).. of
@@ -1428,7 +1428,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GATHER ? W_THREADS_G
             const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
             bool stop = false;
             for (int h = 0; h < 2; ++h) {
-                if (!mbar_wait_bounded(&tfull[h], tph, s_abort, p.dev_status)) {
+                if (!whole_warp(mbar_wait_bounded(&tfull[h], tph, s_abort, p.dev_status))) {
                     stop = true;
                     break;
                 }

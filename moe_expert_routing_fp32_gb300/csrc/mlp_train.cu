@@ -569,7 +569,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             const Tile t = decode_tile<MODE>(p, tile, g, s_off, s_prefix);
             const int nkb = kblocks(t);
             if (has_tail(t)) {                       // a tile's first stage
-                if (!wait_phase(&tail[stage], tails.take(stage), s_abort, p.dev_status)) break;
+                if (!whole_warp(wait_phase(&tail[stage], tails.take(stage), s_abort, p.dev_status))) break;
                 zero_rows(smem + stage * C::STAGE, C::STAGE / (64 * 128), t.row_end - t.row0 - (nkb - 1) * BK, lane);
                 if (lane == 0) mbar_arrive_cluster(lead_full + 8u * static_cast<uint32_t>(stage));
             }
@@ -680,7 +680,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 h_pending = true;
             };
             if (MODE == DACT) fetch_h(span * part);
-            if (!wait_phase(&tfull[u & 1], (u >> 1) & 1, s_abort, p.dev_status)) break;
+            if (!whole_warp(wait_phase(&tfull[u & 1], (u >> 1) & 1, s_abort, p.dev_status))) break;
             tc_fence_after();
             if (MODE == FWD) {
                 // columns [0, span) gate, [span, 2 span) up; this warp takes half of each
@@ -697,7 +697,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 for (int c = span * part; c < span * (part + 1); c += 32) {
                     const int col = t.n_blk * BN + 128 * hq + c;
                     if (col >= p.N) break;               // N = 128 mod 256: no such columns
-                    if (!wait_phase(&h_full[warp - 4], h_phase, s_abort, p.dev_status)) {
+                    if (!whole_warp(wait_phase(&h_full[warp - 4], h_phase, s_abort, p.dev_status))) {
                         lost = true;
                         break;
                     }
@@ -916,7 +916,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             if (nkb == 0) continue;
             stage = (stage + nkb - 1) % W_STAGES;
             if (has_tail(t)) {
-                if (!wait_phase(&tail[stage], tails.take(stage), s_abort, p.dev_status)) break;
+                if (!whole_warp(wait_phase(&tail[stage], tails.take(stage), s_abort, p.dev_status))) break;
                 zero_rows(smem + stage * W_STAGE, W_STAGE / (64 * 128), t.row_end - t.row0 - (nkb - 1) * BK, lane);
                 if (lane == 0) mbar_arrive_cluster(lead_full + 8u * static_cast<uint32_t>(stage));
             }
@@ -1027,7 +1027,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             const uint32_t tq = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
             bool stop = false;
             for (int h = 0; h < 2; ++h) {
-                if (!wait_phase(&tfull[h], tph, s_abort, p.dev_status)) {
+                if (!whole_warp(wait_phase(&tfull[h], tph, s_abort, p.dev_status))) {
                     stop = true;
                     break;
                 }
