@@ -664,10 +664,12 @@ moe_status_t moe_fp4_grouped_mlp(const moe_fp4_t *expanded_x, const int32_t *off
  * is the faster form.
  * Rounding: a row is written exactly in 4-bit digits, 36 bits below the largest
  * magnitude of its block (32 columns, MX; 16, NV): values down to 2^-27 of it are
- * exact, smaller ones off by 2^-35 of it at most (and none by more than 2^-96,
+ * exact, smaller ones off by 2^-35 of it at most (and none by more than 2^-95,
  * MX, or 2^-52, NV, of the row's largest).  Products are exact, sums fp32.
- * Weights' magnitudes stay below 2^90.  Infinities and NaN in a row and NaN
- * scales give what the products give; a row that holds any takes much longer.
+ * Weights' magnitudes stay below 2^90, and times K below 2^105; with MX weights
+ * products below 2^-147 of the row's largest magnitude may count as zero.
+ * Infinities and NaN in a row and NaN scales give what the products give; a row
+ * that holds any takes much longer.
  * Rows past offsets[G] are left untouched.  K, N, I multiples of 128, at most
  * 2^20, G <= 1024.  Bad offsets set MOE_DEV_BAD_OFFSETS and no result is written
  * then.  Results do not depend on the launch.
