@@ -609,12 +609,20 @@ def grouped_mlp_backward(d_y, expanded_x, offsets, h, w13, w2, need=("x", "w13",
 
 
 # ------------------------------------------------- between two blocks
+def _fits(name, *sizes):
+    """Refuses sizes beyond int32, of which ctypes would pass the low 32 bits on:
+    2^32 rows of 8 columns fit the card."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise MoeError(name, 2)
+
+
 def _norm_args(y, res, name, gamma_post, gate, gamma_next, seq_offsets, post_norm, next_norm):
     """(T, H, S, flags, device, the four addresses) of norm_residual's
     arguments; ``res`` has the residual stream's type."""
     if y.dim() != 2:
         raise ValueError("rows [T, H]")
     T, H = y.shape
+    _fits("norm_residual", T, H)
     dev = y.device
     flags = (RES_F32 if _bf16_or_f32(res, name) == torch.float32 else 0) | \
         (Y_F32 if _bf16_or_f32(y, "y") == torch.float32 else 0) | (POST_NORM if post_norm else 0)
@@ -629,6 +637,7 @@ def _norm_args(y, res, name, gamma_post, gate, gamma_next, seq_offsets, post_nor
         S = seq_offsets.numel() - 1 if seq_offsets is not None else 1
         if S < 1:
             raise ValueError("seq_offsets: [S + 1] with S >= 1")
+        _fits("norm_residual", S)
         gt = _arg(gate, torch.bfloat16, dev, (S, H), "gate")
         seq = _arg(seq_offsets, torch.int32, dev, (S + 1,), "seq_offsets")
     return T, H, S, flags, dev, (gp, gt, seq, gn)
@@ -660,6 +669,7 @@ def norm_residual(x, y, gamma_post=None, gate=None, scale=1.0, gamma_next=None, 
 
 @functools.lru_cache(maxsize=256)
 def norm_residual_backward_workspace_size(T, H, S=1) -> int:
+    _fits("moe_norm_residual_backward_workspace_size", T, H, S)
     b = ctypes.c_size_t(0)
     _call("moe_norm_residual_backward_workspace_size", T, H, S, ctypes.byref(b))
     return b.value
