@@ -649,9 +649,11 @@ def norm_residual(x, y, gamma_post=None, gate=None, scale=1.0, gamma_next=None, 
     RMSNorm(r).  ``x`` is the residual stream (bf16 or fp32 [T, H]), ``y`` the
     block's output (bf16 or fp32), ``gate`` [S, H] bf16 one row per sequence of
     ``seq_offsets`` (int32 [S+1]; without them one sequence of all tokens).
+    ``seq_offsets`` say which gate a row takes and are ignored without one: every
+    row then counts, in the gammas' gradients too.
     -> dict(r like x, xn bf16 or None, rstd_post, rstd_next fp32 [T] or None);
-    norm_residual_backward takes the dict.  Rows outside every sequence are not
-    set."""
+    norm_residual_backward takes the dict.  Rows outside every sequence of a gate
+    are not set."""
     T, H, S, flags, dev, (gp, gt, seq, gn) = _norm_args(y, x, "x", gamma_post, gate, gamma_next,
                                                         seq_offsets, post_norm, next_norm)
     xp = _arg(x, x.dtype, dev, (T, H), "x")
@@ -682,7 +684,7 @@ def norm_residual_backward(d_r, d_xn, y, saved, gamma_post=None, gate=None, scal
     forward pass returned (``saved``: r, rstd_post, rstd_next) -> dict(d_x like
     x, d_y like y, d_gamma_post, d_gamma_next fp32 [H], d_gate fp32 [S, H]; None
     where there is no such norm or gate).  Rows of d_x and d_y outside every
-    sequence are not set."""
+    sequence of a gate are not set, and enter no other gradient."""
     r = saved["r"]
     next_norm = d_xn is not None
     T, H, S, flags, dev, (gp, gt, seq, gn) = _norm_args(
