@@ -34,10 +34,15 @@
 // A row with infinities or NaN has them left out of its digits and added by the
 // epilogue, weight by weight: slow, but what the products give.
 //
-// 256 rows on 63 experts, K = 2048, N = 4096: 55 us (floor 44.6, 0.82 of the memory's
-// rate; 86 with mma.sync).  One row on 8 experts, K = 4096, I = 2048: 20.6 us with the digits,
-// 17.7 of them the product (floor 10.5; starting, the first loads and the joining of parts take
-// the rest).  Four rows on one expert: 11.3.
+// 256 rows on 63 experts, K = 2048, N = 4096: 56 us (floor 44.6, 0.80 of the memory's
+// rate; 86 with mma.sync).  One row on 8 experts, K = 4096, I = 2048: 20-21 us with the digits,
+// 18 of them the product (floor 10.5; starting, the first loads and the joining of parts take
+// the rest).  Four rows on one expert: 11.3-12.7.
+//
+// Beyond 8 rows a group a second tile reads the weights again, and the 96 digit columns a
+// tile cost a third of bf16's rate at best: the FFN on 64 experts, H = 4096, I = 2048, MX,
+// takes 142 us with one row each, 166 with 8, 272 with 16 and 526 with 32; on rows
+// quantised first (csrc/fp4_gemm.cu) 147, 140, 142 and 147.
 //
 // Roles (8 warps): 0 TMA of the weights (which start before the rows' digits are
 // ready), 3 TMA of the digits, 1 MMA, 2 setup, 4-7 epilogue.

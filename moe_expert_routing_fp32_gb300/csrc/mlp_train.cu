@@ -38,10 +38,12 @@
 // What bounds it.  Many rows a group: the MMAs.  A pair's 256 x 256 tile needs 64 bytes
 // a cycle of each multiprocessor for them, all that one gets from L2, so depth of
 // the operands' ring and little else on that way decide.  131072 rows of 64 groups, H = 4096,
-// I = 2048: forward 3.5-3.75 ms (0.94-0.96 of the MMAs' rate), backward 7.2-7.9 (DX 0.96,
-// DW 0.89, DACT 0.83), 8.5 in a loop under the power cap; the flops' floors are 3.5 and
-// 7.0.  Few rows: the weights and their gradients; 509 rows, H = 2048, I = 1024: backward 250
-// us, the bytes' floor 218.  Between, both at once: 32768 rows 647 us, floors 311 and 438.
+// I = 2048: forward 3.5-3.9 ms (0.94-0.96 of the MMAs' rate), backward 7.2-8.2 (DX 0.96,
+// DW 0.89, DACT 0.83); in a loop under the power cap 4.25-4.45 and 8.5-8.9; the flops' floors are
+// 3.5 and 7.0.  Few rows: the weights and their gradients; 509 rows, H = 2048, I = 1024: backward
+// 253 us, the bytes' floor 218.  Between, both at once: 32768 rows 650-664 us, floors 311 and
+// 438.  Gradients in fp32 cost 1.13 (32768 rows) to 1.54 (509) of the bf16 pass, added to
+// what their buffers hold 1.56 to 2.64; their bytes alone say 1.0-1.5 and 1.5-2.5.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -1112,6 +1114,8 @@ bool out_map(CUtensorMap *m, void *ptr, int groups, int64_t rows, int64_t cols, 
 // groups (whole backward pass, us, 256 against 512 columns): 16 rows a group 296 : 280,
 // 64 330 : 295, 128 373 : 360, 256 450 : 456, 512 683 : 713, 1024 1210 : 1245, 2048
 // 2252 : 2278; 16384 rows of H = 4096, I = 2048: one group 1030 : 1006, two 1028 : 1022.
+// The rule takes the mean over all groups, which the host knows; the figures are of groups
+// that all have rows.  A few large ones among many idle get the tiles of few rows.
 bool wide_gradient(int n, int G) { return n < 192ll * G || n >= 8192ll * G; }
 
 template <int MODE, bool WIDE = false>

@@ -21,7 +21,8 @@
 // when a sequence ends, team i's sums of sequence s to slot i + s (both only
 // grow along the rows, so no two meet), and a second kernel adds the slots in a
 // fixed order.  16384 rows of 4096, bf16: 89 us forward (6.0 TB/s), 143 backward (5.6);
-// 50021 of 2048 with an fp32 stream: 308 backward (6.0).  One row: 3.7.
+// 50021 of 2048 with an fp32 stream: 308 backward (6.0); 16384 of 8192, bf16: 183 and 260
+// (5.9 and 6.2).  One row: 3.7.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -35,7 +36,9 @@ namespace {
 
 constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
-constexpr int MAX_CTAS = 304;             // two on each of 152 multiprocessors
+// two on each of 152 multiprocessors; rows of more than 4096 columns leave room for one
+// (their registers), and those CTAs run in two rounds
+constexpr int MAX_CTAS = 304;
 constexpr int MAX_SLOTS = 4;
 constexpr int MAX_H = 8192;
 constexpr int MAX_SMEM = 224 * 1024;      // two rows of 8192 columns, all arrays fp32 that can be
